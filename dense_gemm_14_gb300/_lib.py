@@ -64,6 +64,20 @@ SIGNATURES = {
     "gemm14_workspace_bytes_ex": (ctypes.c_size_t, [_int, _int, _int, _i64, _i64, _i64, _vp, _i64,
                                                     _vp, _i64, _vp, _i64, _int]),
     "gemm14_host_synchronize": (_int, []),
+    "gemm14_linear_ce_forward": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                        _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "gemm14_linear_ce_backward": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                         _vp, _vp, _vp, _i64, _vp, _i64, _vp, ctypes.c_size_t,
+                                         _vp]),
+    "gemm14_linear_ce_workspace_bytes": (ctypes.c_size_t, [_int, _int, _i64, _i64, _i64, _vp, _i64,
+                                                           _vp, _i64, _int]),
+    "gemm14_ckpt8_save": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "gemm14_ckpt8_restore": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "gemm14_ckpt8_wgrad": (_int, [_int, _i64, _i64, _i64, ctypes.c_float, _vp, _i64, _vp, _i64,
+                                  _vp, _i64, ctypes.c_float, _vp, _i64, _vp, ctypes.c_size_t,
+                                  _vp]),
+    "gemm14_ckpt8_wgrad_workspace_bytes": (ctypes.c_size_t, [_int, _i64, _i64, _i64, _vp, _i64,
+                                                             _vp, _i64, _int]),
 }
 
 _lib = None
@@ -241,6 +255,70 @@ def host_synchronize(check=True) -> int:
     if check and st:
         raise Gemm14Error(st, "gemm14_host_synchronize")
     return st
+
+
+def linear_ce_forward(dtype: int, T, V, D, H, ldh, W, ldw, targets, ignore_index, loss, lse,
+                      workspace, workspace_bytes, stream=None, check=True) -> int:
+    """C ABI gemm14_linear_ce_forward on raw device pointers (ints)."""
+    st = int(load().gemm14_linear_ce_forward(dtype, T, V, D, H, ldh, W, ldw, targets, ignore_index,
+                                             loss, lse, workspace, workspace_bytes, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_linear_ce_forward")
+    return st
+
+
+def linear_ce_backward(dtype: int, T, V, D, H, ldh, W, ldw, targets, ignore_index, lse, dloss,
+                       dH, lddh, dW, lddw, workspace, workspace_bytes, stream=None,
+                       check=True) -> int:
+    """C ABI gemm14_linear_ce_backward on raw device pointers (ints; dH or dW may be None)."""
+    st = int(load().gemm14_linear_ce_backward(dtype, T, V, D, H, ldh, W, ldw, targets,
+                                              ignore_index, lse, dloss, dH, lddh, dW, lddw,
+                                              workspace, workspace_bytes, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_linear_ce_backward")
+    return st
+
+
+def linear_ce_workspace_bytes(dtype: int, backward, T, V, D, H, ldh, W, ldw,
+                              sm_count: int = 0) -> int:
+    """C ABI gemm14_linear_ce_workspace_bytes: workspace for these exact operands."""
+    return int(load().gemm14_linear_ce_workspace_bytes(dtype, int(backward), T, V, D, H, ldh, W,
+                                                       ldw, sm_count))
+
+
+def ckpt8_save_raw(dtype: int, rows, cols, X, ldx, Q, ldq, S, lds, stream=None,
+                   check=True) -> int:
+    """C ABI gemm14_ckpt8_save on raw device pointers (ints)."""
+    st = int(load().gemm14_ckpt8_save(dtype, rows, cols, X, ldx, Q, ldq, S, lds, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_ckpt8_save")
+    return st
+
+
+def ckpt8_restore_raw(dtype: int, rows, cols, Q, ldq, S, lds, X, ldx, stream=None,
+                      check=True) -> int:
+    """C ABI gemm14_ckpt8_restore on raw device pointers (ints)."""
+    st = int(load().gemm14_ckpt8_restore(dtype, rows, cols, Q, ldq, S, lds, X, ldx, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_ckpt8_restore")
+    return st
+
+
+def ckpt8_wgrad(dtype: int, T, N, K, alpha, dY, lddy, Q, ldq, S, lds, beta, dW, lddw, workspace,
+                workspace_bytes, stream=None, check=True) -> int:
+    """C ABI gemm14_ckpt8_wgrad on raw device pointers (ints)."""
+    st = int(load().gemm14_ckpt8_wgrad(dtype, T, N, K, alpha, dY, lddy, Q, ldq, S, lds, beta, dW,
+                                       lddw, workspace, workspace_bytes, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_ckpt8_wgrad")
+    return st
+
+
+def ckpt8_wgrad_workspace_bytes(dtype: int, T, N, K, dY, lddy, dW, lddw,
+                                sm_count: int = 0) -> int:
+    """C ABI gemm14_ckpt8_wgrad_workspace_bytes: workspace for these exact operands."""
+    return int(load().gemm14_ckpt8_wgrad_workspace_bytes(dtype, T, N, K, dY, lddy, dW, lddw,
+                                                         sm_count))
 
 
 def last_error_string() -> str:

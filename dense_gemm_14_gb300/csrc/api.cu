@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -615,6 +616,24 @@ int take_device_error() {
 }
 
 void note_cuda_error(const char* what, cudaError_t e) { set_cuda_error(what, e); }
+
+void note_error(const char* format, ...) {
+  va_list v;
+  va_start(v, format);
+  std::vsnprintf(t_last_error, sizeof t_last_error, format, v);
+  va_end(v);
+}
+
+int current_sm_count(int* sm_count) {
+  const DeviceInfo* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st == GEMM14_OK) *sm_count = dev->sm_count;
+  return st;
+}
+
+int finish_launch(cudaError_t e, const char* what, cudaStream_t stream) {
+  return finish(e, what, stream);
+}
 
 }  // namespace gemm14
 

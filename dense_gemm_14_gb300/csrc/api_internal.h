@@ -1,5 +1,6 @@
-// api_internal.h -- what the host-buffer runtime (host_path.cu) uses of the
-// C-ABI layer (api.cu). Nothing here crosses the library boundary.
+// api_internal.h -- what the entry points outside api.cu (host_path.cu,
+// ckpt8.cu, linear_ce.cu) use of the C-ABI layer. Nothing here crosses the
+// library boundary.
 #pragma once
 
 #include <cstddef>
@@ -40,6 +41,16 @@ int current_device_index(int* device);
 // Reads and clears the current device's error word once its kernels are
 // known to be done: GEMM14_OK, GEMM14_ERR_TIMEOUT or GEMM14_ERR_CUDA.
 int take_device_error();
+
+// The current device's SM count, checked as by every entry point (a gemm14_status).
+int current_sm_count(int* sm_count);
+
+// The status of a launch on `stream`: a CUDA failure is recorded as this
+// thread's last error; with GEMM14_DEBUG set, the device error word is read.
+int finish_launch(cudaError_t e, const char* what, cudaStream_t stream);
+
+// Records a message (printf-style) as this thread's last error text.
+void note_error(const char* format, ...);
 
 // Records a CUDA failure as this thread's last error text.
 void note_cuda_error(const char* what, cudaError_t e);

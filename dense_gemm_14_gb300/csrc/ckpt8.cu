@@ -1,0 +1,262 @@
+// ckpt8.cu -- activations kept in 8 bits for the backward pass, and the
+// weight gradient formed from them. The format, per block of 32 consecutive
+// columns of a row (the last block of a row may be shorter):
+//     scale byte s, q[j] in [-127, 127], a value stands for q[j] 2^(s - 133),
+// s the exponent field of the block's largest magnitude as an fp32 (so that
+// |x| 2^(133 - s) < 128), at least 7, and 255 for a block that holds an
+// infinity or a NaN (every value of it then stands for NaN).
+// A power of two as the scale makes q 2^(s - 133) exact in bf16 and fp32 (7
+// significant bits, s >= 7 keeps it a normal number), so a product formed from
+// the restored values adds no error of its own; a value is off by at most
+// half a step of its block, 2^-7 of the block's largest magnitude, or by one
+// step where the largest rounds up to 128 and is held at 127.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gemm14.h"
+#include "api_internal.h"
+#include "kernels.h"
+#include "plan.h"
+#include "ptx.cuh"
+
+namespace gemm14 {
+namespace {
+
+constexpr int kBlock = 32;       // columns that share a scale
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+// The scale byte of a block whose largest magnitude has these fp32 bits (a
+// NaN's bits, sign cleared, compare above every number's).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
+  const uint32_t e = top_bits >> 23;
+  return e < 7u ? 7u : e;
+}
+// x in steps of the block: round to nearest even, held within [-127, 127].
+// factor = 2^(133 - s); a block of byte 255 is kept as zeros.
+__device__ __forceinline__ float scale_factor(uint32_t s) {
+  return s == 255u ? 0.0f : __uint_as_float((260u - s) << 23);
+}
+__device__ __forceinline__ int quantise(float x, float factor) {
+  const int q = __float2int_rn(x * factor);
+  return max(-127, min(127, q));
+}
+// 2^(s - 133), NaN for byte 255; bytes below 7, which save never writes, count as 7.
+__device__ __forceinline__ float step_of(uint32_t s) {
+  return s == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((max(s, 7u) - 6u) << 23);
+}
+
+// One warp a block of 32 columns, a lane a column.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_save_kernel(const T* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
+                      int64_t rows, int64_t cols) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t per_row = (cols + kBlock - 1) / kBlock;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+       i < rows * per_row; i += warps) {
+    const int64_t r = i / per_row, b = i - r * per_row, c = b * kBlock + lane;
+    const float x = c < cols ? to_f32(X[r * ldx + c]) : 0.0f;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu);
+    const uint32_t s = scale_byte(top);
+    if (c < cols)
+      Q[r * ldq + c] = static_cast<int8_t>(s == 255u ? 0 : quantise(x, scale_factor(s)));
+    if (lane == 0) S[r * lds + b] = static_cast<uint8_t>(s);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_restore_kernel(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, T* X,
+                         int64_t ldx, int64_t rows, int64_t cols) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t per_row = (cols + kBlock - 1) / kBlock;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+       i < rows * per_row; i += warps) {
+    const int64_t r = i / per_row, b = i - r * per_row, c = b * kBlock + lane;
+    if (c < cols) X[r * ldx + c] = from_f32<T>(Q[r * ldq + c] * step_of(S[r * lds + b]));
+  }
+}
+
+int grid_for(int64_t rows, int64_t cols, int sm_count) {
+  const int64_t blocks = (rows * ((cols + kBlock - 1) / kBlock) + 7) / 8;
+  const int64_t cap = static_cast<int64_t>(sm_count) * 8;
+  return static_cast<int>(blocks < cap ? blocks : cap);
+}
+
+template <typename T>
+cudaError_t save_as(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
+                    int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
+  return launch_kernel(ckpt8_save_kernel<T>, dim3(grid_for(rows, cols, sms)), dim3(kThreads), 0,
+                       stream, static_cast<const T*>(X), ldx, Q, ldq, S, lds, rows, cols);
+}
+template <typename T>
+cudaError_t restore_as(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, void* X,
+                       int64_t ldx, int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
+  return launch_kernel(ckpt8_restore_kernel<T>, dim3(grid_for(rows, cols, sms)), dim3(kThreads),
+                       0, stream, Q, ldq, S, lds, static_cast<T*>(X), ldx, rows, cols);
+}
+
+cudaError_t launch_restore(int dtype, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,
+                           void* X, int64_t ldx, int64_t rows, int64_t cols, int sms,
+                           cudaStream_t stream) {
+  switch (dtype) {
+    case GEMM14_DTYPE_BF16:
+      return restore_as<__nv_bfloat16>(Q, ldq, S, lds, X, ldx, rows, cols, sms, stream);
+    case GEMM14_DTYPE_F16:
+      return restore_as<__half>(Q, ldq, S, lds, X, ldx, rows, cols, sms, stream);
+    default: return restore_as<float>(Q, ldq, S, lds, X, ldx, rows, cols, sms, stream);
+  }
+}
+
+bool size_ok(int64_t n) { return n >= 0 && n <= INT32_MAX; }
+int64_t at_least_one(int64_t n) { return n > 1 ? n : 1; }
+
+// X, Q and S of save and restore.
+int validate_ckpt8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                   const void* Q, int64_t ldq, const void* S, int64_t lds) {
+  if (dtype != GEMM14_DTYPE_F32 && dtype != GEMM14_DTYPE_BF16 && dtype != GEMM14_DTYPE_F16)
+    return GEMM14_ERR_INVALID_ARG;
+  if (!size_ok(rows) || !size_ok(cols)) return GEMM14_ERR_INVALID_ARG;
+  if (ldx < at_least_one(cols) || ldq < at_least_one(cols) ||
+      lds < at_least_one((cols + kBlock - 1) / kBlock))
+    return GEMM14_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return GEMM14_OK;
+  if (!X || !Q || !S || !aligned(X, elem_bytes_of(dtype))) return GEMM14_ERR_INVALID_ARG;
+  return GEMM14_OK;
+}
+
+// ---- the weight gradient: restored values in the workspace, then a product
+
+struct WgradLayout {
+  int64_t ldx = 0;     // pitch of the restored values (elements)
+  size_t x_off = 0;    // their place, after the product's own region
+  size_t total = 0;
+};
+
+void wgrad_layout(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, int64_t lddy,
+                  const float* dW, int64_t lddw, int sms, WgradLayout* l) {
+  const int eb = elem_bytes_of(dtype);
+  const int64_t q = 16 / eb;
+  l->ldx = (K + q - 1) / q * q;
+  const void* notional = reinterpret_cast<const void*>(uintptr_t(1) << 12);
+  const size_t product = gemm14_workspace_bytes_ex(dtype, 1, 0, N, K, T, dY, lddy, notional,
+                                                   l->ldx, dW, lddw, sms);
+  const size_t flags = streamk_flag_bytes(sms);
+  l->x_off = round256(product > flags ? product : flags);
+  l->total = l->x_off + static_cast<size_t>(T) * l->ldx * eb;
+}
+
+int validate_wgrad(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, int64_t lddy,
+                   const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, const float* dW,
+                   int64_t lddw) {
+  if (!size_ok(T) || !size_ok(K)) return GEMM14_ERR_INVALID_ARG;
+  if (ldq < at_least_one(K) || lds < at_least_one((K + kBlock - 1) / kBlock))
+    return GEMM14_ERR_INVALID_ARG;
+  const bool reads = T > 0 && N > 0 && K > 0;
+  // the product's own checks; its second operand (in the workspace) is always sound
+  const void* sound = reinterpret_cast<const void*>(uintptr_t(1) << 12);
+  const int st = validate_product(dtype, 1, 0, N, K, T, dY, lddy, sound, at_least_one(K), dW, lddw);
+  if (st != GEMM14_OK) return st;
+  if (reads && (!Q || !S)) return GEMM14_ERR_INVALID_ARG;
+  return GEMM14_OK;
+}
+
+}  // namespace
+}  // namespace gemm14
+
+using namespace gemm14;
+
+extern "C" {
+
+int gemm14_ckpt8_save(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ldx, int8_t* Q,
+                      int64_t ldq, uint8_t* S, int64_t lds, void* stream_ptr) {
+  int st = validate_ckpt8(dtype, rows, cols, X, ldx, Q, ldq, S, lds);
+  if (st != GEMM14_OK || rows == 0 || cols == 0) return st;
+  int sms = 0;
+  if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  const cudaError_t e =
+      dtype == GEMM14_DTYPE_BF16
+          ? save_as<__nv_bfloat16>(X, ldx, Q, ldq, S, lds, rows, cols, sms, stream)
+      : dtype == GEMM14_DTYPE_F16 ? save_as<__half>(X, ldx, Q, ldq, S, lds, rows, cols, sms, stream)
+                                  : save_as<float>(X, ldx, Q, ldq, S, lds, rows, cols, sms, stream);
+  return finish_launch(e, "ckpt8 save launch", stream);
+}
+
+int gemm14_ckpt8_restore(int dtype, int64_t rows, int64_t cols, const int8_t* Q, int64_t ldq,
+                         const uint8_t* S, int64_t lds, void* X, int64_t ldx, void* stream_ptr) {
+  int st = validate_ckpt8(dtype, rows, cols, X, ldx, Q, ldq, S, lds);
+  if (st != GEMM14_OK || rows == 0 || cols == 0) return st;
+  int sms = 0;
+  if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  return finish_launch(
+      launch_restore(dtype, Q, ldq, S, lds, X, ldx, rows, cols, sms, stream),
+      "ckpt8 restore launch", stream);
+}
+
+size_t gemm14_ckpt8_wgrad_workspace_bytes(int dtype, int64_t T, int64_t N, int64_t K,
+                                          const void* dY, int64_t lddy, const float* dW,
+                                          int64_t lddw, int sm_count) {
+  if (sm_count <= 0 && current_sm_count(&sm_count) != GEMM14_OK) return 0;
+  const void* sound = reinterpret_cast<const void*>(uintptr_t(1) << 12);
+  if (validate_product(dtype, 1, 0, N, K, T, dY, lddy, sound, at_least_one(K), dW, lddw) !=
+          GEMM14_OK ||
+      T == 0 || N == 0 || K == 0)
+    return 0;
+  WgradLayout l;
+  wgrad_layout(dtype, T, N, K, dY, lddy, dW, lddw, sm_count, &l);
+  return l.total;
+}
+
+int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void* dY,
+                       int64_t lddy, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,
+                       float beta, float* dW, int64_t lddw, void* workspace,
+                       size_t workspace_bytes, void* stream_ptr) {
+  int st = validate_wgrad(dtype, T, N, K, dY, lddy, Q, ldq, S, lds, dW, lddw);
+  if (st != GEMM14_OK) return st;
+  if (workspace && !aligned(workspace, 16)) return GEMM14_ERR_INVALID_ARG;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (T == 0 || N == 0 || K == 0 || alpha == 0.0f)  // no product term: dW = beta dW
+    return product_on_stream(dtype, 1, 0, N, K, 0, alpha, nullptr, at_least_one(N), nullptr,
+                             at_least_one(K), beta, dW, lddw, nullptr, 0, stream);
+  int sms = 0;
+  if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
+  WgradLayout l;
+  wgrad_layout(dtype, T, N, K, dY, lddy, dW, lddw, sms, &l);
+  if (!workspace || workspace_bytes < l.total) {
+    note_error("gemm14_ckpt8_wgrad: %zu bytes of workspace given, %zu needed", workspace_bytes,
+               l.total);
+    return GEMM14_ERR_INVALID_ARG;
+  }
+  void* X = static_cast<char*>(workspace) + l.x_off;
+  const cudaError_t e = launch_restore(dtype, Q, ldq, S, lds, X, l.ldx, T, K, sms, stream);
+  if (e != cudaSuccess) return finish_launch(e, "ckpt8 restore launch", stream);
+  return product_on_stream(dtype, 1, 0, N, K, T, alpha, dY, lddy, X, l.ldx, beta, dW, lddw,
+                           workspace, l.x_off, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,214 @@
+"""Tensor-level calls of the training products: softmax cross entropy over a
+projection's outputs, and activations kept in 8 bits (argument marshalling
+only; every step runs in the library's CUDA kernels)."""
+from __future__ import annotations
+
+import contextlib
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from .api import _CODE, _FP32_MODES, _workspace
+
+CKPT8_BLOCK = 32  # columns of a row that share a scale
+
+
+def _code(x: torch.Tensor, fp32_mode: str | None) -> int:
+    if x.dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if fp32_mode not in _FP32_MODES or (fp32_mode not in (None, "fp32") and x.dtype != torch.float32):
+        raise ValueError(f"fp32_mode {fp32_mode!r} needs float32 inputs and one of {list(_FP32_MODES)}")
+    return _FP32_MODES[fp32_mode] if x.dtype == torch.float32 else _CODE[x.dtype]
+
+
+@contextlib.contextmanager
+def _on(stream, device: torch.device):
+    """The stream handle of a call, with that stream current inside: what the
+    call allocates then belongs to the stream its kernels run on."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield torch.cuda.current_stream(device).cuda_stream
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield stream.cuda_stream
+
+
+def _matrix(x: torch.Tensor, name: str, device: torch.device | None = None) -> int:
+    """The row pitch of a row-major CUDA matrix."""
+    if not x.is_cuda or (device is not None and x.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor on the operands' device")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(x.shape)}")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows (row-major)")
+    if rows > 1 and x.stride(0) < max(cols, 1):
+        raise ValueError(f"{name}: rows overlap (stride {x.stride()})")
+    return max(x.stride(0), cols, 1) if rows > 1 else max(cols, 1)
+
+
+def _vector(x: torch.Tensor, name: str, n: int, dtype: torch.dtype, device: torch.device) -> None:
+    if x.device != device or x.dtype != dtype or tuple(x.shape) != (n,) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA vector of {n} values on the "
+                         f"operands' device, got {x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def _ptr(x: torch.Tensor | None) -> int | None:
+    return x.data_ptr() if x is not None and x.numel() else None
+
+
+def _ce_operands(h, w, targets, fp32_mode):
+    code = _code(h, fp32_mode)
+    if w.dtype != h.dtype:
+        raise TypeError(f"h and w differ in dtype: {h.dtype}, {w.dtype}")
+    ldh, ldw = _matrix(h, "h"), _matrix(w, "w", h.device)
+    (T, D), (V, D2) = h.shape, w.shape
+    if D != D2 or V < 1 or D < 1:
+        raise ValueError(f"shape mismatch: h {tuple(h.shape)}, w {tuple(w.shape)}")
+    _vector(targets, "targets", T, torch.int64, h.device)
+    return code, T, V, D, ldh, ldw
+
+
+def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                         ignore_index: int = -100, stream=None, fp32_mode: str | None = None
+                         ) -> tuple[torch.Tensor, torch.Tensor]:
+    """(loss, lse) of softmax cross entropy on the logits h @ w.T, which are
+    formed in pieces of the vocabulary and never kept (gemm14_linear_ce_forward).
+
+    h: (T, D) and w: (V, D) in float32, bfloat16 or float16, row-major views on
+    one GPU; targets: (T,) int64. loss, lse: (T,) float32, 0 for rows whose
+    target is ignore_index; a target outside [0, V) gives NaN. Keep lse for
+    linear_cross_entropy_backward. Runs on `stream` (default: torch's current
+    stream) without synchronising, with a workspace cached per (device, stream).
+    fp32_mode as for gemm_into."""
+    code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
+    with _on(stream, h.device) as handle:
+        out = torch.empty((2, T), dtype=torch.float32, device=h.device)
+        if T:
+            n = _lib.linear_ce_workspace_bytes(code, 0, T, V, D, h.data_ptr(), ldh, w.data_ptr(),
+                                               ldw)
+            ws = _workspace(h.device, handle, n)
+            _lib.linear_ce_forward(code, T, V, D, h.data_ptr(), ldh, w.data_ptr(), ldw,
+                                   targets.data_ptr(), int(ignore_index), out.data_ptr(),
+                                   out.data_ptr() + 4 * T, ws.data_ptr(), ws.numel(), handle)
+    return out[0], out[1]
+
+
+def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                                  lse: torch.Tensor, dloss: torch.Tensor,
+                                  ignore_index: int = -100, need_dh: bool = True,
+                                  need_dw: bool = True, stream=None,
+                                  fp32_mode: str | None = None
+                                  ) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """(dh, dw): the gradients of sum_t dloss[t] * loss[t] in h and w, in their
+    dtype (gemm14_linear_ce_backward). lse: the forward call's; dloss: (T,)
+    float32. Rows that take no part get zero rows in dh and add nothing to dw.
+    need_dh / need_dw: a gradient not needed is not formed (None)."""
+    code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
+    _vector(lse, "lse", T, torch.float32, h.device)
+    _vector(dloss, "dloss", T, torch.float32, h.device)
+    with _on(stream, h.device) as handle:
+        dh = torch.empty((T, D), dtype=h.dtype, device=h.device) if need_dh else None
+        dw = torch.empty((V, D), dtype=w.dtype, device=w.device) if need_dw else None
+        if need_dw or (need_dh and T):
+            n = _lib.linear_ce_workspace_bytes(code, 1, T, V, D, h.data_ptr(), ldh, w.data_ptr(),
+                                               ldw) if T else 0
+            ws = _workspace(h.device, handle, n) if n else None
+            _lib.linear_ce_backward(code, T, V, D, _ptr(h), ldh, w.data_ptr(), ldw, _ptr(targets),
+                                    int(ignore_index), _ptr(lse), _ptr(dloss), _ptr(dh), D,
+                                    _ptr(dw), D, ws.data_ptr() if n else None,
+                                    ws.numel() if n else 0, handle)
+    return dh, dw
+
+
+@dataclass(frozen=True)
+class Ckpt8:
+    """A matrix kept in 8 bits: q (rows, cols) int8 and a scale byte for each
+    block of 32 columns, scale (rows, ceil(cols / 32)) uint8; a value stands
+    for q * 2**(scale - 133). Both are row-major views; 16-byte aligned rows
+    (as ckpt8_save allocates them) give the fastest accesses."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def shape(self) -> torch.Size:
+        return self.q.shape
+
+
+def _ckpt8_operands(c: Ckpt8) -> tuple[int, int]:
+    ldq = _matrix(c.q, "q")
+    lds = _matrix(c.scale, "scale", c.q.device)
+    rows, cols = c.q.shape
+    if c.q.dtype != torch.int8 or c.scale.dtype != torch.uint8 or \
+            tuple(c.scale.shape) != (rows, -(-cols // CKPT8_BLOCK)):
+        raise ValueError(f"q must be int8 (rows, cols) and scale uint8 (rows, ceil(cols / 32)), got "
+                         f"{c.q.dtype} {tuple(c.q.shape)}, {c.scale.dtype} {tuple(c.scale.shape)}")
+    return ldq, lds
+
+
+def ckpt8_save(x: torch.Tensor, stream=None) -> Ckpt8:
+    """x (rows, cols), float32, bfloat16 or float16, kept in 8 bits (gemm14_ckpt8_save)."""
+    if x.dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    blocks = -(-cols // CKPT8_BLOCK)
+    ldq, lds = -(-cols // 16) * 16, -(-blocks // 16) * 16
+    with _on(stream, x.device) as handle:
+        # rows of both on 16 bytes
+        q = torch.empty((rows, ldq), dtype=torch.int8, device=x.device)[:, :cols]
+        scale = torch.empty((rows, lds), dtype=torch.uint8, device=x.device)[:, :blocks]
+        if x.numel():
+            _lib.ckpt8_save_raw(_CODE[x.dtype], rows, cols, x.data_ptr(), ldx, q.data_ptr(), ldq,
+                                scale.data_ptr(), lds, handle)
+    return Ckpt8(q, scale)
+
+
+def ckpt8_restore(c: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values of a checkpoint as a (rows, cols) tensor of dtype (gemm14_ckpt8_restore)."""
+    if dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {dtype}")
+    ldq, lds = _ckpt8_operands(c)
+    rows, cols = c.q.shape
+    with _on(stream, c.q.device) as handle:
+        out = torch.empty((rows, cols), dtype=dtype, device=c.q.device)
+        if out.numel():
+            _lib.ckpt8_restore_raw(_CODE[dtype], rows, cols, c.q.data_ptr(), ldq,
+                                   c.scale.data_ptr(), lds, out.data_ptr(), cols, handle)
+    return out
+
+
+def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = None,
+                      alpha: float = 1.0, beta: float = 0.0, stream=None,
+                      fp32_mode: str | None = None) -> torch.Tensor:
+    """out = alpha * dy.T @ x + beta * out, x the values of the checkpoint: the
+    weight gradient of y = x @ w.T (gemm14_ckpt8_wgrad). dy: (T, N) in float32,
+    bfloat16 or float16; out: (N, K) float32, row-major, allocated if not given
+    (beta is then 0). beta = 1 adds to the gradient that is there."""
+    code = _code(dy, fp32_mode)
+    lddy = _matrix(dy, "dy")
+    ldq, lds = _ckpt8_operands(c)
+    (T, N), (T2, K) = dy.shape, c.q.shape
+    if T != T2 or c.q.device != dy.device:
+        raise ValueError(f"dy {tuple(dy.shape)} and the checkpoint {tuple(c.q.shape)} differ in "
+                         "rows or device")
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs out")
+    elif out.dtype != torch.float32 or tuple(out.shape) != (N, K):
+        raise ValueError(f"out must be float32 of shape {(N, K)}")
+    with _on(stream, dy.device) as handle:
+        if out is None:
+            out = torch.empty((N, K), dtype=torch.float32, device=dy.device)
+        lddw = _matrix(out, "out", dy.device)
+        if not out.numel():
+            return out
+        n = _lib.ckpt8_wgrad_workspace_bytes(code, T, N, K, _ptr(dy), lddy, out.data_ptr(), lddw)
+        ws = _workspace(dy.device, handle, n) if n else None
+        _lib.ckpt8_wgrad(code, T, N, K, float(alpha), _ptr(dy), lddy, _ptr(c.q), ldq,
+                         _ptr(c.scale), lds, float(beta), out.data_ptr(), lddw,
+                         ws.data_ptr() if n else None, ws.numel() if n else 0, handle)
+    return out

@@ -343,6 +343,106 @@ int gemm14_host_wait(uint64_t ticket);
 /* Waits for every host-buffer call in flight (on every device), as gemm14_host_wait. */
 int gemm14_host_synchronize(void);
 
+/*
+ * Softmax cross entropy of a projection's outputs, without keeping them: with
+ * z_t = H[t] W^T the V logits of row t (H is T x D, W is V x D, a row per
+ * entry of the vocabulary),
+ *     lse[t]  = log sum_v exp z_tv,      loss[t] = lse[t] - z_t,targets[t].
+ * The logits are formed and folded away in pieces of the vocabulary; no buffer
+ * of T x V values exists. Each row's statistics are held in fp32.
+ * dtype: the element type of H and W and the arithmetic of the products, as
+ * for gemm14_gemm_ex (F32, BF16, F16, TF32, F32_3XTF32). loss and lse: T fp32.
+ * targets: T int64 on the device. A row whose target is ignore_index takes no
+ * part: its loss and lse are 0 and nothing its row of H holds is used. Any
+ * other target outside [0, V) gives a loss of NaN. A NaN or infinity among a
+ * row's logits makes that row's results NaN and no other's.
+ * workspace: caller-owned, 16-byte aligned, zero-filled before its first use
+ * (one kept for the *_ws calls serves, and the other way round),
+ * gemm14_linear_ce_workspace_bytes(...) bytes at least; a smaller one is
+ * GEMM14_ERR_INVALID_ARG, and gemm14_last_error_string says how many are
+ * needed. Sizes: T >= 0 (0: nothing is done), V >= 1, D >= 1, ldh >= D,
+ * ldw >= D. Other rules (device pointers, stream, errors) as above.
+ */
+int gemm14_linear_ce_forward(int dtype, int64_t T, int64_t V, int64_t D, const void* H,
+                             int64_t ldh, const void* W, int64_t ldw, const int64_t* targets,
+                             int64_t ignore_index, float* loss, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients: with dloss[t] the gradient of the caller's objective in
+ * loss[t] (any reduction or weighting: 1/n for a mean over n rows) and
+ *     dZ_tv = (exp(z_tv - lse[t]) - [v == targets[t]]) dloss[t],
+ *     dH = dZ W  (T x D, pitch lddh),      dW = dZ^T H  (V x D, pitch lddw),
+ * written in the element type of H and W. The logits are formed again, a piece
+ * of the vocabulary at a time, from H, W and the forward call's lse. dH or dW
+ * may be NULL: that gradient is not formed. Rows that take no part (target
+ * ignore_index, or dloss[t] == 0) get dH[t] = 0 and add nothing to dW, also
+ * when their rows of H hold NaN; a target outside [0, V) makes its row of dH
+ * and all of dW NaN. T == 0 sets dW to zero.
+ * Rounding: 16-bit dtypes hold dZ in that type, relative to the largest
+ * |dloss[t]|, for the two products, which accumulate in fp32; each gradient is
+ * rounded once to the type. fp32 dtypes hold dZ in fp32.
+ * Arguments and workspace as for the forward call.
+ */
+int gemm14_linear_ce_backward(int dtype, int64_t T, int64_t V, int64_t D, const void* H,
+                              int64_t ldh, const void* W, int64_t ldw, const int64_t* targets,
+                              int64_t ignore_index, const float* lse, const float* dloss, void* dH,
+                              int64_t lddh, void* dW, int64_t lddw, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes of the forward (backward == 0) or backward call on exactly
+ * these operands (pointers are only inspected for NULL and alignment; no CUDA
+ * call is made when sm_count > 0). 0: T == 0, or the arguments are invalid.
+ */
+size_t gemm14_linear_ce_workspace_bytes(int dtype, int backward, int64_t T, int64_t V, int64_t D,
+                                        const void* H, int64_t ldh, const void* W, int64_t ldw,
+                                        int sm_count);
+
+/*
+ * Activations kept in 8 bits for the backward pass. Each block of 32
+ * consecutive columns of a row (the last of a row may be shorter) has a scale
+ * byte s, and each value a whole number q in [-127, 127]; the value kept is
+ *     q * 2^(s - 133),
+ * s the exponent field of the block's largest magnitude (as an fp32), at least
+ * 7; q = x * 2^(133 - s) rounded to nearest, ties to even, and held at +-127.
+ * So a value is off by at most 2^-7 of its block's largest magnitude (by
+ * 2^-6 where it rounds to 128 and is held). s = 255: the block held an infinity
+ * or a NaN; all of it is restored as NaN.
+ *   save:    X (rows x cols, pitch ldx, dtype F32, BF16 or F16) -> Q (pitch
+ *            ldq >= cols) and S (rows x ceil(cols / 32), pitch lds);
+ *   restore: Q and S -> X in any of the three types (exact in F32 and BF16;
+ *            F16 rounds, which is exact too for what was saved from F16).
+ * Bases and pitches of 16 bytes give the fastest accesses; any are allowed.
+ * rows or cols of 0: nothing is done. Other rules as above.
+ */
+int gemm14_ckpt8_save(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ldx, int8_t* Q,
+                      int64_t ldq, uint8_t* S, int64_t lds, void* stream);
+int gemm14_ckpt8_restore(int dtype, int64_t rows, int64_t cols, const int8_t* Q, int64_t ldq,
+                         const uint8_t* S, int64_t lds, void* X, int64_t ldx, void* stream);
+
+/*
+ * The weight gradient of a projection y = x W^T from its input kept in 8 bits:
+ *     dW = alpha * dY^T X + beta * dW,
+ * dY a T x N matrix (pitch lddy) of dtype, X the T x K values that Q and S
+ * (pitches ldq, lds, as written by gemm14_ckpt8_save) stand for, dW an N x K
+ * fp32 matrix (pitch lddw). dtype selects dY's element type and the product's
+ * arithmetic as for gemm14_gemm_ex; with 16-bit types X enters the product
+ * exactly (F16: rounded where it leaves fp16's range) and sums are fp32.
+ * beta == 0: dW is not read; alpha == 0 or T == 0: dY and the checkpoint are
+ * not read. workspace: as for the *_ws calls, but needed:
+ * gemm14_ckpt8_wgrad_workspace_bytes(...) bytes at least.
+ */
+int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void* dY,
+                       int64_t lddy, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,
+                       float beta, float* dW, int64_t lddw, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Its workspace bytes on these operands (0: none needed, or invalid arguments). */
+size_t gemm14_ckpt8_wgrad_workspace_bytes(int dtype, int64_t T, int64_t N, int64_t K,
+                                          const void* dY, int64_t lddy, const float* dW,
+                                          int64_t lddw, int sm_count);
+
 /* Launch plan chosen for a call (host-side only; no CUDA call is made). */
 typedef struct gemm14_plan {
   int kernel;     /* 1 = fp32 SIMT (FFMA), 2 = tcgen05 on one SM per tile,
