@@ -631,6 +631,26 @@ int current_sm_count(int* sm_count) {
   return st;
 }
 
+int call_context(CallContext* c) {
+  c->fault = t_fault;
+  c->wait_limit_ns = t_wait_limit_ns ? t_wait_limit_ns : kWaitTimeoutNs;
+  t_fault = kFaultNone;
+  t_wait_limit_ns = 0;
+  const DeviceInfo* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st != GEMM14_OK) return st;
+  c->sm_count = dev->sm_count;
+  c->err = dev->err_word;
+  return GEMM14_OK;
+}
+
+int map_16bit(CUtensorMap* map, bool bf16, const void* base, int64_t rows, int64_t cols,
+              int64_t ld, int box_rows) {
+  return make_map(map,
+                  bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  base, rows, cols, ld, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 int finish_launch(cudaError_t e, const char* what, cudaStream_t stream) {
   return finish(e, what, stream);
 }

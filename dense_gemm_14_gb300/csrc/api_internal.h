@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace gemm14 {
@@ -44,6 +45,21 @@ int take_device_error();
 
 // The current device's SM count, checked as by every entry point (a gemm14_status).
 int current_sm_count(int* sm_count);
+
+// What a call's own kernels need of the current device and of this thread's
+// pending gemm14_debug_inject request, which the call consumes.
+struct CallContext {
+  int sm_count = 0;
+  unsigned* err = nullptr;              // the device error word
+  unsigned long long wait_limit_ns = 0;
+  int fault = 0;
+};
+int call_context(CallContext* c);
+
+// A row-major rows x cols matrix of 16-bit elements (pitch ld) as a tensor map
+// of boxes 64 columns wide and box_rows high, 128-byte swizzle, zeros out of range.
+int map_16bit(CUtensorMap* map, bool bf16, const void* base, int64_t rows, int64_t cols,
+              int64_t ld, int box_rows);
 
 // The status of a launch on `stream`: a CUDA failure is recorded as this
 // thread's last error; with GEMM14_DEBUG set, the device error word is read.

@@ -21,6 +21,7 @@
 #include "kernels.h"
 #include "plan.h"
 #include "ptx.cuh"
+#include "train_tc.h"
 
 namespace gemm14 {
 namespace {
@@ -150,23 +151,48 @@ int validate_ckpt8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t
 
 // ---- the weight gradient: restored values in the workspace, then a product
 
+// 16-bit dY, and fp32 dY in the split-precision mode (as three bf16 parts),
+// run on the tensor-core kernel of train_tc.cu; the FFMA and TF32 modes on the
+// library's products, with the values restored in fp32.
 struct WgradLayout {
-  int64_t ldx = 0;     // pitch of the restored values (elements)
-  size_t x_off = 0;    // their place, after the product's own region
-  size_t total = 0;
+  bool tc = false;
+  int parts = 1;           // bf16 parts of dY
+  bool copy_dy = false;    // dY is copied (unaligned) or split
+  int splits = 1;          // ranges of T
+  int64_t ldx = 0, lddy = 0;
+  size_t x_off = 0, dy_off = 0, slots_off = 0, total = 0;
 };
 
 void wgrad_layout(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, int64_t lddy,
                   const float* dW, int64_t lddw, int sms, WgradLayout* l) {
-  const int eb = elem_bytes_of(dtype);
-  const int64_t q = 16 / eb;
-  l->ldx = (K + q - 1) / q * q;
-  const void* notional = reinterpret_cast<const void*>(uintptr_t(1) << 12);
-  const size_t product = gemm14_workspace_bytes_ex(dtype, 1, 0, N, K, T, dY, lddy, notional,
-                                                   l->ldx, dW, lddw, sms);
-  const size_t flags = streamk_flag_bytes(sms);
-  l->x_off = round256(product > flags ? product : flags);
-  l->total = l->x_off + static_cast<size_t>(T) * l->ldx * eb;
+  *l = WgradLayout{};
+  l->tc = dtype != GEMM14_DTYPE_F32 && dtype != GEMM14_DTYPE_TF32;
+  size_t at = streamk_flag_bytes(sms);
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = round256(at + bytes);
+    return here;
+  };
+  if (!l->tc) {
+    l->ldx = (K + 3) / 4 * 4;
+    const void* notional = reinterpret_cast<const void*>(uintptr_t(1) << 12);
+    const size_t product = gemm14_workspace_bytes_ex(dtype, 1, 0, N, K, T, dY, lddy, notional,
+                                                     l->ldx, dW, lddw, sms);
+    at = round256(product > at ? product : at);
+    l->x_off = take(static_cast<size_t>(T) * l->ldx * 4);
+    l->total = at;
+    return;
+  }
+  l->parts = dtype == GEMM14_DTYPE_F32_3XTF32 ? 3 : 1;
+  l->copy_dy = l->parts == 3 || !aligned(dY, 16) || lddy % 8 != 0;
+  l->ldx = (K + 7) / 8 * 8;
+  l->lddy = l->copy_dy ? (N + 7) / 8 * 8 : lddy;
+  l->x_off = take(static_cast<size_t>(T) * l->ldx * 2);
+  if (l->copy_dy) l->dy_off = take(static_cast<size_t>(T) * l->lddy * 2 * l->parts);
+  const int64_t tiles = ((N + 255) / 256) * ((K + 255) / 256);
+  l->splits = train_splits(tiles, (T + 63) / 64, sms > 1 ? sms / 2 : 1, 64);
+  if (l->splits > 1) l->slots_off = take(static_cast<size_t>(l->splits) * tiles * 256 * 256 * 4);
+  l->total = at;
 }
 
 int validate_wgrad(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, int64_t lddy,
@@ -182,6 +208,66 @@ int validate_wgrad(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, i
   if (st != GEMM14_OK) return st;
   if (reads && (!Q || !S)) return GEMM14_ERR_INVALID_ARG;
   return GEMM14_OK;
+}
+
+int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void* dY,
+             int64_t lddy, float beta, float* dW, int64_t lddw, char* ws, const WgradLayout& l,
+             cudaStream_t stream) {
+  CallContext ctx;
+  int st = call_context(&ctx);
+  if (st != GEMM14_OK) return st;
+  const int clusters = train_max_clusters();
+  if (clusters <= 0) {
+    note_error("gemm14_ckpt8_wgrad: clusters of two CTAs cannot run on this device");
+    return GEMM14_ERR_CUDA;
+  }
+  const void* dy = l.copy_dy ? ws + l.dy_off : dY;
+  if (l.copy_dy) {
+    const RepitchJob job{dY, lddy, ws + l.dy_off, l.lddy, T, N, 0, nullptr}, none{};
+    const cudaError_t e =
+        l.parts == 3 ? launch_split3(static_cast<const float*>(dY), lddy, T, N, ws + l.dy_off,
+                                     l.lddy, T * l.lddy, ctx.sm_count, stream)
+                     : launch_repitch(job, none, 2, ctx.sm_count, stream);
+    if (e != cudaSuccess) return finish_launch(e, "ckpt8 copy launch", stream);
+  }
+  TrainArgs a{};
+  a.M = static_cast<int>(N);
+  a.N = static_cast<int>(K);
+  a.K = static_cast<int>(T);
+  a.splits = l.splits;
+  a.err = ctx.err;
+  a.wait_limit_ns = ctx.wait_limit_ns;
+  a.fault = ctx.fault;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.out = dW;
+  a.ld_out = lddw;
+  a.elem = kElemF32;
+  a.out_vec = aligned(dW, 16) && lddw % 4 == 0;
+  a.slots = reinterpret_cast<float4*>(ws + l.slots_off);
+  TrainMaps maps;
+  const TrainOperand A{dy, T, N, l.lddy, l.parts, T * l.lddy};
+  const TrainOperand B{ws + l.x_off, T, K, l.ldx, 1, 0};
+  if ((st = train_operands(dtype != GEMM14_DTYPE_F16, A, true, B, true, &maps, &a)) != GEMM14_OK)
+    return st;
+  const int64_t items = ((N + 255) / 256) * ((K + 255) / 256) * l.splits;
+  const int grid = static_cast<int>(items < clusters ? items : clusters);
+  const bool promote = (T + 63) / 64 > static_cast<int64_t>(TrainShape::CHUNK) * l.splits;
+  st = finish_launch(launch_train_tc(l.splits > 1 ? kTrainSlots : kTrainOut, promote, maps, a,
+                                     grid, stream),
+                     "ckpt8 product launch", stream);
+  if (st != GEMM14_OK || l.splits == 1) return st;
+  SlotsOut s{};
+  s.slots = a.slots;
+  s.splits = l.splits;
+  s.M = a.M;
+  s.N = a.N;
+  s.alpha = alpha;
+  s.beta = beta;
+  s.out = dW;
+  s.ld = lddw;
+  s.elem = kElemF32;
+  return finish_launch(launch_slots_out(s, stream), "ckpt8 output launch", stream);
 }
 
 }  // namespace
@@ -252,9 +338,12 @@ int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, 
                l.total);
     return GEMM14_ERR_INVALID_ARG;
   }
-  void* X = static_cast<char*>(workspace) + l.x_off;
-  const cudaError_t e = launch_restore(dtype, Q, ldq, S, lds, X, l.ldx, T, K, sms, stream);
+  char* ws = static_cast<char*>(workspace);
+  void* X = ws + l.x_off;
+  const int kept_as = !l.tc ? GEMM14_DTYPE_F32 : l.parts == 3 ? GEMM14_DTYPE_BF16 : dtype;
+  const cudaError_t e = launch_restore(kept_as, Q, ldq, S, lds, X, l.ldx, T, K, sms, stream);
   if (e != cudaSuccess) return finish_launch(e, "ckpt8 restore launch", stream);
+  if (l.tc) return wgrad_tc(dtype, T, N, K, alpha, dY, lddy, beta, dW, lddw, ws, l, stream);
   return product_on_stream(dtype, 1, 0, N, K, T, alpha, dY, lddy, X, l.ldx, beta, dW, lddw,
                            workspace, l.x_off, stream);
 }

@@ -5,10 +5,24 @@
 //     lse_t  = log sum_v exp z_tv          loss_t = lse_t - z_t,y(t)
 //     dZ_tv  = (exp(z_tv - lse_t) - [v = y_t]) g_t
 //     dH     = dZ W                        dW     = dZ^T H.
-// The logits exist only a piece of the vocabulary at a time: the forward pass
-// folds each piece into a running maximum and sum per row, the backward pass
-// forms each piece again from H, W and lse_t, turns it into dZ and multiplies
-// it into dH (summed over the pieces in fp32) and into the piece's rows of dW.
+//
+// 16-bit operands, and fp32 ones in the split-precision mode, run on the
+// tensor-core kernel of train_tc.cu. Its epilogues take the logits where they
+// are, in tensor memory: the forward pass keeps of each tile a maximum and a sum
+// per row, merged at the end; the backward pass forms the logits again from H,
+// W and lse, a piece of the vocabulary at a time, writes the piece of dZ (16
+// bits, or three bf16 parts), and multiplies it into dH (fp32 sums over the
+// pieces) and into the piece's rows of dW. What a step reads and writes beside
+// its 8 n V D operations of products (n rows that take part; 2 of the 8 form the
+// logits again) is small against them from a few hundred rows on, so the
+// products bound it; below that, reading W does.
+// Rows that take no part are left out before the products: a first kernel
+// numbers the others, a second gathers their rows of H, and every later one
+// reads their number on the device, so a batch that is mostly prompt costs what
+// its answers cost, and nothing that an ignored row holds is ever multiplied.
+//
+// fp32 operands in the FFMA and TF32 modes take the library's products, a
+// piece of fp32 logits at a time, with row kernels between them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -22,22 +36,12 @@
 #include "kernels.h"
 #include "plan.h"
 #include "ptx.cuh"
+#include "train_tc.h"
 
 namespace gemm14 {
 namespace {
 
 constexpr int kThreads = 256;
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
 // Sum of exponentials held as top + log(sum): (m, l) stands for l exp(m).
 struct ExpSum {
@@ -49,7 +53,183 @@ __device__ __forceinline__ ExpSum merge(ExpSum a, ExpSum b) {
   return {m, a.l * __expf(a.m - m) + b.l * __expf(b.m - m)};
 }
 
-// ---- row passes over a piece of logits (Z: T x C, pitch ldz, columns v0 ..)
+// ---- rows in use
+
+// Numbers the rows that take part (in order): *n of them, row i of them from
+// row index[i] of the batch, position[t] = i or -1; and their data: the target
+// as a column (-1 where it is no row of W), and for the gradient lse and the
+// coefficient. For 16-bit dZ that is g_t / ref * unit with ref = max |g_t|
+// over the rows that take part: dZ then lies in [-unit, unit] whatever the
+// scale of the objective, and the products are multiplied by *back = ref / unit
+// at the end. One block: 8192 rows a turn, each thread 8 of them.
+struct Rows {
+  int* n;
+  float* back;
+  int* index;
+  int* position;
+  int* target;
+  float* lse;
+  float* coef;
+};
+constexpr int kRowsPerThread = 8;
+
+__global__ void __launch_bounds__(1024)
+    ce_rows_kernel(const int64_t* targets, int64_t ignore, const float* lse, const float* g,
+                   int64_t T, int64_t V, bool relative, float unit, Rows out) {
+  __shared__ int count[kRowsPerThread * 32];
+  __shared__ float part[32];
+  __shared__ int total;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float ref = 0.0f;
+  if (relative) {
+    for (int64_t t = threadIdx.x; t < T; t += 1024)
+      if (targets[t] != ignore) ref = fmaxf(ref, fabsf(g[t]));
+    for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    if (lane == 0) part[warp] = ref;
+    __syncthreads();
+    ref = 0.0f;
+    for (int w = 0; w < 32; ++w) ref = fmaxf(ref, part[w]);
+  }
+  if (!(ref > 0.0f && ref < INFINITY)) ref = 1.0f;
+  int base = 0;
+  for (int64_t t0 = 0; t0 < T; t0 += 1024 * kRowsPerThread) {
+    int64_t y[kRowsPerThread];
+    float k[kRowsPerThread];
+    unsigned mask[kRowsPerThread];
+#pragma unroll
+    for (int j = 0; j < kRowsPerThread; ++j) {
+      const int64_t t = t0 + 1024 * j + threadIdx.x;
+      y[j] = t < T ? targets[t] : ignore;
+      k[j] = g && t < T ? g[t] : 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsPerThread; ++j) {
+      mask[j] = __ballot_sync(0xffffffffu, y[j] != ignore && k[j] != 0.0f);
+      if (lane == 0) count[32 * j + warp] = __popc(mask[j]);
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive sums of the 256 counts
+      int c[kRowsPerThread], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kRowsPerThread; ++j) {
+        c[j] = sum;
+        sum += count[kRowsPerThread * lane + j];
+      }
+      int before = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      if (lane == 31) total = before;
+      before -= sum;
+#pragma unroll
+      for (int j = 0; j < kRowsPerThread; ++j) count[kRowsPerThread * lane + j] = before + c[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kRowsPerThread; ++j) {
+      const int64_t t = t0 + 1024 * j + threadIdx.x;
+      if (t >= T) continue;
+      const bool used = (mask[j] >> lane) & 1u;
+      const int i = base + count[32 * j + warp] + __popc(mask[j] & ((1u << lane) - 1u));
+      out.position[t] = used ? i : -1;
+      if (!used) continue;
+      const bool sound = y[j] >= 0 && y[j] < V;
+      out.index[i] = static_cast<int>(t);
+      out.target[i] = sound ? static_cast<int>(y[j]) : -1;
+      if (g) {
+        out.lse[i] = lse[t];
+        out.coef[i] = sound ? k[j] / ref * unit : __uint_as_float(0x7fc00000u);
+      }
+    }
+    base += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    *out.n = base;
+    *out.back = ref / unit;
+  }
+}
+
+// The rows of H in use, one after the other (E = float: as three bf16 parts),
+// zeros up to the next multiple of 64 rows (a product over the rows reads whole
+// k-blocks), and zeros into the rows of dH (where given) that take no part.
+// Block b < T: row b of the batch; the 64 after that: rows past the last.
+template <typename E>
+__global__ void __launch_bounds__(256)
+    ce_gather_kernel(const E* H, int64_t ldh, int64_t T, int64_t D, const int* n,
+                     const int* position, uint16_t* out, int64_t ldo, int64_t part_stride, E* dH,
+                     int64_t lddh, bool vec) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  constexpr int kParts = sizeof(E) == 4 ? 3 : 1;
+  const int64_t b = blockIdx.x;
+  if (b >= T) {
+    const int64_t r = *n + (b - T);
+    if (r >= (*n + 63) / 64 * 64) return;
+    for (int p = 0; p < kParts; ++p)
+      for (int64_t c = threadIdx.x; c < D; c += blockDim.x)
+        out[p * part_stride + r * ldo + c] = 0;
+    return;
+  }
+  const int i = position[b];
+  if (i < 0) {
+    if (dH)
+      for (int64_t c = threadIdx.x; c < D; c += blockDim.x) dH[b * lddh + c] = E(0);
+    return;
+  }
+  const E* h = H + b * ldh;
+  uint16_t* o = out + i * ldo;
+  if constexpr (kParts == 1) {
+    const int64_t whole = vec ? D / 8 : 0;  // 16-byte pieces
+    for (int64_t c = threadIdx.x; c < whole; c += blockDim.x)
+      reinterpret_cast<uint4*>(o)[c] = reinterpret_cast<const uint4*>(h)[c];
+    for (int64_t c = 8 * whole + threadIdx.x; c < D; c += blockDim.x) o[c] = h[c];
+  } else {
+    for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
+      float x = h[c];
+      for (int p = 0; p < kParts; ++p) {
+        const __nv_bfloat16 v = __float2bfloat16_rn(x);
+        o[p * part_stride + c] = *reinterpret_cast<const uint16_t*>(&v);
+        x -= __bfloat162float(v);
+      }
+    }
+  }
+}
+
+// loss and lse of 32 rows of the batch from their rows' parts: lane = row,
+// the 32 warps share the parts. position null: row t is row t in use.
+__global__ void __launch_bounds__(1024)
+    ce_combine_kernel(const float2* part, int64_t part_ld, int parts, const float* target_logit,
+                      const int* position, const int64_t* targets, int64_t ignore, int64_t T,
+                      int64_t V, float* loss, float* lse) {
+  __shared__ ExpSum sums[32][33];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t y = t < T ? targets[t] : ignore;
+  const int64_t i = t >= T || y == ignore ? -1 : position ? position[t] : t;
+  ExpSum s{-INFINITY, 0.0f};
+  if (i >= 0)
+    for (int p = warp; p < parts; p += 32) {
+      const float2 v = part[p * part_ld + i];
+      s = merge(s, {v.x, v.y});
+    }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || t >= T) return;
+  for (int w = 1; w < 32; ++w) s = merge(s, sums[w][lane]);
+  const float total = s.m + logf(s.l);
+  lse[t] = i < 0 ? 0.0f : total;
+  loss[t] = i < 0 ? 0.0f
+            : y < 0 || y >= V ? __uint_as_float(0x7fc00000u) : total - target_logit[i];
+}
+
+// ---- the FFMA and TF32 modes: row passes over a piece of fp32 logits (Z: T x C,
+// pitch ldz, columns v0 ..)
 
 struct RowState {  // per row, carried from piece to piece
   float* m;
@@ -96,86 +276,60 @@ __global__ void __launch_bounds__(kThreads)
   loss[t] = off ? 0.0f : y < 0 || y >= V ? __uint_as_float(0x7fc00000u) : total - zy;
 }
 
-// dZ of a piece, as fp32 in place of the logits or rounded to 16 bits beside them.
-template <typename G>
+// dZ of a piece in place of the logits.
 __global__ void __launch_bounds__(kThreads)
-    ce_grad_kernel(const float* Z, int64_t ldz, G* out, int64_t ldg, int64_t C, int64_t v0,
-                   const int64_t* targets, const float* lse, const float* coef) {
+    ce_grad_kernel(float* Z, int64_t ldz, int64_t C, int64_t v0, const int64_t* targets,
+                   const float* lse, const float* coef) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t t = blockIdx.x;
   const float k = coef[t], top = lse[t];
   const int64_t y = targets[t] - v0;
-  for (int64_t c = threadIdx.x; c < C; c += kThreads) {
-    float d = 0.0f;
-    if (k != 0.0f) d = (__expf(Z[t * ldz + c] - top) - (c == y ? 1.0f : 0.0f)) * k;
-    out[t * ldg + c] = from_f32<G>(d);
-  }
+  float* z = Z + t * ldz;
+  for (int64_t c = threadIdx.x; c < C; c += kThreads)
+    z[c] = k == 0.0f ? 0.0f : (__expf(z[c] - top) - (c == y ? 1.0f : 0.0f)) * k;
 }
 
-// ---- before and after the backward products
-
-// Each row's coefficient g_t, 0 for a row that takes no part and NaN for a
-// target that is no row of W. For 16-bit dZ it is g_t / ref * unit with
-// ref = max |g_t| over the rows that take part: dZ then lies in [-unit, unit]
-// whatever the scale of the objective, and the products are multiplied by
-// ref / unit (*back) at the end. One block.
-__global__ void __launch_bounds__(1024)
-    ce_coef_kernel(const int64_t* targets, int64_t ignore, const float* g, int64_t T, int64_t V,
-                   bool relative, float unit, float* coef, float* back) {
-  __shared__ float part[32];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  float ref = 0.0f;
-  if (relative) {
-    for (int64_t t = threadIdx.x; t < T; t += blockDim.x)
-      if (targets[t] != ignore) ref = fmaxf(ref, fabsf(g[t]));
-    for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ref;
-    __syncthreads();
-    ref = 0.0f;
-    for (int w = 0; w < 32; ++w) ref = fmaxf(ref, part[w]);
-  }
-  if (!(ref > 0.0f && ref < INFINITY)) ref = 1.0f;
-  for (int64_t t = threadIdx.x; t < T; t += blockDim.x) {
-    const int64_t y = targets[t];
-    const float k = y < 0 || y >= V ? __uint_as_float(0x7fc00000u) : g[t] / ref * unit;
-    coef[t] = y == ignore ? 0.0f : k;
-  }
-  if (threadIdx.x == 0) *back = ref / unit;
-}
-
-// H with the rows that take no part set to zero, so that nothing they hold
-// (uninitialised padding, a NaN) reaches dW.
-template <typename E>
+// Each row's coefficient, 0 for a row that takes no part, NaN for a target
+// that is no row of W; and H with the rows that take no part set to zero, so
+// that nothing they hold (uninitialised padding, a NaN) reaches dW.
 __global__ void __launch_bounds__(kThreads)
-    ce_rows_kernel(const E* H, int64_t ldh, const float* coef, E* out, int64_t ldo, int64_t D) {
+    ce_masked_kernel(const float* H, int64_t ldh, int64_t D, const int64_t* targets,
+                     int64_t ignore, int64_t V, const float* g, float* coef, float* out,
+                     int64_t ldo) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t t = blockIdx.x;
-  const bool off = coef[t] == 0.0f;
+  const int64_t t = blockIdx.x, y = targets[t];
+  const float k = y == ignore || g[t] == 0.0f ? 0.0f
+                  : y < 0 || y >= V ? __uint_as_float(0x7fc00000u) : g[t];
   for (int64_t c = threadIdx.x; c < D; c += kThreads)
-    out[t * ldo + c] = off ? E(0) : H[t * ldh + c];
+    out[t * ldo + c] = k == 0.0f ? 0.0f : H[t * ldh + c];
+  if (threadIdx.x == 0) coef[t] = k;
 }
 
-// out = x * back, rows with coefficient 0 set to zero (coef null: none).
-template <typename E>
+// Zero into the rows of dH that take no part.
 __global__ void __launch_bounds__(kThreads)
-    ce_out_kernel(const float* X, int64_t ldx, const float* coef, const float* back, E* out,
-                  int64_t ldo, int64_t cols) {
+    ce_clear_kernel(float* dH, int64_t ldd, int64_t D, const float* coef) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t t = blockIdx.x;
-  const bool off = coef && coef[t] == 0.0f;
-  const float k = *back;
-  for (int64_t c = threadIdx.x; c < cols; c += kThreads)
-    out[t * ldo + c] = from_f32<E>(off ? 0.0f : X[t * ldx + c] * k);
+  if (coef[t] != 0.0f) return;
+  for (int64_t c = threadIdx.x; c < D; c += kThreads) dH[t * ldd + c] = 0.0f;
 }
 
 // ---- host side
 
 bool size_ok(int64_t n) { return n >= 0 && n <= INT32_MAX; }
-bool is_16bit(int dtype) { return dtype == GEMM14_DTYPE_BF16 || dtype == GEMM14_DTYPE_F16; }
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+int64_t tiles_of(int64_t x) { return (x + 255) / 256; }
+// Whether the operands run on the tensor-core kernel: 16-bit ones, and fp32
+// ones in the split-precision mode (as three bf16 parts).
+bool on_tensor_cores(int dtype) {
+  return dtype == GEMM14_DTYPE_BF16 || dtype == GEMM14_DTYPE_F16 ||
+         dtype == GEMM14_DTYPE_F32_3XTF32;
+}
+// TMA can read rows of 16-bit elements at this address and pitch.
+bool tma_rows(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 int validate_ce(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
                 const void* W, int64_t ldw, const int64_t* targets) {
@@ -186,62 +340,99 @@ int validate_ce(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64
   return validate_product(dtype, 0, 1, T, V, D, H, ldh, W, ldw, sound, V);
 }
 
-struct CeLayout {
-  int64_t C = 0;       // vocabulary rows of a piece
-  int64_t ldz = 0;     // pitch of the logits (fp32) and of dZ
-  int64_t ldx = 0;     // pitch of the D-wide buffers
-  size_t state = 0, coef = 0, back = 0, z = 0, g = 0, rows = 0, dh = 0, dw = 0, total = 0;
-};
-
-// Bytes of logits a piece may take: 256 MiB, a piece of 8192 columns for 8192 rows.
+// Bytes a piece of logits or dZ, and a piece of W that has to be copied, may take.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
+
+// Rows of W per piece, a multiple of 256 unless one piece takes all: pieces of
+// about the same size, `per_row` bytes a row of W within the limit.
+int64_t piece_rows(int64_t V, int64_t per_row) {
+  const int64_t most = std::max<int64_t>(kPieceBytes / per_row / 256 * 256, 256);
+  const int64_t pieces = (V + most - 1) / most;
+  return pieces == 1 ? V : round_up((V + pieces - 1) / pieces, 256);
+}
+
+struct CeLayout {
+  bool tc = false;
+  int64_t C = 0;       // vocabulary rows of a piece
+  int64_t ldz = 0;     // pitch of the logits or of dZ
+  int64_t ldx = 0;     // pitch of the D-wide buffers
+  int parts = 1;       // bf16 parts of an operand
+  bool gather = false; // rows in use are numbered and gathered first
+  bool copy_w = false; // pieces of W are copied (unaligned) or split
+  int splits = 1;      // of the dH product
+  int64_t rows = 0;    // T rounded up to whole tiles
+  size_t state = 0, counts = 0, index = 0, position = 0, target = 0, lse = 0, coef = 0, h = 0,
+         w = 0, part = 0, z = 0, slots = 0, total = 0;
+};
 
 void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
                const void* W, int64_t ldw, bool backward, int sms, CeLayout* l) {
-  const int eb = elem_bytes_of(dtype);
-  int64_t C = kPieceBytes / (4 * T) / 256 * 256;
-  C = std::max<int64_t>(C, 256);
-  l->C = std::min(C, V);
-  l->ldz = (l->C + 7) / 8 * 8;
-  l->ldx = (D + 7) / 8 * 8;
-  const void* own = reinterpret_cast<const void*>(uintptr_t(1) << 12);
-  size_t product = streamk_flag_bytes(sms);
-  auto need = [&](int ta, int tb, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
-                  const void* B, int64_t ldb, int64_t ldc) {
-    product = std::max(product, gemm14_workspace_bytes_ex(dtype, ta, tb, M, N, K, A, lda, B, ldb,
-                                                          own, ldc, sms));
-  };
-  const int64_t last = V - (V - 1) / l->C * l->C;
-  for (const int64_t c : {l->C, last}) {
-    need(0, 1, T, c, D, H, ldh, W, ldw, l->ldz);
-    if (!backward) continue;
-    need(0, 0, T, D, c, own, l->ldz, W, ldw, l->ldx);
-    need(1, 0, c, D, T, own, l->ldz, own, l->ldx, l->ldx);
-  }
-  size_t at = round256(product);
+  *l = CeLayout{};
+  l->tc = on_tensor_cores(dtype);
+  l->ldx = round_up(D, 8);
+  l->rows = round_up(T, 256);
+  size_t at = streamk_flag_bytes(sms);
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = round256(at + bytes);
     return here;
   };
-  l->state = take(static_cast<size_t>(T) * 3 * sizeof(float));
-  l->z = take(static_cast<size_t>(T) * l->ldz * sizeof(float));
+  const size_t t4 = static_cast<size_t>(T) * 4;
+  if (l->tc) {
+    l->parts = dtype == GEMM14_DTYPE_F32_3XTF32 ? 3 : 1;
+    l->copy_w = l->parts == 3 || !tma_rows(W, ldw);
+    // one tile row of rows costs the same with and without the ignored ones
+    l->gather = backward || l->parts == 3 || !tma_rows(H, ldh) || T > TrainShape::BM;
+    int64_t per_row = 0;
+    if (backward) per_row = l->rows * 2 * l->parts;
+    if (l->copy_w) per_row = std::max(per_row, l->ldx * 2 * l->parts);
+    l->C = per_row ? piece_rows(V, per_row) : V;
+    l->ldz = round_up(l->C, 64);
+    if (l->gather) {
+      l->counts = take(256);
+      l->index = take(t4);
+      l->position = take(t4);
+      l->target = take(t4);
+      l->h = take(static_cast<size_t>(l->rows) * l->ldx * 2 * l->parts);
+    }
+    if (l->copy_w) l->w = take(static_cast<size_t>(l->C) * l->ldx * 2 * l->parts);
+    if (backward) {
+      l->lse = take(t4);
+      l->coef = take(t4);
+      l->z = take(static_cast<size_t>(l->rows) * l->ldz * 2 * l->parts);
+      const int64_t tiles = tiles_of(T) * tiles_of(D);
+      l->splits = train_splits(tiles, (l->C + 63) / 64, std::max(sms / 2, 1), 64);
+      l->slots = take(static_cast<size_t>(l->splits) * tiles * 256 * 256 * 4);
+    } else {
+      l->part = take(static_cast<size_t>(2 * tiles_of(V)) * l->rows * sizeof(float2));
+      l->state = take(t4);
+    }
+    l->total = at;
+    return;
+  }
+  l->C = piece_rows(V, 4 * T);
+  l->ldz = round_up(l->C, 8);
+  const void* own = reinterpret_cast<const void*>(uintptr_t(1) << 12);
+  auto need = [&](int ta, int tb, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                  const void* B, int64_t ldb, int64_t ldc) {
+    at = std::max(at, gemm14_workspace_bytes_ex(dtype, ta, tb, M, N, K, A, lda, B, ldb, own, ldc,
+                                                sms));
+  };
+  const int64_t last = V - (V - 1) / l->C * l->C;
+  for (const int64_t c : {l->C, last}) {
+    need(0, 1, T, c, D, H, ldh, W, ldw, l->ldz);
+    if (!backward) continue;
+    need(0, 0, T, D, c, own, l->ldz, W, ldw, D);
+    need(1, 0, c, D, T, own, l->ldz, own, l->ldx, D);
+  }
+  at = round256(at);
+  l->state = take(3 * t4);
+  l->z = take(static_cast<size_t>(T) * l->ldz * 4);
   if (backward) {
-    l->coef = take(static_cast<size_t>(T) * sizeof(float));
-    l->back = take(sizeof(float));
-    l->g = is_16bit(dtype) ? take(static_cast<size_t>(T) * l->ldz * eb) : l->z;
-    l->rows = take(static_cast<size_t>(T) * l->ldx * eb);
-    l->dh = take(static_cast<size_t>(T) * l->ldx * sizeof(float));
-    l->dw = take(static_cast<size_t>(l->C) * l->ldx * sizeof(float));
+    l->coef = take(t4);
+    l->h = take(static_cast<size_t>(T) * l->ldx * 4);
   }
   l->total = at;
-}
-
-size_t ce_workspace(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
-                    const void* W, int64_t ldw, bool backward, int sms) {
-  CeLayout l;
-  ce_layout(dtype, T, V, D, H, ldh, W, ldw, backward, sms, &l);
-  return l.total;
 }
 
 int check_room(const char* who, const void* workspace, size_t bytes, size_t need) {
@@ -256,22 +447,268 @@ const void* row_of(const void* W, int64_t v, int64_t ld, int eb) {
   return static_cast<const char*>(W) + v * ld * eb;
 }
 
-template <typename E>
-cudaError_t out_rows(const float* X, int64_t ldx, const float* coef, const float* back, void* out,
-                     int64_t ldo, int64_t rows, int64_t cols, cudaStream_t stream) {
-  return launch_kernel(ce_out_kernel<E>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0,
-                       stream, X, ldx, coef, back, static_cast<E*>(out), ldo, cols);
-}
-cudaError_t out_rows(int dtype, const float* X, int64_t ldx, const float* coef, const float* back,
-                     void* out, int64_t ldo, int64_t rows, int64_t cols, cudaStream_t stream) {
-  switch (dtype) {
-    case GEMM14_DTYPE_BF16:
-      return out_rows<__nv_bfloat16>(X, ldx, coef, back, out, ldo, rows, cols, stream);
-    case GEMM14_DTYPE_F16:
-      return out_rows<__half>(X, ldx, coef, back, out, ldo, rows, cols, stream);
-    default: return out_rows<float>(X, ldx, coef, back, out, ldo, rows, cols, stream);
+// A call of either direction.
+struct CeCall {
+  int dtype;
+  int64_t T, V, D;
+  const void* H;
+  int64_t ldh;
+  const void* W;
+  int64_t ldw;
+  const int64_t* targets;
+  int64_t ignore;
+  char* ws;
+  cudaStream_t stream;
+  CeLayout l;
+  CallContext ctx;
+  int clusters = 0;
+
+  bool bf16() const { return dtype != GEMM14_DTYPE_F16; }
+  int eb() const { return elem_bytes_of(dtype); }
+  template <typename P>
+  P* at(size_t off) const { return reinterpret_cast<P*>(ws + off); }
+
+  int launched(cudaError_t e, const char* what) const { return finish_launch(e, what, stream); }
+
+  Rows rows() const {
+    return Rows{at<int>(l.counts),   at<float>(l.counts) + 1, at<int>(l.index),
+                at<int>(l.position), at<int>(l.target),       at<float>(l.lse),
+                at<float>(l.coef)};
   }
-}
+
+  int prepare_tc() {
+    clusters = train_max_clusters();
+    if (clusters > 0) return GEMM14_OK;
+    note_error("linear_ce: clusters of two CTAs cannot run on this device");
+    return GEMM14_ERR_CUDA;
+  }
+
+  // Numbers and gathers the rows in use.
+  int gather(const float* lse, const float* g, void* dH, int64_t lddh) const {
+    const bool relative = g && dtype != GEMM14_DTYPE_F32_3XTF32;
+    // fp16's range: dZ is held in units of 2^-15, so that probabilities down
+    // to 2^-39 of the largest coefficient are not lost
+    const float unit = dtype == GEMM14_DTYPE_F16 ? 32768.0f : 1.0f;
+    const Rows r = rows();
+    int st = launched(launch_kernel(ce_rows_kernel, dim3(1), dim3(1024), 0, stream, targets,
+                                    ignore, lse, g, T, V, relative, unit, r),
+                      "linear_ce rows launch");
+    if (st != GEMM14_OK) return st;
+    const dim3 grid(static_cast<unsigned>(T + 64)), block(256);
+    uint16_t* out = at<uint16_t>(l.h);
+    const int64_t stride = l.rows * l.ldx;
+    const bool vec = tma_rows(H, ldh);
+    const cudaError_t e =
+        l.parts == 3
+            ? launch_kernel(ce_gather_kernel<float>, grid, block, 0, stream,
+                            static_cast<const float*>(H), ldh, T, D, r.n, r.position, out, l.ldx,
+                            stride, static_cast<float*>(dH), lddh, false)
+            : launch_kernel(ce_gather_kernel<uint16_t>, grid, block, 0, stream,
+                            static_cast<const uint16_t*>(H), ldh, T, D, r.n, r.position, out,
+                            l.ldx, stride, static_cast<uint16_t*>(dH), lddh, vec);
+    return launched(e, "linear_ce gather launch");
+  }
+
+  // The rows of H in use as an operand.
+  TrainOperand h_operand() const {
+    if (!l.gather) return TrainOperand{H, T, D, ldh, 1, 0};
+    return TrainOperand{ws + l.h, l.rows, D, l.ldx, l.parts, l.rows * l.ldx};
+  }
+
+  // c rows of W from v0 as an operand, copied or split first where they must be.
+  int w_operand(int64_t v0, int64_t c, TrainOperand* w) const {
+    const void* src = row_of(W, v0, ldw, eb());
+    if (!l.copy_w) {
+      *w = TrainOperand{src, c, D, ldw, 1, 0};
+      return GEMM14_OK;
+    }
+    void* dst = ws + l.w;
+    *w = TrainOperand{dst, c, D, l.ldx, l.parts, l.C * l.ldx};
+    if (l.parts == 3)
+      return launched(launch_split3(static_cast<const float*>(src), ldw, c, D, dst, l.ldx,
+                                    l.C * l.ldx, ctx.sm_count, stream),
+                      "linear_ce split launch");
+    const RepitchJob job{src, ldw, dst, l.ldx, c, D, 0, nullptr}, none{};
+    return launched(launch_repitch(job, none, 2, ctx.sm_count, stream), "linear_ce copy launch");
+  }
+
+  // Arguments of a product M x N over K, its rows (or its K, n_is_k) being those in use.
+  TrainArgs product(int64_t M, int64_t N, int64_t K, bool n_is_k) const {
+    TrainArgs a{};
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.n = l.gather ? at<int>(l.counts) : nullptr;
+    a.n_is_k = n_is_k;
+    a.splits = 1;
+    a.err = ctx.err;
+    a.wait_limit_ns = ctx.wait_limit_ns;
+    a.fault = ctx.fault;
+    a.alpha = 1.0f;
+    return a;
+  }
+
+  int run(int mode, bool promote, const TrainOperand& A, bool a_mn, const TrainOperand& B,
+          bool b_mn, TrainArgs* a) {
+    TrainMaps maps;
+    const int st = train_operands(bf16(), A, a_mn, B, b_mn, &maps, a);
+    if (st != GEMM14_OK) return st;
+    const int64_t items = tiles_of(a->M) * tiles_of(a->N) * a->splits;
+    const int64_t grid = std::min<int64_t>(items, clusters);
+    ctx.fault = kFaultNone;  // a test's request applies to the call's first product
+    return launched(launch_train_tc(mode, promote, maps, *a, static_cast<int>(grid), stream),
+                    "linear_ce product launch");
+  }
+
+  // Whether sums over K are carried in fp32 registers: what is written in fp32
+  // keeps fp32's accuracy; what is rounded to 16 bits loses nothing by TMEM's.
+  bool long_sum(int64_t K) const { return K > TrainShape::CHUNK * TrainShape::BK; }
+
+  int forward_tc(float* loss, float* lse) {
+    int st = prepare_tc();
+    if (st != GEMM14_OK) return st;
+    if (l.gather && (st = gather(nullptr, nullptr, nullptr, 0)) != GEMM14_OK) return st;
+    const Rows r = rows();
+    for (int64_t v0 = 0; v0 < V; v0 += l.C) {
+      const int64_t c = std::min(l.C, V - v0);
+      TrainOperand w;
+      if ((st = w_operand(v0, c, &w)) != GEMM14_OK) return st;
+      TrainArgs a = product(T, c, D, false);
+      a.v0 = static_cast<int>(v0);
+      a.target = l.gather ? r.target : nullptr;
+      a.target64 = targets;
+      a.part = at<float2>(l.part) + 2 * (v0 / 256) * l.rows;
+      a.part_ld = l.rows;
+      a.target_logit = at<float>(l.state);
+      if ((st = run(kTrainStats, long_sum(D), h_operand(), false, w, false, &a)) != GEMM14_OK)
+        return st;
+    }
+    return launched(
+        launch_kernel(ce_combine_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(1024),
+                      0, stream, at<float2>(l.part), l.rows, static_cast<int>(2 * tiles_of(V)),
+                      at<float>(l.state), l.gather ? r.position : nullptr, targets, ignore, T, V,
+                      loss, lse),
+        "linear_ce combine launch");
+  }
+
+  int backward_tc(const float* lse, const float* g, void* dH, int64_t lddh, void* dW,
+                  int64_t lddw) {
+    int st = prepare_tc();
+    if (st != GEMM14_OK) return st;
+    if ((st = gather(lse, g, dH, lddh)) != GEMM14_OK) return st;
+    const Rows r = rows();
+    const bool exact = l.parts == 3;
+    const int elem = exact ? kElemF32 : bf16() ? kElemBf16 : kElemF16;
+    const int64_t g_part = l.rows * l.ldz;
+    for (int64_t v0 = 0; v0 < V; v0 += l.C) {
+      const int64_t c = std::min(l.C, V - v0);
+      TrainOperand w;
+      if ((st = w_operand(v0, c, &w)) != GEMM14_OK) return st;
+      TrainArgs a = product(T, c, D, false);
+      a.v0 = static_cast<int>(v0);
+      a.target = r.target;
+      a.lse = r.lse;
+      a.coef = r.coef;
+      a.out = ws + l.z;
+      a.ld_out = l.ldz;
+      a.out_part = g_part;
+      a.elem = exact ? kElemBf16x3 : elem;
+      a.out_vec = 1;
+      if ((st = run(kTrainGrad, exact && long_sum(D), h_operand(), false, w, false, &a)) !=
+          GEMM14_OK)
+        return st;
+      const TrainOperand dz{ws + l.z, l.rows, c, l.ldz, l.parts, g_part};
+      if (dH) {
+        a = product(T, D, c, false);
+        a.splits = l.splits;
+        a.slots = at<float4>(l.slots);
+        a.add = v0 > 0;
+        if ((st = run(kTrainSlots, exact && long_sum(c), dz, false, w, true, &a)) != GEMM14_OK)
+          return st;
+      }
+      if (dW) {
+        a = product(c, D, T, true);
+        a.out = static_cast<char*>(dW) + v0 * lddw * eb();
+        a.ld_out = lddw;
+        a.elem = elem;
+        a.out_vec = aligned(dW, 16) && lddw * eb() % 16 == 0;
+        a.scale = r.back;
+        if ((st = run(kTrainOut, exact && long_sum(T), dz, true, h_operand(), true, &a)) !=
+            GEMM14_OK)
+          return st;
+      }
+    }
+    if (!dH) return GEMM14_OK;
+    SlotsOut s{};
+    s.slots = at<float4>(l.slots);
+    s.splits = l.splits;
+    s.M = static_cast<int>(T);
+    s.N = static_cast<int>(D);
+    s.n = r.n;
+    s.rows = r.index;
+    s.alpha = 1.0f;
+    s.scale = r.back;
+    s.out = dH;
+    s.ld = lddh;
+    s.elem = elem;
+    return launched(launch_slots_out(s, stream), "linear_ce output launch");
+  }
+
+  // ---- the FFMA and TF32 modes
+
+  int logits(int64_t v0, int64_t c) const {
+    return product_on_stream(dtype, 0, 1, T, c, D, 1.0f, H, ldh, row_of(W, v0, ldw, 4), ldw, 0.0f,
+                             at<float>(l.z), l.ldz, ws, l.state, stream);
+  }
+
+  int forward_products(float* loss, float* lse) const {
+    float* state = at<float>(l.state);
+    const RowState rs{state, state + T, state + 2 * T};
+    for (int64_t v0 = 0; v0 < V; v0 += l.C) {
+      const int64_t c = std::min(l.C, V - v0);
+      int st = logits(v0, c);
+      if (st == GEMM14_OK)
+        st = launched(launch_kernel(ce_stats_kernel, dim3(static_cast<unsigned>(T)),
+                                    dim3(kThreads), 0, stream, at<float>(l.z), l.ldz, c, v0, V,
+                                    targets, ignore, rs, loss, lse),
+                      "linear_ce statistics launch");
+      if (st != GEMM14_OK) return st;
+    }
+    return GEMM14_OK;
+  }
+
+  int backward_products(const float* lse, const float* g, void* dH, int64_t lddh, void* dW,
+                        int64_t lddw) const {
+    const dim3 per_row(static_cast<unsigned>(T)), block(kThreads);
+    float* z = at<float>(l.z);
+    float* coef = at<float>(l.coef);
+    float* h = at<float>(l.h);
+    float* dh = static_cast<float*>(dH);
+    int st = launched(launch_kernel(ce_masked_kernel, per_row, block, 0, stream,
+                                    static_cast<const float*>(H), ldh, D, targets, ignore, V, g,
+                                    coef, h, l.ldx),
+                      "linear_ce rows launch");
+    for (int64_t v0 = 0; v0 < V && st == GEMM14_OK; v0 += l.C) {
+      const int64_t c = std::min(l.C, V - v0);
+      if ((st = logits(v0, c)) != GEMM14_OK) return st;
+      if ((st = launched(launch_kernel(ce_grad_kernel, per_row, block, 0, stream, z, l.ldz, c, v0,
+                                       targets, lse, coef),
+                         "linear_ce gradient launch")) != GEMM14_OK)
+        return st;
+      if (dH && (st = product_on_stream(dtype, 0, 0, T, D, c, 1.0f, z, l.ldz,
+                                        row_of(W, v0, ldw, 4), ldw, v0 ? 1.0f : 0.0f, dh, lddh, ws,
+                                        l.state, stream)) != GEMM14_OK)
+        return st;
+      if (dW && (st = product_on_stream(dtype, 1, 0, c, D, T, 1.0f, z, l.ldz, h, l.ldx, 0.0f,
+                                        static_cast<float*>(dW) + v0 * lddw, lddw, ws, l.state,
+                                        stream)) != GEMM14_OK)
+        return st;
+    }
+    if (st != GEMM14_OK || !dH) return st;
+    return launched(launch_kernel(ce_clear_kernel, per_row, block, 0, stream, dh, lddh, D, coef),
+                    "linear_ce clear launch");
+  }
+};
 
 }  // namespace
 }  // namespace gemm14
@@ -286,49 +723,37 @@ size_t gemm14_linear_ce_workspace_bytes(int dtype, int backward, int64_t T, int6
   static const int64_t some = 0;
   if (validate_ce(dtype, T, V, D, H, ldh, W, ldw, &some) != GEMM14_OK || T == 0) return 0;
   if (sm_count <= 0 && current_sm_count(&sm_count) != GEMM14_OK) return 0;
-  return ce_workspace(dtype, T, V, D, H, ldh, W, ldw, backward != 0, sm_count);
+  CeLayout l;
+  ce_layout(dtype, T, V, D, H, ldh, W, ldw, backward != 0, sm_count, &l);
+  return l.total;
 }
 
 int gemm14_linear_ce_forward(int dtype, int64_t T, int64_t V, int64_t D, const void* H,
                              int64_t ldh, const void* W, int64_t ldw, const int64_t* targets,
                              int64_t ignore_index, float* loss, float* lse, void* workspace,
-                             size_t workspace_bytes, void* stream_ptr) {
+                             size_t workspace_bytes, void* stream) {
   int st = validate_ce(dtype, T, V, D, H, ldh, W, ldw, targets);
   if (st != GEMM14_OK) return st;
   if (T == 0) return GEMM14_OK;
   if (!loss || !lse || !aligned(loss, 4) || !aligned(lse, 4)) return GEMM14_ERR_INVALID_ARG;
+  CeCall c{dtype,        T, V, D, H, ldh, W, ldw, targets, ignore_index,
+           static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)};
   int sms = 0;
   if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
-  CeLayout l;
-  ce_layout(dtype, T, V, D, H, ldh, W, ldw, false, sms, &l);
-  if ((st = check_room("gemm14_linear_ce_forward", workspace, workspace_bytes, l.total)) !=
+  ce_layout(dtype, T, V, D, H, ldh, W, ldw, false, sms, &c.l);
+  if ((st = check_room("gemm14_linear_ce_forward", workspace, workspace_bytes, c.l.total)) !=
       GEMM14_OK)
     return st;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  char* ws = static_cast<char*>(workspace);
-  const int eb = elem_bytes_of(dtype);
-  float* z = reinterpret_cast<float*>(ws + l.z);
-  float* state = reinterpret_cast<float*>(ws + l.state);
-  const RowState rs{state, state + T, state + 2 * T};
-  for (int64_t v0 = 0; v0 < V; v0 += l.C) {
-    const int64_t c = std::min(l.C, V - v0);
-    if ((st = product_on_stream(dtype, 0, 1, T, c, D, 1.0f, H, ldh, row_of(W, v0, ldw, eb), ldw,
-                                0.0f, z, l.ldz, workspace, l.state, stream)) != GEMM14_OK)
-      return st;
-    if ((st = finish_launch(launch_kernel(ce_stats_kernel, dim3(static_cast<unsigned>(T)),
-                                          dim3(kThreads), 0, stream, z, l.ldz, c, v0, V, targets,
-                                          ignore_index, rs, loss, lse),
-                            "linear_ce statistics launch", stream)) != GEMM14_OK)
-      return st;
-  }
-  return GEMM14_OK;
+  if (!c.l.tc) return c.forward_products(loss, lse);
+  if ((st = call_context(&c.ctx)) != GEMM14_OK) return st;
+  return c.forward_tc(loss, lse);
 }
 
 int gemm14_linear_ce_backward(int dtype, int64_t T, int64_t V, int64_t D, const void* H,
                               int64_t ldh, const void* W, int64_t ldw, const int64_t* targets,
                               int64_t ignore_index, const float* lse, const float* dloss, void* dH,
                               int64_t lddh, void* dW, int64_t lddw, void* workspace,
-                              size_t workspace_bytes, void* stream_ptr) {
+                              size_t workspace_bytes, void* stream) {
   int st = validate_ce(dtype, T, V, D, H, ldh, W, ldw, targets);
   if (st != GEMM14_OK) return st;
   const int eb = elem_bytes_of(dtype);
@@ -337,79 +762,22 @@ int gemm14_linear_ce_backward(int dtype, int64_t T, int64_t V, int64_t D, const 
   if (T > 0 && (!lse || !dloss || !aligned(lse, 4) || !aligned(dloss, 4)))
     return GEMM14_ERR_INVALID_ARG;
   if (!dW && (!dH || T == 0)) return GEMM14_OK;  // nothing is asked for
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  if (T == 0) {
-    int sms = 0;
-    if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
-    return finish_launch(cudaMemset2DAsync(dW, static_cast<size_t>(lddw) * eb, 0,
-                                           static_cast<size_t>(D) * eb, static_cast<size_t>(V),
-                                           stream),
-                         "cudaMemset2DAsync", stream);
-  }
   int sms = 0;
   if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
-  CeLayout l;
-  ce_layout(dtype, T, V, D, H, ldh, W, ldw, true, sms, &l);
-  if ((st = check_room("gemm14_linear_ce_backward", workspace, workspace_bytes, l.total)) !=
+  CeCall c{dtype,        T, V, D, H, ldh, W, ldw, targets, ignore_index,
+           static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)};
+  if (T == 0)
+    return c.launched(cudaMemset2DAsync(dW, static_cast<size_t>(lddw) * eb, 0,
+                                        static_cast<size_t>(D) * eb, static_cast<size_t>(V),
+                                        c.stream),
+                      "cudaMemset2DAsync");
+  ce_layout(dtype, T, V, D, H, ldh, W, ldw, true, sms, &c.l);
+  if ((st = check_room("gemm14_linear_ce_backward", workspace, workspace_bytes, c.l.total)) !=
       GEMM14_OK)
     return st;
-  char* ws = static_cast<char*>(workspace);
-  float* z = reinterpret_cast<float*>(ws + l.z);
-  float* coef = reinterpret_cast<float*>(ws + l.coef);
-  float* back = reinterpret_cast<float*>(ws + l.back);
-  float* dh = reinterpret_cast<float*>(ws + l.dh);
-  float* dw = reinterpret_cast<float*>(ws + l.dw);
-  void* rows = ws + l.rows;
-  void* g = ws + l.g;
-  const bool half = is_16bit(dtype);
-  // fp16's range: dZ is held in units of 2^-15, so that probabilities down to
-  // 2^-39 of the largest coefficient are not lost
-  const float unit = dtype == GEMM14_DTYPE_F16 ? 32768.0f : 1.0f;
-  const dim3 per_row(static_cast<unsigned>(T)), block(kThreads);
-  if ((st = finish_launch(launch_kernel(ce_coef_kernel, dim3(1), dim3(1024), 0, stream, targets,
-                                        ignore_index, dloss, T, V, half, unit, coef, back),
-                          "linear_ce coefficient launch", stream)) != GEMM14_OK)
-    return st;
-  const cudaError_t e =
-      half ? launch_kernel(ce_rows_kernel<uint16_t>, per_row, block, 0, stream,
-                           static_cast<const uint16_t*>(H), ldh, coef,
-                           static_cast<uint16_t*>(rows), l.ldx, D)
-           : launch_kernel(ce_rows_kernel<float>, per_row, block, 0, stream,
-                           static_cast<const float*>(H), ldh, coef, static_cast<float*>(rows),
-                           l.ldx, D);
-  if ((st = finish_launch(e, "linear_ce rows launch", stream)) != GEMM14_OK) return st;
-  for (int64_t v0 = 0; v0 < V; v0 += l.C) {
-    const int64_t c = std::min(l.C, V - v0);
-    const void* w = row_of(W, v0, ldw, eb);
-    if ((st = product_on_stream(dtype, 0, 1, T, c, D, 1.0f, H, ldh, w, ldw, 0.0f, z, l.ldz,
-                                workspace, l.state, stream)) != GEMM14_OK)
-      return st;
-    const cudaError_t eg =
-        dtype == GEMM14_DTYPE_BF16
-            ? launch_kernel(ce_grad_kernel<__nv_bfloat16>, per_row, block, 0, stream, z, l.ldz,
-                            static_cast<__nv_bfloat16*>(g), l.ldz, c, v0, targets, lse, coef)
-        : dtype == GEMM14_DTYPE_F16
-            ? launch_kernel(ce_grad_kernel<__half>, per_row, block, 0, stream, z, l.ldz,
-                            static_cast<__half*>(g), l.ldz, c, v0, targets, lse, coef)
-            : launch_kernel(ce_grad_kernel<float>, per_row, block, 0, stream, z, l.ldz,
-                            static_cast<float*>(g), l.ldz, c, v0, targets, lse, coef);
-    if ((st = finish_launch(eg, "linear_ce gradient launch", stream)) != GEMM14_OK) return st;
-    if (dH && (st = product_on_stream(dtype, 0, 0, T, D, c, 1.0f, g, l.ldz, w, ldw,
-                                      v0 ? 1.0f : 0.0f, dh, l.ldx, workspace, l.state, stream)) !=
-                  GEMM14_OK)
-      return st;
-    if (!dW) continue;
-    if ((st = product_on_stream(dtype, 1, 0, c, D, T, 1.0f, g, l.ldz, rows, l.ldx, 0.0f, dw, l.ldx,
-                                workspace, l.state, stream)) != GEMM14_OK)
-      return st;
-    void* out = static_cast<char*>(dW) + v0 * lddw * eb;
-    if ((st = finish_launch(out_rows(dtype, dw, l.ldx, nullptr, back, out, lddw, c, D, stream),
-                            "linear_ce output launch", stream)) != GEMM14_OK)
-      return st;
-  }
-  if (!dH) return GEMM14_OK;
-  return finish_launch(out_rows(dtype, dh, l.ldx, coef, back, dH, lddh, T, D, stream),
-                       "linear_ce output launch", stream);
+  if (!c.l.tc) return c.backward_products(lse, dloss, dH, lddh, dW, lddw);
+  if ((st = call_context(&c.ctx)) != GEMM14_OK) return st;
+  return c.backward_tc(lse, dloss, dH, lddh, dW, lddw);
 }
 
 }  // extern "C"

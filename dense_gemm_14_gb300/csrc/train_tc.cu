@@ -1,0 +1,746 @@
+// train_tc.cu -- the training products on CTA pairs: tcgen05.mma.cta_group::2,
+// 256 x 256 tiles of bf16 / fp16 operands (or of fp32 ones held as bf16 parts),
+// fp32 accumulation, and epilogues that fold a tile away or turn it into the
+// next product's operand instead of writing its sums (train_tc.h).
+//
+// Roles per CTA (320 threads, cluster of 2, persistent over tiles), as on the
+// library's pair kernel: warp 0 loads this CTA's 128 rows of A and 128 columns
+// of B by TMA into a ring of 6 stages, one lane of the leader's warp 1 issues
+// the pair's MMAs into one of two 256-column accumulators, and warps 2..9
+// drain the other: two warps for each quarter of the lanes, a thread holding
+// one row's 128 columns, so that a row's maximum and sum need no exchange
+// between threads.
+//
+// Long sums (kPromote): the accumulator is drained every 16 k-blocks into 128
+// fp32 registers a thread and starts again from zero while the MMAs go on in
+// the other one. A drain takes about 600 cycles against 8192 of MMAs.
+//
+// Every wait is bounded (ptx.cuh); a CTA that gives up raises its peer's abort
+// flag, and both meet at a cluster barrier before TMEM is freed.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "api_internal.h"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "train_tc.h"
+
+namespace gemm14 {
+namespace {
+
+using S = TrainShape;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct TrainSmem {
+  uint64_t full[S::STAGES];   // leader: both CTAs' bytes of a stage have landed
+  uint64_t empty[S::STAGES];  // each CTA: the pair's MMAs finished reading the stage
+  uint64_t acc_full[2];       // each CTA: accumulator b holds a finished sum
+  uint64_t acc_empty[2];      // leader: all 16 epilogue warps drained accumulator b
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(TrainSmem) <= 256, "barrier block of the training kernel");
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Item i of a launch: a split of the k-blocks and a tile, tiles in groups of 8
+// tile rows so that neighbouring clusters share A and B in L2.
+struct Work {
+  int tiles_m, tiles_n, kblocks, splits;
+  __device__ int items() const { return tiles_m * tiles_n * splits; }
+  __device__ void get(int i, int& split, int& tm, int& tn, int& kb0, int& kb1) const {
+    const int tiles = tiles_m * tiles_n;
+    split = i / tiles;
+    const int t = i - split * tiles;
+    constexpr int kGroupM = 8;
+    const int per_group = kGroupM * tiles_n;
+    const int first = t / per_group * kGroupM;
+    const int gm = min(tiles_m - first, kGroupM);
+    const int r = t - first * tiles_n;
+    tm = first + r % gm;
+    tn = r / gm;
+    kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * split / splits);
+    kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (split + 1) / splits);
+  }
+};
+
+// ---- epilogue pieces. `x` holds 32 consecutive columns (col0 ..) of this
+// thread's row; `buf` is the warp's 32 x 128-byte staging block, its 16-byte
+// pieces spread over the banks (row r's piece p at p ^ (r & 7)).
+
+__device__ __forceinline__ uint32_t stage_at(uint32_t buf, int row, int piece) {
+  return buf + static_cast<uint32_t>(row * 128 + (((piece ^ row) & 7) << 4));
+}
+__device__ __forceinline__ void stage_put(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 stage_get(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The warp's staged block, rows row0 .. +31, to global memory: 8 lanes write a
+// row's 128 bytes. n_cols: elements of the row segment inside the matrix.
+template <typename E, typename Combine>
+__device__ __forceinline__ void stage_out(uint32_t buf, E* out, int64_t ld, int row0, int rows,
+                                          int64_t col0, int n_cols, bool vec, int lane,
+                                          Combine combine) {
+  constexpr int kPer = 16 / sizeof(E);
+  const int p = lane & 7;
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const int r = g * 4 + (lane >> 3);
+    if (row0 + r >= rows || p * kPer >= n_cols) continue;
+    uint4 v = stage_get(stage_at(buf, r, p));
+    E* to = out + static_cast<int64_t>(row0 + r) * ld + col0 + p * kPer;
+    if (vec && (p + 1) * kPer <= n_cols) {
+      combine(v, reinterpret_cast<const uint4*>(to));
+      *reinterpret_cast<uint4*>(to) = v;
+    } else {
+      const E* e = reinterpret_cast<const E*>(&v);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (p * kPer + j < n_cols) combine(to + j, e[j]);
+    }
+  }
+}
+
+// Plain stores of 16-bit elements.
+struct Store16 {
+  __device__ void operator()(uint4&, const uint4*) const {}
+  __device__ void operator()(uint16_t* to, uint16_t e) const { *to = e; }
+};
+// fp32: + beta * what is there (alpha is already in the staged values).
+struct Accum32 {
+  float beta;
+  __device__ void operator()(uint4& v, const uint4* there) const {
+    if (beta == 0.0f) return;
+    const float4 c = *reinterpret_cast<const float4*>(there);
+    v.x = __float_as_uint(fmaf(beta, c.x, __uint_as_float(v.x)));
+    v.y = __float_as_uint(fmaf(beta, c.y, __uint_as_float(v.y)));
+    v.z = __float_as_uint(fmaf(beta, c.z, __uint_as_float(v.z)));
+    v.w = __float_as_uint(fmaf(beta, c.w, __uint_as_float(v.w)));
+  }
+  __device__ void operator()(float* to, float e) const {
+    *to = beta == 0.0f ? e : fmaf(beta, *to, e);
+  }
+};
+
+// Row state of the epilogues that work on logits.
+struct RowData {
+  int y;              // target's column relative to the tile half, or out of [0, 128)
+  float lse, coef;    // gradient
+  float m, l, zy;     // statistics
+};
+
+template <int kMode>
+struct Epilogue {
+  const TrainArgs& args;
+  int M, N, lane, row0, row, half, rank, split;
+  int64_t tile;
+  int col_half;       // first column of this thread's half
+  uint32_t buf;
+  RowData d;
+  float factor;
+
+  __device__ void begin() {
+    if (kMode == kTrainStats || kMode == kTrainGrad) {
+      d.y = -1;
+      d.lse = 0.0f;
+      d.coef = 0.0f;
+      if (row < M) {
+        if (args.target) {
+          d.y = args.target[row];
+        } else {
+          const int64_t y = args.target64[row];
+          d.y = y >= 0 && y < INT_MAX ? static_cast<int>(y) : -1;
+        }
+        d.y = d.y < 0 ? -1 : d.y - args.v0 - col_half;
+        if (kMode == kTrainGrad) {
+          d.lse = args.lse[row];
+          d.coef = args.coef[row];
+        }
+      }
+      d.m = -INFINITY;
+      d.l = 0.0f;
+      d.zy = 0.0f;
+    }
+    if (kMode == kTrainOut) factor = args.alpha * (args.scale ? *args.scale : 1.0f);
+  }
+
+  // Columns 32 c .. of the half, in registers.
+  __device__ void chunk(int c, float (&x)[32]) {
+    const int col0 = col_half + 32 * c;
+    if (kMode == kTrainStats) {
+      if (col0 + 32 > N) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (col0 + j >= N) x[j] = -INFINITY;
+      }
+      float m = d.m;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) m = fmaxf(m, x[j]);
+      // nothing above -inf so far: any finite base gives the sum's zeros
+      const float base = m == -INFINITY ? 0.0f : m;
+      float l = d.l * exp2_approx((d.m - base) * kLog2e);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) l += exp2_approx((x[j] - base) * kLog2e);
+      d.m = m;
+      d.l = l;
+      const int y = d.y - 32 * c;
+      if (y >= 0 && y < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == y) d.zy = x[j];
+      }
+    } else if (kMode == kTrainGrad) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = exp2_approx((x[j] - d.lse) * kLog2e);
+      const int y = d.y - 32 * c;
+      if (y >= 0 && y < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == y) x[j] -= 1.0f;
+      }
+      // a row past the last in use, or one of coefficient 0, is exactly 0
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = d.coef == 0.0f ? 0.0f : x[j] * d.coef;
+      store16(c, x);
+    } else if (kMode == kTrainSlots) {
+      const int64_t tiles = static_cast<int64_t>((args.M + S::BM - 1) / S::BM) *
+                            ((args.N + S::BN - 1) / S::BN);
+      float4* s = args.slots + slot_index(tiles, split, tile, rank, half, c, 0,
+                                          row - (row0 & ~127));
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        float4 w = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+        if (args.add) {
+          const float4 o = __ldcg(s + 128 * v);
+          w.x += o.x;
+          w.y += o.y;
+          w.z += o.z;
+          w.w += o.w;
+        }
+        __stcg(s + 128 * v, w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] *= factor;
+      if (args.elem == kElemF32) {
+        __syncwarp();
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          stage_put(stage_at(buf, lane, p),
+                    make_uint4(__float_as_uint(x[4 * p]), __float_as_uint(x[4 * p + 1]),
+                               __float_as_uint(x[4 * p + 2]), __float_as_uint(x[4 * p + 3])));
+        __syncwarp();
+        stage_out(buf, static_cast<float*>(args.out), args.ld_out, row0, M, col0,
+                  min(32, N - col0), args.out_vec != 0, lane, Accum32{args.beta});
+      } else {
+        store16(c, x);
+      }
+    }
+  }
+
+  // 16-bit output: two chunks of 32 columns share a staged block of 64.
+  __device__ void store16(int c, float (&x)[32]) {
+    const int parts = args.elem == kElemBf16x3 ? 3 : 1;
+    // kTrainGrad writes whole tile rows (zeros past the rows in use): its
+    // buffer has them
+    const int rows = kMode == kTrainGrad ? INT_MAX : M;
+    if (parts == 1) {
+      if ((c & 1) == 0) __syncwarp();
+      const int p0 = (c & 1) * 4;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint4 v;
+        if (args.elem == kElemF16)
+          v = make_uint4(pack_f16(x[8 * p], x[8 * p + 1]), pack_f16(x[8 * p + 2], x[8 * p + 3]),
+                         pack_f16(x[8 * p + 4], x[8 * p + 5]), pack_f16(x[8 * p + 6], x[8 * p + 7]));
+        else
+          v = make_uint4(pack_bf16(x[8 * p], x[8 * p + 1]), pack_bf16(x[8 * p + 2], x[8 * p + 3]),
+                         pack_bf16(x[8 * p + 4], x[8 * p + 5]),
+                         pack_bf16(x[8 * p + 6], x[8 * p + 7]));
+        stage_put(stage_at(buf, lane, p0 + p), v);
+      }
+      if ((c & 1) == 0) return;
+      __syncwarp();
+      const int col0 = col_half + 64 * (c >> 1);
+      stage_out(buf, static_cast<uint16_t*>(args.out), args.ld_out, row0, rows, col0,
+                min(64, N - col0), args.out_vec != 0, lane, Store16{});
+      return;
+    }
+    // three bf16 parts of each value: the nearest, then the nearest to what is left
+    const int col0 = col_half + 32 * c;
+    for (int part = 0; part < 3; ++part) {
+      __syncwarp();
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float& a = x[8 * p + 2 * k];
+          float& b = x[8 * p + 2 * k + 1];
+          w[k] = pack_bf16(a, b);
+          a -= __uint_as_float(w[k] << 16);
+          b -= __uint_as_float(w[k] & 0xffff0000u);
+        }
+        stage_put(stage_at(buf, lane, p), make_uint4(w[0], w[1], w[2], w[3]));
+      }
+      __syncwarp();
+      stage_out(buf, static_cast<uint16_t*>(args.out) + part * args.out_part, args.ld_out, row0,
+                rows, col0, min(32, N - col0), args.out_vec != 0, lane, Store16{});
+    }
+  }
+
+  __device__ void end(int tn) {
+    if (kMode == kTrainStats && row < M) {
+      args.part[(static_cast<int64_t>(tn) * 2 + half) * args.part_ld + row] =
+          make_float2(d.m, d.l);
+      if (d.y >= 0 && d.y < 128) args.target_logit[row] = d.zy;
+    }
+  }
+};
+
+template <int kMode, bool kPromote>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
+    train_tc_kernel(const __grid_constant__ TrainMaps maps, const TrainArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = align1024(smem_raw);
+  uint8_t* out_stage = tiles + S::STAGES * S::STAGE_BYTES;
+  TrainSmem& sm = *reinterpret_cast<TrainSmem*>(out_stage + S::EPI_WARPS * S::OUT_BUF_BYTES);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cid = static_cast<int>(cluster_id_x());
+  const int ncl = static_cast<int>(cluster_count_x());
+  const WaitCtx wc{args.err, &sm.abort_flag, args.wait_limit_ns,
+                   mapa_shared(smem_u32(&sm.abort_flag), rank ^ 1u)};
+  uint32_t prod_it = 0;
+  bool mma_issued = false;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 2 * S::EPI_WARPS);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
+  }
+  cluster_sync();
+  if (warp == 1) {
+    tmem_alloc_pair(&sm.tmem_base, S::TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t tmem_base = sm.tmem_base;
+
+  // Both CTAs of a pair, and all their roles, read the same count.
+  const int n = args.n ? *args.n : 0;
+  const int M = args.n && !args.n_is_k ? min(n, args.M) : args.M;
+  const int K = args.n && args.n_is_k ? min(n, args.K) : args.K;
+  const Work work{(M + S::BM - 1) / S::BM, (args.N + S::BN - 1) / S::BN, (K + S::BK - 1) / S::BK,
+                  args.splits};
+  const int items = work.items();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = cid; i < items && ok; i += ncl) {
+        int split, tm, tn, kb0, kb1;
+        work.get(i, split, tm, tn, kb0, kb1);
+        const int m0 = tm * S::BM + static_cast<int>(rank) * 128;
+        const int n0 = tn * S::BN + static_cast<int>(rank) * 128;
+        const int step = kPromote ? S::CHUNK : kb1 - kb0;
+        for (int c0 = kb0; c0 < kb1 && ok; c0 += step) {
+          const int c1 = min(c0 + step, kb1);
+          for (int t = 0; t < args.terms && ok; ++t) {
+            const uint32_t code = args.term_code >> (4 * t);
+            const CUtensorMap* ma = &maps.a[code & 3];
+            const CUtensorMap* mb = &maps.b[(code >> 2) & 3];
+            for (int kb = c0; kb < c1; ++kb, ++prod_it) {
+              const uint32_t s = prod_it % S::STAGES, ph = (prod_it / S::STAGES) & 1;
+              if (!mbar_wait(&sm.empty[s], ph ^ 1, wc)) { ok = false; break; }
+              // Failure-detection tests: the first stage is never loaded.
+              if (args.fault == kFaultSkipFirstStage && prod_it == 0) continue;
+              uint8_t* a_st = tiles + s * S::STAGE_BYTES;
+              uint8_t* b_st = a_st + S::A_BYTES;
+              const uint32_t full_leader = mapa_shared(smem_u32(&sm.full[s]), 0);
+              if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * S::STAGE_BYTES);
+              if (!args.a_mn) {
+                tma_load_2d_pair(a_st, ma, kb * S::BK, m0, full_leader);
+              } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  tma_load_2d_pair(a_st + c * (64 * S::BK * 2), ma, m0 + c * 64, kb * S::BK,
+                                   full_leader);
+              }
+              if (!args.b_mn) {
+                tma_load_2d_pair(b_st, mb, kb * S::BK, n0, full_leader);
+              } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  tma_load_2d_pair(b_st + c * (64 * S::BK * 2), mb, n0 + c * 64, kb * S::BK,
+                                   full_leader);
+              }
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (leader && lane == 0) {
+      const OperandDesc a_op = operand_desc(args.a_mn == 0);
+      const OperandDesc b_op = operand_desc(args.b_mn == 0);
+      bool ok = true;
+      uint32_t it = 0, unit = 0;
+      for (int i = cid; i < items && ok; i += ncl) {
+        int split, tm, tn, kb0, kb1;
+        work.get(i, split, tm, tn, kb0, kb1);
+        const int step = kPromote ? S::CHUNK : kb1 - kb0;
+        for (int c0 = kb0; c0 < kb1; c0 += step, ++unit) {
+          const int blocks = (min(c0 + step, kb1) - c0) * args.terms;
+          const int b = unit & 1;
+          const uint32_t aph = (unit >> 1) & 1;
+          if (!mbar_wait_cluster(&sm.acc_empty[b], aph ^ 1, wc)) { ok = false; break; }
+          tc_fence_after_sync();
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * S::BN);
+          for (int k = 0; k < blocks; ++k, ++it) {
+            const uint32_t s = it % S::STAGES, ph = (it / S::STAGES) & 1;
+            if (!mbar_wait(&sm.full[s], ph, wc)) { ok = false; break; }
+            tc_fence_after_sync();
+            const uint32_t a_addr = smem_u32(tiles + s * S::STAGE_BYTES);
+            const uint32_t b_addr = a_addr + S::A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < S::BK / 16; ++kk) {
+              const uint64_t a_desc = smem_desc_sw128(a_addr + kk * a_op.step, a_op.lbo, 1024);
+              const uint64_t b_desc = smem_desc_sw128(b_addr + kk * b_op.step, b_op.lbo, 1024);
+              tc_mma_f16_pair(d_tmem, a_desc, b_desc, args.idesc, k != 0 || kk != 0);
+            }
+            mma_issued = true;
+            tc_commit_pair_multicast(&sm.empty[s], 0x3);
+          }
+          if (!ok) break;
+          tc_commit_pair_multicast(&sm.acc_full[b], 0x3);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;             // TMEM lane quarter this warp may access
+    const int half = (warp - 2) >> 2;   // its 128 columns of the tile
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(&sm.acc_empty[0]), 0);
+    const uint32_t acc_empty1 = mapa_shared(smem_u32(&sm.acc_empty[1]), 0);
+    const uint32_t buf = smem_u32(out_stage + (warp - 2) * S::OUT_BUF_BYTES);
+    uint32_t unit = 0;
+    bool ok = true;
+    for (int i = cid; i < items && ok; i += ncl) {
+      int split, tm, tn, kb0, kb1;
+      work.get(i, split, tm, tn, kb0, kb1);
+      const int row0 = tm * S::BM + static_cast<int>(rank) * 128 + q * 32;
+      Epilogue<kMode> e{args, M, args.N, lane, row0, row0 + lane, half, static_cast<int>(rank),
+                        split, static_cast<int64_t>(tm) * work.tiles_n + tn,
+                        tn * S::BN + half * 128, buf, {}, 1.0f};
+      e.begin();
+      const int step = kPromote ? S::CHUNK : kb1 - kb0;
+      float acc[kPromote ? 128 : 1];
+      if (kPromote) {
+#pragma unroll
+        for (int j = 0; j < (kPromote ? 128 : 1); ++j) acc[j] = 0.0f;
+      }
+      for (int c0 = kb0; c0 < kb1; c0 += step, ++unit) {
+        const int b = unit & 1;
+        const uint32_t aph = (unit >> 1) & 1;
+        int got = 1;
+        if (lane == 0) got = mbar_wait(&sm.acc_full[b], aph, wc) ? 1 : 0;
+        got = __shfl_sync(0xffffffffu, got, 0);
+        if (!got) { ok = false; break; }
+        tc_fence_after_sync();
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                               static_cast<uint32_t>(b * S::BN + half * 128);
+        if (kPromote) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_row + c * 32, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[kPromote ? 32 * c + j : 0] += __uint_as_float(r[j]);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            float x[32];
+            tmem_ld_32x32b_x32(t_row + c * 32, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
+            e.chunk(c, x);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(b ? acc_empty1 : acc_empty0);
+      }
+      if (!ok) break;
+      if (kPromote) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = acc[kPromote ? 32 * c + j : 0];
+          e.chunk(c, x);
+        }
+      } else if (kb0 == kb1) {
+        // no products at all (no rows in use): sums of zero
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+          e.chunk(c, x);
+        }
+      }
+      e.end(tn);
+    }
+  }
+
+  // Teardown. On abort, the leader lets its issued MMAs and both CTAs' loads
+  // (counted on its full barriers) finish, bounded, before the pair meets.
+  __syncthreads();
+  if (sm.abort_flag && leader) {
+    if (warp == 1 && lane == 0 && mma_issued) {
+      tc_commit_pair_multicast(&sm.drain, 0x1);
+      mbar_wait_timed(&sm.drain, 0, 100000000ull);
+    }
+    if (warp == 0 && lane == 0) {
+      const uint32_t first = prod_it > S::STAGES ? prod_it - S::STAGES : 0;
+      for (uint32_t j = first; j < prod_it; ++j)
+        if (!(args.fault == kFaultSkipFirstStage && j == 0))
+          mbar_wait_timed(&sm.full[j % S::STAGES], (j / S::STAGES) & 1, 100000000ull);
+    }
+  }
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, S::TMEM_COLS);
+  }
+}
+
+// 32 rows x 128 columns a block: the slots are read along rows (512 bytes a
+// warp) and written along columns, through shared memory.
+__global__ void __launch_bounds__(256) slots_out_kernel(const SlotsOut s) {
+  __shared__ float tile[32][36];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int n = s.n ? min(*s.n, s.M) : s.M;
+  const int row0 = blockIdx.x * 32;
+  if (row0 >= n) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t tiles_n = (s.N + S::BN - 1) / S::BN;
+  const int64_t tiles = static_cast<int64_t>((s.M + S::BM - 1) / S::BM) * tiles_n;
+  const int64_t t = static_cast<int64_t>(row0 / S::BM) * tiles_n + blockIdx.y / 2;
+  const int rank = (row0 / 128) & 1, q = (row0 & 127) + lane, half = blockIdx.y & 1;
+  const float k = s.alpha * (s.scale ? *s.scale : 1.0f);
+  const int r = threadIdx.x >> 3, c4 = (threadIdx.x & 7) * 4;  // this thread's part of the output
+  const int row = row0 + r < n ? (s.rows ? s.rows[row0 + r] : row0 + r) : -1;
+  for (int c = 0; c < 4; ++c) {
+    const int col0 = blockIdx.y * 128 + c * 32;
+    if (col0 >= s.N) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < s.splits; ++p) {
+      const float4 o = __ldcg(s.slots + slot_index(tiles, p, t, rank, half, c, warp, q));
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
+    __syncthreads();
+    *reinterpret_cast<float4*>(&tile[lane][4 * warp]) = v;
+    __syncthreads();
+    if (row < 0) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = col0 + c4 + j;
+      if (col >= s.N) break;
+      const int64_t at = row * s.ld + col;
+      const float x = tile[r][c4 + j] * k;
+      if (s.elem == kElemF32) {
+        float* o = static_cast<float*>(s.out) + at;
+        *o = s.beta == 0.0f ? x : fmaf(s.beta, *o, x);
+      } else if (s.elem == kElemF16) {
+        static_cast<__half*>(s.out)[at] = __float2half_rn(x);
+      } else {
+        static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16_rn(x);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256)
+    split3_kernel(const float* X, int64_t ldx, int64_t rows, int64_t cols, __nv_bfloat16* out,
+                  int64_t ld, int64_t part_stride) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) {
+      float x = X[r * ldx + c];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const __nv_bfloat16 b = __float2bfloat16_rn(x);
+        out[p * part_stride + r * ld + c] = b;
+        x -= __bfloat162float(b);
+      }
+    }
+}
+
+using TrainKernel = void (*)(const TrainMaps, const TrainArgs);
+
+TrainKernel kernel_of(int mode, bool promote) {
+  switch (mode) {
+    case kTrainStats:
+      return promote ? train_tc_kernel<kTrainStats, true> : train_tc_kernel<kTrainStats, false>;
+    case kTrainGrad:
+      return promote ? train_tc_kernel<kTrainGrad, true> : train_tc_kernel<kTrainGrad, false>;
+    case kTrainSlots:
+      return promote ? train_tc_kernel<kTrainSlots, true> : train_tc_kernel<kTrainSlots, false>;
+    default:
+      return promote ? train_tc_kernel<kTrainOut, true> : train_tc_kernel<kTrainOut, false>;
+  }
+}
+
+}  // namespace
+
+int train_max_clusters() {
+  static DeviceOnce cached;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= DeviceOnce::kDevices) return 0;
+  const int n = cached.get(
+      dev,
+      [] {
+        int least = INT_MAX;
+        for (int mode = kTrainStats; mode <= kTrainOut; ++mode)
+          for (const bool promote : {false, true}) {
+            const TrainKernel k = kernel_of(mode, promote);
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     S::SMEM_BYTES) != cudaSuccess)
+              return -1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2, 1, 1);
+            cfg.blockDim = dim3(S::THREADS, 1, 1);
+            cfg.dynamicSmemBytes = S::SMEM_BYTES;
+            int c = 0;
+            if (cudaOccupancyMaxActiveClusters(&c, k, &cfg) != cudaSuccess) c = 0;
+            least = c < least ? c : least;
+          }
+        return least;
+      },
+      [](int v) { return v >= 0; });
+  return n > 0 ? n : 0;
+}
+
+int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOperand& B, bool b_mn,
+                   TrainMaps* maps, TrainArgs* args) {
+  const auto encode = [&](const TrainOperand& x, bool mn, CUtensorMap* m) {
+    for (int p = 0; p < 3; ++p) {
+      if (p >= x.parts) {
+        m[p] = m[0];
+        continue;
+      }
+      const void* base = static_cast<const char*>(x.base) + 2 * p * x.part_stride;
+      const int st = map_16bit(&m[p], bf16, base, x.rows, x.cols, x.ld, mn ? 64 : 128);
+      if (st != 0) return st;
+    }
+    return 0;
+  };
+  int st = encode(A, a_mn, maps->a);
+  if (st == 0) st = encode(B, b_mn, maps->b);
+  if (st != 0) return st;
+  // Terms of split operands, small ones first: of 3 x 3 parts the six whose
+  // product is above 2^-24 of the whole, or A's three parts against one B.
+  const bool split = A.parts == 3;
+  args->terms = !split ? 1 : B.parts == 3 ? 6 : 3;
+  args->term_code = !split ? 0u : B.parts == 3 ? 0x041582u : 0x012u;
+  args->a_mn = a_mn;
+  args->b_mn = b_mn;
+  args->idesc = idesc_f16_f32acc(bf16, S::BM, S::BN, a_mn, b_mn);
+  return 0;
+}
+
+int train_splits(int64_t tiles, int64_t kblocks, int clusters, int most) {
+  int best = 1;
+  double best_time = 1e30;
+  for (int s = 1; s <= most && (s == 1 || kblocks / s >= 4); ++s) {
+    const int64_t waves = (tiles * s + clusters - 1) / clusters;
+    // a range more costs the write and read of its sums
+    const double time = static_cast<double>(waves) / s * (1.0 + 0.02 * s);
+    if (time < best_time * 0.97) {
+      best_time = time;
+      best = s;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_slots_out(const SlotsOut& s, cudaStream_t stream) {
+  return launch_kernel(slots_out_kernel, dim3((s.M + 31) / 32, (s.N + 127) / 128), dim3(256), 0,
+                       stream, s);
+}
+
+cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
+                          int64_t ld, int64_t part_stride, int sm_count, cudaStream_t stream) {
+  const int64_t cap = static_cast<int64_t>(sm_count) * 8;
+  return launch_kernel(split3_kernel, dim3(static_cast<unsigned>(rows < cap ? rows : cap)),
+                       dim3(256), 0, stream, X, ldx, rows, cols,
+                       static_cast<__nv_bfloat16*>(out), ld, part_stride);
+}
+
+cudaError_t launch_train_tc(int mode, bool promote, const TrainMaps& maps, const TrainArgs& args,
+                            int clusters, cudaStream_t stream) {
+  return launch_kernel(kernel_of(mode, promote), dim3(2 * clusters), dim3(S::THREADS),
+                       S::SMEM_BYTES, stream, maps, args);
+}
+
+}  // namespace gemm14

@@ -1,0 +1,141 @@
+// train_tc.h -- the tensor-core kernel behind the training products
+// (train_tc.cu): one mainloop on CTA pairs with the epilogues that the linear
+// cross entropy and the weight gradient from 8-bit checkpoints need.
+// Internal; nothing here crosses the library boundary.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace gemm14 {
+
+// What becomes of a finished 256 x 256 tile of sums s (row i, column j):
+//   kTrainStats  the tile's part of each row's sum of exponentials, and the
+//                target's logit where the tile holds it (nothing else is kept);
+//   kTrainGrad   (exp(s - lse[i]) - [j == target[i]]) coef[i], in 16 bits (or as
+//                three bf16 parts of the fp32 value), rows from n on zero;
+//   kTrainSlots  s into (or added to) the tile's slot of a private fp32 buffer;
+//   kTrainOut    alpha s (+ beta out), row-major, in fp32, bf16 or fp16.
+enum : int { kTrainStats = 0, kTrainGrad = 1, kTrainSlots = 2, kTrainOut = 3 };
+
+// Element types of what an epilogue writes.
+enum : int { kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2, kElemBf16x3 = 3 };
+
+struct TrainShape {
+  static constexpr int BM = 256, BN = 256, BK = 64, STAGES = 6;
+  static constexpr int EPI_WARPS = 8;                   // two for each TMEM lane quarter
+  static constexpr int THREADS = (2 + EPI_WARPS) * 32;  // + producer, MMA
+  static constexpr int A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int OUT_BUF_BYTES = 32 * 128;  // per epilogue warp: 32 rows of 128 bytes
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int SMEM_BYTES =
+      STAGES * STAGE_BYTES + EPI_WARPS * OUT_BUF_BYTES + 256 + 1024;
+  // k-blocks whose products one TMEM accumulator takes before the sum goes to
+  // fp32 registers. The tensor cores add with truncation: measured on GB300,
+  // n MMAs of K = 16 in a row leave a relative error of about 0.4 n 2^-24 (512
+  // of them, K = 8192: 6.7e-6, against 6e-7 for an fp32 FMA sum). 64 MMAs, 16
+  // k-blocks, keep it under 1e-6.
+  static constexpr int CHUNK = 16;
+};
+
+struct TrainArgs {
+  // The product: M x N sums over K. n: the device's count of rows in use, in
+  // place of M (or of K where n_is_k), or null.
+  int M, N, K;
+  const int* n;
+  int n_is_k;
+  int a_mn, b_mn;       // operand stored with its M (N) dimension contiguous
+  // The sum over terms of products of operand parts (a value split in bf16
+  // parts): nibble t of term_code is part(A) | part(B) << 2 of term t.
+  int terms;
+  uint32_t term_code;
+  int splits;           // ranges of k-blocks worked on apart (slots only; 1 otherwise)
+  uint32_t idesc;
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+  int fault;
+
+  // kTrainStats, kTrainGrad: the vocabulary column of tile column 0 and
+  // per-row data of the rows in use
+  int v0;
+  const int* target;            // column of the target, < 0: none
+  const int64_t* target64;      // the same as the caller holds it (where target is null)
+  const float* lse;
+  const float* coef;
+  float2* part;                 // [(tile column) * 2 + half][row], pitch part_ld
+  int64_t part_ld;
+  float* target_logit;          // [row]
+  // kTrainGrad, kTrainOut: the output (part p of three at out + p * out_part)
+  void* out;
+  int64_t ld_out, out_part;
+  int elem, out_vec;            // element type; rows start and end on 16 bytes
+  float alpha, beta;
+  const float* scale;           // device factor on alpha, or null
+  // kTrainSlots
+  float4* slots;
+  int add;                      // add to what the slots hold
+};
+
+// Slots: float4 v (columns 4v ..) of chunk c (32 columns) of half h (128
+// columns) of CTA r's 128 rows of tile t, split s, row q: see slot_index.
+__host__ __device__ inline int64_t slot_index(int64_t tiles, int split, int64_t tile, int r, int h,
+                                              int c, int v, int q) {
+  return ((((split * tiles + tile) * 2 + r) * 2 + h) * 4 + c) * 1024 + v * 128 + q;
+}
+
+// Clusters of two that fit at once on the current device (0: they cannot run).
+int train_max_clusters();
+
+// The parts' tensor maps (boxes of 64 k x 128 rows, K-major, or 64 x 64, with
+// the 128-byte swizzle).
+struct TrainMaps {
+  CUtensorMap a[3], b[3];
+};
+
+// One operand of a launch: `parts` matrices of 16-bit elements, part p at
+// base + p * part_stride (elements), rows x cols as stored, pitch ld.
+struct TrainOperand {
+  const void* base;
+  int64_t rows, cols, ld;
+  int parts;
+  int64_t part_stride;
+};
+// The maps of A (M x K, or stored K x M when a_mn) and B (N x K, or K x N when
+// b_mn), and the terms, instruction descriptor and a_mn / b_mn of *args.
+// Returns a gemm14_status.
+int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOperand& B, bool b_mn,
+                   TrainMaps* maps, TrainArgs* args);
+
+// Ranges of k-blocks to split `tiles` tiles of kblocks k-blocks into on
+// `clusters` clusters: the count whose last wave leaves least idle, each range
+// of 4 k-blocks or more, at most `most`.
+int train_splits(int64_t tiles, int64_t kblocks, int clusters, int most);
+
+// out[r] = alpha * *scale * (sum over splits of row r's slots) + beta * out[r]
+// for the first n rows (*n, or M), r going through `rows` where it is set.
+struct SlotsOut {
+  const float4* slots;
+  int splits;
+  int M, N;
+  const int* n;
+  const int* rows;
+  float alpha, beta;
+  const float* scale;
+  void* out;
+  int64_t ld;
+  int elem;
+};
+cudaError_t launch_slots_out(const SlotsOut& s, cudaStream_t stream);
+
+// A rows x cols fp32 matrix as three bf16 parts whose sum is each value (to
+// 24 bits): the nearest bf16, the nearest to the rest, and to the rest of that.
+cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
+                          int64_t ld, int64_t part_stride, int sm_count, cudaStream_t stream);
+
+// promote: sums leave the accumulators for fp32 registers every CHUNK k-blocks.
+cudaError_t launch_train_tc(int mode, bool promote, const TrainMaps& maps, const TrainArgs& args,
+                            int clusters, cudaStream_t stream);
+
+}  // namespace gemm14
