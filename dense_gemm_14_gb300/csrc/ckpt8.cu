@@ -63,7 +63,170 @@ __device__ __forceinline__ float step_of(uint32_t s) {
   return s == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((max(s, 7u) - 6u) << 23);
 }
 
-// One warp a block of 32 columns, a lane a column.
+// A thread's place in a matrix of rows x per_row items taken in order, moved on
+// by a fixed step without dividing again.
+struct Place {
+  int64_t row, item;
+  __device__ Place(int64_t i, int64_t per_row) : row(i / per_row), item(i - row * per_row) {}
+  __device__ void move(const Place& step, int64_t per_row) {
+    row += step.row;
+    item += step.item;
+    if (item >= per_row) {
+      item -= per_row;
+      ++row;
+    }
+  }
+};
+
+// Both kernels come in two forms. Where rows start on 16 bytes a lane moves a
+// piece of 16 bytes of X (8 or 4 values; 4 or 8 lanes a block, whose largest
+// magnitude they find with two or three shuffles) and 8 or 4 bytes of Q;
+// otherwise a lane is one column, a warp one block, with coalesced accesses of
+// single elements whatever the addresses. Either way a thread has kUnroll
+// loads in flight before it works on the first: the passes are bound by memory.
+constexpr int kUnroll = 4;
+
+// Pieces of a row, whole blocks (the last ones may hold no column).
+template <typename T>
+__host__ __device__ constexpr int piece_values() { return 16 / static_cast<int>(sizeof(T)); }
+
+template <typename T>
+union Piece {
+  uint4 raw;
+  T x[16 / sizeof(T)];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_save_vec_kernel(const T* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
+                          int64_t rows, int64_t cols) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  constexpr int kPer = piece_values<T>(), kLanes = kBlock / kPer;
+  const int64_t per_row = (cols + kBlock - 1) / kBlock * kLanes;
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
+  const Place step(threads, per_row);
+  Place at(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, per_row);
+  // whole warps go round together (the shuffles need every lane of a block)
+  const int64_t turns = (rows * per_row + threads * kUnroll - 1) / (threads * kUnroll);
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    Piece<T> p[kUnroll];
+    Place place[kUnroll] = {at, at, at, at};
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      place[u] = at;
+      const int64_t c = at.item * kPer;
+      p[u].raw = make_uint4(0, 0, 0, 0);
+      if (at.row < rows) {
+        const T* x = X + at.row * ldx + c;
+        if (c + kPer <= cols) {
+          p[u].raw = __ldcs(reinterpret_cast<const uint4*>(x));
+        } else {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            if (c + j < cols) p[u].x[j] = x[j];
+        }
+      }
+      at.move(step, per_row);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float x[kPer];
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        x[j] = to_f32(p[u].x[j]);
+        top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const uint32_t s = scale_byte(top);
+      const float factor = scale_factor(s);
+      uint32_t w[kPer / 4];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const uint32_t q = static_cast<uint32_t>(s == 255u ? 0 : quantise(x[j], factor)) & 0xffu;
+        w[j / 4] = j % 4 == 0 ? q : w[j / 4] | q << (8 * (j % 4));
+      }
+      const int64_t r = place[u].row, c = place[u].item * kPer;
+      if (r >= rows || c >= cols) continue;
+      int8_t* to = Q + r * ldq + c;
+      if (c + kPer <= cols) {
+        if constexpr (kPer == 8)
+          *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        else
+          *reinterpret_cast<uint32_t*>(to) = w[0];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (c + j < cols) to[j] = static_cast<int8_t>(w[j / 4] >> (8 * (j % 4)));
+      }
+      if (place[u].item % kLanes == 0) S[r * lds + c / kBlock] = static_cast<uint8_t>(s);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_restore_vec_kernel(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, T* X,
+                             int64_t ldx, int64_t rows, int64_t cols) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  constexpr int kPer = piece_values<T>();
+  const int64_t per_row = (cols + kPer - 1) / kPer;
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
+  const Place step(threads, per_row);
+  Place at(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, per_row);
+  while (at.row < rows) {
+    uint32_t w[kUnroll][kPer / 4], s[kUnroll];
+    Place place[kUnroll] = {at, at, at, at};
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      place[u] = at;
+      const int64_t c = at.item * kPer;
+      if (at.row < rows) {
+        const int8_t* q = Q + at.row * ldq + c;
+        s[u] = S[at.row * lds + c / kBlock];
+        if (c + kPer <= cols) {
+          if constexpr (kPer == 8) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(q));
+            w[u][0] = v.x;
+            w[u][1] = v.y;
+          } else {
+            w[u][0] = __ldcs(reinterpret_cast<const uint32_t*>(q));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const uint32_t v = c + j < cols ? static_cast<uint8_t>(q[j]) : 0u;
+            w[u][j / 4] = j % 4 == 0 ? v : w[u][j / 4] | v << (8 * (j % 4));
+          }
+        }
+      }
+      at.move(step, per_row);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t r = place[u].row, c = place[u].item * kPer;
+      if (r >= rows) break;
+      const float k = step_of(s[u]);
+      Piece<T> p;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        p.x[j] = from_f32<T>(static_cast<float>(static_cast<int8_t>(w[u][j / 4] >> (8 * (j % 4)))) *
+                             k);
+      T* to = X + r * ldx + c;
+      if (c + kPer <= cols) {
+        *reinterpret_cast<uint4*>(to) = p.raw;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (c + j < cols) to[j] = p.x[j];
+      }
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     ckpt8_save_kernel(const T* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
@@ -73,15 +236,28 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31;
   const int64_t per_row = (cols + kBlock - 1) / kBlock;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-       i < rows * per_row; i += warps) {
-    const int64_t r = i / per_row, b = i - r * per_row, c = b * kBlock + lane;
-    const float x = c < cols ? to_f32(X[r * ldx + c]) : 0.0f;
-    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu);
-    const uint32_t s = scale_byte(top);
-    if (c < cols)
-      Q[r * ldq + c] = static_cast<int8_t>(s == 255u ? 0 : quantise(x, scale_factor(s)));
-    if (lane == 0) S[r * lds + b] = static_cast<uint8_t>(s);
+  const Place step(warps, per_row);
+  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), per_row);
+  while (at.row < rows) {
+    float x[kUnroll];
+    Place place[kUnroll] = {at, at, at, at};
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      place[u] = at;
+      const int64_t c = at.item * kBlock + lane;
+      x[u] = at.row < rows && c < cols ? to_f32(X[at.row * ldx + c]) : 0.0f;
+      at.move(step, per_row);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t r = place[u].row, b = place[u].item, c = b * kBlock + lane;
+      if (r >= rows) break;
+      const uint32_t s = scale_byte(
+          __reduce_max_sync(0xffffffffu, __float_as_uint(x[u]) & 0x7fffffffu));
+      if (c < cols)
+        Q[r * ldq + c] = static_cast<int8_t>(s == 255u ? 0 : quantise(x[u], scale_factor(s)));
+      if (lane == 0) S[r * lds + b] = static_cast<uint8_t>(s);
+    }
   }
 }
 
@@ -94,30 +270,62 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31;
   const int64_t per_row = (cols + kBlock - 1) / kBlock;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-       i < rows * per_row; i += warps) {
-    const int64_t r = i / per_row, b = i - r * per_row, c = b * kBlock + lane;
-    if (c < cols) X[r * ldx + c] = from_f32<T>(Q[r * ldq + c] * step_of(S[r * lds + b]));
+  const Place step(warps, per_row);
+  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), per_row);
+  while (at.row < rows) {
+    int q[kUnroll];
+    uint32_t s[kUnroll];
+    Place place[kUnroll] = {at, at, at, at};
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      place[u] = at;
+      const int64_t c = at.item * kBlock + lane;
+      const bool in = at.row < rows && c < cols;
+      q[u] = in ? Q[at.row * ldq + c] : 0;
+      s[u] = in ? S[at.row * lds + at.item] : 0u;
+      at.move(step, per_row);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t r = place[u].row, c = place[u].item * kBlock + lane;
+      if (r < rows && c < cols) X[r * ldx + c] = from_f32<T>(q[u] * step_of(s[u]));
+    }
   }
 }
 
-int grid_for(int64_t rows, int64_t cols, int sm_count) {
-  const int64_t blocks = (rows * ((cols + kBlock - 1) / kBlock) + 7) / 8;
+// Blocks for `threads_needed` threads of one item each, at most 8 an SM.
+int grid_for(int64_t threads_needed, int sm_count) {
+  const int64_t blocks = (threads_needed + kThreads - 1) / kThreads;
   const int64_t cap = static_cast<int64_t>(sm_count) * 8;
   return static_cast<int>(blocks < cap ? blocks : cap);
+}
+
+// Whether rows of X and Q take the wide accesses.
+template <typename T>
+bool wide(const void* X, int64_t ldx, const void* Q, int64_t ldq) {
+  constexpr int kPer = piece_values<T>();
+  return aligned(X, 16) && ldx % kPer == 0 && aligned(Q, kPer) && ldq % kPer == 0;
 }
 
 template <typename T>
 cudaError_t save_as(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
                     int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
-  return launch_kernel(ckpt8_save_kernel<T>, dim3(grid_for(rows, cols, sms)), dim3(kThreads), 0,
-                       stream, static_cast<const T*>(X), ldx, Q, ldq, S, lds, rows, cols);
+  const int64_t blocks = (cols + kBlock - 1) / kBlock;
+  const bool vec = wide<T>(X, ldx, Q, ldq);
+  const int grid = grid_for(rows * blocks * (vec ? kBlock / piece_values<T>() : 32), sms);
+  return launch_kernel(vec ? ckpt8_save_vec_kernel<T> : ckpt8_save_kernel<T>, dim3(grid),
+                       dim3(kThreads), 0, stream, static_cast<const T*>(X), ldx, Q, ldq, S, lds,
+                       rows, cols);
 }
 template <typename T>
 cudaError_t restore_as(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, void* X,
                        int64_t ldx, int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
-  return launch_kernel(ckpt8_restore_kernel<T>, dim3(grid_for(rows, cols, sms)), dim3(kThreads),
-                       0, stream, Q, ldq, S, lds, static_cast<T*>(X), ldx, rows, cols);
+  const bool vec = wide<T>(X, ldx, Q, ldq);
+  const int64_t items = vec ? (cols + piece_values<T>() - 1) / piece_values<T>()
+                            : (cols + kBlock - 1) / kBlock * 32;
+  return launch_kernel(vec ? ckpt8_restore_vec_kernel<T> : ckpt8_restore_kernel<T>,
+                       dim3(grid_for(rows * items, sms)), dim3(kThreads), 0, stream, Q, ldq, S,
+                       lds, static_cast<T*>(X), ldx, rows, cols);
 }
 
 cudaError_t launch_restore(int dtype, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,

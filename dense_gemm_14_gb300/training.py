@@ -3,7 +3,6 @@ projection's outputs, and activations kept in 8 bits (argument marshalling
 only; every step runs in the library's CUDA kernels)."""
 from __future__ import annotations
 
-import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -22,18 +21,18 @@ def _code(x: torch.Tensor, fp32_mode: str | None) -> int:
     return _FP32_MODES[fp32_mode] if x.dtype == torch.float32 else _CODE[x.dtype]
 
 
-@contextlib.contextmanager
-def _on(stream, device: torch.device):
-    """The stream handle of a call, with that stream current inside: what the
-    call allocates then belongs to the stream its kernels run on."""
+def _on(stream, device: torch.device, body):
+    """body(stream handle) with `device` and, where one is given, `stream`
+    current: what the call allocates then belongs to the stream its kernels run on."""
     if stream is None:
+        if device.index == torch.cuda.current_device():
+            return body(torch.cuda.current_stream().cuda_stream)
         with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-        return
+            return body(torch.cuda.current_stream().cuda_stream)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield stream.cuda_stream
+        return body(stream.cuda_stream)
 
 
 def _matrix(x: torch.Tensor, name: str, device: torch.device | None = None) -> int:
@@ -85,7 +84,8 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     stream) without synchronising, with a workspace cached per (device, stream).
     fp32_mode as for gemm_into."""
     code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
-    with _on(stream, h.device) as handle:
+
+    def body(handle):
         out = torch.empty((2, T), dtype=torch.float32, device=h.device)
         if T:
             n = _lib.linear_ce_workspace_bytes(code, 0, T, V, D, h.data_ptr(), ldh, w.data_ptr(),
@@ -94,7 +94,9 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
             _lib.linear_ce_forward(code, T, V, D, h.data_ptr(), ldh, w.data_ptr(), ldw,
                                    targets.data_ptr(), int(ignore_index), out.data_ptr(),
                                    out.data_ptr() + 4 * T, ws.data_ptr(), ws.numel(), handle)
-    return out[0], out[1]
+        return out[0], out[1]
+
+    return _on(stream, h.device, body)
 
 
 def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
@@ -110,7 +112,8 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor, targets: tor
     code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
     _vector(lse, "lse", T, torch.float32, h.device)
     _vector(dloss, "dloss", T, torch.float32, h.device)
-    with _on(stream, h.device) as handle:
+
+    def body(handle):
         dh = torch.empty((T, D), dtype=h.dtype, device=h.device) if need_dh else None
         dw = torch.empty((V, D), dtype=w.dtype, device=w.device) if need_dw else None
         if need_dw or (need_dh and T):
@@ -121,10 +124,12 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor, targets: tor
                                     int(ignore_index), _ptr(lse), _ptr(dloss), _ptr(dh), D,
                                     _ptr(dw), D, ws.data_ptr() if n else None,
                                     ws.numel() if n else 0, handle)
-    return dh, dw
+        return dh, dw
+
+    return _on(stream, h.device, body)
 
 
-@dataclass(frozen=True)
+@dataclass(slots=True, eq=False)
 class Ckpt8:
     """A matrix kept in 8 bits: q (rows, cols) int8 and a scale byte for each
     block of 32 columns, scale (rows, ceil(cols / 32)) uint8; a value stands
@@ -157,14 +162,17 @@ def ckpt8_save(x: torch.Tensor, stream=None) -> Ckpt8:
     rows, cols = x.shape
     blocks = -(-cols // CKPT8_BLOCK)
     ldq, lds = -(-cols // 16) * 16, -(-blocks // 16) * 16
-    with _on(stream, x.device) as handle:
+
+    def body(handle):
         # rows of both on 16 bytes
-        q = torch.empty((rows, ldq), dtype=torch.int8, device=x.device)[:, :cols]
-        scale = torch.empty((rows, lds), dtype=torch.uint8, device=x.device)[:, :blocks]
+        q = torch.empty((rows, ldq), dtype=torch.int8, device=x.device)
+        scale = torch.empty((rows, lds), dtype=torch.uint8, device=x.device)
         if x.numel():
             _lib.ckpt8_save_raw(_CODE[x.dtype], rows, cols, x.data_ptr(), ldx, q.data_ptr(), ldq,
                                 scale.data_ptr(), lds, handle)
-    return Ckpt8(q, scale)
+        return Ckpt8(q if ldq == cols else q[:, :cols], scale if lds == blocks else scale[:, :blocks])
+
+    return _on(stream, x.device, body)
 
 
 def ckpt8_restore(c: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
@@ -173,12 +181,15 @@ def ckpt8_restore(c: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) ->
         raise TypeError(f"unsupported dtype {dtype}")
     ldq, lds = _ckpt8_operands(c)
     rows, cols = c.q.shape
-    with _on(stream, c.q.device) as handle:
+
+    def body(handle):
         out = torch.empty((rows, cols), dtype=dtype, device=c.q.device)
         if out.numel():
             _lib.ckpt8_restore_raw(_CODE[dtype], rows, cols, c.q.data_ptr(), ldq,
                                    c.scale.data_ptr(), lds, out.data_ptr(), cols, handle)
-    return out
+        return out
+
+    return _on(stream, c.q.device, body)
 
 
 def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = None,
@@ -200,15 +211,17 @@ def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = Non
             raise ValueError("beta != 0 needs out")
     elif out.dtype != torch.float32 or tuple(out.shape) != (N, K):
         raise ValueError(f"out must be float32 of shape {(N, K)}")
-    with _on(stream, dy.device) as handle:
-        if out is None:
-            out = torch.empty((N, K), dtype=torch.float32, device=dy.device)
-        lddw = _matrix(out, "out", dy.device)
-        if not out.numel():
-            return out
-        n = _lib.ckpt8_wgrad_workspace_bytes(code, T, N, K, _ptr(dy), lddy, out.data_ptr(), lddw)
+
+    def body(handle):
+        dw = out if out is not None else torch.empty((N, K), dtype=torch.float32, device=dy.device)
+        lddw = _matrix(dw, "out", dy.device)
+        if not dw.numel():
+            return dw
+        n = _lib.ckpt8_wgrad_workspace_bytes(code, T, N, K, _ptr(dy), lddy, dw.data_ptr(), lddw)
         ws = _workspace(dy.device, handle, n) if n else None
         _lib.ckpt8_wgrad(code, T, N, K, float(alpha), _ptr(dy), lddy, _ptr(c.q), ldq,
-                         _ptr(c.scale), lds, float(beta), out.data_ptr(), lddw,
+                         _ptr(c.scale), lds, float(beta), dw.data_ptr(), lddw,
                          ws.data_ptr() if n else None, ws.numel() if n else 0, handle)
-    return out
+        return dw
+
+    return _on(stream, dy.device, body)
