@@ -58,6 +58,33 @@ __device__ __forceinline__ int quantise(float x, float factor) {
   const int q = __float2int_rn(x * factor);
   return max(-127, min(127, q));
 }
+// The same in the low byte of the result: 1.5 2^23 added to a value of
+// [-127, 127] rounds it to the nearest whole number, ties to even, in the low
+// bits of the sum (its clamp first: 127 is whole, so the order does not matter).
+__device__ __forceinline__ uint32_t quantise_byte(float x, float factor) {
+  return __float_as_uint(fminf(fmaxf(x * factor, -127.0f), 127.0f) + 12582912.0f);
+}
+// Four low bytes as one word.
+__device__ __forceinline__ uint32_t pack4(const uint32_t (&q)[4]) {
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+}
+// The fp32 bits, sign cleared, of the largest magnitude among a piece's values:
+// magnitudes of a 16-bit type are ordered as whole numbers, two at a time.
+__device__ __forceinline__ uint32_t top_of(const uint4& v, float) {
+  return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+}
+__device__ __forceinline__ uint32_t top16(const uint4& v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+__device__ __forceinline__ uint32_t top_of(const uint4& v, __nv_bfloat16) {
+  return top16(v) << 16;
+}
+__device__ __forceinline__ uint32_t top_of(const uint4& v, __half) {
+  return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top16(v))))) &
+         0x7fffffffu;
+}
 // 2^(s - 133), NaN for byte 255; bytes below 7, which save never writes, count as 7.
 __device__ __forceinline__ float step_of(uint32_t s) {
   return s == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((max(s, 7u) - 6u) << 23);
@@ -131,22 +158,18 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      float x[kPer];
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        x[j] = to_f32(p[u].x[j]);
-        top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-      }
+      uint32_t top = top_of(p[u].raw, T());
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const uint32_t s = scale_byte(top);
       const float factor = scale_factor(s);
       uint32_t w[kPer / 4];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const uint32_t q = static_cast<uint32_t>(s == 255u ? 0 : quantise(x[j], factor)) & 0xffu;
-        w[j / 4] = j % 4 == 0 ? q : w[j / 4] | q << (8 * (j % 4));
+      for (int k = 0; k < kPer / 4; ++k) {
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = quantise_byte(to_f32(p[u].x[4 * k + j]), factor);
+        w[k] = s == 255u ? 0u : pack4(q);  // (an infinity times 0 is no number)
       }
       const int64_t r = place[u].row, c = place[u].item * kPer;
       if (r >= rows || c >= cols) continue;
@@ -366,7 +389,6 @@ struct WgradLayout {
   bool tc = false;
   int parts = 1;           // bf16 parts of dY
   bool copy_dy = false;    // dY is copied (unaligned) or split
-  int splits = 1;          // ranges of T
   int64_t ldx = 0, lddy = 0;
   size_t x_off = 0, dy_off = 0, slots_off = 0, total = 0;
 };
@@ -398,8 +420,8 @@ void wgrad_layout(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, in
   l->x_off = take(static_cast<size_t>(T) * l->ldx * 2);
   if (l->copy_dy) l->dy_off = take(static_cast<size_t>(T) * l->lddy * 2 * l->parts);
   const int64_t tiles = ((N + 255) / 256) * ((K + 255) / 256);
-  l->splits = train_splits(tiles, (T + 63) / 64, sms > 1 ? sms / 2 : 1, 64);
-  if (l->splits > 1) l->slots_off = take(static_cast<size_t>(l->splits) * tiles * 256 * 256 * 4);
+  l->slots_off = take(static_cast<size_t>(slots_needed(tiles, sms > 1 ? sms / 2 : 1, false)) *
+                      kSlotBytes);
   l->total = at;
 }
 
@@ -442,7 +464,7 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   a.M = static_cast<int>(N);
   a.N = static_cast<int>(K);
   a.K = static_cast<int>(T);
-  a.splits = l.splits;
+  a.split_k = a.K;
   a.err = ctx.err;
   a.wait_limit_ns = ctx.wait_limit_ns;
   a.fault = ctx.fault;
@@ -458,24 +480,12 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   const TrainOperand B{ws + l.x_off, T, K, l.ldx, 1, 0};
   if ((st = train_operands(dtype != GEMM14_DTYPE_F16, A, true, B, true, &maps, &a)) != GEMM14_OK)
     return st;
-  const int64_t items = ((N + 255) / 256) * ((K + 255) / 256) * l.splits;
-  const int grid = static_cast<int>(items < clusters ? items : clusters);
-  const bool promote = (T + 63) / 64 > static_cast<int64_t>(TrainShape::CHUNK) * l.splits;
-  st = finish_launch(launch_train_tc(l.splits > 1 ? kTrainSlots : kTrainOut, promote, maps, a,
-                                     grid, stream),
+  const bool promote = T > TrainShape::CHUNK * TrainShape::BK;
+  st = finish_launch(launch_train_tc(kTrainOut, promote, maps, a, clusters, stream),
                      "ckpt8 product launch", stream);
-  if (st != GEMM14_OK || l.splits == 1) return st;
-  SlotsOut s{};
-  s.slots = a.slots;
-  s.splits = l.splits;
-  s.M = a.M;
-  s.N = a.N;
-  s.alpha = alpha;
-  s.beta = beta;
-  s.out = dW;
-  s.ld = lddw;
-  s.elem = kElemF32;
-  return finish_launch(launch_slots_out(s, stream), "ckpt8 output launch", stream);
+  if (st != GEMM14_OK || !may_split(a, clusters)) return st;
+  const SlotsOut s{false, nullptr, alpha, beta, nullptr, dW, lddw, kElemF32};
+  return finish_launch(launch_slots_out(a, s, clusters, stream), "ckpt8 output launch", stream);
 }
 
 }  // namespace

@@ -359,10 +359,9 @@ struct CeLayout {
   int parts = 1;       // bf16 parts of an operand
   bool gather = false; // rows in use are numbered and gathered first
   bool copy_w = false; // pieces of W are copied (unaligned) or split
-  int splits = 1;      // of the dH product
   int64_t rows = 0;    // T rounded up to whole tiles
   size_t state = 0, counts = 0, index = 0, position = 0, target = 0, lse = 0, coef = 0, h = 0,
-         w = 0, part = 0, z = 0, slots = 0, total = 0;
+         w = 0, part = 0, z = 0, slots = 0, tail = 0, total = 0;
 };
 
 void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
@@ -379,6 +378,7 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
   };
   const size_t t4 = static_cast<size_t>(T) * 4;
   if (l->tc) {
+    l->ldx = round_up(D, 64);  // rows that start on 128-byte lines
     l->parts = dtype == GEMM14_DTYPE_F32_3XTF32 ? 3 : 1;
     l->copy_w = l->parts == 3 || !tma_rows(W, ldw);
     // one tile row of rows costs the same with and without the ignored ones
@@ -400,9 +400,12 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
       l->lse = take(t4);
       l->coef = take(t4);
       l->z = take(static_cast<size_t>(l->rows) * l->ldz * 2 * l->parts);
-      const int64_t tiles = tiles_of(T) * tiles_of(D);
-      l->splits = train_splits(tiles, (l->C + 63) / 64, std::max(sms / 2, 1), 64);
-      l->slots = take(static_cast<size_t>(l->splits) * tiles * 256 * 256 * 4);
+      // dH's sums over the pieces, and what dW's split tiles need after them
+      const int clusters = std::max(sms / 2, 1);
+      l->slots = take(static_cast<size_t>(slots_needed(tiles_of(T) * tiles_of(D), clusters, true)) *
+                      kSlotBytes);
+      l->tail = take(static_cast<size_t>(slots_needed(tiles_of(l->C) * tiles_of(D), clusters,
+                                                      false)) * kSlotBytes);
     } else {
       l->part = take(static_cast<size_t>(2 * tiles_of(V)) * l->rows * sizeof(float2));
       l->state = take(t4);
@@ -540,7 +543,6 @@ struct CeCall {
     a.K = static_cast<int>(K);
     a.n = l.gather ? at<int>(l.counts) : nullptr;
     a.n_is_k = n_is_k;
-    a.splits = 1;
     a.err = ctx.err;
     a.wait_limit_ns = ctx.wait_limit_ns;
     a.fault = ctx.fault;
@@ -553,10 +555,8 @@ struct CeCall {
     TrainMaps maps;
     const int st = train_operands(bf16(), A, a_mn, B, b_mn, &maps, a);
     if (st != GEMM14_OK) return st;
-    const int64_t items = tiles_of(a->M) * tiles_of(a->N) * a->splits;
-    const int64_t grid = std::min<int64_t>(items, clusters);
     ctx.fault = kFaultNone;  // a test's request applies to the call's first product
-    return launched(launch_train_tc(mode, promote, maps, *a, static_cast<int>(grid), stream),
+    return launched(launch_train_tc(mode, promote, maps, *a, clusters, stream),
                     "linear_ce product launch");
   }
 
@@ -620,7 +620,7 @@ struct CeCall {
       const TrainOperand dz{ws + l.z, l.rows, c, l.ldz, l.parts, g_part};
       if (dH) {
         a = product(T, D, c, false);
-        a.splits = l.splits;
+        a.split_k = static_cast<int>(l.C);  // the same plan for every piece
         a.slots = at<float4>(l.slots);
         a.add = v0 > 0;
         if ((st = run(kTrainSlots, exact && long_sum(c), dz, false, w, true, &a)) != GEMM14_OK)
@@ -633,25 +633,26 @@ struct CeCall {
         a.elem = elem;
         a.out_vec = aligned(dW, 16) && lddw * eb() % 16 == 0;
         a.scale = r.back;
+        a.split_k = static_cast<int>(T);
+        a.slots = at<float4>(l.tail);
         if ((st = run(kTrainOut, exact && long_sum(T), dz, true, h_operand(), true, &a)) !=
             GEMM14_OK)
           return st;
+        if (may_split(a, clusters)) {
+          const SlotsOut s{false, nullptr, 1.0f, 0.0f, r.back, a.out, lddw, elem};
+          if ((st = launched(launch_slots_out(a, s, clusters, stream),
+                             "linear_ce output launch")) != GEMM14_OK)
+            return st;
+        }
       }
     }
     if (!dH) return GEMM14_OK;
-    SlotsOut s{};
-    s.slots = at<float4>(l.slots);
-    s.splits = l.splits;
-    s.M = static_cast<int>(T);
-    s.N = static_cast<int>(D);
-    s.n = r.n;
-    s.rows = r.index;
-    s.alpha = 1.0f;
-    s.scale = r.back;
-    s.out = dH;
-    s.ld = lddh;
-    s.elem = elem;
-    return launched(launch_slots_out(s, stream), "linear_ce output launch");
+    TrainArgs a = product(T, D, V, false);
+    a.split_k = static_cast<int>(l.C);
+    a.terms = exact ? 6 : 1;
+    a.slots = at<float4>(l.slots);
+    const SlotsOut s{true, r.index, 1.0f, 0.0f, r.back, dH, lddh, elem};
+    return launched(launch_slots_out(a, s, clusters, stream), "linear_ce output launch");
   }
 
   // ---- the FFMA and TF32 modes

@@ -16,7 +16,8 @@ namespace gemm14 {
 //   kTrainGrad   (exp(s - lse[i]) - [j == target[i]]) coef[i], in 16 bits (or as
 //                three bf16 parts of the fp32 value), rows from n on zero;
 //   kTrainSlots  s into (or added to) the tile's slot of a private fp32 buffer;
-//   kTrainOut    alpha s (+ beta out), row-major, in fp32, bf16 or fp16.
+//   kTrainOut    alpha s (+ beta out), row-major, in fp32, bf16 or fp16 (split
+//                tiles: their sums into slots).
 enum : int { kTrainStats = 0, kTrainGrad = 1, kTrainSlots = 2, kTrainOut = 3 };
 
 // Element types of what an epilogue writes.
@@ -51,7 +52,7 @@ struct TrainArgs {
   // parts): nibble t of term_code is part(A) | part(B) << 2 of term t.
   int terms;
   uint32_t term_code;
-  int splits;           // ranges of k-blocks worked on apart (slots only; 1 otherwise)
+  int split_k;          // K that the split of tiles is planned for (0: none are split)
   uint32_t idesc;
   unsigned* err;
   unsigned long long wait_limit_ns;
@@ -78,12 +79,49 @@ struct TrainArgs {
   int add;                      // add to what the slots hold
 };
 
-// Slots: float4 v (columns 4v ..) of chunk c (32 columns) of half h (128
-// columns) of CTA r's 128 rows of tile t, split s, row q: see slot_index.
-__host__ __device__ inline int64_t slot_index(int64_t tiles, int split, int64_t tile, int r, int h,
-                                              int c, int v, int q) {
-  return ((((split * tiles + tile) * 2 + r) * 2 + h) * 4 + c) * 1024 + v * 128 + q;
+// How a launch's tiles are worked on by `clusters` clusters: the first `direct`
+// tiles whole, in full waves; each of the rest, which would leave clusters idle
+// in a last partial wave, by `splits` ranges of its k-blocks whose sums go to
+// slots and are added up by launch_slots_out (1: those tiles are whole too, and
+// direct counts them). The count of ranges is the one whose partial waves are
+// shortest; a split has to save 24 k-blocks' time (about 8 us: the second launch
+// takes 4 to 6), and a range has 4 k-blocks or more. Both launches work it out
+// on the device, from the rows in use. `units`: k-blocks times terms.
+struct TilePlan {
+  int tiles, direct, splits;
+};
+constexpr int kTailWaves = 4;  // splits x tail tiles stay within this many waves
+__host__ __device__ inline TilePlan plan_tiles(int tiles, int kblocks, int units, int clusters) {
+  const int tail = tiles % clusters;
+  int best = 1;
+  float best_time = 1.0f;
+  for (int s = 2; s * 4 <= kblocks && tail && tail * s <= kTailWaves * clusters; ++s) {
+    const float time = static_cast<float>((tail * s + clusters - 1) / clusters) / s + 0.01f * s;
+    if (time < best_time) {
+      best_time = time;
+      best = s;
+    }
+  }
+  if ((1.0f - best_time) * units < 24.0f) best = 1;
+  return TilePlan{tiles, best > 1 ? tiles - tail : tiles, best};
 }
+// The slot of split s of a tile. all: every tile has slots (kTrainSlots).
+__host__ __device__ inline int64_t slot_of(const TilePlan& p, bool all, int tile, int s) {
+  if (tile < p.direct) return tile;
+  return (all ? p.direct : 0) + static_cast<int64_t>(tile - p.direct) * p.splits + s;
+}
+// Slots that a launch of at most this many tiles can need.
+inline int64_t slots_needed(int64_t tiles, int clusters, bool all) {
+  const int64_t tail = tiles < clusters ? tiles : clusters;
+  const int64_t split = static_cast<int64_t>(kTailWaves) * clusters;
+  return (all ? tiles + split : split) + tail;
+}
+// float4 v (columns 4v ..) of chunk c (32 columns) of half h (128 columns) of row
+// q of CTA r's 128 rows, in slot k: rows next to one another.
+__host__ __device__ inline int64_t slot_index(int64_t k, int r, int h, int c, int v, int q) {
+  return (((k * 2 + r) * 2 + h) * 4 + c) * 1024 + v * 128 + q;
+}
+constexpr int64_t kSlotBytes = 256 * 256 * 4;
 
 // Clusters of two that fit at once on the current device (0: they cannot run).
 int train_max_clusters();
@@ -108,18 +146,12 @@ struct TrainOperand {
 int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOperand& B, bool b_mn,
                    TrainMaps* maps, TrainArgs* args);
 
-// Ranges of k-blocks to split `tiles` tiles of kblocks k-blocks into on
-// `clusters` clusters: the count whose last wave leaves least idle, each range
-// of 4 k-blocks or more, at most `most`.
-int train_splits(int64_t tiles, int64_t kblocks, int clusters, int most);
-
-// out[r] = alpha * *scale * (sum over splits of row r's slots) + beta * out[r]
-// for the first n rows (*n, or M), r going through `rows` where it is set.
+// What follows a launch with slots: out[r] = alpha * *scale * (sum of row r's
+// slots) + beta * out[r], for the rows in use (all: of every tile; otherwise of
+// the split ones), row r going through `rows` where it is set. The other
+// arguments are the launch's.
 struct SlotsOut {
-  const float4* slots;
-  int splits;
-  int M, N;
-  const int* n;
+  bool all;
   const int* rows;
   float alpha, beta;
   const float* scale;
@@ -127,7 +159,11 @@ struct SlotsOut {
   int64_t ld;
   int elem;
 };
-cudaError_t launch_slots_out(const SlotsOut& s, cudaStream_t stream);
+// clusters: the launch's.
+cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clusters,
+                             cudaStream_t stream);
+// Whether a kTrainOut launch may split tiles (then launch_slots_out follows it).
+bool may_split(const TrainArgs& args, int clusters);
 
 // A rows x cols fp32 matrix as three bf16 parts whose sum is each value (to
 // 24 bits): the nearest bf16, the nearest to the rest, and to the rest of that.

@@ -44,7 +44,7 @@ def _matrix(x: torch.Tensor, name: str, device: torch.device | None = None) -> i
     rows, cols = x.shape
     if cols > 1 and x.stride(1) != 1:
         raise ValueError(f"{name} must have unit stride along its rows (row-major)")
-    if rows > 1 and x.stride(0) < max(cols, 1):
+    if rows > 1 and cols > 0 and x.stride(0) < cols:
         raise ValueError(f"{name}: rows overlap (stride {x.stride()})")
     return max(x.stride(0), cols, 1) if rows > 1 else max(cols, 1)
 
@@ -165,12 +165,12 @@ def ckpt8_save(x: torch.Tensor, stream=None) -> Ckpt8:
 
     def body(handle):
         # rows of both on 16 bytes
-        q = torch.empty((rows, ldq), dtype=torch.int8, device=x.device)
-        scale = torch.empty((rows, lds), dtype=torch.uint8, device=x.device)
+        q = torch.empty_strided((rows, cols), (ldq, 1), dtype=torch.int8, device=x.device)
+        scale = torch.empty_strided((rows, blocks), (lds, 1), dtype=torch.uint8, device=x.device)
         if x.numel():
             _lib.ckpt8_save_raw(_CODE[x.dtype], rows, cols, x.data_ptr(), ldx, q.data_ptr(), ldq,
                                 scale.data_ptr(), lds, handle)
-        return Ckpt8(q if ldq == cols else q[:, :cols], scale if lds == blocks else scale[:, :blocks])
+        return Ckpt8(q, scale)
 
     return _on(stream, x.device, body)
 
