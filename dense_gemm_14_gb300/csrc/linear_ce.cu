@@ -357,12 +357,19 @@ struct CeLayout {
   int64_t ldz = 0;     // pitch of the logits or of dZ
   int64_t ldx = 0;     // pitch of the D-wide buffers
   int parts = 1;       // bf16 parts of an operand
+  bool few = false;    // the logits come from the kernel for few rows
   bool gather = false; // rows in use are numbered and gathered first
   bool copy_w = false; // pieces of W are copied (unaligned) or split
   int64_t rows = 0;    // T rounded up to whole tiles
   size_t state = 0, counts = 0, index = 0, position = 0, target = 0, lse = 0, coef = 0, h = 0,
          w = 0, part = 0, z = 0, slots = 0, tail = 0, total = 0;
 };
+
+// Parts of a row's statistics that c columns leave: two a tile.
+int64_t stat_parts(bool few, int64_t c, int sms) {
+  const int64_t w = few ? few_width(c, sms) : 256;
+  return 2 * ((c + w - 1) / w);
+}
 
 void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
                const void* W, int64_t ldw, bool backward, int sms, CeLayout* l) {
@@ -388,6 +395,7 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
     if (l->copy_w) per_row = std::max(per_row, l->ldx * 2 * l->parts);
     l->C = per_row ? piece_rows(V, per_row) : V;
     l->ldz = round_up(l->C, 64);
+    l->few = l->parts == 1 && T <= FewShape::MAX_ROWS;
     if (l->gather) {
       l->counts = take(256);
       l->index = take(t4);
@@ -407,7 +415,8 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
       l->tail = take(static_cast<size_t>(slots_needed(tiles_of(l->C) * tiles_of(D), clusters,
                                                       false)) * kSlotBytes);
     } else {
-      l->part = take(static_cast<size_t>(2 * tiles_of(V)) * l->rows * sizeof(float2));
+      l->part = take(static_cast<size_t>((V + l->C - 1) / l->C) * stat_parts(l->few, l->C, sms) *
+                     l->rows * sizeof(float2));
       l->state = take(t4);
     }
     l->total = at;
@@ -560,6 +569,21 @@ struct CeCall {
                     "linear_ce product launch");
   }
 
+  int64_t parts_of(int64_t c) const { return stat_parts(l.few, c, ctx.sm_count); }
+
+  // A product of few rows (its arguments in *a) with c rows of W.
+  int run_few(int mode, const TrainOperand& w, const TrainArgs& a) {
+    const TrainOperand h = h_operand();
+    const int width = few_width(a.N, ctx.sm_count);
+    CUtensorMap map_h, map_w;
+    int st = map_16bit(&map_h, bf16(), h.base, h.rows, h.cols, h.ld, few_rows(T));
+    if (st == GEMM14_OK) st = map_16bit(&map_w, bf16(), w.base, w.rows, w.cols, w.ld, width);
+    if (st != GEMM14_OK) return st;
+    ctx.fault = kFaultNone;
+    return launched(launch_train_few(mode, map_h, map_w, a, bf16(), width, ctx.sm_count, stream),
+                    "linear_ce few rows launch");
+  }
+
   // Whether sums over K are carried in fp32 registers: what is written in fp32
   // keeps fp32's accuracy; what is rounded to 16 bits loses nothing by TMEM's.
   bool long_sum(int64_t K) const { return K > TrainShape::CHUNK * TrainShape::BK; }
@@ -569,6 +593,7 @@ struct CeCall {
     if (st != GEMM14_OK) return st;
     if (l.gather && (st = gather(nullptr, nullptr, nullptr, 0)) != GEMM14_OK) return st;
     const Rows r = rows();
+    int64_t parts = 0;
     for (int64_t v0 = 0; v0 < V; v0 += l.C) {
       const int64_t c = std::min(l.C, V - v0);
       TrainOperand w;
@@ -577,15 +602,17 @@ struct CeCall {
       a.v0 = static_cast<int>(v0);
       a.target = l.gather ? r.target : nullptr;
       a.target64 = targets;
-      a.part = at<float2>(l.part) + 2 * (v0 / 256) * l.rows;
+      a.part = at<float2>(l.part) + v0 / l.C * parts_of(l.C) * l.rows;
       a.part_ld = l.rows;
       a.target_logit = at<float>(l.state);
-      if ((st = run(kTrainStats, long_sum(D), h_operand(), false, w, false, &a)) != GEMM14_OK)
-        return st;
+      st = l.few ? run_few(kTrainStats, w, a)
+                 : run(kTrainStats, long_sum(D), h_operand(), false, w, false, &a);
+      if (st != GEMM14_OK) return st;
+      parts = v0 / l.C * parts_of(l.C) + parts_of(c);
     }
     return launched(
         launch_kernel(ce_combine_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(1024),
-                      0, stream, at<float2>(l.part), l.rows, static_cast<int>(2 * tiles_of(V)),
+                      0, stream, at<float2>(l.part), l.rows, static_cast<int>(parts),
                       at<float>(l.state), l.gather ? r.position : nullptr, targets, ignore, T, V,
                       loss, lse),
         "linear_ce combine launch");
@@ -614,9 +641,9 @@ struct CeCall {
       a.out_part = g_part;
       a.elem = exact ? kElemBf16x3 : elem;
       a.out_vec = 1;
-      if ((st = run(kTrainGrad, exact && long_sum(D), h_operand(), false, w, false, &a)) !=
-          GEMM14_OK)
-        return st;
+      st = l.few ? run_few(kTrainGrad, w, a)
+                 : run(kTrainGrad, exact && long_sum(D), h_operand(), false, w, false, &a);
+      if (st != GEMM14_OK) return st;
       const TrainOperand dz{ws + l.z, l.rows, c, l.ldz, l.parts, g_part};
       if (dH) {
         a = product(T, D, c, false);

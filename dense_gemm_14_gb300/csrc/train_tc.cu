@@ -363,7 +363,7 @@ struct Epilogue {
     if (kMode == kTrainStats && row < M) {
       args.part[(static_cast<int64_t>(tn) * 2 + half) * args.part_ld + row] =
           make_float2(d.m, d.l);
-      if (d.y >= 0 && d.y < 128) args.target_logit[row] = d.zy;
+      if (d.y >= 0 && d.y < 128 && col_half + d.y < N) args.target_logit[row] = d.zy;
     }
   }
 };
@@ -610,6 +610,203 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
   }
 }
 
+// The logits of few rows (up to 128): the call is one read of B, and the
+// kernel's business is to keep it flowing. One SM a tile (M = 128, N = width): a
+// k-block of 256 rows of B is 512 cycles of MMAs for 32 KB, 18 TB/s over 152 SMs,
+// where the pair's M = 256 spends them on 16 KB an SM. The rows of A in use alone
+// are loaded; the MMA reads 128 rows' bytes, the others being whatever the
+// ring holds there, and the rows of D they make are not looked at. Tiles are as
+// wide as spreads the columns evenly (32768 columns: 147 tiles of 224 on 152
+// SMs, where 128 of 256 on 76 pairs are 1.7 waves). With B on the MMA's M side
+// (N = 16 for one row) a k-block took 0.33 us whatever its height, N that small
+// leaving the tensor cores waiting: 268 MB of weights took 62 us.
+struct FewSmem {
+  uint64_t full[FewShape::MAX_STAGES];
+  uint64_t empty[FewShape::MAX_STAGES];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(FewSmem) <= 512, "barrier block of the few-rows kernel");
+
+struct FewTiles {
+  int width, rows, stages, quarters;  // quarters: of the 128 rows that are looked at
+};
+
+template <int kMode>
+__global__ void __launch_bounds__(FewShape::THREADS, 1)
+    train_few_kernel(const __grid_constant__ CUtensorMap map_a,
+                     const __grid_constant__ CUtensorMap map_b, const TrainArgs args,
+                     const FewTiles few) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = align1024(smem_raw);
+  uint8_t* out_stage = ring + FewShape::RING_BYTES;
+  FewSmem& sm = *reinterpret_cast<FewSmem*>(out_stage + S::EPI_WARPS * S::OUT_BUF_BYTES);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t b_bytes = static_cast<uint32_t>(few.width) * 128u;
+  const uint32_t stage_bytes = b_bytes + static_cast<uint32_t>(few.rows) * 128u;
+  const uint32_t stages = static_cast<uint32_t>(few.stages);
+  const int tiles = (args.N + few.width - 1) / few.width;
+  const int kblocks = (args.K + S::BK - 1) / S::BK;
+  const WaitCtx wc{args.err, &sm.abort_flag, args.wait_limit_ns, 0};
+  uint32_t prod_it = 0;
+  bool mma_issued = false;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < stages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 2 * few.quarters);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_b);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, S::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t tmem_base = sm.tmem_base;
+  const int M = args.n ? min(*args.n, args.M) : args.M;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t s = 0, ph = 0;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < kblocks; ++kb, ++prod_it) {
+          if (!mbar_wait(&sm.empty[s], ph ^ 1, wc)) { ok = false; break; }
+          // Failure-detection tests: the first stage is never loaded.
+          if (!(args.fault == kFaultSkipFirstStage && prod_it == 0)) {
+            uint8_t* st = ring + s * stage_bytes;
+            mbar_arrive_expect_tx(&sm.full[s], stage_bytes);
+            tma_load_2d(st, &map_b, kb * S::BK, t * few.width, &sm.full[s]);
+            tma_load_2d(st + b_bytes, &map_a, kb * S::BK, 0, &sm.full[s]);
+          }
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t s = 0, ph = 0, unit = 0;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int k0 = 0; k0 < kblocks; k0 += S::CHUNK, ++unit) {
+          const int k1 = min(k0 + S::CHUNK, kblocks);
+          const int b = unit & 1;
+          if (!mbar_wait(&sm.acc_empty[b], ((unit >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+          tc_fence_after_sync();
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(&sm.full[s], ph, wc)) { ok = false; break; }
+            tc_fence_after_sync();
+            const uint32_t b_addr = smem_u32(ring + s * stage_bytes);
+#pragma unroll
+            for (int kk = 0; kk < S::BK / 16; ++kk)
+              tc_mma_f16(tmem_base + static_cast<uint32_t>(b * S::BN),
+                         smem_desc_sw128(b_addr + b_bytes + kk * 32, 16, 1024),
+                         smem_desc_sw128(b_addr + kk * 32, 16, 1024), args.idesc,
+                         kb > k0 || kk != 0);
+            mma_issued = true;
+            tc_commit(&sm.empty[s]);
+            if (++s == stages) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+          if (!ok) break;
+          tc_commit(&sm.acc_full[b]);
+        }
+      }
+    }
+  } else if ((warp & 3) < few.quarters) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const uint32_t buf = smem_u32(out_stage + (warp - 2) * S::OUT_BUF_BYTES);
+    uint32_t unit = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const int limit = min(args.N, (t + 1) * few.width);
+      Epilogue<kMode> e{args, M, limit, lane, q * 32, q * 32 + lane, half, 0, -1,
+                        t * few.width + half * 128, buf, {}, 1.0f};
+      e.begin();
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      for (int k0 = 0; k0 < kblocks; k0 += S::CHUNK, ++unit) {
+        const int b = unit & 1;
+        int got = 1;
+        if (lane == 0) got = mbar_wait(&sm.acc_full[b], (unit >> 1) & 1, wc) ? 1 : 0;
+        got = __shfl_sync(0xffffffffu, got, 0);
+        if (!got) { ok = false; break; }
+        tc_fence_after_sync();
+        const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                              static_cast<uint32_t>(b * S::BN + half * 128);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(from + c * 32, r);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[32 * c + j] += __uint_as_float(r[j]);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = acc[32 * c + j];
+        e.chunk(c, x);
+      }
+      e.end(t);
+    }
+  }
+
+  // Teardown: on abort, what was issued finishes (bounded) before TMEM is freed.
+  __syncthreads();
+  if (sm.abort_flag) {
+    if (warp == 1 && lane == 0 && mma_issued) {
+      tc_commit(&sm.drain);
+      mbar_wait_timed(&sm.drain, 0, 100000000ull);
+    }
+    if (warp == 0 && lane == 0) {
+      const uint32_t first = prod_it > stages ? prod_it - stages : 0;
+      for (uint32_t j = first; j < prod_it; ++j)
+        if (!(args.fault == kFaultSkipFirstStage && j == 0))
+          mbar_wait_timed(&sm.full[j % stages], (j / stages) & 1, 100000000ull);
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, S::TMEM_COLS);
+  }
+}
+
 // 32 rows x 32 columns of a tile a block: slots are read along rows (512 bytes
 // a warp), the output is written along columns, through shared memory.
 __global__ void __launch_bounds__(256)
@@ -761,6 +958,43 @@ int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOpera
   args->b_mn = b_mn;
   args->idesc = idesc_f16_f32acc(bf16, S::BM, S::BN, a_mn, b_mn);
   return 0;
+}
+
+int few_width(int64_t N, int sms) {
+  int best = 256;
+  int64_t best_cols = INT64_MAX;  // of the SM with the most
+  for (int w = 256; w >= 128; w -= 16) {
+    const int64_t cols = ((N + w - 1) / w + sms - 1) / sms * w;
+    if (cols < best_cols) {
+      best_cols = cols;
+      best = w;
+    }
+  }
+  return best;
+}
+
+int few_rows(int64_t M) { return M <= 16 ? 16 : static_cast<int>((M + 31) / 32 * 32); }
+
+cudaError_t launch_train_few(int mode, const CUtensorMap& map_a, const CUtensorMap& map_b,
+                             TrainArgs args, bool bf16, int width, int sm_count,
+                             cudaStream_t stream) {
+  FewTiles few{};
+  few.width = width;
+  few.rows = few_rows(args.M);
+  const int stage = (few.width + few.rows) * 128;
+  // the last stage's MMAs read 128 rows' bytes of A, however many were loaded
+  few.stages = (FewShape::RING_BYTES - (FewShape::A_BYTES - few.rows * 128)) / stage;
+  if (few.stages > FewShape::MAX_STAGES) few.stages = FewShape::MAX_STAGES;
+  // dZ is read in k-blocks of 64 rows by the product over them
+  few.quarters = mode == kTrainGrad ? (args.M + 63) / 64 * 2 : (args.M + 31) / 32;
+  args.idesc = idesc_f16_f32acc(bf16, 128, width, false, false);
+  const auto kernel = mode == kTrainGrad ? train_few_kernel<kTrainGrad> : train_few_kernel<kTrainStats>;
+  static DeviceOnce once[2];
+  const cudaError_t e = set_smem_once(once[mode == kTrainGrad], kernel, FewShape::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int tiles = (args.N + width - 1) / width;
+  return launch_kernel(kernel, dim3(tiles < sm_count ? tiles : sm_count), dim3(FewShape::THREADS),
+                       FewShape::SMEM_BYTES, stream, map_a, map_b, args, few);
 }
 
 bool may_split(const TrainArgs& args, int clusters) {

@@ -170,6 +170,27 @@ bool may_split(const TrainArgs& args, int clusters);
 cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
                           int64_t ld, int64_t part_stride, int sm_count, cudaStream_t stream);
 
+// ---- few rows (train_tc.cu, train_few_kernel): kTrainStats or kTrainGrad with
+// M <= 128 on one SM a tile of `width` columns; sums are always promoted.
+struct FewShape {
+  static constexpr int MAX_ROWS = 128;
+  static constexpr int THREADS = TrainShape::THREADS;
+  static constexpr int A_BYTES = 128 * 128;  // a k-block of 128 rows, as the MMA reads it
+  static constexpr int MAX_STAGES = 12;
+  static constexpr int RING_BYTES = 192 * 1024;
+  static constexpr int SMEM_BYTES =
+      RING_BYTES + TrainShape::EPI_WARPS * TrainShape::OUT_BUF_BYTES + 512 + 1024;
+};
+// Columns a tile, a multiple of 16 up to 256: the width at which the SM with
+// the most tiles has the fewest columns.
+int few_width(int64_t N, int sms);
+// A's k-blocks are loaded with `rows` rows (16, or a multiple of 32 that holds M).
+int few_rows(int64_t M);
+// map_a: boxes of 64 k x few_rows(M) rows; map_b: 64 k x width rows, both K-major.
+cudaError_t launch_train_few(int mode, const CUtensorMap& map_a, const CUtensorMap& map_b,
+                             TrainArgs args, bool bf16, int width, int sm_count,
+                             cudaStream_t stream);
+
 // promote: sums leave the accumulators for fp32 registers every CHUNK k-blocks.
 cudaError_t launch_train_tc(int mode, bool promote, const TrainMaps& maps, const TrainArgs& args,
                             int clusters, cudaStream_t stream);
