@@ -562,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(b ? acc_empty1 : acc_empty0);
+        if (lane == 0) mbar_arrive_peer(b ? acc_empty1 : acc_empty0);
       }
       if (!ok) break;
       if (kPromote) {
