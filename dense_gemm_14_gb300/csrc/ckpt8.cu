@@ -58,15 +58,29 @@ __device__ __forceinline__ int quantise(float x, float factor) {
   const int q = __float2int_rn(x * factor);
   return max(-127, min(127, q));
 }
-// The same in the low byte of the result: 1.5 2^23 added to a value of
-// [-127, 127] rounds it to the nearest whole number, ties to even, in the low
-// bits of the sum (its clamp first: 127 is whole, so the order does not matter).
-__device__ __forceinline__ uint32_t quantise_byte(float x, float factor) {
-  return __float_as_uint(fminf(fmaxf(x * factor, -127.0f), 127.0f) + 12582912.0f);
+// Two values at once, each in the low byte of its result: one packed multiply
+// and add of 1.5 2^23 rounds x factor to the nearest whole number, ties to even,
+// in the low bits of the sum (the product is exact, so there is one rounding).
+__device__ __forceinline__ void quantise2(uint32_t a, uint32_t b, float factor, uint32_t& qa,
+                                          uint32_t& qb) {
+  asm("{\n\t.reg .b64 x, f, m;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\tmov.b64 m, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, f, m;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=r"(qa), "=r"(qb)
+      : "r"(a), "r"(b), "f"(factor), "f"(12582912.0f));
+}
+// Two whole numbers u = q + 128, each as the fp32 2^23 + u, to q times the
+// block's step (less 2^23 + 128 first: the step times that may leave fp32's range).
+__device__ __forceinline__ void scale2(uint32_t a, uint32_t b, float step, float& xa, float& xb) {
+  asm("{\n\t.reg .b64 x, s, o;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 o, {%5, %5};\n\t"
+      "add.rn.f32x2 x, x, o;\n\tmul.rn.f32x2 x, x, s;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(xa), "=f"(xb)
+      : "r"(a), "r"(b), "f"(step), "f"(-8388736.0f));
 }
 // Four low bytes as one word.
-__device__ __forceinline__ uint32_t pack4(const uint32_t (&q)[4]) {
-  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 // The fp32 bits, sign cleared, of the largest magnitude among a piece's values:
 // magnitudes of a 16-bit type are ordered as whole numbers, two at a time.
@@ -109,11 +123,15 @@ struct Place {
 // piece of 16 bytes of X (8 or 4 values; 4 or 8 lanes a block, whose largest
 // magnitude they find with two or three shuffles) and 8 or 4 bytes of Q;
 // otherwise a lane is one column, a warp one block, with coalesced accesses of
-// single elements whatever the addresses. Either way a thread has kUnroll
-// loads in flight before it works on the first: the passes are bound by memory.
-constexpr int kUnroll = 4;
+// single elements whatever the addresses. The passes should be bound by
+// memory, and what held the wide form back was its instructions (21 a value,
+// 72 % of the issue slots): so a thread keeps to its place in the rows and
+// steps by whole rows (no division, no multiply in the loop), two values share
+// an instruction where they can, and q is only clamped where the block's
+// largest value rounds to 128. kAhead loads are in flight before the first is
+// used.
+constexpr int kUnroll = 4, kAhead = 6;
 
-// Pieces of a row, whole blocks (the last ones may hold no column).
 template <typename T>
 __host__ __device__ constexpr int piece_values() { return 16 / static_cast<int>(sizeof(T)); }
 
@@ -123,128 +141,200 @@ union Piece {
   T x[16 / sizeof(T)];
 };
 
+// Threads along a row, a power of two from 32 up: those that its pieces fill,
+// or the block's 256; the block's other threads take other rows.
+int threads_along(int64_t pieces) {
+  int x = 32;
+  while (x < kThreads && x < pieces) x *= 2;
+  return x;
+}
+
+// A piece's values as fp32 bits, and back.
+__device__ __forceinline__ void unpack(const Piece<float>& p, uint32_t (&x)[4]) {
+  x[0] = p.raw.x;
+  x[1] = p.raw.y;
+  x[2] = p.raw.z;
+  x[3] = p.raw.w;
+}
+__device__ __forceinline__ void unpack(const Piece<__nv_bfloat16>& p, uint32_t (&x)[8]) {
+  const uint32_t w[4] = {p.raw.x, p.raw.y, p.raw.z, p.raw.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = w[j] << 16;
+    x[2 * j + 1] = w[j] & 0xffff0000u;
+  }
+}
+__device__ __forceinline__ void unpack(const Piece<__half>& p, uint32_t (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = __float_as_uint(__half2float(p.x[j]));
+}
+__device__ __forceinline__ void pack(const float (&x)[4], Piece<float>& p) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p.x[j] = x[j];
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Piece<__nv_bfloat16>& p) {
+  uint32_t* w = &p.raw.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Piece<__half>& p) {
+  uint32_t* w = &p.raw.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 v = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     ckpt8_save_vec_kernel(const T* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
-                          int64_t rows, int64_t cols) {
+                          int64_t rows, uint32_t cols, int along) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int kPer = piece_values<T>(), kLanes = kBlock / kPer;
-  const int64_t per_row = (cols + kBlock - 1) / kBlock * kLanes;
-  const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
-  const Place step(threads, per_row);
-  Place at(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, per_row);
-  // whole warps go round together (the shuffles need every lane of a block)
-  const int64_t turns = (rows * per_row + threads * kUnroll - 1) / (threads * kUnroll);
-  for (int64_t turn = 0; turn < turns; ++turn) {
-    Piece<T> p[kUnroll];
-    Place place[kUnroll] = {at, at, at, at};
+  const int tx = threadIdx.x & (along - 1), ty = threadIdx.x / along;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (kThreads / along);
+  // pieces of a row, whole blocks: every lane of a warp goes round as often (the
+  // shuffles need every lane of a block)
+  const uint32_t pieces = (cols + kBlock - 1) / kBlock * kLanes;
+  const uint32_t turns = (pieces + along * kAhead - 1) / (along * kAhead);
+  int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / along) + ty;
+  const int64_t rounds = (rows + row_step - 1) / row_step;
+  const T* xr = X + r * ldx;
+  int8_t* qr = Q + r * ldq;
+  uint8_t* sr = S + r * lds;
+  for (int64_t round = 0; round < rounds; ++round) {
+    const bool in_rows = r < rows;
+    for (uint32_t turn = 0; turn < turns; ++turn) {
+      const uint32_t p0 = tx + turn * along * kAhead;
+      Piece<T> p[kAhead];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      place[u] = at;
-      const int64_t c = at.item * kPer;
-      p[u].raw = make_uint4(0, 0, 0, 0);
-      if (at.row < rows) {
-        const T* x = X + at.row * ldx + c;
+      for (int u = 0; u < kAhead; ++u) {
+        const uint32_t c = (p0 + u * along) * kPer;
+        p[u].raw = make_uint4(0, 0, 0, 0);
+        if (in_rows && c + kPer <= cols) {
+          p[u].raw = __ldcs(reinterpret_cast<const uint4*>(xr + c));
+        } else if (in_rows && c < cols) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            if (c + j < cols) p[u].x[j] = xr[c + j];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const uint32_t c = (p0 + u * along) * kPer;
+        uint32_t top = top_of(p[u].raw, T());
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (!in_rows || c >= cols) continue;
+        const uint32_t s = scale_byte(top);
+        const float factor = scale_factor(s);
+        uint32_t x[kPer], w[kPer / 4];
+        unpack(p[u], x);
+        if (__uint_as_float(top) * factor >= 127.5f || s == 255u) {
+          // the largest rounds to 128, or the block is kept as zeros (an infinity
+          // times 0 is no number)
+          const float most = s == 255u ? 0.0f : 127.0f / factor;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            x[j] = s == 255u ? 0u
+                             : __float_as_uint(fminf(fmaxf(__uint_as_float(x[j]), -most), most));
+        }
+#pragma unroll
+        for (int k = 0; k < kPer / 4; ++k) {
+          uint32_t q[4];
+          quantise2(x[4 * k], x[4 * k + 1], factor, q[0], q[1]);
+          quantise2(x[4 * k + 2], x[4 * k + 3], factor, q[2], q[3]);
+          w[k] = pack4(q[0], q[1], q[2], q[3]);
+        }
+        int8_t* to = qr + c;
         if (c + kPer <= cols) {
-          p[u].raw = __ldcs(reinterpret_cast<const uint4*>(x));
+          if constexpr (kPer == 8)
+            *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+          else
+            *reinterpret_cast<uint32_t*>(to) = w[0];
         } else {
 #pragma unroll
           for (int j = 0; j < kPer; ++j)
-            if (c + j < cols) p[u].x[j] = x[j];
+            if (c + j < cols) to[j] = static_cast<int8_t>(w[j / 4] >> (8 * (j % 4)));
         }
+        if ((tx & (kLanes - 1)) == 0) sr[c / kBlock] = static_cast<uint8_t>(s);
       }
-      at.move(step, per_row);
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      uint32_t top = top_of(p[u].raw, T());
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const uint32_t s = scale_byte(top);
-      const float factor = scale_factor(s);
-      uint32_t w[kPer / 4];
-#pragma unroll
-      for (int k = 0; k < kPer / 4; ++k) {
-        uint32_t q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = quantise_byte(to_f32(p[u].x[4 * k + j]), factor);
-        w[k] = s == 255u ? 0u : pack4(q);  // (an infinity times 0 is no number)
-      }
-      const int64_t r = place[u].row, c = place[u].item * kPer;
-      if (r >= rows || c >= cols) continue;
-      int8_t* to = Q + r * ldq + c;
-      if (c + kPer <= cols) {
-        if constexpr (kPer == 8)
-          *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-        else
-          *reinterpret_cast<uint32_t*>(to) = w[0];
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (c + j < cols) to[j] = static_cast<int8_t>(w[j / 4] >> (8 * (j % 4)));
-      }
-      if (place[u].item % kLanes == 0) S[r * lds + c / kBlock] = static_cast<uint8_t>(s);
-    }
+    r += row_step;
+    xr += row_step * ldx;
+    qr += row_step * ldq;
+    sr += row_step * lds;
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     ckpt8_restore_vec_kernel(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, T* X,
-                             int64_t ldx, int64_t rows, int64_t cols) {
+                             int64_t ldx, int64_t rows, uint32_t cols, int along) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int kPer = piece_values<T>();
-  const int64_t per_row = (cols + kPer - 1) / kPer;
-  const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
-  const Place step(threads, per_row);
-  Place at(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, per_row);
-  while (at.row < rows) {
-    uint32_t w[kUnroll][kPer / 4], s[kUnroll];
-    Place place[kUnroll] = {at, at, at, at};
+  const int tx = threadIdx.x & (along - 1), ty = threadIdx.x / along;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (kThreads / along);
+  int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / along) + ty;
+  const int8_t* qr = Q + r * ldq;
+  const uint8_t* sr = S + r * lds;
+  T* xr = X + r * ldx;
+  for (; r < rows; r += row_step, qr += row_step * ldq, sr += row_step * lds, xr += row_step * ldx) {
+    for (uint32_t c0 = tx * kPer; c0 < cols; c0 += along * kAhead * kPer) {
+      uint32_t w[kAhead][kPer / 4], s[kAhead];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      place[u] = at;
-      const int64_t c = at.item * kPer;
-      if (at.row < rows) {
-        const int8_t* q = Q + at.row * ldq + c;
-        s[u] = S[at.row * lds + c / kBlock];
+      for (int u = 0; u < kAhead; ++u) {
+        const uint32_t c = c0 + u * along * kPer;
+        s[u] = 7u;
+#pragma unroll
+        for (int j = 0; j < kPer / 4; ++j) w[u][j] = 0u;
+        if (c >= cols) continue;
+        s[u] = sr[c / kBlock];
         if (c + kPer <= cols) {
           if constexpr (kPer == 8) {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(q));
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(qr + c));
             w[u][0] = v.x;
             w[u][1] = v.y;
           } else {
-            w[u][0] = __ldcs(reinterpret_cast<const uint32_t*>(q));
+            w[u][0] = __ldcs(reinterpret_cast<const uint32_t*>(qr + c));
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const uint32_t v = c + j < cols ? static_cast<uint8_t>(q[j]) : 0u;
-            w[u][j / 4] = j % 4 == 0 ? v : w[u][j / 4] | v << (8 * (j % 4));
-          }
+          for (int j = 0; j < kPer; ++j)
+            if (c + j < cols)
+              w[u][j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(qr[c + j])) << (8 * (j % 4));
         }
       }
-      at.move(step, per_row);
-    }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = place[u].row, c = place[u].item * kPer;
-      if (r >= rows) break;
-      const float k = step_of(s[u]);
-      Piece<T> p;
+      for (int u = 0; u < kAhead; ++u) {
+        const uint32_t c = c0 + u * along * kPer;
+        if (c >= cols) break;
+        const float step = step_of(s[u]);
+        float x[kPer];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        p.x[j] = from_f32<T>(static_cast<float>(static_cast<int8_t>(w[u][j / 4] >> (8 * (j % 4)))) *
-                             k);
-      T* to = X + r * ldx + c;
-      if (c + kPer <= cols) {
-        *reinterpret_cast<uint4*>(to) = p.raw;
-      } else {
+        for (int k = 0; k < kPer / 4; ++k) {
+          const uint32_t v = w[u][k] ^ 0x80808080u;  // q + 128 in each byte
+          scale2(__byte_perm(v, 0x4b000000u, 0x7440), __byte_perm(v, 0x4b000000u, 0x7441), step,
+                 x[4 * k], x[4 * k + 1]);
+          scale2(__byte_perm(v, 0x4b000000u, 0x7442), __byte_perm(v, 0x4b000000u, 0x7443), step,
+                 x[4 * k + 2], x[4 * k + 3]);
+        }
+        Piece<T> p;
+        pack(x, p);
+        T* to = xr + c;
+        if (c + kPer <= cols) {
+          *reinterpret_cast<uint4*>(to) = p.raw;
+        } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (c + j < cols) to[j] = p.x[j];
+          for (int j = 0; j < kPer; ++j)
+            if (c + j < cols) to[j] = p.x[j];
+        }
       }
     }
   }
@@ -334,21 +424,27 @@ template <typename T>
 cudaError_t save_as(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
                     int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
   const int64_t blocks = (cols + kBlock - 1) / kBlock;
-  const bool vec = wide<T>(X, ldx, Q, ldq);
-  const int grid = grid_for(rows * blocks * (vec ? kBlock / piece_values<T>() : 32), sms);
-  return launch_kernel(vec ? ckpt8_save_vec_kernel<T> : ckpt8_save_kernel<T>, dim3(grid),
-                       dim3(kThreads), 0, stream, static_cast<const T*>(X), ldx, Q, ldq, S, lds,
-                       rows, cols);
+  const T* x = static_cast<const T*>(X);
+  if (!wide<T>(X, ldx, Q, ldq))
+    return launch_kernel(ckpt8_save_kernel<T>, dim3(grid_for(rows * blocks * 32, sms)),
+                         dim3(kThreads), 0, stream, x, ldx, Q, ldq, S, lds, rows, cols);
+  const int along = threads_along(blocks * kBlock / piece_values<T>());
+  return launch_kernel(ckpt8_save_vec_kernel<T>, dim3(grid_for(rows * along, sms)),
+                       dim3(kThreads), 0, stream, x, ldx, Q, ldq, S, lds, rows,
+                       static_cast<uint32_t>(cols), along);
 }
 template <typename T>
 cudaError_t restore_as(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, void* X,
                        int64_t ldx, int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
-  const bool vec = wide<T>(X, ldx, Q, ldq);
-  const int64_t items = vec ? (cols + piece_values<T>() - 1) / piece_values<T>()
-                            : (cols + kBlock - 1) / kBlock * 32;
-  return launch_kernel(vec ? ckpt8_restore_vec_kernel<T> : ckpt8_restore_kernel<T>,
-                       dim3(grid_for(rows * items, sms)), dim3(kThreads), 0, stream, Q, ldq, S,
-                       lds, static_cast<T*>(X), ldx, rows, cols);
+  T* x = static_cast<T*>(X);
+  if (!wide<T>(X, ldx, Q, ldq))
+    return launch_kernel(ckpt8_restore_kernel<T>,
+                         dim3(grid_for(rows * ((cols + kBlock - 1) / kBlock) * 32, sms)),
+                         dim3(kThreads), 0, stream, Q, ldq, S, lds, x, ldx, rows, cols);
+  const int along = threads_along((cols + piece_values<T>() - 1) / piece_values<T>());
+  return launch_kernel(ckpt8_restore_vec_kernel<T>, dim3(grid_for(rows * along, sms)),
+                       dim3(kThreads), 0, stream, Q, ldq, S, lds, x, ldx, rows,
+                       static_cast<uint32_t>(cols), along);
 }
 
 cudaError_t launch_restore(int dtype, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,

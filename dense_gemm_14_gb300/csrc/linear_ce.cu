@@ -213,11 +213,18 @@ __global__ void __launch_bounds__(1024)
   const int64_t y = t < T ? targets[t] : ignore;
   const int64_t i = t >= T || y == ignore ? -1 : position ? position[t] : t;
   ExpSum s{-INFINITY, 0.0f};
-  if (i >= 0)
-    for (int p = warp; p < parts; p += 32) {
-      const float2 v = part[p * part_ld + i];
-      s = merge(s, {v.x, v.y});
+  if (i >= 0) {
+    constexpr int kAhead = 8;  // loads in flight
+    for (int p0 = warp; p0 < parts; p0 += 32 * kAhead) {
+      float2 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        v[u] = p0 + 32 * u < parts ? part[(p0 + 32 * u) * part_ld + i]
+                                   : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) s = merge(s, {v[u].x, v[u].y});
     }
+  }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || t >= T) return;
@@ -341,7 +348,7 @@ int validate_ce(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64
 }
 
 // Bytes a piece of logits or dZ, and a piece of W that has to be copied, may take.
-constexpr int64_t kPieceBytes = int64_t(256) << 20;
+constexpr int64_t kPieceBytes = int64_t(384) << 20;
 
 // Rows of W per piece, a multiple of 256 unless one piece takes all: pieces of
 // about the same size, `per_row` bytes a row of W within the limit.

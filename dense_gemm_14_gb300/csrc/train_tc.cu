@@ -237,7 +237,18 @@ struct Epilogue {
       d.l = 0.0f;
       d.zy = 0.0f;
     }
-    if (kMode == kTrainOut) factor = args.alpha * (args.scale ? *args.scale : 1.0f);
+    if (kMode == kTrainOut) {
+      factor = args.alpha * (args.scale ? *args.scale : 1.0f);
+      // the old values are asked for before the sums are ready
+      if (args.beta != 0.0f && slot < 0 && row < M) {
+        const float* from = static_cast<const float*>(args.out) +
+                            static_cast<int64_t>(row) * args.ld_out + col_half;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (col_half + 32 * c < N)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(from + 32 * c));
+      }
+    }
   }
 
   // Columns 32 c .. of the half, in registers.
@@ -807,54 +818,59 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
   }
 }
 
-// 32 rows x 32 columns of a tile a block: slots are read along rows (512 bytes
-// a warp), the output is written along columns, through shared memory.
+// 32 rows x 32 columns of a tile at a time: slots are read along rows (512 bytes
+// a warp), the output is written along columns, through shared memory. The
+// blocks go round the tiles that have slots (few, or none, after a launch whose
+// last wave was full: a block for each that might be took 13 us to find so).
 __global__ void __launch_bounds__(256)
     slots_out_kernel(const TrainArgs args, const SlotsOut s, int clusters) {
   __shared__ float tile[32][36];
   grid_dependency_wait();
   grid_launch_dependents();
   const Work work(args, clusters);
-  const int t = (s.all ? 0 : work.plan.direct) + static_cast<int>(blockIdx.x >> 3);
-  if (t >= work.plan.tiles) return;
-  int tm, tn;
-  work.tile_at(t, tm, tn);
-  const int rank = (blockIdx.x >> 2) & 1, q0 = (blockIdx.x & 3) * 32;
-  const int half = blockIdx.y >> 2, c = blockIdx.y & 3;
-  const int row0 = tm * S::BM + rank * 128 + q0, col0 = tn * S::BN + half * 128 + c * 32;
-  if (row0 >= work.M || col0 >= work.N) return;
+  const int first = s.all ? 0 : work.plan.direct;
+  const int64_t pieces = static_cast<int64_t>(work.plan.tiles - first) * 64;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float k = s.alpha * (s.scale ? *s.scale : 1.0f);
-  const int ranges = t < work.plan.direct ? 1 : work.plan.splits;
-  const float4* from = args.slots + slot_index(slot_of(work.plan, s.all, t, 0), rank, half, c, warp,
-                                               q0 + lane);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = 0; p < ranges; ++p) {
-    const float4 o = __ldcg(from + p * (kSlotBytes / 16));
-    v.x += o.x;
-    v.y += o.y;
-    v.z += o.z;
-    v.w += o.w;
-  }
-  *reinterpret_cast<float4*>(&tile[lane][4 * warp]) = v;
-  __syncthreads();
   const int r = threadIdx.x >> 3, c4 = (threadIdx.x & 7) * 4;
-  if (row0 + r >= work.M) return;
-  const int64_t row = s.rows ? s.rows[row0 + r] : row0 + r;
+  const float k = pieces ? s.alpha * (s.scale ? *s.scale : 1.0f) : 0.0f;
+  for (int64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+    const int t = first + static_cast<int>(i >> 6), part = static_cast<int>(i & 63);
+    int tm, tn;
+    work.tile_at(t, tm, tn);
+    const int rank = part >> 5, q0 = ((part >> 3) & 3) * 32, half = (part >> 2) & 1, c = part & 3;
+    const int row0 = tm * S::BM + rank * 128 + q0, col0 = tn * S::BN + half * 128 + c * 32;
+    if (row0 >= work.M || col0 >= work.N) continue;
+    const int ranges = t < work.plan.direct ? 1 : work.plan.splits;
+    const float4* from = args.slots + slot_index(slot_of(work.plan, s.all, t, 0), rank, half, c,
+                                                 warp, q0 + lane);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int p = 0; p < ranges; ++p) {
+      const float4 o = __ldcg(from + p * (kSlotBytes / 16));
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
+    __syncthreads();
+    *reinterpret_cast<float4*>(&tile[lane][4 * warp]) = v;
+    __syncthreads();
+    if (row0 + r >= work.M) continue;
+    const int64_t row = s.rows ? s.rows[row0 + r] : row0 + r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int col = col0 + c4 + j;
-    if (col >= work.N) break;
-    const int64_t at = row * s.ld + col;
-    const float x = tile[r][c4 + j] * k;
-    if (s.elem == kElemF32) {
-      float* o = static_cast<float*>(s.out) + at;
-      *o = s.beta == 0.0f ? x : fmaf(s.beta, *o, x);
-    } else if (s.elem == kElemF16) {
-      static_cast<__half*>(s.out)[at] = __float2half_rn(x);
-    } else {
-      static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16_rn(x);
+    for (int j = 0; j < 4; ++j) {
+      const int col = col0 + c4 + j;
+      if (col >= work.N) break;
+      const int64_t at = row * s.ld + col;
+      const float x = tile[r][c4 + j] * k;
+      if (s.elem == kElemF32) {
+        float* o = static_cast<float*>(s.out) + at;
+        *o = s.beta == 0.0f ? x : fmaf(s.beta, *o, x);
+      } else if (s.elem == kElemF16) {
+        static_cast<__half*>(s.out)[at] = __float2half_rn(x);
+      } else {
+        static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16_rn(x);
+      }
     }
   }
 }
@@ -1007,10 +1023,12 @@ bool may_split(const TrainArgs& args, int clusters) {
 
 cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clusters,
                              cudaStream_t stream) {
-  const int tiles = ((args.M + S::BM - 1) / S::BM) * ((args.N + S::BN - 1) / S::BN);
-  const int most = s.all || tiles < clusters ? tiles : clusters;  // a tail is under a wave
-  return launch_kernel(slots_out_kernel, dim3(8 * most, 8), dim3(256), 0, stream, args, s,
-                       clusters);
+  const int64_t tiles = static_cast<int64_t>((args.M + S::BM - 1) / S::BM) *
+                        ((args.N + S::BN - 1) / S::BN);
+  const int64_t most = 64 * (s.all || tiles < clusters ? tiles : clusters);  // a tail is under a wave
+  const int64_t cap = 16 * clusters;  // 8 blocks an SM
+  return launch_kernel(slots_out_kernel, dim3(static_cast<unsigned>(most < cap ? most : cap)),
+                       dim3(256), 0, stream, args, s, clusters);
 }
 
 cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,

@@ -83,26 +83,32 @@ struct TrainArgs {
 // tiles whole, in full waves; each of the rest, which would leave clusters idle
 // in a last partial wave, by `splits` ranges of its k-blocks whose sums go to
 // slots and are added up by launch_slots_out (1: those tiles are whole too, and
-// direct counts them). The count of ranges is the one whose partial waves are
-// shortest; a split has to save 24 k-blocks' time (about 8 us: the second launch
-// takes 4 to 6), and a range has 4 k-blocks or more. Both launches work it out
-// on the device, from the rows in use. `units`: k-blocks times terms.
+// direct counts them). For each number of partial waves, 1 to 4, the most ranges
+// that fit it are a candidate; the shortest wins (1 % of a tile's time is counted
+// for each range's sums). A split has to save 24 k-blocks' time (about 8 us: the
+// second launch takes 4 to 6), and a range has 4 k-blocks or more. Both launches
+// work it out on the device, every thread from the rows in use: in whole
+// numbers, a few instructions (trying every count took 5 us of each launch).
+// `units`: k-blocks times terms.
 struct TilePlan {
   int tiles, direct, splits;
 };
-constexpr int kTailWaves = 4;  // splits x tail tiles stay within this many waves
+constexpr int kTailWaves = 4;
 __host__ __device__ inline TilePlan plan_tiles(int tiles, int kblocks, int units, int clusters) {
   const int tail = tiles % clusters;
-  int best = 1;
-  float best_time = 1.0f;
-  for (int s = 2; s * 4 <= kblocks && tail && tail * s <= kTailWaves * clusters; ++s) {
-    const float time = static_cast<float>((tail * s + clusters - 1) / clusters) / s + 0.01f * s;
+  int best = 1, best_time = 1000;  // thousandths of a tile's time
+  for (int waves = 1; waves <= kTailWaves && tail; ++waves) {
+    int s = waves * clusters / tail;
+    if (s > kblocks / 4) s = kblocks / 4;
+    if (s > 64) s = 64;
+    if (s < 2) continue;
+    const int time = 1000 * waves / s + 10 * s;
     if (time < best_time) {
       best_time = time;
       best = s;
     }
   }
-  if ((1.0f - best_time) * units < 24.0f) best = 1;
+  if ((1000 - best_time) * static_cast<int64_t>(units) < 24000) best = 1;
   return TilePlan{tiles, best > 1 ? tiles - tail : tiles, best};
 }
 // The slot of split s of a tile. all: every tile has slots (kTrainSlots).

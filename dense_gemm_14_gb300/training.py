@@ -10,6 +10,8 @@ import torch
 from . import _lib
 from .api import _CODE, _FP32_MODES, _workspace
 
+_current_stream = torch._C._cuda_getCurrentRawStream
+
 CKPT8_BLOCK = 32  # columns of a row that share a scale
 
 
@@ -25,10 +27,11 @@ def _on(stream, device: torch.device, body):
     """body(stream handle) with `device` and, where one is given, `stream`
     current: what the call allocates then belongs to the stream its kernels run on."""
     if stream is None:
+        # the handle itself: making a Stream object of it takes as long as a launch
         if device.index == torch.cuda.current_device():
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(_current_stream(device.index))
         with torch.cuda.device(device):
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(_current_stream(device.index))
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
