@@ -130,7 +130,7 @@ struct Place {
 // an instruction where they can, and q is only clamped where the block's
 // largest value rounds to 128. kAhead loads are in flight before the first is
 // used.
-constexpr int kUnroll = 4, kAhead = 6;
+constexpr int kUnroll = 8, kAhead = 6;
 
 template <typename T>
 __host__ __device__ constexpr int piece_values() { return 16 / static_cast<int>(sizeof(T)); }
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads)
   Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), per_row);
   while (at.row < rows) {
     float x[kUnroll];
-    Place place[kUnroll] = {at, at, at, at};
+    Place place[kUnroll] = {at, at, at, at, at, at, at, at};
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       place[u] = at;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads)
   while (at.row < rows) {
     int q[kUnroll];
     uint32_t s[kUnroll];
-    Place place[kUnroll] = {at, at, at, at};
+    Place place[kUnroll] = {at, at, at, at, at, at, at, at};
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       place[u] = at;
@@ -486,6 +486,7 @@ struct WgradLayout {
   int parts = 1;           // bf16 parts of dY
   bool copy_dy = false;    // dY is copied (unaligned) or split
   int64_t ldx = 0, lddy = 0;
+  int64_t slot_count = 0;  // for split tiles
   size_t x_off = 0, dy_off = 0, slots_off = 0, total = 0;
 };
 
@@ -515,9 +516,10 @@ void wgrad_layout(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, in
   l->lddy = l->copy_dy ? (N + 7) / 8 * 8 : lddy;
   l->x_off = take(static_cast<size_t>(T) * l->ldx * 2);
   if (l->copy_dy) l->dy_off = take(static_cast<size_t>(T) * l->lddy * 2 * l->parts);
-  const int64_t tiles = ((N + 255) / 256) * ((K + 255) / 256);
-  l->slots_off = take(static_cast<size_t>(slots_needed(tiles, sms > 1 ? sms / 2 : 1, false)) *
-                      kSlotBytes);
+  const int clusters = sms > 1 ? sms / 2 : 1;
+  l->slot_count = slots_needed(((N + 255) / 256) * ((K + 127) / 128), (T + 63) / 64, clusters,
+                               false);
+  l->slots_off = take(static_cast<size_t>(l->slot_count) * kSlotBytes);
   l->total = at;
 }
 
@@ -560,6 +562,7 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   a.M = static_cast<int>(N);
   a.N = static_cast<int>(K);
   a.K = static_cast<int>(T);
+  a.width = tile_width((T + 63) / 64 * (l.parts == 3 ? 3 : 1));
   a.split_k = a.K;
   a.err = ctx.err;
   a.wait_limit_ns = ctx.wait_limit_ns;
@@ -571,6 +574,9 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   a.elem = kElemF32;
   a.out_vec = aligned(dW, 16) && lddw % 4 == 0;
   a.slots = reinterpret_cast<float4*>(ws + l.slots_off);
+  a.slot_count = l.slot_count;
+  a.out_rows = N;
+  a.out_cols = K;
   TrainMaps maps;
   const TrainOperand A{dy, T, N, l.lddy, l.parts, T * l.lddy};
   const TrainOperand B{ws + l.x_off, T, K, l.ldx, 1, 0};
@@ -580,7 +586,7 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   st = finish_launch(launch_train_tc(kTrainOut, promote, maps, a, clusters, stream),
                      "ckpt8 product launch", stream);
   if (st != GEMM14_OK || !may_split(a, clusters)) return st;
-  const SlotsOut s{false, nullptr, alpha, beta, nullptr, dW, lddw, kElemF32};
+  const SlotsOut s{false, nullptr, alpha, beta, nullptr, dW, lddw, kElemF32, N};
   return finish_launch(launch_slots_out(a, s, clusters, stream), "ckpt8 output launch", stream);
 }
 

@@ -367,6 +367,7 @@ struct CeLayout {
   bool few = false;    // the logits come from the kernel for few rows
   bool gather = false; // rows in use are numbered and gathered first
   bool copy_w = false; // pieces of W are copied (unaligned) or split
+  int64_t slot_count = 0, tail_count = 0;  // of dH, and of dW's split tiles
   int64_t rows = 0;    // T rounded up to whole tiles
   size_t state = 0, counts = 0, index = 0, position = 0, target = 0, lse = 0, coef = 0, h = 0,
          w = 0, part = 0, z = 0, slots = 0, tail = 0, total = 0;
@@ -374,7 +375,7 @@ struct CeLayout {
 
 // Parts of a row's statistics that c columns leave: two a tile.
 int64_t stat_parts(bool few, int64_t c, int sms) {
-  const int64_t w = few ? few_width(c, sms) : 256;
+  const int64_t w = few ? few_width(c, sms) : TrainShape::BN;
   return 2 * ((c + w - 1) / w);
 }
 
@@ -417,10 +418,10 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
       l->z = take(static_cast<size_t>(l->rows) * l->ldz * 2 * l->parts);
       // dH's sums over the pieces, and what dW's split tiles need after them
       const int clusters = std::max(sms / 2, 1);
-      l->slots = take(static_cast<size_t>(slots_needed(tiles_of(T) * tiles_of(D), clusters, true)) *
-                      kSlotBytes);
-      l->tail = take(static_cast<size_t>(slots_needed(tiles_of(l->C) * tiles_of(D), clusters,
-                                                      false)) * kSlotBytes);
+      l->slot_count = slots_needed(tiles_of(T) * tiles_of(D), (l->C + 63) / 64, clusters, true);
+      l->tail_count = slots_needed(2 * tiles_of(l->C) * tiles_of(D), (T + 63) / 64, clusters, false);
+      l->slots = take(static_cast<size_t>(l->slot_count) * kSlotBytes);
+      l->tail = take(static_cast<size_t>(l->tail_count) * kSlotBytes);
     } else {
       l->part = take(static_cast<size_t>((V + l->C - 1) / l->C) * stat_parts(l->few, l->C, sms) *
                      l->rows * sizeof(float2));
@@ -563,6 +564,7 @@ struct CeCall {
     a.wait_limit_ns = ctx.wait_limit_ns;
     a.fault = ctx.fault;
     a.alpha = 1.0f;
+    a.width = TrainShape::BN;
     return a;
   }
 
@@ -611,6 +613,7 @@ struct CeCall {
       a.target64 = targets;
       a.part = at<float2>(l.part) + v0 / l.C * parts_of(l.C) * l.rows;
       a.part_ld = l.rows;
+      a.part_count = parts_of(c) * l.rows;
       a.target_logit = at<float>(l.state);
       st = l.few ? run_few(kTrainStats, w, a)
                  : run(kTrainStats, long_sum(D), h_operand(), false, w, false, &a);
@@ -648,6 +651,8 @@ struct CeCall {
       a.out_part = g_part;
       a.elem = exact ? kElemBf16x3 : elem;
       a.out_vec = 1;
+      a.out_rows = l.rows;
+      a.out_cols = c;
       st = l.few ? run_few(kTrainGrad, w, a)
                  : run(kTrainGrad, exact && long_sum(D), h_operand(), false, w, false, &a);
       if (st != GEMM14_OK) return st;
@@ -656,12 +661,14 @@ struct CeCall {
         a = product(T, D, c, false);
         a.split_k = static_cast<int>(l.C);  // the same plan for every piece
         a.slots = at<float4>(l.slots);
+        a.slot_count = l.slot_count;
         a.add = v0 > 0;
         if ((st = run(kTrainSlots, exact && long_sum(c), dz, false, w, true, &a)) != GEMM14_OK)
           return st;
       }
       if (dW) {
         a = product(c, D, T, true);
+        a.width = tile_width((T + 63) / 64 * (exact ? 6 : 1));
         a.out = static_cast<char*>(dW) + v0 * lddw * eb();
         a.ld_out = lddw;
         a.elem = elem;
@@ -669,11 +676,14 @@ struct CeCall {
         a.scale = r.back;
         a.split_k = static_cast<int>(T);
         a.slots = at<float4>(l.tail);
+        a.slot_count = l.tail_count;
+        a.out_rows = c;
+        a.out_cols = D;
         if ((st = run(kTrainOut, exact && long_sum(T), dz, true, h_operand(), true, &a)) !=
             GEMM14_OK)
           return st;
         if (may_split(a, clusters)) {
-          const SlotsOut s{false, nullptr, 1.0f, 0.0f, r.back, a.out, lddw, elem};
+          const SlotsOut s{false, nullptr, 1.0f, 0.0f, r.back, a.out, lddw, elem, c};
           if ((st = launched(launch_slots_out(a, s, clusters, stream),
                              "linear_ce output launch")) != GEMM14_OK)
             return st;
@@ -685,7 +695,7 @@ struct CeCall {
     a.split_k = static_cast<int>(l.C);
     a.terms = exact ? 6 : 1;
     a.slots = at<float4>(l.slots);
-    const SlotsOut s{true, r.index, 1.0f, 0.0f, r.back, dH, lddh, elem};
+    const SlotsOut s{true, r.index, 1.0f, 0.0f, r.back, dH, lddh, elem, T};
     return launched(launch_slots_out(a, s, clusters, stream), "linear_ce output launch");
   }
 

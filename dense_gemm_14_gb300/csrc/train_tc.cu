@@ -66,7 +66,7 @@ struct Work {
     M = args.n && !args.n_is_k ? min(n, args.M) : args.M;
     K = args.n && args.n_is_k ? min(n, args.K) : args.K;
     tiles_m = (M + S::BM - 1) / S::BM;
-    tiles_n = (N + S::BN - 1) / S::BN;
+    tiles_n = (N + args.width - 1) / args.width;
     kblocks = (K + S::BK - 1) / S::BK;
     const int split_k = args.n && args.n_is_k ? min(n, args.split_k) : args.split_k;
     const int split_blocks = (split_k + S::BK - 1) / S::BK;
@@ -130,11 +130,18 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The bounds checks of `width` elements of the output at row r, column c.
+__device__ __forceinline__ bool out_ok(const TrainArgs& a, int64_t r, int64_t c, int width) {
+  return dev_check(c_span_ok(r * a.ld_out + c, a.ld_out, a.out_rows, a.out_cols, width), a.err);
+}
+
 // The warp's staged block, rows row0 .. +31, to global memory: 8 lanes write a
 // row's 128 bytes. n_cols: elements of the row segment inside the matrix.
-__device__ __forceinline__ void stage_out16(uint32_t buf, uint16_t* out, int64_t ld, int row0,
-                                            int rows, int64_t col0, int n_cols, bool vec,
+__device__ __forceinline__ void stage_out16(const TrainArgs& args, uint32_t buf, uint16_t* out,
+                                            int row0, int rows, int64_t col0, int n_cols,
                                             int lane) {
+  const int64_t ld = args.ld_out;
+  const bool vec = args.out_vec != 0;
   const int p = lane & 7;
 #pragma unroll
   for (int g = 0; g < 8; ++g) {
@@ -142,6 +149,7 @@ __device__ __forceinline__ void stage_out16(uint32_t buf, uint16_t* out, int64_t
     if (row0 + r >= rows || p * 8 >= n_cols) continue;
     const uint4 v = stage_get(stage_at(buf, r, p));
     uint16_t* to = out + static_cast<int64_t>(row0 + r) * ld + col0 + p * 8;
+    if (!out_ok(args, row0 + r, col0 + p * 8, min(8, n_cols - p * 8))) continue;
     if (vec && (p + 1) * 8 <= n_cols) {
       *reinterpret_cast<uint4*>(to) = v;
     } else {
@@ -155,9 +163,12 @@ __device__ __forceinline__ void stage_out16(uint32_t buf, uint16_t* out, int64_t
 // fp32, + beta times what is there: all 8 rows' old values are asked for before
 // the first is used (one by one, a tile took 32 round trips to memory: 93 us for
 // a 4096 x 4096 gradient of 16 rows, against 27 with them together).
-__device__ __forceinline__ void stage_out32(uint32_t buf, float* out, int64_t ld, int row0,
-                                            int rows, int64_t col0, int n_cols, bool vec, int lane,
-                                            float beta) {
+__device__ __forceinline__ void stage_out32(const TrainArgs& args, uint32_t buf, int row0,
+                                            int rows, int64_t col0, int n_cols, int lane) {
+  float* out = static_cast<float*>(args.out);
+  const int64_t ld = args.ld_out;
+  const bool vec = args.out_vec != 0;
+  const float beta = args.beta;
   const int p = lane & 7;
   const bool whole = vec && (p + 1) * 4 <= n_cols;
   float4 old[8];
@@ -165,7 +176,8 @@ __device__ __forceinline__ void stage_out32(uint32_t buf, float* out, int64_t ld
   for (int g = 0; g < 8; ++g) {
     const int r = row0 + g * 4 + (lane >> 3);
     old[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (beta == 0.0f || r >= rows) continue;
+    if (beta == 0.0f || r >= rows || p * 4 >= n_cols) continue;
+    if (!out_ok(args, r, col0 + p * 4, min(4, n_cols - p * 4))) continue;
     const float* from = out + static_cast<int64_t>(r) * ld + col0 + p * 4;
     if (whole) {
       old[g] = *reinterpret_cast<const float4*>(from);
@@ -186,6 +198,7 @@ __device__ __forceinline__ void stage_out32(uint32_t buf, float* out, int64_t ld
     if (beta != 0.0f)
       v = make_float4(fmaf(beta, old[g].x, v.x), fmaf(beta, old[g].y, v.y),
                       fmaf(beta, old[g].z, v.z), fmaf(beta, old[g].w, v.w));
+    if (!out_ok(args, row0 + r, col0 + p * 4, min(4, n_cols - p * 4))) continue;
     float* to = out + static_cast<int64_t>(row0 + r) * ld + col0 + p * 4;
     if (whole) {
       *reinterpret_cast<float4*>(to) = v;
@@ -205,12 +218,12 @@ struct RowData {
   float m, l, zy;     // statistics
 };
 
-template <int kMode>
+template <int kMode, int kChunks = 4>
 struct Epilogue {
   const TrainArgs& args;
   int M, N, lane, row0, row, half, rank;
   int64_t slot;       // of this item, < 0: the tile is written to its place
-  int col_half;       // first column of this thread's half
+  int col_half;       // first column of this thread's kChunks x 32
   uint32_t buf;
   RowData d;
   float factor;
@@ -244,7 +257,7 @@ struct Epilogue {
         const float* from = static_cast<const float*>(args.out) +
                             static_cast<int64_t>(row) * args.ld_out + col_half;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < kChunks; ++c)
           if (col_half + 32 * c < N)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(from + 32 * c));
       }
@@ -290,7 +303,12 @@ struct Epilogue {
       for (int j = 0; j < 32; ++j) x[j] = d.coef == 0.0f ? 0.0f : x[j] * d.coef;
       store16(c, x);
     } else if (kMode == kTrainSlots || slot >= 0) {
-      float4* s = args.slots + slot_index(slot, rank, half, c, 0, row - (row0 & ~127));
+      const int64_t at = slot_index(slot, rank, half, c, 0, row - (row0 & ~127));
+      if (!dev_check(slot_span_ok(at, slot, kSlotBytes / 16, args.slot_count, 1) &&
+                         slot_span_ok(at + 128 * 7, slot, kSlotBytes / 16, args.slot_count, 1),
+                     args.err))
+        return;
+      float4* s = args.slots + at;
       float4 old[8];
 #pragma unroll
       for (int v = 0; v < 8; ++v)
@@ -311,8 +329,7 @@ struct Epilogue {
                     make_uint4(__float_as_uint(x[4 * p]), __float_as_uint(x[4 * p + 1]),
                                __float_as_uint(x[4 * p + 2]), __float_as_uint(x[4 * p + 3])));
         __syncwarp();
-        stage_out32(buf, static_cast<float*>(args.out), args.ld_out, row0, M, col0,
-                    min(32, N - col0), args.out_vec != 0, lane, args.beta);
+        stage_out32(args, buf, row0, M, col0, min(32, N - col0), lane);
       } else {
         store16(c, x);
       }
@@ -340,11 +357,11 @@ struct Epilogue {
                          pack_bf16(x[8 * p + 6], x[8 * p + 7]));
         stage_put(stage_at(buf, lane, p0 + p), v);
       }
-      if ((c & 1) == 0) return;
+      if ((c & 1) == 0 && c + 1 < kChunks) return;
       __syncwarp();
       const int col0 = col_half + 64 * (c >> 1);
-      stage_out16(buf, static_cast<uint16_t*>(args.out), args.ld_out, row0, rows, col0,
-                  min(64, N - col0), args.out_vec != 0, lane);
+      stage_out16(args, buf, static_cast<uint16_t*>(args.out), row0, rows, col0,
+                  min(c & 1 ? 64 : 32, N - col0), lane);
       return;
     }
     // three bf16 parts of each value: the nearest, then the nearest to what is left
@@ -365,23 +382,27 @@ struct Epilogue {
         stage_put(stage_at(buf, lane, p), make_uint4(w[0], w[1], w[2], w[3]));
       }
       __syncwarp();
-      stage_out16(buf, static_cast<uint16_t*>(args.out) + part * args.out_part, args.ld_out, row0,
-                  rows, col0, min(32, N - col0), args.out_vec != 0, lane);
+      stage_out16(args, buf, static_cast<uint16_t*>(args.out) + part * args.out_part, row0, rows,
+                  col0, min(32, N - col0), lane);
     }
   }
 
   __device__ void end(int tn) {
     if (kMode == kTrainStats && row < M) {
-      args.part[(static_cast<int64_t>(tn) * 2 + half) * args.part_ld + row] =
-          make_float2(d.m, d.l);
-      if (d.y >= 0 && d.y < 128 && col_half + d.y < N) args.target_logit[row] = d.zy;
+      const int64_t at = (static_cast<int64_t>(tn) * 2 + half) * args.part_ld + row;
+      if (!dev_check(index_ok(at, args.part_count), args.err)) return;
+      args.part[at] = make_float2(d.m, d.l);
+      if (d.y >= 0 && d.y < 32 * kChunks && col_half + d.y < N) args.target_logit[row] = d.zy;
     }
   }
 };
 
-template <int kMode, bool kPromote>
+// kWidth: columns of a tile, args.width.
+template <int kMode, bool kPromote, int kWidth>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
     train_tc_kernel(const __grid_constant__ TrainMaps maps, const TrainArgs args) {
+  constexpr int kHalf = kWidth / 2;  // a CTA's columns of B, and a warp's of D
+  constexpr int kChunks = kHalf / 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = align1024(smem_raw);
   uint8_t* out_stage = tiles + S::STAGES * S::STAGE_BYTES;
@@ -439,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
         work.get(i, t, split, kb0, kb1);
         work.tile_at(t, tm, tn);
         const int m0 = tm * S::BM + static_cast<int>(rank) * 128;
-        const int n0 = tn * S::BN + static_cast<int>(rank) * 128;
+        const int n0 = tn * kWidth + static_cast<int>(rank) * kHalf;
         const int step = kPromote ? S::CHUNK : kb1 - kb0;
         for (int c0 = kb0; c0 < kb1 && ok; c0 += step) {
           const int c1 = min(c0 + step, kb1);
@@ -455,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
               uint8_t* a_st = tiles + s * S::STAGE_BYTES;
               uint8_t* b_st = a_st + S::A_BYTES;
               const uint32_t full_leader = mapa_shared(smem_u32(&sm.full[s]), 0);
-              if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * S::STAGE_BYTES);
+              if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * (S::A_BYTES + kHalf * 128));
               if (!args.a_mn) {
                 tma_load_2d_pair(a_st, ma, kb * S::BK, m0, full_leader);
               } else {
@@ -467,8 +488,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
               if (!args.b_mn) {
                 tma_load_2d_pair(b_st, mb, kb * S::BK, n0, full_leader);
               } else {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
+                #pragma unroll
+                for (int c = 0; 64 * c < kHalf; ++c)
                   tma_load_2d_pair(b_st + c * (64 * S::BK * 2), mb, n0 + c * 64, kb * S::BK,
                                    full_leader);
               }
@@ -531,8 +552,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
       const int64_t slot = kMode == kTrainSlots || t >= work.plan.direct
                                ? slot_of(work.plan, kMode == kTrainSlots, t, split) : -1;
       const int row0 = tm * S::BM + static_cast<int>(rank) * 128 + q * 32;
-      Epilogue<kMode> e{args, M, args.N, lane, row0, row0 + lane, half, static_cast<int>(rank),
-                        slot, tn * S::BN + half * 128, buf, {}, 1.0f};
+      Epilogue<kMode, kChunks> e{args, M, args.N, lane, row0, row0 + lane, half,
+                                 static_cast<int>(rank), slot, tn * kWidth + half * kHalf, buf,
+                                 {}, 1.0f};
       e.begin();
       const int step = kPromote ? S::CHUNK : kb1 - kb0;
       float acc[kPromote ? 128 : 1];
@@ -549,10 +571,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
         if (!got) { ok = false; break; }
         tc_fence_after_sync();
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                               static_cast<uint32_t>(b * S::BN + half * 128);
+                               static_cast<uint32_t>(b * S::BN + half * kHalf);
         if (kPromote) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
             uint32_t r[32];
             tmem_ld_32x32b_x32(t_row + c * 32, r);
             tc_wait_ld();
@@ -561,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
             uint32_t r[32];
             float x[32];
             tmem_ld_32x32b_x32(t_row + c * 32, r);
@@ -578,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
       if (!ok) break;
       if (kPromote) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           float x[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) x[j] = acc[kPromote ? 32 * c + j : 0];
@@ -587,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
       } else if (kb0 == kb1) {
         // no products at all (no rows in use): sums of zero
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           float x[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) x[j] = 0.0f;
@@ -838,8 +860,9 @@ __global__ void __launch_bounds__(256)
     int tm, tn;
     work.tile_at(t, tm, tn);
     const int rank = part >> 5, q0 = ((part >> 3) & 3) * 32, half = (part >> 2) & 1, c = part & 3;
-    const int row0 = tm * S::BM + rank * 128 + q0, col0 = tn * S::BN + half * 128 + c * 32;
-    if (row0 >= work.M || col0 >= work.N) continue;
+    const int row0 = tm * S::BM + rank * 128 + q0;
+    const int col0 = tn * args.width + half * (args.width / 2) + c * 32;
+    if (64 * c >= args.width || row0 >= work.M || col0 >= work.N) continue;
     const int ranges = t < work.plan.direct ? 1 : work.plan.splits;
     const float4* from = args.slots + slot_index(slot_of(work.plan, s.all, t, 0), rank, half, c,
                                                  warp, q0 + lane);
@@ -857,20 +880,28 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     if (row0 + r >= work.M) continue;
     const int64_t row = s.rows ? s.rows[row0 + r] : row0 + r;
+    const int col = col0 + c4, cols = min(4, work.N - col);
+    const int64_t at = row * s.ld + col;
+    if (cols <= 0 ||
+        !dev_check(c_span_ok(at, s.ld, s.out_rows, work.N, cols), args.err))
+      continue;
+    if (s.elem == kElemF32) {
+      float* o = static_cast<float*>(s.out) + at;
+      float x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = col0 + c4 + j;
-      if (col >= work.N) break;
-      const int64_t at = row * s.ld + col;
-      const float x = tile[r][c4 + j] * k;
-      if (s.elem == kElemF32) {
-        float* o = static_cast<float*>(s.out) + at;
-        *o = s.beta == 0.0f ? x : fmaf(s.beta, *o, x);
-      } else if (s.elem == kElemF16) {
-        static_cast<__half*>(s.out)[at] = __float2half_rn(x);
-      } else {
-        static_cast<__nv_bfloat16*>(s.out)[at] = __float2bfloat16_rn(x);
-      }
+      for (int j = 0; j < 4; ++j) x[j] = s.beta != 0.0f && j < cols ? o[j] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < cols) o[j] = fmaf(s.beta, x[j], tile[r][c4 + j] * k);
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(s.out) + at;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < cols) {
+          const float x = tile[r][c4 + j] * k;
+          o[j] = s.elem == kElemF16 ? __half_as_ushort(__float2half_rn(x))
+                                    : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        }
     }
   }
 }
@@ -905,16 +936,21 @@ __global__ void __launch_bounds__(256)
 
 using TrainKernel = void (*)(const TrainMaps, const TrainArgs);
 
-TrainKernel kernel_of(int mode, bool promote) {
+TrainKernel kernel_of(int mode, bool promote, int width) {
   switch (mode) {
     case kTrainStats:
-      return promote ? train_tc_kernel<kTrainStats, true> : train_tc_kernel<kTrainStats, false>;
+      return promote ? train_tc_kernel<kTrainStats, true, 256>
+                     : train_tc_kernel<kTrainStats, false, 256>;
     case kTrainGrad:
-      return promote ? train_tc_kernel<kTrainGrad, true> : train_tc_kernel<kTrainGrad, false>;
+      return promote ? train_tc_kernel<kTrainGrad, true, 256>
+                     : train_tc_kernel<kTrainGrad, false, 256>;
     case kTrainSlots:
-      return promote ? train_tc_kernel<kTrainSlots, true> : train_tc_kernel<kTrainSlots, false>;
-    default:
-      return promote ? train_tc_kernel<kTrainOut, true> : train_tc_kernel<kTrainOut, false>;
+      return promote ? train_tc_kernel<kTrainSlots, true, 256>
+                     : train_tc_kernel<kTrainSlots, false, 256>;
+    default:  // (sums short enough for half the width are never promoted)
+      return width == 128 ? train_tc_kernel<kTrainOut, false, 128>
+             : promote    ? train_tc_kernel<kTrainOut, true, 256>
+                          : train_tc_kernel<kTrainOut, false, 256>;
   }
 }
 
@@ -928,9 +964,9 @@ int train_max_clusters() {
       dev,
       [] {
         int least = INT_MAX;
-        for (int mode = kTrainStats; mode <= kTrainOut; ++mode)
-          for (const bool promote : {false, true}) {
-            const TrainKernel k = kernel_of(mode, promote);
+        for (int i = 0; i < 9; ++i) {
+            const TrainKernel k = i < 8 ? kernel_of(i / 2, i % 2 != 0, 256)
+                                        : kernel_of(kTrainOut, false, 128);
             if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      S::SMEM_BYTES) != cudaSuccess)
               return -1;
@@ -950,20 +986,20 @@ int train_max_clusters() {
 
 int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOperand& B, bool b_mn,
                    TrainMaps* maps, TrainArgs* args) {
-  const auto encode = [&](const TrainOperand& x, bool mn, CUtensorMap* m) {
+  const auto encode = [&](const TrainOperand& x, bool mn, int box_rows, CUtensorMap* m) {
     for (int p = 0; p < 3; ++p) {
       if (p >= x.parts) {
         m[p] = m[0];
         continue;
       }
       const void* base = static_cast<const char*>(x.base) + 2 * p * x.part_stride;
-      const int st = map_16bit(&m[p], bf16, base, x.rows, x.cols, x.ld, mn ? 64 : 128);
+      const int st = map_16bit(&m[p], bf16, base, x.rows, x.cols, x.ld, mn ? 64 : box_rows);
       if (st != 0) return st;
     }
     return 0;
   };
-  int st = encode(A, a_mn, maps->a);
-  if (st == 0) st = encode(B, b_mn, maps->b);
+  int st = encode(A, a_mn, 128, maps->a);
+  if (st == 0) st = encode(B, b_mn, args->width / 2, maps->b);
   if (st != 0) return st;
   // Terms of split operands, small ones first: of 3 x 3 parts the six whose
   // product is above 2^-24 of the whole, or A's three parts against one B.
@@ -972,7 +1008,7 @@ int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOpera
   args->term_code = !split ? 0u : B.parts == 3 ? 0x041582u : 0x012u;
   args->a_mn = a_mn;
   args->b_mn = b_mn;
-  args->idesc = idesc_f16_f32acc(bf16, S::BM, S::BN, a_mn, b_mn);
+  args->idesc = idesc_f16_f32acc(bf16, S::BM, args->width, a_mn, b_mn);
   return 0;
 }
 
@@ -1014,7 +1050,7 @@ cudaError_t launch_train_few(int mode, const CUtensorMap& map_a, const CUtensorM
 }
 
 bool may_split(const TrainArgs& args, int clusters) {
-  const int tiles = ((args.M + S::BM - 1) / S::BM) * ((args.N + S::BN - 1) / S::BN);
+  const int tiles = ((args.M + S::BM - 1) / S::BM) * ((args.N + args.width - 1) / args.width);
   const int blocks = (args.split_k + S::BK - 1) / S::BK;
   // with the rows in use known on the device only, any smaller plan may be the one
   return args.n ? blocks >= 8 && blocks * args.terms > 24
@@ -1024,7 +1060,7 @@ bool may_split(const TrainArgs& args, int clusters) {
 cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clusters,
                              cudaStream_t stream) {
   const int64_t tiles = static_cast<int64_t>((args.M + S::BM - 1) / S::BM) *
-                        ((args.N + S::BN - 1) / S::BN);
+                        ((args.N + args.width - 1) / args.width);
   const int64_t most = 64 * (s.all || tiles < clusters ? tiles : clusters);  // a tail is under a wave
   const int64_t cap = 16 * clusters;  // 8 blocks an SM
   return launch_kernel(slots_out_kernel, dim3(static_cast<unsigned>(most < cap ? most : cap)),
@@ -1042,7 +1078,7 @@ cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t col
 
 cudaError_t launch_train_tc(int mode, bool promote, const TrainMaps& maps, const TrainArgs& args,
                             int clusters, cudaStream_t stream) {
-  return launch_kernel(kernel_of(mode, promote), dim3(2 * clusters), dim3(S::THREADS),
+  return launch_kernel(kernel_of(mode, promote, args.width), dim3(2 * clusters), dim3(S::THREADS),
                        S::SMEM_BYTES, stream, maps, args);
 }
 

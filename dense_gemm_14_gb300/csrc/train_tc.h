@@ -52,6 +52,7 @@ struct TrainArgs {
   // parts): nibble t of term_code is part(A) | part(B) << 2 of term t.
   int terms;
   uint32_t term_code;
+  int width;            // columns of a tile: 256, or 128 (B stored K x N)
   int split_k;          // K that the split of tiles is planned for (0: none are split)
   uint32_t idesc;
   unsigned* err;
@@ -77,6 +78,9 @@ struct TrainArgs {
   // kTrainSlots
   float4* slots;
   int add;                      // add to what the slots hold
+  // what the buffers hold, for the bounds checks of a checked build: rows and
+  // columns of out, slots, entries of part
+  int64_t out_rows, out_cols, slot_count, part_count;
 };
 
 // How a launch's tiles are worked on by `clusters` clusters: the first `direct`
@@ -116,11 +120,13 @@ __host__ __device__ inline int64_t slot_of(const TilePlan& p, bool all, int tile
   if (tile < p.direct) return tile;
   return (all ? p.direct : 0) + static_cast<int64_t>(tile - p.direct) * p.splits + s;
 }
-// Slots that a launch of at most this many tiles can need.
-inline int64_t slots_needed(int64_t tiles, int clusters, bool all) {
-  const int64_t tail = tiles < clusters ? tiles : clusters;
-  const int64_t split = static_cast<int64_t>(kTailWaves) * clusters;
-  return (all ? tiles + split : split) + tail;
+// Slots that a launch of at most this many tiles of at most this many k-blocks
+// can need.
+inline int64_t slots_needed(int64_t tiles, int64_t kblocks, int clusters, bool all) {
+  const int64_t ranges = kblocks / 4 < 64 ? kblocks / 4 : 64;
+  const int64_t most = static_cast<int64_t>(kTailWaves) * clusters;
+  const int64_t split = ranges < 2 ? 0 : tiles * ranges < most ? tiles * ranges : most;
+  return (all ? tiles : 0) + split;
 }
 // float4 v (columns 4v ..) of chunk c (32 columns) of half h (128 columns) of row
 // q of CTA r's 128 rows, in slot k: rows next to one another.
@@ -128,6 +134,14 @@ __host__ __device__ inline int64_t slot_index(int64_t k, int r, int h, int c, in
   return (((k * 2 + r) * 2 + h) * 4 + c) * 1024 + v * 128 + q;
 }
 constexpr int64_t kSlotBytes = 256 * 256 * 4;
+
+// Columns of a tile of a kTrainOut product over `units` k-blocks times terms.
+// Half the width halves the sums a tile writes (and reads, with beta) beside its
+// products, and spreads short ones more evenly: dW of 4096 x 4096 from 16 rows 37
+// -> 32 us, 4096 x 11008 from 256 rows 97 -> 92; from 1000 rows it loses (56 ->
+// 58): A's k-blocks then feed half as many MMAs, and shared memory holds those to
+// 58 % of their rate (2458 x 131072 x 2048: 785 us, 1359 on 128 columns, 945 on 192).
+inline int tile_width(int64_t units) { return units <= 4 ? 128 : 256; }
 
 // Clusters of two that fit at once on the current device (0: they cannot run).
 int train_max_clusters();
@@ -147,7 +161,8 @@ struct TrainOperand {
   int64_t part_stride;
 };
 // The maps of A (M x K, or stored K x M when a_mn) and B (N x K, or K x N when
-// b_mn), and the terms, instruction descriptor and a_mn / b_mn of *args.
+// b_mn), and the terms, instruction descriptor and a_mn / b_mn of *args, whose
+// width is set.
 // Returns a gemm14_status.
 int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOperand& B, bool b_mn,
                    TrainMaps* maps, TrainArgs* args);
@@ -164,6 +179,7 @@ struct SlotsOut {
   void* out;
   int64_t ld;
   int elem;
+  int64_t out_rows;
 };
 // clusters: the launch's.
 cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clusters,
