@@ -22,6 +22,7 @@
 #include "plan.h"
 #include "ptx.cuh"
 #include "train_tc.h"
+#include "unaligned.cuh"
 
 namespace gemm14 {
 namespace {
@@ -69,14 +70,15 @@ __device__ __forceinline__ void quantise2(uint32_t a, uint32_t b, float factor, 
       : "=r"(qa), "=r"(qb)
       : "r"(a), "r"(b), "f"(factor), "f"(12582912.0f));
 }
-// Two whole numbers u = q + 128, each as the fp32 2^23 + u, to q times the
+// Two whole numbers u = q + 128, each as the fp32 2^23 + u, to q times its
 // block's step (less 2^23 + 128 first: the step times that may leave fp32's range).
-__device__ __forceinline__ void scale2(uint32_t a, uint32_t b, float step, float& xa, float& xb) {
+__device__ __forceinline__ void scale2(uint32_t a, uint32_t b, float step_a, float step_b,
+                                       float& xa, float& xb) {
   asm("{\n\t.reg .b64 x, s, o;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 o, {%5, %5};\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\tmov.b64 o, {%6, %6};\n\t"
       "add.rn.f32x2 x, x, o;\n\tmul.rn.f32x2 x, x, s;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "=f"(xa), "=f"(xb)
-      : "r"(a), "r"(b), "f"(step), "f"(-8388736.0f));
+      : "r"(a), "r"(b), "f"(step_a), "f"(step_b), "f"(-8388736.0f));
 }
 // Four low bytes as one word.
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -119,18 +121,18 @@ struct Place {
   }
 };
 
-// Both kernels come in two forms. Where rows start on 16 bytes a lane moves a
-// piece of 16 bytes of X (8 or 4 values; 4 or 8 lanes a block, whose largest
-// magnitude they find with two or three shuffles) and 8 or 4 bytes of Q;
-// otherwise a lane is one column, a warp one block, with coalesced accesses of
-// single elements whatever the addresses. The passes should be bound by
-// memory, and what held the wide form back was its instructions (21 a value,
-// 72 % of the issue slots): so a thread keeps to its place in the rows and
-// steps by whole rows (no division, no multiply in the loop), two values share
-// an instruction where they can, and q is only clamped where the block's
-// largest value rounds to 128. kAhead loads are in flight before the first is
-// used.
-constexpr int kUnroll = 8, kAhead = 6;
+// Wide forms: a lane moves a piece of 16 bytes of X (8 or 4 values; 4 or 8 lanes
+// a block, whose largest magnitude they find with two or three shuffles) and 8
+// or 4 bytes of Q. Rows of X that do not start on 16 bytes are read as two
+// aligned words and a shift; restore writes the aligned pieces of its rows and
+// reads Q with the shift. (Where Q's rows do not start on 8 or 4 bytes, save is
+// a warp a block and a lane a column.) The passes should be bound by memory,
+// and what held them back was their instructions (21 a value, 72 % of the issue
+// slots): so a thread keeps to its place in the rows and steps by whole rows (no
+// division, no multiply in the loop), two values share an instruction where
+// they can, and q is only clamped where the block's largest value rounds to
+// 128. kAhead loads are in flight before the first is used.
+constexpr int kUnroll = 8, kAhead = 6;  // (kUnroll: of the element form)
 
 template <typename T>
 __host__ __device__ constexpr int piece_values() { return 16 / static_cast<int>(sizeof(T)); }
@@ -141,11 +143,13 @@ union Piece {
   T x[16 / sizeof(T)];
 };
 
-// Threads along a row, a power of two from 32 up: those that its pieces fill,
-// or the block's 256; the block's other threads take other rows.
-int threads_along(int64_t pieces) {
-  int x = 32;
-  while (x < kThreads && x < pieces) x *= 2;
+// Threads along a row of so many pieces, a power of two: as many as leave each
+// kAhead pieces, the block's other threads taking other rows (8 at least: a
+// block's lanes stay together); more where the rows are too few for the SMs.
+int threads_along(int64_t rows, int64_t pieces, int sms) {
+  int x = 8;
+  while (x < kThreads && x * kAhead < pieces) x *= 2;
+  while (x < kThreads && x < pieces && rows * x < static_cast<int64_t>(sms) * 1024) x *= 2;
   return x;
 }
 
@@ -189,7 +193,8 @@ __device__ __forceinline__ void pack(const float (&x)[8], Piece<__half>& p) {
   }
 }
 
-template <typename T>
+// kAny: X at any address and pitch.
+template <typename T, bool kAny>
 __global__ void __launch_bounds__(kThreads)
     ckpt8_save_vec_kernel(const T* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
                           int64_t rows, uint32_t cols, int along) {
@@ -205,6 +210,7 @@ __global__ void __launch_bounds__(kThreads)
   int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / along) + ty;
   const int64_t rounds = (rows + row_step - 1) / row_step;
   const T* xr = X + r * ldx;
+  const T* end = X + (rows - 1) * ldx + cols;
   int8_t* qr = Q + r * ldq;
   uint8_t* sr = S + r * lds;
   for (int64_t round = 0; round < rounds; ++round) {
@@ -216,8 +222,8 @@ __global__ void __launch_bounds__(kThreads)
       for (int u = 0; u < kAhead; ++u) {
         const uint32_t c = (p0 + u * along) * kPer;
         p[u].raw = make_uint4(0, 0, 0, 0);
-        if (in_rows && c + kPer <= cols) {
-          p[u].raw = __ldcs(reinterpret_cast<const uint4*>(xr + c));
+        if (in_rows && c + kPer <= cols && (!kAny || words_inside(xr + c, 16, X, end))) {
+          p[u].raw = kAny ? load16_any(xr + c) : __ldcs(reinterpret_cast<const uint4*>(xr + c));
         } else if (in_rows && c < cols) {
 #pragma unroll
           for (int j = 0; j < kPer; ++j)
@@ -272,10 +278,12 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename T>
+// kAny: X and Q at any address and pitch. Column c of a piece is then its
+// place in X's aligned words, from -(values before the row in its first word).
+template <typename T, bool kAny>
 __global__ void __launch_bounds__(kThreads)
-    ckpt8_restore_vec_kernel(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, T* X,
-                             int64_t ldx, int64_t rows, uint32_t cols, int along) {
+    ckpt8_restore_kernel(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, T* X,
+                         int64_t ldx, int64_t rows, int64_t cols, int along) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int kPer = piece_values<T>();
@@ -283,57 +291,68 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * (kThreads / along);
   int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / along) + ty;
   const int8_t* qr = Q + r * ldq;
+  const int8_t* end = Q + (rows - 1) * ldq + cols;
   const uint8_t* sr = S + r * lds;
   T* xr = X + r * ldx;
   for (; r < rows; r += row_step, qr += row_step * ldq, sr += row_step * lds, xr += row_step * ldx) {
-    for (uint32_t c0 = tx * kPer; c0 < cols; c0 += along * kAhead * kPer) {
-      uint32_t w[kAhead][kPer / 4], s[kAhead];
+    const int before =
+        kAny ? static_cast<int>(reinterpret_cast<uintptr_t>(xr) & 15u) / static_cast<int>(sizeof(T))
+             : 0;
+    for (int64_t c0 = tx * kPer - before; c0 < cols; c0 += along * kAhead * kPer) {
+      uint32_t w[kAhead][kPer / 4], s[kAhead][kAny ? 2 : 1];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const uint32_t c = c0 + u * along * kPer;
-        s[u] = 7u;
+        const int64_t c = c0 + u * along * kPer;
+        s[u][0] = 7u;
+        if (kAny) s[u][kAny ? 1 : 0] = 7u;
 #pragma unroll
         for (int j = 0; j < kPer / 4; ++j) w[u][j] = 0u;
         if (c >= cols) continue;
-        s[u] = sr[c / kBlock];
-        if (c + kPer <= cols) {
+        s[u][0] = sr[max(c, int64_t(0)) / kBlock];
+        if (kAny) s[u][kAny ? 1 : 0] = sr[min(c + kPer, cols) > 0 ? (min(c + kPer, cols) - 1) / kBlock : 0];
+        if (c >= 0 && c + kPer <= cols && (!kAny || words_inside(qr + c, kPer, Q, end))) {
           if constexpr (kPer == 8) {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(qr + c));
+            const uint2 v = kAny ? load8_any(qr + c) : __ldcs(reinterpret_cast<const uint2*>(qr + c));
             w[u][0] = v.x;
             w[u][1] = v.y;
           } else {
-            w[u][0] = __ldcs(reinterpret_cast<const uint32_t*>(qr + c));
+            w[u][0] = kAny ? load4_any(qr + c) : __ldcs(reinterpret_cast<const uint32_t*>(qr + c));
           }
         } else {
 #pragma unroll
           for (int j = 0; j < kPer; ++j)
-            if (c + j < cols)
+            if (c + j >= 0 && c + j < cols)
               w[u][j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(qr[c + j])) << (8 * (j % 4));
         }
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const uint32_t c = c0 + u * along * kPer;
+        const int64_t c = c0 + u * along * kPer;
         if (c >= cols) break;
-        const float step = step_of(s[u]);
+        // a piece holds columns of one block, or (kAny) of two: those from `split` on
+        const float step0 = step_of(s[u][0]), step1 = step_of(s[u][kAny ? 1 : 0]);
+        const int split = kAny ? kBlock - static_cast<int>(max(c, int64_t(0)) % kBlock) -
+                                     static_cast<int>(min(c, int64_t(0)))
+                               : kBlock;
+        const auto step = [&](int j) { return !kAny || j < split ? step0 : step1; };
         float x[kPer];
 #pragma unroll
         for (int k = 0; k < kPer / 4; ++k) {
           const uint32_t v = w[u][k] ^ 0x80808080u;  // q + 128 in each byte
-          scale2(__byte_perm(v, 0x4b000000u, 0x7440), __byte_perm(v, 0x4b000000u, 0x7441), step,
-                 x[4 * k], x[4 * k + 1]);
-          scale2(__byte_perm(v, 0x4b000000u, 0x7442), __byte_perm(v, 0x4b000000u, 0x7443), step,
-                 x[4 * k + 2], x[4 * k + 3]);
+          scale2(__byte_perm(v, 0x4b000000u, 0x7440), __byte_perm(v, 0x4b000000u, 0x7441),
+                 step(4 * k), step(4 * k + 1), x[4 * k], x[4 * k + 1]);
+          scale2(__byte_perm(v, 0x4b000000u, 0x7442), __byte_perm(v, 0x4b000000u, 0x7443),
+                 step(4 * k + 2), step(4 * k + 3), x[4 * k + 2], x[4 * k + 3]);
         }
         Piece<T> p;
         pack(x, p);
         T* to = xr + c;
-        if (c + kPer <= cols) {
+        if (c >= 0 && c + kPer <= cols) {
           *reinterpret_cast<uint4*>(to) = p.raw;
         } else {
 #pragma unroll
           for (int j = 0; j < kPer; ++j)
-            if (c + j < cols) to[j] = p.x[j];
+            if (c + j >= 0 && c + j < cols) to[j] = p.x[j];
         }
       }
     }
@@ -374,38 +393,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    ckpt8_restore_kernel(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, T* X,
-                         int64_t ldx, int64_t rows, int64_t cols) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t per_row = (cols + kBlock - 1) / kBlock;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  const Place step(warps, per_row);
-  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), per_row);
-  while (at.row < rows) {
-    int q[kUnroll];
-    uint32_t s[kUnroll];
-    Place place[kUnroll] = {at, at, at, at, at, at, at, at};
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      place[u] = at;
-      const int64_t c = at.item * kBlock + lane;
-      const bool in = at.row < rows && c < cols;
-      q[u] = in ? Q[at.row * ldq + c] : 0;
-      s[u] = in ? S[at.row * lds + at.item] : 0u;
-      at.move(step, per_row);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = place[u].row, c = place[u].item * kBlock + lane;
-      if (r < rows && c < cols) X[r * ldx + c] = from_f32<T>(q[u] * step_of(s[u]));
-    }
-  }
-}
-
 // Blocks for `threads_needed` threads of one item each, at most 8 an SM.
 int grid_for(int64_t threads_needed, int sm_count) {
   const int64_t blocks = (threads_needed + kThreads - 1) / kThreads;
@@ -413,38 +400,37 @@ int grid_for(int64_t threads_needed, int sm_count) {
   return static_cast<int>(blocks < cap ? blocks : cap);
 }
 
-// Whether rows of X and Q take the wide accesses.
-template <typename T>
-bool wide(const void* X, int64_t ldx, const void* Q, int64_t ldq) {
-  constexpr int kPer = piece_values<T>();
-  return aligned(X, 16) && ldx % kPer == 0 && aligned(Q, kPer) && ldq % kPer == 0;
+// Whether rows start on `bytes` bytes (elements of `size` bytes).
+bool rows_on(const void* p, int64_t ld, int size, int bytes) {
+  return aligned(p, bytes) && ld * size % bytes == 0;
 }
 
 template <typename T>
 cudaError_t save_as(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, uint8_t* S, int64_t lds,
                     int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
+  constexpr int kPer = piece_values<T>();
   const int64_t blocks = (cols + kBlock - 1) / kBlock;
   const T* x = static_cast<const T*>(X);
-  if (!wide<T>(X, ldx, Q, ldq))
+  if (!rows_on(Q, ldq, 1, kPer))
     return launch_kernel(ckpt8_save_kernel<T>, dim3(grid_for(rows * blocks * 32, sms)),
                          dim3(kThreads), 0, stream, x, ldx, Q, ldq, S, lds, rows, cols);
-  const int along = threads_along(blocks * kBlock / piece_values<T>());
-  return launch_kernel(ckpt8_save_vec_kernel<T>, dim3(grid_for(rows * along, sms)),
-                       dim3(kThreads), 0, stream, x, ldx, Q, ldq, S, lds, rows,
-                       static_cast<uint32_t>(cols), along);
+  const int along = threads_along(rows, blocks * kBlock / kPer, sms);
+  const auto kernel = rows_on(X, ldx, sizeof(T), 16) ? ckpt8_save_vec_kernel<T, false>
+                                                     : ckpt8_save_vec_kernel<T, true>;
+  return launch_kernel(kernel, dim3(grid_for(rows * along, sms)), dim3(kThreads), 0, stream, x, ldx,
+                       Q, ldq, S, lds, rows, static_cast<uint32_t>(cols), along);
 }
 template <typename T>
 cudaError_t restore_as(const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, void* X,
                        int64_t ldx, int64_t rows, int64_t cols, int sms, cudaStream_t stream) {
+  constexpr int kPer = piece_values<T>();
   T* x = static_cast<T*>(X);
-  if (!wide<T>(X, ldx, Q, ldq))
-    return launch_kernel(ckpt8_restore_kernel<T>,
-                         dim3(grid_for(rows * ((cols + kBlock - 1) / kBlock) * 32, sms)),
-                         dim3(kThreads), 0, stream, Q, ldq, S, lds, x, ldx, rows, cols);
-  const int along = threads_along((cols + piece_values<T>() - 1) / piece_values<T>());
-  return launch_kernel(ckpt8_restore_vec_kernel<T>, dim3(grid_for(rows * along, sms)),
-                       dim3(kThreads), 0, stream, Q, ldq, S, lds, x, ldx, rows,
-                       static_cast<uint32_t>(cols), along);
+  const bool any = !rows_on(X, ldx, sizeof(T), 16) || !rows_on(Q, ldq, 1, kPer);
+  const int64_t pieces = (cols + (any ? kPer - 1 : 0) + kPer - 1) / kPer;
+  const int along = threads_along(rows, pieces, sms);
+  const auto kernel = any ? ckpt8_restore_kernel<T, true> : ckpt8_restore_kernel<T, false>;
+  return launch_kernel(kernel, dim3(grid_for(rows * along, sms)), dim3(kThreads), 0, stream, Q, ldq,
+                       S, lds, x, ldx, rows, cols, along);
 }
 
 cudaError_t launch_restore(int dtype, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,
@@ -551,11 +537,10 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   }
   const void* dy = l.copy_dy ? ws + l.dy_off : dY;
   if (l.copy_dy) {
-    const RepitchJob job{dY, lddy, ws + l.dy_off, l.lddy, T, N, 0, nullptr}, none{};
     const cudaError_t e =
         l.parts == 3 ? launch_split3(static_cast<const float*>(dY), lddy, T, N, ws + l.dy_off,
                                      l.lddy, T * l.lddy, ctx.sm_count, stream)
-                     : launch_repitch(job, none, 2, ctx.sm_count, stream);
+                     : launch_realign(dY, lddy, T, N, ws + l.dy_off, l.lddy, ctx.sm_count, stream);
     if (e != cudaSuccess) return finish_launch(e, "ckpt8 copy launch", stream);
   }
   TrainArgs a{};

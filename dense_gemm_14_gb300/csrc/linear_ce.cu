@@ -37,6 +37,7 @@
 #include "plan.h"
 #include "ptx.cuh"
 #include "train_tc.h"
+#include "unaligned.cuh"
 
 namespace gemm14 {
 namespace {
@@ -183,10 +184,15 @@ __global__ void __launch_bounds__(256)
   const E* h = H + b * ldh;
   uint16_t* o = out + i * ldo;
   if constexpr (kParts == 1) {
-    const int64_t whole = vec ? D / 8 : 0;  // 16-byte pieces
-    for (int64_t c = threadIdx.x; c < whole; c += blockDim.x)
-      reinterpret_cast<uint4*>(o)[c] = reinterpret_cast<const uint4*>(h)[c];
-    for (int64_t c = 8 * whole + threadIdx.x; c < D; c += blockDim.x) o[c] = h[c];
+    const E* end = H + (T - 1) * ldh + D;
+    for (int64_t c = 8 * threadIdx.x; c < D; c += 8 * blockDim.x) {
+      if (c + 8 <= D && (vec || words_inside(h + c, 16, H, end))) {
+        *reinterpret_cast<uint4*>(o + c) =
+            vec ? *reinterpret_cast<const uint4*>(h + c) : load16_any(h + c);
+      } else {
+        for (int j = 0; j < 8 && c + j < D; ++j) o[c + j] = h[c + j];
+      }
+    }
   } else {
     for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
       float x = h[c];
@@ -548,8 +554,8 @@ struct CeCall {
       return launched(launch_split3(static_cast<const float*>(src), ldw, c, D, dst, l.ldx,
                                     l.C * l.ldx, ctx.sm_count, stream),
                       "linear_ce split launch");
-    const RepitchJob job{src, ldw, dst, l.ldx, c, D, 0, nullptr}, none{};
-    return launched(launch_repitch(job, none, 2, ctx.sm_count, stream), "linear_ce copy launch");
+    return launched(launch_realign(src, ldw, c, D, dst, l.ldx, ctx.sm_count, stream),
+                    "linear_ce copy launch");
   }
 
   // Arguments of a product M x N over K, its rows (or its K, n_is_k) being those in use.

@@ -11,9 +11,9 @@
 // one row's 128 columns, so that a row's maximum and sum need no exchange
 // between threads.
 //
-// Long sums (kPromote): the accumulator is drained every 16 k-blocks into 128
+// Long sums (kPromote): the accumulator is drained every CHUNK k-blocks into 128
 // fp32 registers a thread and starts again from zero while the MMAs go on in
-// the other one. A drain takes about 600 cycles against 8192 of MMAs.
+// the other one.
 //
 // Every wait is bounded (ptx.cuh); a CTA that gives up raises its peer's abort
 // flag, and both meet at a cluster barrier before TMEM is freed.
@@ -24,6 +24,7 @@
 #include "kernels.h"
 #include "ptx.cuh"
 #include "train_tc.h"
+#include "unaligned.cuh"
 
 namespace gemm14 {
 namespace {
@@ -743,8 +744,8 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
       bool ok = true;
       uint32_t s = 0, ph = 0, unit = 0;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int k0 = 0; k0 < kblocks; k0 += S::CHUNK, ++unit) {
-          const int k1 = min(k0 + S::CHUNK, kblocks);
+        for (int k0 = 0; k0 < kblocks; k0 += FewShape::CHUNK, ++unit) {
+          const int k1 = min(k0 + FewShape::CHUNK, kblocks);
           const int b = unit & 1;
           if (!mbar_wait(&sm.acc_empty[b], ((unit >> 1) & 1) ^ 1, wc)) { ok = false; break; }
           tc_fence_after_sync();
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-      for (int k0 = 0; k0 < kblocks; k0 += S::CHUNK, ++unit) {
+      for (int k0 = 0; k0 < kblocks; k0 += FewShape::CHUNK, ++unit) {
         const int b = unit & 1;
         int got = 1;
         if (lane == 0) got = mbar_wait(&sm.acc_full[b], (unit >> 1) & 1, wc) ? 1 : 0;
@@ -902,6 +903,42 @@ __global__ void __launch_bounds__(256)
           o[j] = s.elem == kElemF16 ? __half_as_ushort(__float2half_rn(x))
                                     : __bfloat16_as_ushort(__float2bfloat16_rn(x));
         }
+    }
+  }
+}
+
+// A thread moves 16 bytes, 4 of them in flight; a warp 128 pieces of a row.
+__global__ void __launch_bounds__(256)
+    realign_kernel(const uint16_t* X, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
+                   int64_t ld) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  constexpr int kUnroll = 4;
+  const int lane = threadIdx.x & 31;
+  const uint16_t* end = X + (rows - 1) * ldx + cols;
+  const int64_t per_row = (cols + 256 * kUnroll - 1) / (256 * kUnroll);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows * per_row;
+       i += warps) {
+    const int64_t r = i / per_row, c0 = (i - r * per_row) * 256 * kUnroll + 8 * lane;
+    const uint16_t* x = X + r * ldx;
+    uint16_t* o = out + r * ld;
+    uint4 v[kUnroll];
+    bool wide[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t c = c0 + 256 * u;
+      wide[u] = c + 8 <= cols && words_inside(x + c, 16, X, end);
+      if (wide[u]) v[u] = load16_any(x + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t c = c0 + 256 * u;
+      if (wide[u]) {
+        *reinterpret_cast<uint4*>(o + c) = v[u];
+      } else {
+        for (int j = 0; j < 8 && c + j < cols; ++j) o[c + j] = x[c + j];
+      }
     }
   }
 }
@@ -1065,6 +1102,15 @@ cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clust
   const int64_t cap = 16 * clusters;  // 8 blocks an SM
   return launch_kernel(slots_out_kernel, dim3(static_cast<unsigned>(most < cap ? most : cap)),
                        dim3(256), 0, stream, args, s, clusters);
+}
+
+cudaError_t launch_realign(const void* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
+                           int64_t ld, int sm_count, cudaStream_t stream) {
+  const int64_t cap = static_cast<int64_t>(sm_count) * 8;
+  const int64_t blocks = (rows * ((cols + 1023) / 1024) + 7) / 8;
+  return launch_kernel(realign_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
+                       dim3(256), 0, stream, static_cast<const uint16_t*>(X), ldx, rows, cols,
+                       static_cast<uint16_t*>(out), ld);
 }
 
 cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,

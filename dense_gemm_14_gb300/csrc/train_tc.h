@@ -37,7 +37,8 @@ struct TrainShape {
   // fp32 registers. The tensor cores add with truncation: measured on GB300,
   // n MMAs of K = 16 in a row leave a relative error of about 0.4 n 2^-24 (512
   // of them, K = 8192: 6.7e-6, against 6e-7 for an fp32 FMA sum). 64 MMAs, 16
-  // k-blocks, keep it under 1e-6.
+  // k-blocks, leave 6e-7. Half as many leave 3e-7 and cost 1 to 5 % (wgrad 8192 x
+  // 4096 x 11008: 535 -> 563 us): the drains then wait for each other.
   static constexpr int CHUNK = 16;
 };
 
@@ -187,6 +188,11 @@ cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clust
 // Whether a kTrainOut launch may split tiles (then launch_slots_out follows it).
 bool may_split(const TrainArgs& args, int clusters);
 
+// A rows x cols matrix of 16-bit elements, rows at any address and pitch, to
+// rows that start on 16 bytes.
+cudaError_t launch_realign(const void* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
+                           int64_t ld, int sm_count, cudaStream_t stream);
+
 // A rows x cols fp32 matrix as three bf16 parts whose sum is each value (to
 // 24 bits): the nearest bf16, the nearest to the rest, and to the rest of that.
 cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
@@ -196,6 +202,9 @@ cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t col
 // M <= 128 on one SM a tile of `width` columns; sums are always promoted.
 struct FewShape {
   static constexpr int MAX_ROWS = 128;
+  // As TrainShape::CHUNK; memory bounds this kernel, and one row's loss may be a
+  // small difference of large numbers (1e-6 off with 16, 5e-7 with 4).
+  static constexpr int CHUNK = 4;
   static constexpr int THREADS = TrainShape::THREADS;
   static constexpr int A_BYTES = 128 * 128;  // a k-block of 128 rows, as the MMA reads it
   static constexpr int MAX_STAGES = 12;
