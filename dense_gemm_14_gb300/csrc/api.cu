@@ -631,11 +631,19 @@ int current_sm_count(int* sm_count) {
   return st;
 }
 
-int call_context(CallContext* c) {
+void take_request(CallContext* c) {
   c->fault = t_fault;
   c->wait_limit_ns = t_wait_limit_ns ? t_wait_limit_ns : kWaitTimeoutNs;
   t_fault = kFaultNone;
   t_wait_limit_ns = 0;
+}
+
+void give_request(const CallContext& c) {
+  t_fault = c.fault;
+  t_wait_limit_ns = c.wait_limit_ns;
+}
+
+int call_device(CallContext* c) {
   const DeviceInfo* dev = nullptr;
   const int st = current_device(&dev);
   if (st != GEMM14_OK) return st;

@@ -46,15 +46,19 @@ int take_device_error();
 // The current device's SM count, checked as by every entry point (a gemm14_status).
 int current_sm_count(int* sm_count);
 
-// What a call's own kernels need of the current device and of this thread's
-// pending gemm14_debug_inject request, which the call consumes.
+// What a call's own kernels need: this thread's pending gemm14_debug_inject
+// request, which the call takes at its start, whatever its outcome (take_request;
+// give_request hands it on to the products the call is made of), and the current
+// device (call_device, a gemm14_status).
 struct CallContext {
   int sm_count = 0;
   unsigned* err = nullptr;              // the device error word
   unsigned long long wait_limit_ns = 0;
   int fault = 0;
 };
-int call_context(CallContext* c);
+void take_request(CallContext* c);
+void give_request(const CallContext& c);
+int call_device(CallContext* c);
 
 // A row-major rows x cols matrix of 16-bit elements (pitch ld) as a tensor map
 // of boxes 64 columns wide and box_rows high, 128-byte swizzle, zeros out of range.

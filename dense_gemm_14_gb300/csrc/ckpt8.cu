@@ -526,10 +526,8 @@ int validate_wgrad(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, i
 
 int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void* dY,
              int64_t lddy, float beta, float* dW, int64_t lddw, char* ws, const WgradLayout& l,
-             cudaStream_t stream) {
-  CallContext ctx;
-  int st = call_context(&ctx);
-  if (st != GEMM14_OK) return st;
+             const CallContext& ctx, cudaStream_t stream) {
+  int st;
   const int clusters = train_max_clusters();
   if (clusters <= 0) {
     note_error("gemm14_ckpt8_wgrad: clusters of two CTAs cannot run on this device");
@@ -627,6 +625,8 @@ int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, 
                        int64_t lddy, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,
                        float beta, float* dW, int64_t lddw, void* workspace,
                        size_t workspace_bytes, void* stream_ptr) {
+  CallContext ctx;
+  take_request(&ctx);
   int st = validate_wgrad(dtype, T, N, K, dY, lddy, Q, ldq, S, lds, dW, lddw);
   if (st != GEMM14_OK) return st;
   if (workspace && !aligned(workspace, 16)) return GEMM14_ERR_INVALID_ARG;
@@ -634,8 +634,8 @@ int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, 
   if (T == 0 || N == 0 || K == 0 || alpha == 0.0f)  // no product term: dW = beta dW
     return product_on_stream(dtype, 1, 0, N, K, 0, alpha, nullptr, at_least_one(N), nullptr,
                              at_least_one(K), beta, dW, lddw, nullptr, 0, stream);
-  int sms = 0;
-  if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
+  if ((st = call_device(&ctx)) != GEMM14_OK) return st;
+  const int sms = ctx.sm_count;
   WgradLayout l;
   wgrad_layout(dtype, T, N, K, dY, lddy, dW, lddw, sms, &l);
   if (!workspace || workspace_bytes < l.total) {
@@ -648,7 +648,8 @@ int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, 
   const int kept_as = !l.tc ? GEMM14_DTYPE_F32 : l.parts == 3 ? GEMM14_DTYPE_BF16 : dtype;
   const cudaError_t e = launch_restore(kept_as, Q, ldq, S, lds, X, l.ldx, T, K, sms, stream);
   if (e != cudaSuccess) return finish_launch(e, "ckpt8 restore launch", stream);
-  if (l.tc) return wgrad_tc(dtype, T, N, K, alpha, dY, lddy, beta, dW, lddw, ws, l, stream);
+  if (l.tc) return wgrad_tc(dtype, T, N, K, alpha, dY, lddy, beta, dW, lddw, ws, l, ctx, stream);
+  give_request(ctx);
   return product_on_stream(dtype, 1, 0, N, K, T, alpha, dY, lddy, X, l.ldx, beta, dW, lddw,
                            workspace, l.x_off, stream);
 }

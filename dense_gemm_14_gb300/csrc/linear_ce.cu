@@ -783,21 +783,21 @@ int gemm14_linear_ce_forward(int dtype, int64_t T, int64_t V, int64_t D, const v
                              int64_t ldh, const void* W, int64_t ldw, const int64_t* targets,
                              int64_t ignore_index, float* loss, float* lse, void* workspace,
                              size_t workspace_bytes, void* stream) {
+  CeCall c{dtype,        T, V, D, H, ldh, W, ldw, targets, ignore_index,
+           static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)};
+  take_request(&c.ctx);
   int st = validate_ce(dtype, T, V, D, H, ldh, W, ldw, targets);
   if (st != GEMM14_OK) return st;
   if (T == 0) return GEMM14_OK;
   if (!loss || !lse || !aligned(loss, 4) || !aligned(lse, 4)) return GEMM14_ERR_INVALID_ARG;
-  CeCall c{dtype,        T, V, D, H, ldh, W, ldw, targets, ignore_index,
-           static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)};
-  int sms = 0;
-  if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
-  ce_layout(dtype, T, V, D, H, ldh, W, ldw, false, sms, &c.l);
+  if ((st = call_device(&c.ctx)) != GEMM14_OK) return st;
+  ce_layout(dtype, T, V, D, H, ldh, W, ldw, false, c.ctx.sm_count, &c.l);
   if ((st = check_room("gemm14_linear_ce_forward", workspace, workspace_bytes, c.l.total)) !=
       GEMM14_OK)
     return st;
-  if (!c.l.tc) return c.forward_products(loss, lse);
-  if ((st = call_context(&c.ctx)) != GEMM14_OK) return st;
-  return c.forward_tc(loss, lse);
+  if (c.l.tc) return c.forward_tc(loss, lse);
+  give_request(c.ctx);
+  return c.forward_products(loss, lse);
 }
 
 int gemm14_linear_ce_backward(int dtype, int64_t T, int64_t V, int64_t D, const void* H,
@@ -805,6 +805,9 @@ int gemm14_linear_ce_backward(int dtype, int64_t T, int64_t V, int64_t D, const 
                               int64_t ignore_index, const float* lse, const float* dloss, void* dH,
                               int64_t lddh, void* dW, int64_t lddw, void* workspace,
                               size_t workspace_bytes, void* stream) {
+  CeCall c{dtype,        T, V, D, H, ldh, W, ldw, targets, ignore_index,
+           static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)};
+  take_request(&c.ctx);
   int st = validate_ce(dtype, T, V, D, H, ldh, W, ldw, targets);
   if (st != GEMM14_OK) return st;
   const int eb = elem_bytes_of(dtype);
@@ -813,22 +816,19 @@ int gemm14_linear_ce_backward(int dtype, int64_t T, int64_t V, int64_t D, const 
   if (T > 0 && (!lse || !dloss || !aligned(lse, 4) || !aligned(dloss, 4)))
     return GEMM14_ERR_INVALID_ARG;
   if (!dW && (!dH || T == 0)) return GEMM14_OK;  // nothing is asked for
-  int sms = 0;
-  if ((st = current_sm_count(&sms)) != GEMM14_OK) return st;
-  CeCall c{dtype,        T, V, D, H, ldh, W, ldw, targets, ignore_index,
-           static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)};
+  if ((st = call_device(&c.ctx)) != GEMM14_OK) return st;
   if (T == 0)
     return c.launched(cudaMemset2DAsync(dW, static_cast<size_t>(lddw) * eb, 0,
                                         static_cast<size_t>(D) * eb, static_cast<size_t>(V),
                                         c.stream),
                       "cudaMemset2DAsync");
-  ce_layout(dtype, T, V, D, H, ldh, W, ldw, true, sms, &c.l);
+  ce_layout(dtype, T, V, D, H, ldh, W, ldw, true, c.ctx.sm_count, &c.l);
   if ((st = check_room("gemm14_linear_ce_backward", workspace, workspace_bytes, c.l.total)) !=
       GEMM14_OK)
     return st;
-  if (!c.l.tc) return c.backward_products(lse, dloss, dH, lddh, dW, lddw);
-  if ((st = call_context(&c.ctx)) != GEMM14_OK) return st;
-  return c.backward_tc(lse, dloss, dH, lddh, dW, lddw);
+  if (c.l.tc) return c.backward_tc(lse, dloss, dH, lddh, dW, lddw);
+  give_request(c.ctx);
+  return c.backward_products(lse, dloss, dH, lddh, dW, lddw);
 }
 
 }  // extern "C"
