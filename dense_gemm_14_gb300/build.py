@@ -33,6 +33,7 @@ SOURCES = ["api.cu", "sgemm_simt.cu", "sgemm_small.cu", "hgemm_tc.cu", "hgemm_tc
            "linear_ce.cu", "ckpt8.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "streamk.cuh", "api_internal.h", "plan.h", "checks.h", "train_tc.h",
            "unaligned.cuh",
+           "operand_copy.cuh",
            "libgemm14.map"]
 
 NVCC_FLAGS = [

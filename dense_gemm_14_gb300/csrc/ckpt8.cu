@@ -535,10 +535,8 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   }
   const void* dy = l.copy_dy ? ws + l.dy_off : dY;
   if (l.copy_dy) {
-    const cudaError_t e =
-        l.parts == 3 ? launch_split3(static_cast<const float*>(dY), lddy, T, N, ws + l.dy_off,
-                                     l.lddy, T * l.lddy, ctx.sm_count, stream)
-                     : launch_realign(dY, lddy, T, N, ws + l.dy_off, l.lddy, ctx.sm_count, stream);
+    const OperandCopy job{dY, lddy, T, N, ws + l.dy_off, l.lddy, T * l.lddy, l.parts};
+    const cudaError_t e = launch_operand_copy(job, ctx.sm_count, stream);
     if (e != cudaSuccess) return finish_launch(e, "ckpt8 copy launch", stream);
   }
   TrainArgs a{};

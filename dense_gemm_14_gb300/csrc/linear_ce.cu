@@ -34,10 +34,10 @@
 #include "../../include/gemm14.h"
 #include "api_internal.h"
 #include "kernels.h"
+#include "operand_copy.cuh"
 #include "plan.h"
 #include "ptx.cuh"
 #include "train_tc.h"
-#include "unaligned.cuh"
 
 namespace gemm14 {
 namespace {
@@ -56,13 +56,13 @@ __device__ __forceinline__ ExpSum merge(ExpSum a, ExpSum b) {
 
 // ---- rows in use
 
-// Numbers the rows that take part (in order): *n of them, row i of them from
+// The rows that take part are numbered in order: *n of them, row i of them from
 // row index[i] of the batch, position[t] = i or -1; and their data: the target
 // as a column (-1 where it is no row of W), and for the gradient lse and the
 // coefficient. For 16-bit dZ that is g_t / ref * unit with ref = max |g_t|
 // over the rows that take part: dZ then lies in [-unit, unit] whatever the
 // scale of the objective, and the products are multiplied by *back = ref / unit
-// at the end. One block: 8192 rows a turn, each thread 8 of them.
+// at the end.
 struct Rows {
   int* n;
   float* back;
@@ -72,28 +72,54 @@ struct Rows {
   float* lse;
   float* coef;
 };
+// What numbering reads; g null: the forward pass.
+struct RowsIn {
+  const int64_t* targets;
+  int64_t ignore;
+  const float* lse;
+  const float* g;
+  int64_t T, V;
+  bool relative;
+  float unit;
+};
+
+__device__ __forceinline__ float sound_ref(float ref) {
+  return ref > 0.0f && ref < INFINITY ? ref : 1.0f;
+}
+// The data of row t of the batch, which takes part as row i.
+__device__ __forceinline__ void put_row(const RowsIn& in, const Rows& out, int64_t t, int i,
+                                        int64_t y, float g, float ref) {
+  const bool sound = y >= 0 && y < in.V;
+  out.index[i] = static_cast<int>(t);
+  out.target[i] = sound ? static_cast<int>(y) : -1;
+  if (in.g) {
+    out.lse[i] = in.lse[t];
+    out.coef[i] = sound ? g / ref * in.unit : __uint_as_float(0x7fc00000u);
+  }
+}
+
+// One block: 8192 rows a turn, each thread 8 of them.
 constexpr int kRowsPerThread = 8;
 
-__global__ void __launch_bounds__(1024)
-    ce_rows_kernel(const int64_t* targets, int64_t ignore, const float* lse, const float* g,
-                   int64_t T, int64_t V, bool relative, float unit, Rows out) {
+__global__ void __launch_bounds__(1024) ce_rows_kernel(const RowsIn in, const Rows out) {
   __shared__ int count[kRowsPerThread * 32];
   __shared__ float part[32];
   __shared__ int total;
   grid_dependency_wait();
   grid_launch_dependents();
+  const int64_t T = in.T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float ref = 0.0f;
-  if (relative) {
+  if (in.relative) {
     for (int64_t t = threadIdx.x; t < T; t += 1024)
-      if (targets[t] != ignore) ref = fmaxf(ref, fabsf(g[t]));
+      if (in.targets[t] != in.ignore) ref = fmaxf(ref, fabsf(in.g[t]));
     for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
     if (lane == 0) part[warp] = ref;
     __syncthreads();
     ref = 0.0f;
     for (int w = 0; w < 32; ++w) ref = fmaxf(ref, part[w]);
   }
-  if (!(ref > 0.0f && ref < INFINITY)) ref = 1.0f;
+  ref = sound_ref(ref);
   int base = 0;
   for (int64_t t0 = 0; t0 < T; t0 += 1024 * kRowsPerThread) {
     int64_t y[kRowsPerThread];
@@ -102,12 +128,12 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int j = 0; j < kRowsPerThread; ++j) {
       const int64_t t = t0 + 1024 * j + threadIdx.x;
-      y[j] = t < T ? targets[t] : ignore;
-      k[j] = g && t < T ? g[t] : 1.0f;
+      y[j] = t < T ? in.targets[t] : in.ignore;
+      k[j] = in.g && t < T ? in.g[t] : 1.0f;
     }
 #pragma unroll
     for (int j = 0; j < kRowsPerThread; ++j) {
-      mask[j] = __ballot_sync(0xffffffffu, y[j] != ignore && k[j] != 0.0f);
+      mask[j] = __ballot_sync(0xffffffffu, y[j] != in.ignore && k[j] != 0.0f);
       if (lane == 0) count[32 * j + warp] = __popc(mask[j]);
     }
     __syncthreads();
@@ -136,46 +162,89 @@ __global__ void __launch_bounds__(1024)
       const bool used = (mask[j] >> lane) & 1u;
       const int i = base + count[32 * j + warp] + __popc(mask[j] & ((1u << lane) - 1u));
       out.position[t] = used ? i : -1;
-      if (!used) continue;
-      const bool sound = y[j] >= 0 && y[j] < V;
-      out.index[i] = static_cast<int>(t);
-      out.target[i] = sound ? static_cast<int>(y[j]) : -1;
-      if (g) {
-        out.lse[i] = lse[t];
-        out.coef[i] = sound ? k[j] / ref * unit : __uint_as_float(0x7fc00000u);
-      }
+      if (used) put_row(in, out, t, i, y[j], k[j], ref);
     }
     base += total;
     __syncthreads();
   }
   if (threadIdx.x == 0) {
     *out.n = base;
-    *out.back = ref / unit;
+    *out.back = ref / in.unit;
   }
 }
 
 // The rows of H in use, one after the other (E = float: as three bf16 parts),
 // zeros up to the next multiple of 64 rows (a product over the rows reads whole
-// k-blocks), and zeros into the rows of dH (where given) that take no part.
-// Block b < T: row b of the batch; the 64 after that: rows past the last.
-template <typename E>
+// k-blocks), and zeros into the rows of dH (where given) that take no part; and
+// beside that the first piece of W, where it is copied. Block b < T: row b of the
+// batch; the 64 after that: rows past the last; the rest: W.
+// kNumber: the rows are not numbered yet. Up to 1024 of them each block counts
+// for itself, which takes less than the launch of the kernel that does it once.
+constexpr int kSelfNumbered = 1024;
+
+template <typename E, bool kNumber>
 __global__ void __launch_bounds__(256)
-    ce_gather_kernel(const E* H, int64_t ldh, int64_t T, int64_t D, const int* n,
-                     const int* position, uint16_t* out, int64_t ldo, int64_t part_stride, E* dH,
-                     int64_t lddh, bool vec) {
+    ce_gather_kernel(const E* H, int64_t ldh, int64_t D, const RowsIn in, const Rows rows,
+                     uint16_t* out, int64_t ldo, int64_t part_stride, E* dH, int64_t lddh,
+                     bool vec, const OperandCopy w, int w_blocks) {
+  __shared__ float part[8];
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int kParts = sizeof(E) == 4 ? 3 : 1;
-  const int64_t b = blockIdx.x;
+  const int64_t T = in.T, b = blockIdx.x;
+  if (b >= T + 64) {
+    operand_copy(w, static_cast<int>(b - T - 64), w_blocks);
+    return;
+  }
+  int i = -1, n = 0;
+  if constexpr (kNumber) {
+    int64_t y[4];
+    float g[4], ref = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = threadIdx.x + 256 * j;
+      y[j] = t < T ? in.targets[t] : in.ignore;
+      g[j] = in.g && t < T ? in.g[t] : 1.0f;
+      if (in.relative && y[j] != in.ignore) ref = fmaxf(ref, fabsf(g[j]));
+    }
+    for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ref;
+    bool mine = false;
+    int before = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = threadIdx.x + 256 * j;
+      const bool used = y[j] != in.ignore && g[j] != 0.0f;
+      n += __syncthreads_count(used);
+      before += __syncthreads_count(used && t < b);
+      mine = __syncthreads_or(used && t == b) || mine;
+    }
+    ref = 0.0f;
+    for (int k = 0; k < 8; ++k) ref = fmaxf(ref, part[k]);
+    ref = sound_ref(ref);
+    i = mine ? before : -1;
+    if (threadIdx.x == 0) {
+      if (b < T) {
+        rows.position[b] = i;
+        if (mine) put_row(in, rows, b, i, in.targets[b], in.g ? in.g[b] : 1.0f, ref);
+      }
+      if (b == 0) {
+        *rows.n = n;
+        *rows.back = ref / in.unit;
+      }
+    }
+  } else {
+    n = *rows.n;
+    if (b < T) i = rows.position[b];
+  }
   if (b >= T) {
-    const int64_t r = *n + (b - T);
-    if (r >= (*n + 63) / 64 * 64) return;
+    const int64_t r = n + (b - T);
+    if (r >= (n + 63) / 64 * 64) return;
     for (int p = 0; p < kParts; ++p)
       for (int64_t c = threadIdx.x; c < D; c += blockDim.x)
         out[p * part_stride + r * ldo + c] = 0;
     return;
   }
-  const int i = position[b];
   if (i < 0) {
     if (dH)
       for (int64_t c = threadIdx.x; c < D; c += blockDim.x) dH[b * lddh + c] = E(0);
@@ -509,29 +578,35 @@ struct CeCall {
     return GEMM14_ERR_CUDA;
   }
 
-  // Numbers and gathers the rows in use.
+  // Numbers and gathers the rows in use, and copies the first piece of W where
+  // it has to be.
   int gather(const float* lse, const float* g, void* dH, int64_t lddh) const {
-    const bool relative = g && dtype != GEMM14_DTYPE_F32_3XTF32;
     // fp16's range: dZ is held in units of 2^-15, so that probabilities down
     // to 2^-39 of the largest coefficient are not lost
-    const float unit = dtype == GEMM14_DTYPE_F16 ? 32768.0f : 1.0f;
-    const Rows r = rows();
-    int st = launched(launch_kernel(ce_rows_kernel, dim3(1), dim3(1024), 0, stream, targets,
-                                    ignore, lse, g, T, V, relative, unit, r),
-                      "linear_ce rows launch");
-    if (st != GEMM14_OK) return st;
-    const dim3 grid(static_cast<unsigned>(T + 64)), block(256);
+    const RowsIn in{targets, ignore, lse, g, T, V, g && dtype != GEMM14_DTYPE_F32_3XTF32,
+                    dtype == GEMM14_DTYPE_F16 ? 32768.0f : 1.0f};
+    const bool number = T <= kSelfNumbered;
+    if (!number) {
+      const int st = launched(launch_kernel(ce_rows_kernel, dim3(1), dim3(1024), 0, stream, in,
+                                            rows()),
+                              "linear_ce rows launch");
+      if (st != GEMM14_OK) return st;
+    }
+    const OperandCopy w = w_copy(0, l.copy_w ? std::min(l.C, V) : 0);
+    const int w_blocks = l.copy_w ? operand_copy_blocks(w, ctx.sm_count) : 0;
+    const dim3 grid(static_cast<unsigned>(T + 64 + w_blocks)), block(256);
     uint16_t* out = at<uint16_t>(l.h);
     const int64_t stride = l.rows * l.ldx;
-    const bool vec = tma_rows(H, ldh);
     const cudaError_t e =
         l.parts == 3
-            ? launch_kernel(ce_gather_kernel<float>, grid, block, 0, stream,
-                            static_cast<const float*>(H), ldh, T, D, r.n, r.position, out, l.ldx,
-                            stride, static_cast<float*>(dH), lddh, false)
-            : launch_kernel(ce_gather_kernel<uint16_t>, grid, block, 0, stream,
-                            static_cast<const uint16_t*>(H), ldh, T, D, r.n, r.position, out,
-                            l.ldx, stride, static_cast<uint16_t*>(dH), lddh, vec);
+            ? launch_kernel(number ? ce_gather_kernel<float, true> : ce_gather_kernel<float, false>,
+                            grid, block, 0, stream, static_cast<const float*>(H), ldh, D, in,
+                            rows(), out, l.ldx, stride, static_cast<float*>(dH), lddh, false, w,
+                            w_blocks)
+            : launch_kernel(
+                  number ? ce_gather_kernel<uint16_t, true> : ce_gather_kernel<uint16_t, false>,
+                  grid, block, 0, stream, static_cast<const uint16_t*>(H), ldh, D, in, rows(), out,
+                  l.ldx, stride, static_cast<uint16_t*>(dH), lddh, tma_rows(H, ldh), w, w_blocks);
     return launched(e, "linear_ce gather launch");
   }
 
@@ -541,20 +616,21 @@ struct CeCall {
     return TrainOperand{ws + l.h, l.rows, D, l.ldx, l.parts, l.rows * l.ldx};
   }
 
-  // c rows of W from v0 as an operand, copied or split first where they must be.
+  // The copy of c rows of W from v0 as the products read them.
+  OperandCopy w_copy(int64_t v0, int64_t c) const {
+    return OperandCopy{row_of(W, v0, ldw, eb()), ldw, c, D, ws + l.w, l.ldx, l.C * l.ldx, l.parts};
+  }
+
+  // c rows of W from v0 as an operand, copied or split first where they must be
+  // (the first piece: by gather, where there is one).
   int w_operand(int64_t v0, int64_t c, TrainOperand* w) const {
-    const void* src = row_of(W, v0, ldw, eb());
     if (!l.copy_w) {
-      *w = TrainOperand{src, c, D, ldw, 1, 0};
+      *w = TrainOperand{row_of(W, v0, ldw, eb()), c, D, ldw, 1, 0};
       return GEMM14_OK;
     }
-    void* dst = ws + l.w;
-    *w = TrainOperand{dst, c, D, l.ldx, l.parts, l.C * l.ldx};
-    if (l.parts == 3)
-      return launched(launch_split3(static_cast<const float*>(src), ldw, c, D, dst, l.ldx,
-                                    l.C * l.ldx, ctx.sm_count, stream),
-                      "linear_ce split launch");
-    return launched(launch_realign(src, ldw, c, D, dst, l.ldx, ctx.sm_count, stream),
+    *w = TrainOperand{ws + l.w, c, D, l.ldx, l.parts, l.C * l.ldx};
+    if (v0 == 0 && l.gather) return GEMM14_OK;
+    return launched(launch_operand_copy(w_copy(v0, c), ctx.sm_count, stream),
                     "linear_ce copy launch");
   }
 

@@ -22,9 +22,9 @@
 
 #include "api_internal.h"
 #include "kernels.h"
+#include "operand_copy.cuh"
 #include "ptx.cuh"
 #include "train_tc.h"
-#include "unaligned.cuh"
 
 namespace gemm14 {
 namespace {
@@ -907,68 +907,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// A thread moves 16 bytes, 4 of them in flight; a warp 128 pieces of a row.
-__global__ void __launch_bounds__(256)
-    realign_kernel(const uint16_t* X, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
-                   int64_t ld) {
+__global__ void __launch_bounds__(256) operand_copy_kernel(const OperandCopy job) {
   grid_dependency_wait();
   grid_launch_dependents();
-  constexpr int kUnroll = 4;
-  const int lane = threadIdx.x & 31;
-  const uint16_t* end = X + (rows - 1) * ldx + cols;
-  const int64_t per_row = (cols + 256 * kUnroll - 1) / (256 * kUnroll);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows * per_row;
-       i += warps) {
-    const int64_t r = i / per_row, c0 = (i - r * per_row) * 256 * kUnroll + 8 * lane;
-    const uint16_t* x = X + r * ldx;
-    uint16_t* o = out + r * ld;
-    uint4 v[kUnroll];
-    bool wide[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t c = c0 + 256 * u;
-      wide[u] = c + 8 <= cols && words_inside(x + c, 16, X, end);
-      if (wide[u]) v[u] = load16_any(x + c);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t c = c0 + 256 * u;
-      if (wide[u]) {
-        *reinterpret_cast<uint4*>(o + c) = v[u];
-      } else {
-        for (int j = 0; j < 8 && c + j < cols; ++j) o[c + j] = x[c + j];
-      }
-    }
-  }
-}
-
-// A warp takes 256 columns of a row, 8 loads in flight a lane.
-__global__ void __launch_bounds__(256)
-    split3_kernel(const float* X, int64_t ldx, int64_t rows, int64_t cols, __nv_bfloat16* out,
-                  int64_t ld, int64_t part_stride) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  constexpr int kUnroll = 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t per_row = (cols + 32 * kUnroll - 1) / (32 * kUnroll);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows * per_row;
-       i += warps) {
-    const int64_t r = i / per_row, c0 = (i - r * per_row) * 32 * kUnroll + lane;
-    float x[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      x[u] = c0 + 32 * u < cols ? X[r * ldx + c0 + 32 * u] : 0.0f;
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const __nv_bfloat16 b = __float2bfloat16_rn(x[u]);
-        if (c0 + 32 * u < cols) out[p * part_stride + r * ld + c0 + 32 * u] = b;
-        x[u] -= __bfloat162float(b);
-      }
-  }
+  operand_copy(job, blockIdx.x, gridDim.x);
 }
 
 using TrainKernel = void (*)(const TrainMaps, const TrainArgs);
@@ -1104,22 +1046,9 @@ cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clust
                        dim3(256), 0, stream, args, s, clusters);
 }
 
-cudaError_t launch_realign(const void* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
-                           int64_t ld, int sm_count, cudaStream_t stream) {
-  const int64_t cap = static_cast<int64_t>(sm_count) * 8;
-  const int64_t blocks = (rows * ((cols + 1023) / 1024) + 7) / 8;
-  return launch_kernel(realign_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
-                       dim3(256), 0, stream, static_cast<const uint16_t*>(X), ldx, rows, cols,
-                       static_cast<uint16_t*>(out), ld);
-}
-
-cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
-                          int64_t ld, int64_t part_stride, int sm_count, cudaStream_t stream) {
-  const int64_t cap = static_cast<int64_t>(sm_count) * 8;
-  const int64_t blocks = (rows * ((cols + 255) / 256) + 7) / 8;
-  return launch_kernel(split3_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
-                       dim3(256), 0, stream, X, ldx, rows, cols,
-                       static_cast<__nv_bfloat16*>(out), ld, part_stride);
+cudaError_t launch_operand_copy(const OperandCopy& job, int sm_count, cudaStream_t stream) {
+  return launch_kernel(operand_copy_kernel, dim3(operand_copy_blocks(job, sm_count)), dim3(256), 0,
+                       stream, job);
 }
 
 cudaError_t launch_train_tc(int mode, bool promote, const TrainMaps& maps, const TrainArgs& args,

@@ -188,15 +188,24 @@ cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clust
 // Whether a kTrainOut launch may split tiles (then launch_slots_out follows it).
 bool may_split(const TrainArgs& args, int clusters);
 
-// A rows x cols matrix of 16-bit elements, rows at any address and pitch, to
-// rows that start on 16 bytes.
-cudaError_t launch_realign(const void* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
-                           int64_t ld, int sm_count, cudaStream_t stream);
-
-// A rows x cols fp32 matrix as three bf16 parts whose sum is each value (to
-// 24 bits): the nearest bf16, the nearest to the rest, and to the rest of that.
-cudaError_t launch_split3(const float* X, int64_t ldx, int64_t rows, int64_t cols, void* out,
-                          int64_t ld, int64_t part_stride, int sm_count, cudaStream_t stream);
+// A rows x cols operand to copy (operand_copy.cuh): parts = 1, 16-bit elements
+// at any address and pitch to rows that start on 16 bytes; parts = 3, fp32 values
+// to three bf16 parts, part_stride elements apart. rows = 0: nothing.
+struct OperandCopy {
+  const void* src;
+  int64_t ld_src, rows, cols;
+  void* dst;
+  int64_t ld_dst, part_stride;
+  int parts;
+};
+// Blocks of 256 threads for it, at most 8 an SM.
+inline int operand_copy_blocks(const OperandCopy& j, int sm_count) {
+  const int64_t per_warp = j.parts == 3 ? 256 : 1024;  // columns of a row
+  const int64_t blocks = (j.rows * ((j.cols + per_warp - 1) / per_warp) + 7) / 8;
+  const int64_t cap = static_cast<int64_t>(sm_count) * 8;
+  return static_cast<int>(blocks < cap ? blocks : cap);
+}
+cudaError_t launch_operand_copy(const OperandCopy& job, int sm_count, cudaStream_t stream);
 
 // ---- few rows (train_tc.cu, train_few_kernel): kTrainStats or kTrainGrad with
 // M <= 128 on one SM a tile of `width` columns; sums are always promoted.

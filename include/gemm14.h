@@ -351,7 +351,14 @@ int gemm14_host_synchronize(void);
  * The logits are formed and folded away in pieces of the vocabulary; no buffer
  * of T x V values exists. Each row's statistics are held in fp32.
  * dtype: the element type of H and W and the arithmetic of the products, as
- * for gemm14_gemm_ex (F32, BF16, F16, TF32, F32_3XTF32). loss and lse: T fp32.
+ * for gemm14_gemm_ex (F32, BF16, F16, TF32, F32_3XTF32). F32_3XTF32 here
+ * splits each fp32 value into three bf16 parts (their sum is the value to 24
+ * bits) and sums the six products of parts above 2^-24 of the whole: the fp32
+ * bound, at tensor-core speed; an infinite input gives NaN. Sums of more than
+ * 1024 terms whose result is fp32 (losses, fp32 gradients, gemm14_ckpt8_wgrad)
+ * leave the tensor cores' accumulators every 1024 terms and are carried in
+ * fp32 registers, as the accumulators add with truncation.
+ * loss and lse: T fp32.
  * targets: T int64 on the device. A row whose target is ignore_index takes no
  * part: its loss and lse are 0 and nothing its row of H holds is used. Any
  * other target outside [0, V) gives a loss of NaN. A NaN or infinity among a
@@ -427,8 +434,9 @@ int gemm14_ckpt8_restore(int dtype, int64_t rows, int64_t cols, const int8_t* Q,
  * dY a T x N matrix (pitch lddy) of dtype, X the T x K values that Q and S
  * (pitches ldq, lds, as written by gemm14_ckpt8_save) stand for, dW an N x K
  * fp32 matrix (pitch lddw). dtype selects dY's element type and the product's
- * arithmetic as for gemm14_gemm_ex; with 16-bit types X enters the product
- * exactly (F16: rounded where it leaves fp16's range) and sums are fp32.
+ * arithmetic as for gemm14_linear_ce_forward; with 16-bit types and F32_3XTF32
+ * X enters the product exactly (F16: rounded where it leaves fp16's range) and
+ * sums are fp32.
  * beta == 0: dW is not read; alpha == 0 or T == 0: dY and the checkpoint are
  * not read. workspace: as for the *_ws calls, but needed:
  * gemm14_ckpt8_wgrad_workspace_bytes(...) bytes at least.

@@ -126,6 +126,23 @@ def test_fp32_modes(T, V, D, mode):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,V,D", [(5, 300, 64), (257, 1031, 136)])
+def test_tf32_mode(T, V, D):
+    """TF32's bound, 4e-3 of |h||w|, in place of fp32's in the logits and in each product."""
+    h, w, y, up = make(T, V, D, "f32", T + V + D)
+    r = reference(h, w, y, up)
+    loss, lse, dh, dw = both(on_gpu(h), on_gpu(w), y.cuda(), up.cuda(), "f32", "tf32")
+    d = 4e-3 * (h.double().abs() @ w.double().abs().t()).amax(dim=1)
+    for got, want in ((loss, r["loss"]), (lse, r["lse"])):
+        assert bool(((got.cpu().double() - want).abs() <= 2 * d + 1e-4).all())
+    p = torch.exp(h.double() @ w.double().t() - r["lse"].unsqueeze(1)) * up.double().unsqueeze(1)
+    e = p * torch.expm1(2 * d + 1e-4).unsqueeze(1) + 4e-3 * r["dz"].abs()
+    e = e + 4e-3 * e
+    assert bool(((dh.cpu().double() - r["dh"]).abs() <= e @ r["w"].abs() + 1e-30).all())
+    assert bool(((dw.cpu().double() - r["dw"]).abs() <= e.t() @ r["h"].abs() + 1e-30).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("hp,ho,wp,wo", [(1, 0, 0, 0), (0, 0, 1, 0), (3, 1, 5, 1), (8, 8, 16, 8),
                                          (0, 2, 0, 3)])
