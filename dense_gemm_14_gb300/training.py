@@ -8,7 +8,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from .api import _CODE, _FP32_MODES, _workspace
+from .api import _CODE, _FP32_MODES, _workspace, _workspaces
 
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -36,6 +36,19 @@ def _on(stream, device: torch.device, body):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
         return body(stream.cuda_stream)
+
+
+def _in_workspace(device: torch.device, handle: int, call, need, where: str) -> None:
+    """call(workspace pointer, bytes) on the stream's workspace as it is; where
+    it is refused, on one of need() bytes (asked for only then)."""
+    ws = _workspaces.get((device.index, handle))
+    if ws is not None and call(ws.data_ptr(), ws.numel()) == _lib.GEMM14_OK:
+        return
+    n = need()
+    ws = _workspace(device, handle, n) if n else None
+    status = call(ws.data_ptr() if n else None, ws.numel() if n else 0)
+    if status:
+        raise _lib.Gemm14Error(status, where)
 
 
 def _matrix(x: torch.Tensor, name: str, device: torch.device | None = None) -> int:
@@ -89,15 +102,19 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
 
     def body(handle):
-        out = torch.empty((2, T), dtype=torch.float32, device=h.device)
+        loss = torch.empty(T, dtype=torch.float32, device=h.device)
+        lse = torch.empty(T, dtype=torch.float32, device=h.device)
         if T:
-            n = _lib.linear_ce_workspace_bytes(code, 0, T, V, D, h.data_ptr(), ldh, w.data_ptr(),
-                                               ldw)
-            ws = _workspace(h.device, handle, n)
-            _lib.linear_ce_forward(code, T, V, D, h.data_ptr(), ldh, w.data_ptr(), ldw,
-                                   targets.data_ptr(), int(ignore_index), out.data_ptr(),
-                                   out.data_ptr() + 4 * T, ws.data_ptr(), ws.numel(), handle)
-        return out[0], out[1]
+            hp, wp = h.data_ptr(), w.data_ptr()
+            _in_workspace(
+                h.device, handle,
+                lambda ws, n: _lib.linear_ce_forward(code, T, V, D, hp, ldh, wp, ldw,
+                                                     targets.data_ptr(), int(ignore_index),
+                                                     loss.data_ptr(), lse.data_ptr(), ws, n, handle,
+                                                     check=False),
+                lambda: _lib.linear_ce_workspace_bytes(code, 0, T, V, D, hp, ldh, wp, ldw),
+                "gemm14_linear_ce_forward")
+        return loss, lse
 
     return _on(stream, h.device, body)
 
@@ -120,13 +137,15 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor, targets: tor
         dh = torch.empty((T, D), dtype=h.dtype, device=h.device) if need_dh else None
         dw = torch.empty((V, D), dtype=w.dtype, device=w.device) if need_dw else None
         if need_dw or (need_dh and T):
-            n = _lib.linear_ce_workspace_bytes(code, 1, T, V, D, h.data_ptr(), ldh, w.data_ptr(),
-                                               ldw) if T else 0
-            ws = _workspace(h.device, handle, n) if n else None
-            _lib.linear_ce_backward(code, T, V, D, _ptr(h), ldh, w.data_ptr(), ldw, _ptr(targets),
-                                    int(ignore_index), _ptr(lse), _ptr(dloss), _ptr(dh), D,
-                                    _ptr(dw), D, ws.data_ptr() if n else None,
-                                    ws.numel() if n else 0, handle)
+            hp, wp = _ptr(h), w.data_ptr()
+            _in_workspace(
+                h.device, handle,
+                lambda ws, n: _lib.linear_ce_backward(code, T, V, D, hp, ldh, wp, ldw, _ptr(targets),
+                                                      int(ignore_index), _ptr(lse), _ptr(dloss),
+                                                      _ptr(dh), D, _ptr(dw), D, ws, n, handle,
+                                                      check=False),
+                lambda: _lib.linear_ce_workspace_bytes(code, 1, T, V, D, hp, ldh, wp, ldw),
+                "gemm14_linear_ce_backward")
         return dh, dw
 
     return _on(stream, h.device, body)
@@ -220,11 +239,14 @@ def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = Non
         lddw = _matrix(dw, "out", dy.device)
         if not dw.numel():
             return dw
-        n = _lib.ckpt8_wgrad_workspace_bytes(code, T, N, K, _ptr(dy), lddy, dw.data_ptr(), lddw)
-        ws = _workspace(dy.device, handle, n) if n else None
-        _lib.ckpt8_wgrad(code, T, N, K, float(alpha), _ptr(dy), lddy, _ptr(c.q), ldq,
-                         _ptr(c.scale), lds, float(beta), dw.data_ptr(), lddw,
-                         ws.data_ptr() if n else None, ws.numel() if n else 0, handle)
+        _in_workspace(
+            dy.device, handle,
+            lambda ws, n: _lib.ckpt8_wgrad(code, T, N, K, float(alpha), _ptr(dy), lddy, _ptr(c.q),
+                                           ldq, _ptr(c.scale), lds, float(beta), dw.data_ptr(),
+                                           lddw, ws, n, handle, check=False),
+            lambda: _lib.ckpt8_wgrad_workspace_bytes(code, T, N, K, _ptr(dy), lddy, dw.data_ptr(),
+                                                     lddw),
+            "gemm14_ckpt8_wgrad")
         return dw
 
     return _on(stream, dy.device, body)
