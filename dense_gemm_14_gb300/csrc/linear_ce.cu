@@ -109,9 +109,23 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const RowsIn in, const Ro
   grid_launch_dependents();
   const int64_t T = in.T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t y[kRowsPerThread];
+  float k[kRowsPerThread];
+  const auto load = [&](int64_t t0) {
+#pragma unroll
+    for (int j = 0; j < kRowsPerThread; ++j) {
+      const int64_t t = t0 + 1024 * j + threadIdx.x;
+      y[j] = t < T ? in.targets[t] : in.ignore;
+      k[j] = in.g && t < T ? in.g[t] : 1.0f;
+    }
+  };
+  load(0);  // (all there is, for most batches)
   float ref = 0.0f;
   if (in.relative) {
-    for (int64_t t = threadIdx.x; t < T; t += 1024)
+#pragma unroll
+    for (int j = 0; j < kRowsPerThread; ++j)
+      if (y[j] != in.ignore) ref = fmaxf(ref, fabsf(k[j]));
+    for (int64_t t = 1024 * kRowsPerThread + threadIdx.x; t < T; t += 1024)
       if (in.targets[t] != in.ignore) ref = fmaxf(ref, fabsf(in.g[t]));
     for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
     if (lane == 0) part[warp] = ref;
@@ -122,15 +136,8 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const RowsIn in, const Ro
   ref = sound_ref(ref);
   int base = 0;
   for (int64_t t0 = 0; t0 < T; t0 += 1024 * kRowsPerThread) {
-    int64_t y[kRowsPerThread];
-    float k[kRowsPerThread];
+    if (t0 > 0) load(t0);
     unsigned mask[kRowsPerThread];
-#pragma unroll
-    for (int j = 0; j < kRowsPerThread; ++j) {
-      const int64_t t = t0 + 1024 * j + threadIdx.x;
-      y[j] = t < T ? in.targets[t] : in.ignore;
-      k[j] = in.g && t < T ? in.g[t] : 1.0f;
-    }
 #pragma unroll
     for (int j = 0; j < kRowsPerThread; ++j) {
       mask[j] = __ballot_sync(0xffffffffu, y[j] != in.ignore && k[j] != 0.0f);
@@ -302,8 +309,11 @@ __global__ void __launch_bounds__(1024)
   }
   sums[warp][lane] = s;
   __syncthreads();
+  for (int half = 16; half >= 1; half /= 2) {
+    if (warp < half) sums[warp][lane] = s = merge(s, sums[warp + half][lane]);
+    __syncthreads();
+  }
   if (warp != 0 || t >= T) return;
-  for (int w = 1; w < 32; ++w) s = merge(s, sums[w][lane]);
   const float total = s.m + logf(s.l);
   lse[t] = i < 0 ? 0.0f : total;
   loss[t] = i < 0 ? 0.0f

@@ -108,7 +108,7 @@ __host__ __device__ inline TilePlan plan_tiles(int tiles, int kblocks, int units
     if (s > 64) s = 64;
     if (s < 2) continue;
     const int time = 1000 * waves / s + 10 * s;
-    if (time < best_time) {
+    if (time < best_time - 30) {
       best_time = time;
       best = s;
     }
