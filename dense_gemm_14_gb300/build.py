@@ -30,10 +30,12 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cu", "sgemm_simt.cu", "sgemm_small.cu", "hgemm_tc.cu", "hgemm_tc2.cu",
            "sgemm_tc3.cu", "epilogue.cu", "host_path.cu", "copy.cu", "plan.cu",
            "train_tc.cu",
-           "linear_ce.cu", "ckpt8.cu"]
+           "linear_ce.cu",
+           "linear_ce_narrow.cu", "ckpt8.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "streamk.cuh", "api_internal.h", "plan.h", "checks.h", "train_tc.h",
            "unaligned.cuh",
            "operand_copy.cuh",
+           "linear_ce_narrow.h",
            "libgemm14.map"]
 
 NVCC_FLAGS = [

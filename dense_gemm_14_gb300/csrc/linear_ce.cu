@@ -34,6 +34,7 @@
 #include "../../include/gemm14.h"
 #include "api_internal.h"
 #include "kernels.h"
+#include "linear_ce_narrow.h"
 #include "operand_copy.cuh"
 #include "plan.h"
 #include "ptx.cuh"
@@ -443,7 +444,14 @@ int64_t piece_rows(int64_t V, int64_t per_row) {
   return pieces == 1 ? V : round_up((V + pieces - 1) / pieces, 256);
 }
 
+// Whether a handful of rows run on the CUDA cores (linear_ce_narrow.cu): fp32
+// ones, in the modes that keep the fp32 bound.
+bool on_cuda_cores(int dtype, int64_t T) {
+  return (dtype == GEMM14_DTYPE_F32 || dtype == GEMM14_DTYPE_F32_3XTF32) && T <= kNarrowRows;
+}
+
 struct CeLayout {
+  bool narrow = false;
   bool tc = false;
   int64_t C = 0;       // vocabulary rows of a piece
   int64_t ldz = 0;     // pitch of the logits or of dZ
@@ -467,6 +475,7 @@ int64_t stat_parts(bool few, int64_t c, int sms) {
 void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
                const void* W, int64_t ldw, bool backward, int sms, CeLayout* l) {
   *l = CeLayout{};
+  l->narrow = on_cuda_cores(dtype, T);
   l->tc = on_tensor_cores(dtype);
   l->ldx = round_up(D, 8);
   l->rows = round_up(T, 256);
@@ -477,6 +486,18 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
     return here;
   };
   const size_t t4 = static_cast<size_t>(T) * 4;
+  if (l->narrow) {
+    l->ldz = V;
+    if (backward) {
+      l->z = take(static_cast<size_t>(T) * l->ldz * 4);
+      l->slots = take(static_cast<size_t>(narrow_splits(static_cast<int>(T), V, D, sms)) * T * D * 4);
+    } else {
+      l->part = take(static_cast<size_t>(narrow_blocks(V, sms)) * T * sizeof(float2));
+      l->state = take(t4);
+    }
+    l->total = at;
+    return;
+  }
   if (l->tc) {
     l->ldx = round_up(D, 64);  // rows that start on 128-byte lines
     l->parts = dtype == GEMM14_DTYPE_F32_3XTF32 ? 3 : 1;
@@ -488,7 +509,7 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
     if (l->copy_w) per_row = std::max(per_row, l->ldx * 2 * l->parts);
     l->C = per_row ? piece_rows(V, per_row) : V;
     l->ldz = round_up(l->C, 64);
-    l->few = l->parts == 1 && T <= FewShape::MAX_ROWS;
+    l->few = T <= FewShape::MAX_ROWS;
     if (l->gather) {
       l->counts = take(256);
       l->index = take(t4);
@@ -672,22 +693,73 @@ struct CeCall {
 
   int64_t parts_of(int64_t c) const { return stat_parts(l.few, c, ctx.sm_count); }
 
-  // A product of few rows (its arguments in *a) with c rows of W.
-  int run_few(int mode, const TrainOperand& w, const TrainArgs& a) {
-    const TrainOperand h = h_operand();
+  // A product of few rows with c rows of W, its arguments in a.
+  int run_few(int mode, const TrainOperand& w, TrainArgs a) {
+    TrainMaps maps;
     const int width = few_width(a.N, ctx.sm_count);
-    CUtensorMap map_h, map_w;
-    int st = map_16bit(&map_h, bf16(), h.base, h.rows, h.cols, h.ld, few_rows(T));
-    if (st == GEMM14_OK) st = map_16bit(&map_w, bf16(), w.base, w.rows, w.cols, w.ld, width);
+    const int st = train_operands(bf16(), h_operand(), false, w, false, &maps, &a, few_rows(T),
+                                  width);
     if (st != GEMM14_OK) return st;
     ctx.fault = kFaultNone;
-    return launched(launch_train_few(mode, map_h, map_w, a, bf16(), width, ctx.sm_count, stream),
+    return launched(launch_train_few(mode, maps, a, bf16(), width, ctx.sm_count, stream),
                     "linear_ce few rows launch");
   }
 
   // Whether sums over K are carried in fp32 registers: what is written in fp32
   // keeps fp32's accuracy; what is rounded to 16 bits loses nothing by TMEM's.
   bool long_sum(int64_t K) const { return K > TrainShape::CHUNK * TrainShape::BK; }
+
+  // ---- a handful of rows
+
+  NarrowArgs narrow_args() const {
+    NarrowArgs a{};
+    a.T = static_cast<int>(T);
+    a.V = V;
+    a.D = D;
+    a.H = static_cast<const float*>(H);
+    a.ldh = ldh;
+    a.W = static_cast<const float*>(W);
+    a.ldw = ldw;
+    a.targets = targets;
+    a.ignore = ignore;
+    return a;
+  }
+
+  int forward_narrow(float* loss, float* lse) const {
+    NarrowArgs a = narrow_args();
+    a.part = at<float2>(l.part);
+    a.part_ld = T;
+    a.target_logit = at<float>(l.state);
+    const int st = launched(launch_narrow_stats(a, ctx.sm_count, stream),
+                            "linear_ce narrow launch");
+    if (st != GEMM14_OK) return st;
+    return combine(a.part, T, narrow_blocks(V, ctx.sm_count), a.target_logit, nullptr, loss, lse);
+  }
+
+  int backward_narrow(const float* lse, const float* g, void* dH, int64_t lddh, void* dW,
+                      int64_t lddw) const {
+    NarrowArgs a = narrow_args();
+    a.lse = lse;
+    a.dloss = g;
+    a.dz = at<float>(l.z);
+    a.ldz = l.ldz;
+    a.sums = at<float>(l.slots);
+    a.dH = static_cast<float*>(dH);
+    a.lddh = lddh;
+    a.dW = static_cast<float*>(dW);
+    a.lddw = lddw;
+    return launched(launch_narrow_backward(a, ctx.sm_count, stream), "linear_ce narrow launch");
+  }
+
+  // The rows' parts to loss and lse.
+  int combine(const float2* part, int64_t part_ld, int64_t parts, const float* target_logit,
+              const int* position, float* loss, float* lse) const {
+    return launched(
+        launch_kernel(ce_combine_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(1024),
+                      0, stream, part, part_ld, static_cast<int>(parts), target_logit, position,
+                      targets, ignore, T, V, loss, lse),
+        "linear_ce combine launch");
+  }
 
   int forward_tc(float* loss, float* lse) {
     int st = prepare_tc();
@@ -712,12 +784,8 @@ struct CeCall {
       if (st != GEMM14_OK) return st;
       parts = v0 / l.C * parts_of(l.C) + parts_of(c);
     }
-    return launched(
-        launch_kernel(ce_combine_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(1024),
-                      0, stream, at<float2>(l.part), l.rows, static_cast<int>(parts),
-                      at<float>(l.state), l.gather ? r.position : nullptr, targets, ignore, T, V,
-                      loss, lse),
-        "linear_ce combine launch");
+    return combine(at<float2>(l.part), l.rows, parts, at<float>(l.state),
+                   l.gather ? r.position : nullptr, loss, lse);
   }
 
   int backward_tc(const float* lse, const float* g, void* dH, int64_t lddh, void* dW,
@@ -881,6 +949,7 @@ int gemm14_linear_ce_forward(int dtype, int64_t T, int64_t V, int64_t D, const v
   if ((st = check_room("gemm14_linear_ce_forward", workspace, workspace_bytes, c.l.total)) !=
       GEMM14_OK)
     return st;
+  if (c.l.narrow) return c.forward_narrow(loss, lse);
   if (c.l.tc) return c.forward_tc(loss, lse);
   give_request(c.ctx);
   return c.forward_products(loss, lse);
@@ -912,6 +981,7 @@ int gemm14_linear_ce_backward(int dtype, int64_t T, int64_t V, int64_t D, const 
   if ((st = check_room("gemm14_linear_ce_backward", workspace, workspace_bytes, c.l.total)) !=
       GEMM14_OK)
     return st;
+  if (c.l.narrow) return c.backward_narrow(lse, dloss, dH, lddh, dW, lddw);
   if (c.l.tc) return c.backward_tc(lse, dloss, dH, lddh, dW, lddw);
   give_request(c.ctx);
   return c.backward_products(lse, dloss, dH, lddh, dW, lddw);

@@ -142,7 +142,25 @@ __device__ __forceinline__ void stage_out16(const TrainArgs& args, uint32_t buf,
                                             int row0, int rows, int64_t col0, int n_cols,
                                             int lane) {
   const int64_t ld = args.ld_out;
-  const bool vec = args.out_vec != 0;
+  if (!args.out_vec) {
+    // rows at any address: a row at a time, lanes on neighbouring elements
+#pragma unroll 4
+    for (int r = 0; r < 32; ++r) {
+      if (row0 + r >= rows) break;
+      uint16_t* to = out + static_cast<int64_t>(row0 + r) * ld + col0;
+#pragma unroll
+      for (int c = lane; c < 64; c += 32) {
+        if (c >= n_cols || !out_ok(args, row0 + r, col0 + c, 1)) continue;
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(v)
+                     : "r"(stage_at(buf, r, c >> 3) + 2 * (c & 7))
+                     : "memory");
+        to[c] = v;
+      }
+    }
+    return;
+  }
   const int p = lane & 7;
 #pragma unroll
   for (int g = 0; g < 8; ++g) {
@@ -151,7 +169,7 @@ __device__ __forceinline__ void stage_out16(const TrainArgs& args, uint32_t buf,
     const uint4 v = stage_get(stage_at(buf, r, p));
     uint16_t* to = out + static_cast<int64_t>(row0 + r) * ld + col0 + p * 8;
     if (!out_ok(args, row0 + r, col0 + p * 8, min(8, n_cols - p * 8))) continue;
-    if (vec && (p + 1) * 8 <= n_cols) {
+    if ((p + 1) * 8 <= n_cols) {
       *reinterpret_cast<uint4*>(to) = v;
     } else {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -654,6 +672,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
 // SMs, where 128 of 256 on 76 pairs are 1.7 waves). With B on the MMA's M side
 // (N = 16 for one row) a k-block took 0.33 us whatever its height, N that small
 // leaving the tensor cores waiting: 268 MB of weights took 62 us.
+// Split operands: a stage holds a k-block of one part of B and of the parts of A
+// that it meets (part p: the first 3 - p), so that B's parts are read once each.
 struct FewSmem {
   uint64_t full[FewShape::MAX_STAGES];
   uint64_t empty[FewShape::MAX_STAGES];
@@ -669,10 +689,9 @@ struct FewTiles {
   int width, rows, stages, quarters;  // quarters: of the 128 rows that are looked at
 };
 
-template <int kMode>
+template <int kMode, int kParts>
 __global__ void __launch_bounds__(FewShape::THREADS, 1)
-    train_few_kernel(const __grid_constant__ CUtensorMap map_a,
-                     const __grid_constant__ CUtensorMap map_b, const TrainArgs args,
+    train_few_kernel(const __grid_constant__ TrainMaps maps, const TrainArgs args,
                      const FewTiles few) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align1024(smem_raw);
@@ -681,7 +700,8 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t b_bytes = static_cast<uint32_t>(few.width) * 128u;
-  const uint32_t stage_bytes = b_bytes + static_cast<uint32_t>(few.rows) * 128u;
+  const uint32_t a_bytes = static_cast<uint32_t>(few.rows) * 128u;
+  const uint32_t stage_bytes = b_bytes + kParts * a_bytes;
   const uint32_t stages = static_cast<uint32_t>(few.stages);
   const int tiles = (args.N + few.width - 1) / few.width;
   const int kblocks = (args.K + S::BK - 1) / S::BK;
@@ -701,8 +721,8 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&map_a);
-    tma_prefetch_desc(&map_b);
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
   }
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, S::TMEM_COLS);
@@ -722,18 +742,24 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
       bool ok = true;
       uint32_t s = 0, ph = 0;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int kb = 0; kb < kblocks; ++kb, ++prod_it) {
-          if (!mbar_wait(&sm.empty[s], ph ^ 1, wc)) { ok = false; break; }
-          // Failure-detection tests: the first stage is never loaded.
-          if (!(args.fault == kFaultSkipFirstStage && prod_it == 0)) {
-            uint8_t* st = ring + s * stage_bytes;
-            mbar_arrive_expect_tx(&sm.full[s], stage_bytes);
-            tma_load_2d(st, &map_b, kb * S::BK, t * few.width, &sm.full[s]);
-            tma_load_2d(st + b_bytes, &map_a, kb * S::BK, 0, &sm.full[s]);
-          }
-          if (++s == stages) {
-            s = 0;
-            ph ^= 1;
+        for (int k0 = 0; k0 < kblocks && ok; k0 += FewShape::CHUNK) {
+          const int k1 = min(k0 + FewShape::CHUNK, kblocks);
+          for (int p = kParts - 1; p >= 0 && ok; --p) {
+            for (int kb = k0; kb < k1; ++kb, ++prod_it) {
+              if (!mbar_wait(&sm.empty[s], ph ^ 1, wc)) { ok = false; break; }
+              // Failure-detection tests: the first stage is never loaded.
+              if (!(args.fault == kFaultSkipFirstStage && prod_it == 0)) {
+                uint8_t* st = ring + s * stage_bytes;
+                mbar_arrive_expect_tx(&sm.full[s], b_bytes + (kParts - p) * a_bytes);
+                tma_load_2d(st, &maps.b[p], kb * S::BK, t * few.width, &sm.full[s]);
+                for (int a = 0; a < kParts - p; ++a)
+                  tma_load_2d(st + b_bytes + a * a_bytes, &maps.a[a], kb * S::BK, 0, &sm.full[s]);
+              }
+              if (++s == stages) {
+                s = 0;
+                ph ^= 1;
+              }
+            }
           }
         }
       }
@@ -749,21 +775,27 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
           const int b = unit & 1;
           if (!mbar_wait(&sm.acc_empty[b], ((unit >> 1) & 1) ^ 1, wc)) { ok = false; break; }
           tc_fence_after_sync();
-          for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait(&sm.full[s], ph, wc)) { ok = false; break; }
-            tc_fence_after_sync();
-            const uint32_t b_addr = smem_u32(ring + s * stage_bytes);
+          bool add = false;
+          for (int p = kParts - 1; p >= 0 && ok; --p) {
+            for (int kb = k0; kb < k1; ++kb) {
+              if (!mbar_wait(&sm.full[s], ph, wc)) { ok = false; break; }
+              tc_fence_after_sync();
+              const uint32_t b_addr = smem_u32(ring + s * stage_bytes);
+              for (int a = kParts - 1 - p; a >= 0; --a) {
 #pragma unroll
-            for (int kk = 0; kk < S::BK / 16; ++kk)
-              tc_mma_f16(tmem_base + static_cast<uint32_t>(b * S::BN),
-                         smem_desc_sw128(b_addr + b_bytes + kk * 32, 16, 1024),
-                         smem_desc_sw128(b_addr + kk * 32, 16, 1024), args.idesc,
-                         kb > k0 || kk != 0);
-            mma_issued = true;
-            tc_commit(&sm.empty[s]);
-            if (++s == stages) {
-              s = 0;
-              ph ^= 1;
+                for (int kk = 0; kk < S::BK / 16; ++kk) {
+                  tc_mma_f16(tmem_base + static_cast<uint32_t>(b * S::BN),
+                             smem_desc_sw128(b_addr + b_bytes + a * a_bytes + kk * 32, 16, 1024),
+                             smem_desc_sw128(b_addr + kk * 32, 16, 1024), args.idesc, add);
+                  add = true;
+                }
+              }
+              mma_issued = true;
+              tc_commit(&sm.empty[s]);
+              if (++s == stages) {
+                s = 0;
+                ph ^= 1;
+              }
             }
           }
           if (!ok) break;
@@ -964,7 +996,7 @@ int train_max_clusters() {
 }
 
 int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOperand& B, bool b_mn,
-                   TrainMaps* maps, TrainArgs* args) {
+                   TrainMaps* maps, TrainArgs* args, int a_rows, int b_rows) {
   const auto encode = [&](const TrainOperand& x, bool mn, int box_rows, CUtensorMap* m) {
     for (int p = 0; p < 3; ++p) {
       if (p >= x.parts) {
@@ -977,8 +1009,8 @@ int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOpera
     }
     return 0;
   };
-  int st = encode(A, a_mn, 128, maps->a);
-  if (st == 0) st = encode(B, b_mn, args->width / 2, maps->b);
+  int st = encode(A, a_mn, a_rows ? a_rows : 128, maps->a);
+  if (st == 0) st = encode(B, b_mn, b_rows ? b_rows : args->width / 2, maps->b);
   if (st != 0) return st;
   // Terms of split operands, small ones first: of 3 x 3 parts the six whose
   // product is above 2^-24 of the whole, or A's three parts against one B.
@@ -1006,26 +1038,28 @@ int few_width(int64_t N, int sms) {
 
 int few_rows(int64_t M) { return M <= 16 ? 16 : static_cast<int>((M + 31) / 32 * 32); }
 
-cudaError_t launch_train_few(int mode, const CUtensorMap& map_a, const CUtensorMap& map_b,
-                             TrainArgs args, bool bf16, int width, int sm_count,
-                             cudaStream_t stream) {
+cudaError_t launch_train_few(int mode, const TrainMaps& maps, TrainArgs args, bool bf16, int width,
+                             int sm_count, cudaStream_t stream) {
   FewTiles few{};
   few.width = width;
   few.rows = few_rows(args.M);
-  const int stage = (few.width + few.rows) * 128;
+  const int parts = args.terms == 6 ? 3 : 1;
+  const int stage = (few.width + parts * few.rows) * 128;
   // the last stage's MMAs read 128 rows' bytes of A, however many were loaded
   few.stages = (FewShape::RING_BYTES - (FewShape::A_BYTES - few.rows * 128)) / stage;
   if (few.stages > FewShape::MAX_STAGES) few.stages = FewShape::MAX_STAGES;
   // dZ is read in k-blocks of 64 rows by the product over them
   few.quarters = mode == kTrainGrad ? (args.M + 63) / 64 * 2 : (args.M + 31) / 32;
   args.idesc = idesc_f16_f32acc(bf16, 128, width, false, false);
-  const auto kernel = mode == kTrainGrad ? train_few_kernel<kTrainGrad> : train_few_kernel<kTrainStats>;
-  static DeviceOnce once[2];
-  const cudaError_t e = set_smem_once(once[mode == kTrainGrad], kernel, FewShape::SMEM_BYTES);
+  const bool grad = mode == kTrainGrad;
+  const auto kernel = parts == 3 ? (grad ? train_few_kernel<kTrainGrad, 3> : train_few_kernel<kTrainStats, 3>)
+                                 : (grad ? train_few_kernel<kTrainGrad, 1> : train_few_kernel<kTrainStats, 1>);
+  static DeviceOnce once[2][2];
+  const cudaError_t e = set_smem_once(once[grad][parts == 3], kernel, FewShape::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int tiles = (args.N + width - 1) / width;
   return launch_kernel(kernel, dim3(tiles < sm_count ? tiles : sm_count), dim3(FewShape::THREADS),
-                       FewShape::SMEM_BYTES, stream, map_a, map_b, args, few);
+                       FewShape::SMEM_BYTES, stream, maps, args, few);
 }
 
 bool may_split(const TrainArgs& args, int clusters) {

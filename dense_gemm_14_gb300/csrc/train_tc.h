@@ -165,8 +165,9 @@ struct TrainOperand {
 // b_mn), and the terms, instruction descriptor and a_mn / b_mn of *args, whose
 // width is set.
 // Returns a gemm14_status.
+// a_rows, b_rows: of the K-major operands' boxes (0: a CTA's of a pair).
 int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOperand& B, bool b_mn,
-                   TrainMaps* maps, TrainArgs* args);
+                   TrainMaps* maps, TrainArgs* args, int a_rows = 0, int b_rows = 0);
 
 // What follows a launch with slots: out[r] = alpha * *scale * (sum of row r's
 // slots) + beta * out[r], for the rows in use (all: of every tile; otherwise of
@@ -226,10 +227,9 @@ struct FewShape {
 int few_width(int64_t N, int sms);
 // A's k-blocks are loaded with `rows` rows (16, or a multiple of 32 that holds M).
 int few_rows(int64_t M);
-// map_a: boxes of 64 k x few_rows(M) rows; map_b: 64 k x width rows, both K-major.
-cudaError_t launch_train_few(int mode, const CUtensorMap& map_a, const CUtensorMap& map_b,
-                             TrainArgs args, bool bf16, int width, int sm_count,
-                             cudaStream_t stream);
+// maps.a: boxes of 64 k x few_rows(M) rows; maps.b: 64 k x width rows, both K-major.
+cudaError_t launch_train_few(int mode, const TrainMaps& maps, TrainArgs args, bool bf16, int width,
+                             int sm_count, cudaStream_t stream);
 
 // promote: sums leave the accumulators for fp32 registers every CHUNK k-blocks.
 cudaError_t launch_train_tc(int mode, bool promote, const TrainMaps& maps, const TrainArgs& args,

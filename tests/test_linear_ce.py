@@ -100,7 +100,8 @@ def both(h, w, y, up, dtype, mode=None, **kw):
 
 SIZES = [(1, 1, 1), (1, 7, 3), (2, 256, 8), (3, 255, 64), (5, 257, 65), (61, 1000, 200),
          (128, 512, 72), (129, 300, 128), (257, 1031, 136), (300, 4099, 96), (1023, 770, 40),
-         (16, 40000, 64)]
+         (16, 40000, 64), (7, 5000, 1000), (8, 333, 4104), (13, 4000, 777), (32, 2049, 2050),
+         (31, 100, 6000), (4, 70, 12000)]
 
 
 @pytest.mark.gpu
