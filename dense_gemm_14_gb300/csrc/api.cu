@@ -824,7 +824,7 @@ int gemm14_debug_inject(int fault, uint64_t wait_limit_ns) {
   return GEMM14_OK;
 }
 
-int gemm14_version(void) { return 200; }
+int gemm14_version(void) { return 210; }
 
 }  // extern "C"
 

@@ -356,8 +356,9 @@ int gemm14_host_synchronize(void);
  * bits) and sums the six products of parts above 2^-24 of the whole: the fp32
  * bound, at tensor-core speed; an infinite input gives NaN. Sums of more than
  * 1024 terms whose result is fp32 (losses, fp32 gradients, gemm14_ckpt8_wgrad)
- * leave the tensor cores' accumulators every 1024 terms and are carried in
- * fp32 registers, as the accumulators add with truncation.
+ * leave the tensor cores' accumulators every 1024 terms or fewer and are carried
+ * in fp32 registers, as the accumulators add with truncation. Up to 32 rows of F32
+ * or F32_3XTF32 run as fp32 FMAs on the CUDA cores.
  * loss and lse: T fp32.
  * targets: T int64 on the device. A row whose target is ignore_index takes no
  * part: its loss and lse are 0 and nothing its row of H holds is used. Any
@@ -519,7 +520,9 @@ int gemm14_set_pair_kernel(int enable);
  * stays usable, and gemm14_check_device_error reports the timeout.
  * The fp32 small-product kernel (plan kernel 6) synchronises only through
  * block and cluster barriers, with no mbarrier wait to expire: a call that
- * runs on it consumes the request and computes C as usual.
+ * runs on it consumes the request and computes C as usual; so do
+ * gemm14_linear_ce_* calls of up to 32 fp32 rows. (gemm14_ckpt8_save and
+ * _restore wait for nothing and leave the request to the next call.)
  * Returns GEMM14_ERR_INVALID_ARG for an unknown mode.
  */
 int gemm14_debug_inject(int fault, uint64_t wait_limit_ns);
