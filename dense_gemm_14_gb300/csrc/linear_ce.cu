@@ -23,8 +23,6 @@
 //
 // fp32 operands in the FFMA and TF32 modes take the library's products, a
 // piece of fp32 logits at a time, with row kernels between them.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -273,11 +271,8 @@ __global__ void __launch_bounds__(256)
   } else {
     for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
       float x = h[c];
-      for (int p = 0; p < kParts; ++p) {
-        const __nv_bfloat16 v = __float2bfloat16_rn(x);
-        o[p * part_stride + c] = *reinterpret_cast<const uint16_t*>(&v);
-        x -= __bfloat162float(v);
-      }
+      for (int p = 0; p < kParts; ++p)
+        o[p * part_stride + c] = __bfloat16_as_ushort(take_part(x, p));
     }
   }
 }

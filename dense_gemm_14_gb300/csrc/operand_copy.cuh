@@ -15,6 +15,16 @@
 
 namespace gemm14 {
 
+// Part p of the three bf16 parts of x, taken from it: the nearest bf16, but a
+// finite one where a finite x would round to an infinity (only the first part
+// can; the rest makes up for it). An infinity or a NaN goes to the later parts.
+__device__ __forceinline__ __nv_bfloat16 take_part(float& x, int p) {
+  constexpr float kMost = 3.3895313892515355e38f;  // the largest bf16
+  const __nv_bfloat16 b = __float2bfloat16_rn(p == 0 ? fminf(fmaxf(x, -kMost), kMost) : x);
+  x -= __bfloat162float(b);
+  return b;
+}
+
 // A thread moves 16 bytes, 4 of them in flight; a warp 128 pieces of a row.
 __device__ __forceinline__ void realign_rows(const OperandCopy& j, int block, int blocks) {
   constexpr int kUnroll = 4;
@@ -65,9 +75,8 @@ __device__ __forceinline__ void split_rows(const OperandCopy& j, int block, int 
     for (int p = 0; p < 3; ++p)
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const __nv_bfloat16 b = __float2bfloat16_rn(x[u]);
+        const __nv_bfloat16 b = take_part(x[u], p);
         if (c0 + 32 * u < j.cols) out[p * j.part_stride + r * j.ld_dst + c0 + 32 * u] = b;
-        x[u] -= __bfloat162float(b);
       }
   }
 }

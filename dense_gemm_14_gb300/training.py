@@ -3,8 +3,6 @@ projection's outputs, and activations kept in 8 bits (argument marshalling
 only; every step runs in the library's CUDA kernels)."""
 from __future__ import annotations
 
-from dataclasses import dataclass
-
 import torch
 
 from . import _lib
@@ -51,22 +49,24 @@ def _in_workspace(device: torch.device, handle: int, call, need, where: str) -> 
         raise _lib.Gemm14Error(status, where)
 
 
-def _matrix(x: torch.Tensor, name: str, device: torch.device | None = None) -> int:
-    """The row pitch of a row-major CUDA matrix."""
-    if not x.is_cuda or (device is not None and x.device != device):
+def _matrix(x: torch.Tensor, name: str, device: int | None = None) -> int:
+    """The row pitch of a row-major CUDA matrix (on the device of this index)."""
+    if not x.is_cuda or (device is not None and x.get_device() != device):
         raise ValueError(f"{name} must be a CUDA tensor on the operands' device")
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(x.shape)}")
-    rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    (rows, cols), (pitch, step) = x.shape, x.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have unit stride along its rows (row-major)")
-    if rows > 1 and cols > 0 and x.stride(0) < cols:
+    if rows <= 1 or cols == 0:
+        return max(cols, 1)
+    if pitch < cols:
         raise ValueError(f"{name}: rows overlap (stride {x.stride()})")
-    return max(x.stride(0), cols, 1) if rows > 1 else max(cols, 1)
+    return pitch
 
 
-def _vector(x: torch.Tensor, name: str, n: int, dtype: torch.dtype, device: torch.device) -> None:
-    if x.device != device or x.dtype != dtype or tuple(x.shape) != (n,) or not x.is_contiguous():
+def _vector(x: torch.Tensor, name: str, n: int, dtype: torch.dtype, device: int) -> None:
+    if x.get_device() != device or x.dtype != dtype or x.shape != (n,) or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA vector of {n} values on the "
                          f"operands' device, got {x.dtype} {tuple(x.shape)} on {x.device}")
 
@@ -79,11 +79,12 @@ def _ce_operands(h, w, targets, fp32_mode):
     code = _code(h, fp32_mode)
     if w.dtype != h.dtype:
         raise TypeError(f"h and w differ in dtype: {h.dtype}, {w.dtype}")
-    ldh, ldw = _matrix(h, "h"), _matrix(w, "w", h.device)
+    device = h.get_device()
+    ldh, ldw = _matrix(h, "h"), _matrix(w, "w", device)
     (T, D), (V, D2) = h.shape, w.shape
     if D != D2 or V < 1 or D < 1:
         raise ValueError(f"shape mismatch: h {tuple(h.shape)}, w {tuple(w.shape)}")
-    _vector(targets, "targets", T, torch.int64, h.device)
+    _vector(targets, "targets", T, torch.int64, device)
     return code, T, V, D, ldh, ldw
 
 
@@ -97,7 +98,9 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     one GPU; targets: (T,) int64. loss, lse: (T,) float32, 0 for rows whose
     target is ignore_index; a target outside [0, V) gives NaN. Keep lse for
     linear_cross_entropy_backward. Runs on `stream` (default: torch's current
-    stream) without synchronising, with a workspace cached per (device, stream).
+    stream) without synchronising, with a workspace cached per (device, stream);
+    what it allocates belongs to that stream, and operands made on another are
+    the caller's to order and keep (wait_stream, record_stream).
     fp32_mode as for gemm_into."""
     code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
 
@@ -130,8 +133,8 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor, targets: tor
     float32. Rows that take no part get zero rows in dh and add nothing to dw.
     need_dh / need_dw: a gradient not needed is not formed (None)."""
     code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
-    _vector(lse, "lse", T, torch.float32, h.device)
-    _vector(dloss, "dloss", T, torch.float32, h.device)
+    _vector(lse, "lse", T, torch.float32, h.get_device())
+    _vector(dloss, "dloss", T, torch.float32, h.get_device())
 
     def body(handle):
         dh = torch.empty((T, D), dtype=h.dtype, device=h.device) if need_dh else None
@@ -151,29 +154,42 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor, targets: tor
     return _on(stream, h.device, body)
 
 
-@dataclass(slots=True, eq=False)
 class Ckpt8:
     """A matrix kept in 8 bits: q (rows, cols) int8 and a scale byte for each
     block of 32 columns, scale (rows, ceil(cols / 32)) uint8; a value stands
-    for q * 2**(scale - 133). Both are row-major views; 16-byte aligned rows
-    (as ckpt8_save allocates them) give the fastest accesses."""
-    q: torch.Tensor
-    scale: torch.Tensor
+    for q * 2**(scale - 133). Both are row-major views on one GPU; 16-byte
+    aligned rows (as ckpt8_save allocates them) give the fastest accesses."""
+
+    __slots__ = ("_q", "_scale", "_pitches")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        self._q, self._scale, self._pitches = q, scale, None
+
+    def _operands(self) -> tuple[torch.Tensor, torch.Tensor, int, int]:
+        """q, scale and their pitches, checked at their first use."""
+        q, scale = self._q, self._scale
+        if self._pitches is None:
+            ldq = _matrix(q, "q")
+            lds = _matrix(scale, "scale", q.get_device())
+            rows, cols = q.shape
+            if q.dtype != torch.int8 or scale.dtype != torch.uint8 or \
+                    scale.shape != (rows, -(-cols // CKPT8_BLOCK)):
+                raise ValueError("q must be int8 (rows, cols) and scale uint8 (rows, ceil(cols / 32)), "
+                                 f"got {q.dtype} {tuple(q.shape)}, {scale.dtype} {tuple(scale.shape)}")
+            self._pitches = (ldq, lds)
+        return q, scale, *self._pitches
+
+    @property
+    def q(self) -> torch.Tensor:
+        return self._q
+
+    @property
+    def scale(self) -> torch.Tensor:
+        return self._scale
 
     @property
     def shape(self) -> torch.Size:
-        return self.q.shape
-
-
-def _ckpt8_operands(c: Ckpt8) -> tuple[int, int]:
-    ldq = _matrix(c.q, "q")
-    lds = _matrix(c.scale, "scale", c.q.device)
-    rows, cols = c.q.shape
-    if c.q.dtype != torch.int8 or c.scale.dtype != torch.uint8 or \
-            tuple(c.scale.shape) != (rows, -(-cols // CKPT8_BLOCK)):
-        raise ValueError(f"q must be int8 (rows, cols) and scale uint8 (rows, ceil(cols / 32)), got "
-                         f"{c.q.dtype} {tuple(c.q.shape)}, {c.scale.dtype} {tuple(c.scale.shape)}")
-    return ldq, lds
+        return self._q.shape
 
 
 def ckpt8_save(x: torch.Tensor, stream=None) -> Ckpt8:
@@ -192,7 +208,9 @@ def ckpt8_save(x: torch.Tensor, stream=None) -> Ckpt8:
         if x.numel():
             _lib.ckpt8_save_raw(_CODE[x.dtype], rows, cols, x.data_ptr(), ldx, q.data_ptr(), ldq,
                                 scale.data_ptr(), lds, handle)
-        return Ckpt8(q, scale)
+        kept = Ckpt8(q, scale)
+        kept._pitches = (max(ldq, 1), max(lds, 1))
+        return kept
 
     return _on(stream, x.device, body)
 
@@ -201,17 +219,18 @@ def ckpt8_restore(c: Ckpt8, dtype: torch.dtype = torch.bfloat16, stream=None) ->
     """The values of a checkpoint as a (rows, cols) tensor of dtype (gemm14_ckpt8_restore)."""
     if dtype not in _CODE:
         raise TypeError(f"unsupported dtype {dtype}")
-    ldq, lds = _ckpt8_operands(c)
-    rows, cols = c.q.shape
+    q, scale, ldq, lds = c._operands()
+    rows, cols = q.shape
+    device = q.device
 
     def body(handle):
-        out = torch.empty((rows, cols), dtype=dtype, device=c.q.device)
+        out = torch.empty((rows, cols), dtype=dtype, device=device)
         if out.numel():
-            _lib.ckpt8_restore_raw(_CODE[dtype], rows, cols, c.q.data_ptr(), ldq,
-                                   c.scale.data_ptr(), lds, out.data_ptr(), cols, handle)
+            _lib.ckpt8_restore_raw(_CODE[dtype], rows, cols, q.data_ptr(), ldq, scale.data_ptr(),
+                                   lds, out.data_ptr(), cols, handle)
         return out
 
-    return _on(stream, c.q.device, body)
+    return _on(stream, device, body)
 
 
 def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = None,
@@ -223,26 +242,26 @@ def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = Non
     (beta is then 0). beta = 1 adds to the gradient that is there."""
     code = _code(dy, fp32_mode)
     lddy = _matrix(dy, "dy")
-    ldq, lds = _ckpt8_operands(c)
-    (T, N), (T2, K) = dy.shape, c.q.shape
-    if T != T2 or c.q.device != dy.device:
-        raise ValueError(f"dy {tuple(dy.shape)} and the checkpoint {tuple(c.q.shape)} differ in "
+    q, scale, ldq, lds = c._operands()
+    (T, N), (T2, K) = dy.shape, q.shape
+    if T != T2 or q.get_device() != dy.get_device():
+        raise ValueError(f"dy {tuple(dy.shape)} and the checkpoint {tuple(q.shape)} differ in "
                          "rows or device")
     if out is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs out")
-    elif out.dtype != torch.float32 or tuple(out.shape) != (N, K):
+    elif out.dtype != torch.float32 or out.shape != (N, K):
         raise ValueError(f"out must be float32 of shape {(N, K)}")
 
     def body(handle):
         dw = out if out is not None else torch.empty((N, K), dtype=torch.float32, device=dy.device)
-        lddw = _matrix(dw, "out", dy.device)
+        lddw = _matrix(dw, "out", dy.get_device())
         if not dw.numel():
             return dw
         _in_workspace(
             dy.device, handle,
-            lambda ws, n: _lib.ckpt8_wgrad(code, T, N, K, float(alpha), _ptr(dy), lddy, _ptr(c.q),
-                                           ldq, _ptr(c.scale), lds, float(beta), dw.data_ptr(),
+            lambda ws, n: _lib.ckpt8_wgrad(code, T, N, K, float(alpha), _ptr(dy), lddy, _ptr(q),
+                                           ldq, _ptr(scale), lds, float(beta), dw.data_ptr(),
                                            lddw, ws, n, handle, check=False),
             lambda: _lib.ckpt8_wgrad_workspace_bytes(code, T, N, K, _ptr(dy), lddy, dw.data_ptr(),
                                                      lddw),

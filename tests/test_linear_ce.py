@@ -227,6 +227,28 @@ def test_entries_masked_with_the_lowest_value_and_large_logits(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 70, 300])
+@pytest.mark.parametrize("dtype,mode", [("bf16", None), ("f16", None), ("f32", "fp32"), ("f32", "3xtf32")])
+def test_entries_at_the_lowest_value_and_at_minus_infinity(T, dtype, mode):
+    """Entries shut out by the type's lowest value itself (which, as an fp32, rounds to no finite
+    bf16), or by minus infinity in the forward pass: the others' loss and gradients are as without them."""
+    h, w, y, up = make(T, 600, 64, dtype, 31, spread=2.0)
+    h[:, 0] = 1.0
+    w[:, 0] = 0.0
+    w[300:] = 0.0
+    w[300:, 0] = torch.finfo(DT[dtype]).min
+    y = y % 300
+    r = reference(h[:, 1:], w[:300, 1:], y, up)
+    loss, lse, dh, dw = both(h.cuda(), w.cuda(), y.cuda(), up.cuda(), dtype, mode)
+    check_loss(loss, lse, r)
+    assert not dw[300:].any()
+    check_grads(dh[:, 1:], dw[:300, 1:], r, dtype)
+    w[300:, 0] = -float("inf")
+    if mode != "3xtf32" or T <= 32:  # (an infinite operand is no number in split arithmetic)
+        check_loss(*g14.linear_cross_entropy(h.cuda(), w.cuda(), y.cuda(), fp32_mode=mode), r)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_gradient_alone_is_the_same(dtype):
     h, w, y, up = (x.cuda() for x in make(300, 700, 72, dtype, 3))
