@@ -38,10 +38,15 @@ def _on(stream, device: torch.device, body):
 
 def _in_workspace(device: torch.device, handle: int, call, need, where: str) -> None:
     """call(workspace pointer, bytes) on the stream's workspace as it is; where
-    it is refused, on one of need() bytes (asked for only then)."""
+    it is refused, on one of need() bytes (asked for only then). A call that
+    fails otherwise may have run in part, and is not repeated."""
     ws = _workspaces.get((device.index, handle))
-    if ws is not None and call(ws.data_ptr(), ws.numel()) == _lib.GEMM14_OK:
-        return
+    if ws is not None:
+        status = call(ws.data_ptr(), ws.numel())
+        if status == _lib.GEMM14_OK:
+            return
+        if status != _lib.GEMM14_ERR_INVALID_ARG:
+            raise _lib.Gemm14Error(status, where)
     n = need()
     ws = _workspace(device, handle, n) if n else None
     status = call(ws.data_ptr() if n else None, ws.numel() if n else 0)

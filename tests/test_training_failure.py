@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import dense_gemm_14_gb300 as g14
+from dense_gemm_14_gb300 import training
 
 
 def ce_inputs(T, dtype, seed=1, V=3000, D=136):
@@ -189,3 +190,37 @@ def test_the_example_learns():
     losses = train_head.train(steps=20)
     assert all(x == x for x in losses)
     assert losses[-1] < 0.7 * losses[0], losses
+
+
+@pytest.mark.parametrize("status", [g14.GEMM14_ERR_TIMEOUT, g14.GEMM14_ERR_CUDA])
+def test_a_failed_call_is_reported_and_not_repeated(status, monkeypatch):
+    """A call that failed after its launches may have added to its output: only
+    one that was refused for its workspace is made again."""
+    device, handle = torch.device("cuda", 0), 7
+    monkeypatch.setitem(training._workspaces, (device.index, handle),
+                        torch.empty(64, dtype=torch.uint8))
+    calls = []
+
+    def call(pointer, size):
+        calls.append(size)
+        return status
+
+    with pytest.raises(g14.Gemm14Error):
+        training._in_workspace(device, handle, call, lambda: 128, "a call")
+    assert calls == [64]
+
+
+def test_a_call_refused_for_its_workspace_is_made_again(monkeypatch):
+    device, handle = torch.device("cuda", 0), 7
+    monkeypatch.setitem(training._workspaces, (device.index, handle),
+                        torch.empty(64, dtype=torch.uint8))
+    monkeypatch.setattr(training, "_workspace",
+                        lambda d, h, n: torch.empty(n, dtype=torch.uint8))
+    calls = []
+
+    def call(pointer, size):
+        calls.append(size)
+        return g14.GEMM14_OK if size >= 128 else g14.GEMM14_ERR_INVALID_ARG
+
+    training._in_workspace(device, handle, call, lambda: 128, "a call")
+    assert calls == [64, 128]
