@@ -522,10 +522,15 @@ void wgrad_layout(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, in
   l->total = at;
 }
 
+bool product_size_ok(int64_t T, int64_t N, int64_t K) {
+  return T >= 0 && N >= 0 && K >= 0 && T <= kTrainMaxSize && N <= kTrainMaxSize &&
+         K <= kTrainMaxSize;
+}
+
 int validate_wgrad(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, int64_t lddy,
                    const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds, const float* dW,
                    int64_t lddw) {
-  if (!size_ok(T) || !size_ok(K)) return GEMM14_ERR_INVALID_ARG;
+  if (!product_size_ok(T, N, K)) return GEMM14_ERR_INVALID_ARG;
   if (ldq < at_least_one(K) || lds < at_least_one((K + kBlock - 1) / kBlock))
     return GEMM14_ERR_INVALID_ARG;
   const bool reads = T > 0 && N > 0 && K > 0;
@@ -618,7 +623,8 @@ size_t gemm14_ckpt8_wgrad_workspace_bytes(int dtype, int64_t T, int64_t N, int64
                                           int64_t lddw, int sm_count) {
   if (sm_count <= 0 && current_sm_count(&sm_count) != GEMM14_OK) return 0;
   const void* sound = reinterpret_cast<const void*>(uintptr_t(1) << 12);
-  if (validate_product(dtype, 1, 0, N, K, T, dY, lddy, sound, at_least_one(K), dW, lddw) !=
+  if (!product_size_ok(T, N, K) ||
+      validate_product(dtype, 1, 0, N, K, T, dY, lddy, sound, at_least_one(K), dW, lddw) !=
           GEMM14_OK ||
       T == 0 || N == 0 || K == 0)
     return 0;

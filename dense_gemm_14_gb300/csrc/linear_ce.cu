@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- host side
 
-bool size_ok(int64_t n) { return n >= 0 && n <= INT32_MAX; }
+bool size_ok(int64_t n) { return n >= 0 && n <= kTrainMaxSize; }
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t tiles_of(int64_t x) { return (x + 255) / 256; }
 // Whether the operands run on the tensor-core kernel: 16-bit ones, and fp32
@@ -499,10 +499,10 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
     l->copy_w = l->parts == 3 || !tma_rows(W, ldw);
     // one tile row of rows costs the same with and without the ignored ones
     l->gather = backward || l->parts == 3 || !tma_rows(H, ldh) || T > TrainShape::BM;
-    int64_t per_row = 0;
+    int64_t per_row = 1;  // (a piece is well within 32 bits in any case)
     if (backward) per_row = l->rows * 2 * l->parts;
     if (l->copy_w) per_row = std::max(per_row, l->ldx * 2 * l->parts);
-    l->C = per_row ? piece_rows(V, per_row) : V;
+    l->C = piece_rows(V, per_row);
     l->ldz = round_up(l->C, 64);
     l->few = T <= FewShape::MAX_ROWS;
     if (l->gather) {

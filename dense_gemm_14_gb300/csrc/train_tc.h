@@ -23,6 +23,10 @@ enum : int { kTrainStats = 0, kTrainGrad = 1, kTrainSlots = 2, kTrainOut = 3 };
 // Element types of what an epilogue writes.
 enum : int { kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2, kElemBf16x3 = 3 };
 
+// Largest size of a product: whole tiles of it are counted, and a tile's last
+// column numbered, in 32 bits.
+constexpr int64_t kTrainMaxSize = (int64_t(1) << 31) - 256;
+
 struct TrainShape {
   static constexpr int BM = 256, BN = 256, BK = 64, STAGES = 6;
   static constexpr int EPI_WARPS = 8;                   // two for each TMEM lane quarter

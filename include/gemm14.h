@@ -368,8 +368,8 @@ int gemm14_host_synchronize(void);
  * (one kept for the *_ws calls serves, and the other way round),
  * gemm14_linear_ce_workspace_bytes(...) bytes at least; a smaller one is
  * GEMM14_ERR_INVALID_ARG, and gemm14_last_error_string says how many are
- * needed. Sizes: T >= 0 (0: nothing is done), V >= 1, D >= 1, ldh >= D,
- * ldw >= D. Other rules (device pointers, stream, errors) as above.
+ * needed. Sizes: T >= 0 (0: nothing is done), V >= 1, D >= 1, each at most
+ * 2^31 - 256, ldh >= D, ldw >= D. Other rules (device pointers, stream, errors) as above.
  */
 int gemm14_linear_ce_forward(int dtype, int64_t T, int64_t V, int64_t D, const void* H,
                              int64_t ldh, const void* W, int64_t ldw, const int64_t* targets,
@@ -440,8 +440,8 @@ int gemm14_ckpt8_restore(int dtype, int64_t rows, int64_t cols, const int8_t* Q,
  * X enters the product exactly (F16: rounded where it leaves fp16's range) and
  * sums are fp32.
  * beta == 0: dW is not read; alpha == 0 or T == 0: dY and the checkpoint are
- * not read. workspace: as for the *_ws calls, but needed:
- * gemm14_ckpt8_wgrad_workspace_bytes(...) bytes at least.
+ * not read. Sizes at most 2^31 - 256. workspace: as for the *_ws calls, but
+ * needed: gemm14_ckpt8_wgrad_workspace_bytes(...) bytes at least.
  */
 int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void* dY,
                        int64_t lddy, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,

@@ -275,6 +275,20 @@ def test_weight_gradient_refusals(bad):
                            check=False) == g14.GEMM14_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("size", ["T", "N", "K"])
+def test_sizes_whose_tiles_pass_32_bits_are_refused(size):
+    """Within 255 of 2^31 a count of whole tiles does not fit 32 bits."""
+    for n in ((1 << 31) - 255, (1 << 31) - 1):
+        a = dict(T=1, N=1, K=1) | {size: n}
+        pitch = 1 << 31
+        assert g14.ckpt8_wgrad(1, a["T"], a["N"], a["K"], 1.0, P, pitch, P, pitch, P, pitch, 0.0, P,
+                               pitch, P, 1 << 30, check=False) == g14.GEMM14_ERR_INVALID_ARG
+        assert g14.ckpt8_wgrad_workspace_bytes(1, a["T"], a["N"], a["K"], P, pitch, P, pitch,
+                                               152) == 0
+    a = dict(T=1, N=1, K=1) | {size: (1 << 31) - 256}
+    assert g14.ckpt8_wgrad_workspace_bytes(1, a["T"], a["N"], a["K"], P, pitch, P, pitch, 152) > 0
+
+
 @pytest.mark.gpu
 def test_weight_gradient_small_workspace_is_refused():
     x, dy = data(64, 64, "bf16", 1).cuda(), data(64, 64, "bf16", 2).cuda()

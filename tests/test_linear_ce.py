@@ -407,6 +407,16 @@ def test_workspace_query_is_host_only():
     assert g14.linear_ce_workspace_bytes(1, 0, 4, 8, 8, P, 7, P, 8, 152) == 0
 
 
+def test_sizes_whose_tiles_pass_32_bits_are_refused():
+    """Within 255 of 2^31 a count of whole tiles does not fit 32 bits."""
+    most = (1 << 31) - 256
+    for bad in (dict(T=most + 1), dict(V=most + 1), dict(D=most + 1, ldh=1 << 31, ldw=1 << 31)):
+        assert forward(**bad) == g14.GEMM14_ERR_INVALID_ARG
+        assert backward(**bad) == g14.GEMM14_ERR_INVALID_ARG
+    assert g14.linear_ce_workspace_bytes(1, 0, 4, most, 8, P, 8, P, 8, 152) > 0
+    assert g14.linear_ce_workspace_bytes(1, 0, 4, most + 1, 8, P, 8, P, 8, 152) == 0
+
+
 @pytest.mark.gpu
 def test_small_workspace_is_refused_with_the_bytes_needed():
     h, w, y, _ = make(4, 300, 64, "bf16", 1)
