@@ -440,9 +440,11 @@ int64_t piece_rows(int64_t V, int64_t per_row) {
 }
 
 // Whether a handful of rows run on the CUDA cores (linear_ce_narrow.cu): fp32
-// ones, in the modes that keep the fp32 bound.
-bool on_cuda_cores(int dtype, int64_t T) {
-  return (dtype == GEMM14_DTYPE_F32 || dtype == GEMM14_DTYPE_F32_3XTF32) && T <= kNarrowRows;
+// ones, in the modes that keep the fp32 bound (and no wider than a grid's second
+// dimension reaches).
+bool on_cuda_cores(int dtype, int64_t T, int64_t D) {
+  return (dtype == GEMM14_DTYPE_F32 || dtype == GEMM14_DTYPE_F32_3XTF32) && T <= kNarrowRows &&
+         D <= kNarrowMaxD;
 }
 
 struct CeLayout {
@@ -470,7 +472,7 @@ int64_t stat_parts(bool few, int64_t c, int sms) {
 void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
                const void* W, int64_t ldw, bool backward, int sms, CeLayout* l) {
   *l = CeLayout{};
-  l->narrow = on_cuda_cores(dtype, T);
+  l->narrow = on_cuda_cores(dtype, T, D);
   l->tc = on_tensor_cores(dtype);
   l->ldx = round_up(D, 8);
   l->rows = round_up(T, 256);

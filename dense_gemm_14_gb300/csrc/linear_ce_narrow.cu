@@ -28,7 +28,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // Warps of a logits block (one an SM): 4 x 32 sums a thread leave room for 8.
 constexpr int warps_of(int kT) { return kT > 16 ? 8 : 16; }
 constexpr int kSliceBytes = 200 * 1024;     // of H in shared memory
-constexpr int kCols = 4 * 256;              // columns of a dH or dW block
+constexpr int kCols = kNarrowCols;
 constexpr int kDown = 32;                   // rows of W between two loads of dZ
 constexpr int kStep = 128;                  // columns a warp reads of a row at a time
 

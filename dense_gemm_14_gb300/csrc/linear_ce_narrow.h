@@ -10,6 +10,8 @@
 namespace gemm14 {
 
 constexpr int kNarrowRows = 32;  // rows at most
+constexpr int kNarrowCols = 4 * 256;  // columns of a dH or dW block
+constexpr int64_t kNarrowMaxD = int64_t(65535) * kNarrowCols;
 
 struct NarrowArgs {
   int T;

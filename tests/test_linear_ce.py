@@ -12,6 +12,8 @@ dZ = (p - 1_y) g: the error of p is p (2 d_t + 1e-5), of rounding dZ to the
 type u |dZ| (u = 2^-8 bf16, 2^-11 fp16, 2^-24 fp32; fp16 also ref 2^-40 where
 dZ, held in units of ref 2^-15, is subnormal); the products add
 1e-5 |dZ||W|; the result is rounded once (u, fp16: 2^-25 where subnormal)."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -405,6 +407,24 @@ def test_workspace_query_is_host_only():
     assert 0 < n <= m < 1 << 30
     assert g14.linear_ce_workspace_bytes(1, 0, 0, 8, 8, P, 8, P, 8, 152) == 0
     assert g14.linear_ce_workspace_bytes(1, 0, 4, 8, 8, P, 7, P, 8, 152) == 0
+
+
+@pytest.mark.gpu
+def test_a_row_wider_than_a_grid_of_narrow_blocks():
+    """One fp32 row of more than 65535 x 1024 columns; logits 0 and 2, so that
+    every sum has one term and only exp and log round (2^-20 of values below 3)."""
+    D = 65535 * 1024 + 5
+    h, w = torch.zeros(1, D, device="cuda"), torch.zeros(2, D, device="cuda")
+    h[0, -1], w[1, -1] = 1.0, 2.0
+    y, up = torch.ones(1, dtype=torch.int64, device="cuda"), torch.ones(1, device="cuda")
+    loss, lse = g14.linear_cross_entropy(h, w, y)
+    p0 = 1.0 / (1.0 + math.exp(2.0))
+    assert abs(float(lse) - math.log(1.0 + math.exp(2.0))) < 3e-6
+    assert abs(float(loss) + math.log(1.0 - p0)) < 3e-6
+    dh, dw = g14.linear_cross_entropy_backward(h, w, y, lse, up)
+    assert abs(float(dh[0, -1]) + 2.0 * p0) < 6e-6
+    assert abs(float(dw[0, -1]) - p0) < 3e-6 and abs(float(dw[1, -1]) + p0) < 3e-6
+    assert int(torch.count_nonzero(dh)) == 1 and int(torch.count_nonzero(dw)) == 2
 
 
 def test_sizes_whose_tiles_pass_32_bits_are_refused():
