@@ -182,6 +182,50 @@ def test_weight_gradient_pitches(dy_pad, dy_off, q_pad, out_pad, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,mode", [("bf16", None), ("f16", None), ("f32", None),
+                                        ("f32", "3xtf32")])
+@pytest.mark.parametrize("T", [1, 3, 4, 5, 15, 16, 17])
+@pytest.mark.parametrize("N,K,pad", [(5, 31, 0), (700, 1500, 0), (257, 1027, 1), (3001, 96, 4)])
+def test_weight_gradient_of_a_handful_of_rows(T, N, K, pad, dtype, mode):
+    """Rows and columns over several blocks, rows of dW on 16 bytes and not, from an
+    offset and with room beside them that stays as it is."""
+    x, dy = data(T, K, dtype, T + K), data(T, N, dtype, T + N + 1)
+    c = g14.ckpt8_save(x.cuda())
+    dyv = view_of(dy, pad, pad)
+    for off in (0, 1):
+        buf = torch.full((N * (K + pad) + 8,), float("nan"), device="cuda")
+        out = buf[off:off + N * (K + pad)].view(N, K + pad)
+        g14.ckpt8_weight_grad(dyv, c, out=out[:, :K], fp32_mode=mode)  # NaN there is not read
+        wgrad_check(dy, c, out[:, :K])
+        before = out[:, :K].cpu()
+        g14.ckpt8_weight_grad(dyv, c, out=out[:, :K], alpha=-0.5, beta=0.75, fp32_mode=mode)
+        wgrad_check(dy, c, out[:, :K], -0.5, 0.75, before)
+        assert bool(torch.isnan(out[:, K:]).all()) and bool(torch.isnan(buf[off + N * (K + pad):]).all())
+        assert off == 0 or bool(torch.isnan(buf[:off]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [16, 40])
+def test_f16_values_beyond_its_range_enter_as_infinities(T):
+    x = torch.ones(T, 64)
+    x[:, 32:] = 1e6  # kept from fp32; beyond fp16's range
+    c = g14.ckpt8_save(x.cuda())
+    got = g14.ckpt8_weight_grad(torch.ones(T, 8, dtype=torch.float16, device="cuda"), c).cpu()
+    assert bool((got[:, :32] == float(T)).all()) and bool((got[:, 32:] == float("inf")).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_a_poisoned_block_in_a_handful_of_rows(dtype):
+    x, dy = data(9, 96, dtype, 1), data(9, 70, dtype, 2)
+    x[3, 35] = float("nan")
+    c = g14.ckpt8_save(x.cuda())
+    got = g14.ckpt8_weight_grad(dy.cuda(), c).cpu()
+    assert bool(torch.isnan(got[:, 32:64]).all())
+    assert not bool(torch.isnan(got[:, :32]).any()) and not bool(torch.isnan(got[:, 64:]).any())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_poisoned_block_reaches_its_columns_only(dtype):
     x, dy = data(40, 96, dtype, 1), data(40, 70, dtype, 2)
