@@ -776,8 +776,9 @@ struct CeCall {
       a.part_ld = l.rows;
       a.part_count = parts_of(c) * l.rows;
       a.target_logit = at<float>(l.state);
+      const bool promote = D > TrainShape::STATS_CHUNK * TrainShape::BK;
       st = l.few ? run_few(kTrainStats, w, a)
-                 : run(kTrainStats, long_sum(D), h_operand(), false, w, false, &a);
+                 : run(kTrainStats, promote, h_operand(), false, w, false, &a);
       if (st != GEMM14_OK) return st;
       parts = v0 / l.C * parts_of(l.C) + parts_of(c);
     }

@@ -424,6 +424,7 @@ struct Epilogue {
 template <int kMode, bool kPromote, int kWidth>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
     train_tc_kernel(const __grid_constant__ TrainMaps maps, const TrainArgs args) {
+  constexpr int kChunk = kMode == kTrainStats ? S::STATS_CHUNK : S::CHUNK;
   constexpr int kHalf = kWidth / 2;  // a CTA's columns of B, and a warp's of D
   constexpr int kChunks = kHalf / 32;
   extern __shared__ uint8_t smem_raw[];
@@ -484,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
         work.tile_at(t, tm, tn);
         const int m0 = tm * S::BM + static_cast<int>(rank) * 128;
         const int n0 = tn * kWidth + static_cast<int>(rank) * kHalf;
-        const int step = kPromote ? S::CHUNK : kb1 - kb0;
+        const int step = kPromote ? kChunk : kb1 - kb0;
         for (int c0 = kb0; c0 < kb1 && ok; c0 += step) {
           const int c1 = min(c0 + step, kb1);
           for (int term = 0; term < args.terms && ok; ++term) {
@@ -531,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
       for (int i = cid; i < items && ok; i += ncl) {
         int t, split, kb0, kb1;
         work.get(i, t, split, kb0, kb1);
-        const int step = kPromote ? S::CHUNK : kb1 - kb0;
+        const int step = kPromote ? kChunk : kb1 - kb0;
         for (int c0 = kb0; c0 < kb1; c0 += step, ++unit) {
           const int blocks = (min(c0 + step, kb1) - c0) * args.terms;
           const int b = unit & 1;
@@ -579,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
                                  static_cast<int>(rank), slot, tn * kWidth + half * kHalf, buf,
                                  {}, 1.0f};
       e.begin();
-      const int step = kPromote ? S::CHUNK : kb1 - kb0;
+      const int step = kPromote ? kChunk : kb1 - kb0;
       float acc[kPromote ? 128 : 1];
       if (kPromote) {
 #pragma unroll

@@ -354,10 +354,10 @@ int gemm14_host_synchronize(void);
  * for gemm14_gemm_ex (F32, BF16, F16, TF32, F32_3XTF32). F32_3XTF32 here
  * splits each fp32 value into three bf16 parts (their sum is the value to 24
  * bits) and sums the six products of parts above 2^-24 of the whole: the fp32
- * bound, at tensor-core speed; an infinite input gives NaN. Sums of more than
- * 1024 terms whose result is fp32 (losses, fp32 gradients, gemm14_ckpt8_wgrad)
- * leave the tensor cores' accumulators every 1024 terms or fewer and are carried
- * in fp32 registers, as the accumulators add with truncation. Up to 32 rows of F32
+ * bound, at tensor-core speed; an infinite input gives NaN. Sums whose result is
+ * fp32 leave the tensor cores' accumulators every 1024 terms (fp32 gradients,
+ * gemm14_ckpt8_wgrad), or every 512 or fewer (losses), and are carried in fp32
+ * registers, as the accumulators add with truncation. Up to 32 rows of F32
  * or F32_3XTF32 run as fp32 FMAs on the CUDA cores.
  * loss and lse: T fp32.
  * targets: T int64 on the device. A row whose target is ignore_index takes no
