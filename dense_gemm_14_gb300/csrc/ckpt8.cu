@@ -474,6 +474,203 @@ int validate_ckpt8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t
   return GEMM14_OK;
 }
 
+// ---- the weight gradient of a handful of rows, on the CUDA cores
+
+// dW = alpha dY^T X (+ beta dW) of T <= 16 rows reads and writes dW and little
+// else, so memory bounds it: a thread holds its 4 columns of X, from the
+// checkpoint, in registers and goes down dW with 4 kT fp32 FMAs (two to an
+// instruction) for each 16 bytes, dY's values coming from shared memory, the next
+// rows of dW in flight meanwhile (without that, and with single FMAs, it took
+// 37.6 us for the 29.5 below). One launch and no copy of X or dY, against two or
+// three on the tensor cores, whose epilogue moves dW at 3.9 TB/s: 16 x 4096 x 4096
+// fp16, added, 36.4 -> 29.5 us (4.6 TB/s with the launch).
+// `along` threads (a power of two, 32 at least) side by side take 4 along
+// columns, the block's others other rows. kVec: dW's rows start on 16 bytes, and
+// a thread's columns lie together; else they lie `along` apart, so that a warp's
+// accesses do. Sums of T products in fp32.
+constexpr int kNarrowRows = 16;
+constexpr int kNarrowDown = 64;  // rows of dW between two loads of dY
+constexpr int kNarrowAhead = 4;  // rows of dW in flight beside the 4 at work
+
+__device__ __forceinline__ void fma2(uint64_t& s, uint64_t d, uint64_t x) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(s) : "l"(d), "l"(x));
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+
+template <typename T, int kT, bool kVec, bool kAdd>
+__global__ void __launch_bounds__(kThreads, 2)
+    ckpt8_wgrad_narrow_kernel(const T* dY, int64_t lddy, const int8_t* Q, int64_t ldq,
+                              const uint8_t* S, int64_t lds, float* dW, int64_t lddw, int rows,
+                              int64_t N, int64_t K, float alpha, float beta, int along,
+                              int64_t across, int64_t share) {
+  __shared__ __align__(16) float2 dy[kNarrowDown][kT];  // each value twice
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int tx = threadIdx.x & (along - 1), ty = threadIdx.x / along;
+  const int step = kThreads / along;
+  const int64_t part = blockIdx.x / across, n_begin = part * share;
+  const int64_t n_end = min(N, n_begin + share);
+  const int64_t c0 = (blockIdx.x - part * across) * (4 * static_cast<int64_t>(along));
+  int64_t col[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) col[j] = c0 + (kVec ? 4 * tx + j : tx + j * along);
+  const bool q_words = kVec && col[3] < K && ((reinterpret_cast<uintptr_t>(Q) | ldq) & 3) == 0;
+  uint64_t x[kT][2];
+  {
+    uint32_t q[kT], sc[kT][kVec ? 1 : 4];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      q[t] = 0u;
+#pragma unroll
+      for (int j = 0; j < (kVec ? 1 : 4); ++j) sc[t][j] = 7u;
+      if (t >= rows) continue;
+      if (q_words) {
+        q[t] = *reinterpret_cast<const uint32_t*>(Q + t * ldq + col[0]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col[j] < K)
+            q[t] |= static_cast<uint32_t>(static_cast<uint8_t>(Q[t * ldq + col[j]])) << (8 * j);
+      }
+#pragma unroll
+      for (int j = 0; j < (kVec ? 1 : 4); ++j)
+        if (col[j] < K) sc[t][j] = S[t * lds + col[j] / kBlock];
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = to_f32(from_f32<T>(static_cast<float>(static_cast<int8_t>(q[t] >> (8 * j))) *
+                                  step_of(sc[t][kVec ? 0 : j])));
+      x[t][0] = pair_of(v[0], v[1]);
+      x[t][1] = pair_of(v[2], v[3]);
+    }
+  }
+  for (int64_t n0 = n_begin; n0 < n_end; n0 += kNarrowDown) {
+    const int down = static_cast<int>(min(static_cast<int64_t>(kNarrowDown), n_end - n0));
+    float old[kNarrowAhead][4];
+    const auto load = [&](int u0) {
+#pragma unroll
+      for (int a = 0; a < kNarrowAhead; ++a) {
+        const int u = u0 + a * step;
+        const float* from = dW + (n0 + u) * lddw;
+        if (kVec && u < down && col[3] < K) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(from + col[0]));
+          old[a][0] = v.x;
+          old[a][1] = v.y;
+          old[a][2] = v.z;
+          old[a][3] = v.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) old[a][j] = u < down && col[j] < K ? from[col[j]] : 0.0f;
+        }
+      }
+    };
+    if constexpr (kAdd) load(ty);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kNarrowDown * kT; i += kThreads) {
+      const int v = i % kNarrowDown, t = i / kNarrowDown;
+      const float d = t < rows && n0 + v < n_end ? to_f32(dY[t * lddy + n0 + v]) : 0.0f;
+      dy[v][t] = make_float2(d, d);
+    }
+    __syncthreads();
+    for (int u0 = ty; u0 < down; u0 += kNarrowAhead * step) {
+      float was[kNarrowAhead][4];
+      if constexpr (kAdd) {
+#pragma unroll
+        for (int a = 0; a < kNarrowAhead; ++a)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) was[a][j] = old[a][j];
+        load(u0 + kNarrowAhead * step);
+      }
+#pragma unroll
+      for (int a = 0; a < kNarrowAhead; ++a) {
+        const int u = u0 + a * step;
+        if (u >= down) break;
+        uint64_t s2[2] = {0u, 0u};
+        const ulonglong2* d = reinterpret_cast<const ulonglong2*>(dy[u]);
+#pragma unroll
+        for (int t = 0; t < kT; t += 2) {
+          const ulonglong2 two = d[t / 2];
+          fma2(s2[0], two.x, x[t][0]);
+          fma2(s2[1], two.x, x[t][1]);
+          fma2(s2[0], two.y, x[t + 1][0]);
+          fma2(s2[1], two.y, x[t + 1][1]);
+        }
+        float s[4] = {__uint_as_float(static_cast<uint32_t>(s2[0])),
+                      __uint_as_float(static_cast<uint32_t>(s2[0] >> 32)),
+                      __uint_as_float(static_cast<uint32_t>(s2[1])),
+                      __uint_as_float(static_cast<uint32_t>(s2[1] >> 32))};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[j] *= alpha;
+          if constexpr (kAdd) s[j] = fmaf(beta, was[a][j], s[j]);
+        }
+        float* to = dW + (n0 + u) * lddw;
+        if (kVec && col[3] < K) {
+          *reinterpret_cast<float4*>(to + col[0]) = make_float4(s[0], s[1], s[2], s[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col[j] < K) to[col[j]] = s[j];
+        }
+      }
+    }
+  }
+}
+
+// Whether dW's rows start on 16 bytes.
+bool wide_rows(const float* dW, int64_t lddw) { return aligned(dW, 16) && lddw % 4 == 0; }
+
+// Up to 16 rows, and half as many where dW takes 4-byte accesses (bf16 4001 x
+// 4099, added: 5 rows 42.6 us against 52.5, 16 rows 61.4 against 53.7; 4096 x 4096:
+// 5 rows 30.7 against 39.6, 16 rows 34.1 against 39.5, with cold caches). TF32 asks
+// for the tensor cores' rounding of dY, and keeps it.
+bool wgrad_narrow(int dtype, int64_t T, const float* dW, int64_t lddw) {
+  return T <= (wide_rows(dW, lddw) ? kNarrowRows : kNarrowRows / 2) && dtype != GEMM14_DTYPE_TF32;
+}
+
+template <typename T, int kT, bool kVec, bool kAdd>
+cudaError_t launch_narrow_wgrad(const T* dY, int64_t lddy, const int8_t* Q, int64_t ldq,
+                                const uint8_t* S, int64_t lds, float* dW, int64_t lddw, int rows,
+                                int64_t N, int64_t K, float alpha, float beta, int sms,
+                                cudaStream_t stream) {
+  int along = 32;
+  while (along < kThreads && 4 * along < K) along *= 2;
+  const int64_t across = (K + 4 * along - 1) / (4 * along);
+  // one wave of blocks, each with rows enough for its threads
+  const int64_t blocks = static_cast<int64_t>(sms) * 2;
+  const int64_t least = kNarrowAhead / 2 * (kThreads / along);
+  int64_t splits = blocks / across > 1 ? blocks / across : 1;
+  if (splits > (N + least - 1) / least) splits = (N + least - 1) / least;
+  const int64_t share = (N + splits - 1) / splits, parts = (N + share - 1) / share;
+  return launch_kernel(ckpt8_wgrad_narrow_kernel<T, kT, kVec, kAdd>,
+                       dim3(static_cast<unsigned>(parts * across)), dim3(kThreads), 0, stream, dY,
+                       lddy, Q, ldq, S, lds, dW, lddw, rows, N, K, alpha, beta, along, across,
+                       share);
+}
+template <typename T>
+cudaError_t narrow_wgrad_as(const void* dY, int64_t lddy, const int8_t* Q, int64_t ldq,
+                            const uint8_t* S, int64_t lds, float* dW, int64_t lddw, int64_t rows,
+                            int64_t N, int64_t K, float alpha, float beta, int sms,
+                            cudaStream_t stream) {
+  const bool vec = wide_rows(dW, lddw), add = beta != 0.0f;
+  const auto run = [&](auto kernel) {
+    return kernel(static_cast<const T*>(dY), lddy, Q, ldq, S, lds, dW, lddw,
+                  static_cast<int>(rows), N, K, alpha, beta, sms, stream);
+  };
+  if (rows <= 4)
+    return run(vec ? add ? launch_narrow_wgrad<T, 4, true, true> : launch_narrow_wgrad<T, 4, true, false>
+                   : add ? launch_narrow_wgrad<T, 4, false, true> : launch_narrow_wgrad<T, 4, false, false>);
+  if (rows <= 8)
+    return run(vec ? add ? launch_narrow_wgrad<T, 8, true, true> : launch_narrow_wgrad<T, 8, true, false>
+                   : add ? launch_narrow_wgrad<T, 8, false, true> : launch_narrow_wgrad<T, 8, false, false>);
+  return run(add ? launch_narrow_wgrad<T, 16, true, true> : launch_narrow_wgrad<T, 16, true, false>);
+}
+
 // ---- the weight gradient: restored values (and dY, where it is copied) in the
 // workspace, then a product
 
@@ -481,6 +678,7 @@ int validate_ckpt8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t
 // run on the tensor-core kernel of train_tc.cu; the FFMA and TF32 modes on the
 // library's products, with the values restored in fp32.
 struct WgradLayout {
+  bool narrow = false;     // a handful of rows, on the CUDA cores (no workspace)
   bool tc = false;
   int parts = 1;           // bf16 parts of dY
   bool copy_dy = false;    // dY is copied (unaligned) or split
@@ -492,6 +690,8 @@ struct WgradLayout {
 void wgrad_layout(int dtype, int64_t T, int64_t N, int64_t K, const void* dY, int64_t lddy,
                   const float* dW, int64_t lddw, int sms, WgradLayout* l) {
   *l = WgradLayout{};
+  l->narrow = wgrad_narrow(dtype, T, dW, lddw);
+  if (l->narrow) return;
   l->tc = dtype != GEMM14_DTYPE_F32 && dtype != GEMM14_DTYPE_TF32;
   size_t at = streamk_flag_bytes(sms);
   auto take = [&](size_t bytes) {
@@ -566,7 +766,7 @@ int wgrad_tc(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void
   a.out = dW;
   a.ld_out = lddw;
   a.elem = kElemF32;
-  a.out_vec = aligned(dW, 16) && lddw % 4 == 0;
+  a.out_vec = wide_rows(dW, lddw);
   a.slots = reinterpret_cast<float4*>(ws + l.slots_off);
   a.slot_count = l.slot_count;
   a.out_rows = N;
@@ -650,6 +850,14 @@ int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, 
   const int sms = ctx.sm_count;
   WgradLayout l;
   wgrad_layout(dtype, T, N, K, dY, lddy, dW, lddw, sms, &l);
+  if (l.narrow) {
+    const auto launch = dtype == GEMM14_DTYPE_BF16  ? narrow_wgrad_as<__nv_bfloat16>
+                        : dtype == GEMM14_DTYPE_F16 ? narrow_wgrad_as<__half>
+                                                    : narrow_wgrad_as<float>;
+    return finish_launch(launch(dY, lddy, Q, ldq, S, lds, dW, lddw, T, N, K, alpha, beta, sms,
+                                stream),
+                         "ckpt8 narrow product launch", stream);
+  }
   if (!workspace || workspace_bytes < l.total) {
     note_error("gemm14_ckpt8_wgrad: %zu bytes of workspace given, %zu needed", workspace_bytes,
                l.total);

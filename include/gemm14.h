@@ -440,8 +440,11 @@ int gemm14_ckpt8_restore(int dtype, int64_t rows, int64_t cols, const int8_t* Q,
  * X enters the product exactly (F16: rounded where it leaves fp16's range) and
  * sums are fp32.
  * beta == 0: dW is not read; alpha == 0 or T == 0: dY and the checkpoint are
- * not read. Sizes at most 2^31 - 256. workspace: as for the *_ws calls, but
- * needed: gemm14_ckpt8_wgrad_workspace_bytes(...) bytes at least.
+ * not read. Up to 16 rows (8 where dW's rows do not start on 16 bytes) run as
+ * fp32 FMAs on the CUDA cores, TF32 aside, and need no workspace; otherwise
+ * workspace: as for the *_ws calls, but needed:
+ * gemm14_ckpt8_wgrad_workspace_bytes(...) bytes at least. Sizes at most
+ * 2^31 - 256.
  */
 int gemm14_ckpt8_wgrad(int dtype, int64_t T, int64_t N, int64_t K, float alpha, const void* dY,
                        int64_t lddy, const int8_t* Q, int64_t ldq, const uint8_t* S, int64_t lds,
@@ -522,8 +525,9 @@ int gemm14_set_pair_kernel(int enable);
  * The fp32 small-product kernel (plan kernel 6) synchronises only through
  * block and cluster barriers, with no mbarrier wait to expire: a call that
  * runs on it consumes the request and computes C as usual; so do
- * gemm14_linear_ce_* calls of up to 32 fp32 rows. (gemm14_ckpt8_save and
- * _restore wait for nothing and leave the request to the next call.)
+ * gemm14_linear_ce_* calls of up to 32 fp32 rows and gemm14_ckpt8_wgrad calls of up
+ * to 16 rows. (gemm14_ckpt8_save and _restore wait for nothing and leave the
+ * request to the next call.)
  * Returns GEMM14_ERR_INVALID_ARG for an unknown mode.
  */
 int gemm14_debug_inject(int fault, uint64_t wait_limit_ns);

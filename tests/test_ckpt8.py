@@ -184,7 +184,7 @@ def test_weight_gradient_pitches(dy_pad, dy_off, q_pad, out_pad, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,mode", [("bf16", None), ("f16", None), ("f32", None),
                                         ("f32", "3xtf32")])
-@pytest.mark.parametrize("T", [1, 3, 4, 5, 15, 16, 17])
+@pytest.mark.parametrize("T", [1, 3, 4, 5, 8, 9, 15, 16, 17])
 @pytest.mark.parametrize("N,K,pad", [(5, 31, 0), (700, 1500, 0), (257, 1027, 1), (3001, 96, 4)])
 def test_weight_gradient_of_a_handful_of_rows(T, N, K, pad, dtype, mode):
     """Rows and columns over several blocks, rows of dW on 16 bytes and not, from an
@@ -323,13 +323,13 @@ def test_weight_gradient_refusals(bad):
 def test_sizes_whose_tiles_pass_32_bits_are_refused(size):
     """Within 255 of 2^31 a count of whole tiles does not fit 32 bits."""
     for n in ((1 << 31) - 255, (1 << 31) - 1):
-        a = dict(T=1, N=1, K=1) | {size: n}
+        a = dict(T=17, N=1, K=1) | {size: n}
         pitch = 1 << 31
         assert g14.ckpt8_wgrad(1, a["T"], a["N"], a["K"], 1.0, P, pitch, P, pitch, P, pitch, 0.0, P,
                                pitch, P, 1 << 30, check=False) == g14.GEMM14_ERR_INVALID_ARG
         assert g14.ckpt8_wgrad_workspace_bytes(1, a["T"], a["N"], a["K"], P, pitch, P, pitch,
                                                152) == 0
-    a = dict(T=1, N=1, K=1) | {size: (1 << 31) - 256}
+    a = dict(T=17, N=1, K=1) | {size: (1 << 31) - 256}
     assert g14.ckpt8_wgrad_workspace_bytes(1, a["T"], a["N"], a["K"], P, pitch, P, pitch, 152) > 0
 
 
