@@ -11,7 +11,7 @@
 // are, in tensor memory: the forward pass keeps of each tile a maximum and a sum
 // per row, merged at the end; the backward pass forms the logits again from H,
 // W and lse, a piece of the vocabulary at a time, writes the piece of dZ (16
-// bits, or three bf16 parts), and multiplies it into dH (fp32 sums over the
+// bits, two 16-bit parts for up to 128 rows, or three bf16 parts), and multiplies it into dH (fp32 sums over the
 // pieces) and into the piece's rows of dW. What a step reads and writes beside
 // its 8 n V D operations of products (n rows that take part; 2 of the 8 form the
 // logits again) is small against them from a few hundred rows on, so the
@@ -454,6 +454,7 @@ struct CeLayout {
   int64_t ldz = 0;     // pitch of the logits or of dZ
   int64_t ldx = 0;     // pitch of the D-wide buffers
   int parts = 1;       // bf16 parts of an operand
+  int dz_parts = 1;    // parts of dZ
   bool few = false;    // the logits come from the kernel for few rows
   bool gather = false; // rows in use are numbered and gathered first
   bool copy_w = false; // pieces of W are copied (unaligned) or split
@@ -501,12 +502,17 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
     l->copy_w = l->parts == 3 || !tma_rows(W, ldw);
     // one tile row of rows costs the same with and without the ignored ones
     l->gather = backward || l->parts == 3 || !tma_rows(H, ldh) || T > TrainShape::BM;
+    l->few = T <= FewShape::MAX_ROWS;
+    // 16-bit dZ of few rows is held in two parts. Its rounding makes gradients 1.33
+    // times as far off as their own does; over many rows that is all, over few it
+    // is one row's luck (up to 1.6 times). The parts share the 256 rows of a tile, so
+    // dH's products take no longer.
+    l->dz_parts = l->parts == 3 ? 3 : l->few ? 2 : 1;
     int64_t per_row = 1;  // (a piece is well within 32 bits in any case)
     if (backward) per_row = l->rows * 2 * l->parts;
     if (l->copy_w) per_row = std::max(per_row, l->ldx * 2 * l->parts);
     l->C = piece_rows(V, per_row);
     l->ldz = round_up(l->C, 64);
-    l->few = T <= FewShape::MAX_ROWS;
     if (l->gather) {
       l->counts = take(256);
       l->index = take(t4);
@@ -794,7 +800,8 @@ struct CeCall {
     const Rows r = rows();
     const bool exact = l.parts == 3;
     const int elem = exact ? kElemF32 : bf16() ? kElemBf16 : kElemF16;
-    const int64_t g_part = l.rows * l.ldz;
+    const bool two = l.dz_parts == 2;  // dZ's second part: rows 128 .. of its tile
+    const int64_t z_rows = two ? FewShape::MAX_ROWS : l.rows, g_part = z_rows * l.ldz;
     for (int64_t v0 = 0; v0 < V; v0 += l.C) {
       const int64_t c = std::min(l.C, V - v0);
       TrainOperand w;
@@ -809,19 +816,26 @@ struct CeCall {
       a.out_part = g_part;
       a.elem = exact ? kElemBf16x3 : elem;
       a.out_vec = 1;
-      a.out_rows = l.rows;
+      a.out_rows = z_rows;
       a.out_cols = c;
       st = l.few ? run_few(kTrainGrad, w, a)
                  : run(kTrainGrad, exact && long_sum(D), h_operand(), false, w, false, &a);
       if (st != GEMM14_OK) return st;
-      const TrainOperand dz{ws + l.z, l.rows, c, l.ldz, l.parts, g_part};
+      // (rows past T's last block of 64 are zeros without being read)
+      const TrainOperand dz{ws + l.z, round_up(T, 64), c, l.ldz, l.dz_parts, g_part};
       if (dH) {
         a = product(T, D, c, false);
+        TrainOperand both = dz;
+        if (two) {  // all 256 rows: what is past the rows in use stays in its rows
+          both = TrainOperand{ws + l.z, 2 * z_rows, c, l.ldz, 1, 0};
+          a.M = static_cast<int>(2 * z_rows);
+          a.n = nullptr;
+        }
         a.split_k = static_cast<int>(l.C);  // the same plan for every piece
         a.slots = at<float4>(l.slots);
         a.slot_count = l.slot_count;
         a.add = v0 > 0;
-        if ((st = run(kTrainSlots, exact && long_sum(c), dz, false, w, true, &a)) != GEMM14_OK)
+        if ((st = run(kTrainSlots, exact && long_sum(c), both, false, w, true, &a)) != GEMM14_OK)
           return st;
       }
       if (dW) {
@@ -853,7 +867,7 @@ struct CeCall {
     a.split_k = static_cast<int>(l.C);
     a.terms = exact ? 6 : 1;
     a.slots = at<float4>(l.slots);
-    const SlotsOut s{true, r.index, 1.0f, 0.0f, r.back, dH, lddh, elem, T};
+    const SlotsOut s{true, r.index, 1.0f, 0.0f, r.back, dH, lddh, elem, T, two ? 1 : 0};
     return launched(launch_slots_out(a, s, clusters, stream), "linear_ce output launch");
   }
 

@@ -241,7 +241,8 @@ struct RowData {
   float m, l, zy;     // statistics
 };
 
-template <int kMode, int kChunks = 4>
+// kDzParts: 16-bit parts of a dZ of 16-bit operands (kTrainGrad).
+template <int kMode, int kChunks = 4, int kDzParts = 1>
 struct Epilogue {
   const TrainArgs& args;
   int M, N, lane, row0, row, half, rank;
@@ -361,7 +362,7 @@ struct Epilogue {
 
   // 16-bit output: two chunks of 32 columns share a staged block of 64.
   __device__ void store16(int c, float (&x)[32]) {
-    const int parts = args.elem == kElemBf16x3 ? 3 : 1;
+    const int parts = args.elem == kElemBf16x3 ? 3 : kDzParts;
     // kTrainGrad writes whole tile rows (zeros past the rows in use): its
     // buffer has them
     const int rows = kMode == kTrainGrad ? INT_MAX : M;
@@ -387,9 +388,9 @@ struct Epilogue {
                   min(c & 1 ? 64 : 32, N - col0), lane);
       return;
     }
-    // three bf16 parts of each value: the nearest, then the nearest to what is left
+    // parts of each value: the nearest, then the nearest to what is left
     const int col0 = col_half + 32 * c;
-    for (int part = 0; part < 3; ++part) {
+    for (int part = 0; part < parts; ++part) {
       __syncwarp();
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
@@ -398,9 +399,15 @@ struct Epilogue {
         for (int k = 0; k < 4; ++k) {
           float& a = x[8 * p + 2 * k];
           float& b = x[8 * p + 2 * k + 1];
-          w[k] = pack_bf16(a, b);
-          a -= __uint_as_float(w[k] << 16);
-          b -= __uint_as_float(w[k] & 0xffff0000u);
+          if (kDzParts == 2 && args.elem == kElemF16) {
+            w[k] = pack_f16(a, b);
+            a -= __half2float(__ushort_as_half(static_cast<unsigned short>(w[k])));
+            b -= __half2float(__ushort_as_half(static_cast<unsigned short>(w[k] >> 16)));
+          } else {
+            w[k] = pack_bf16(a, b);
+            a -= __uint_as_float(w[k] << 16);
+            b -= __uint_as_float(w[k] & 0xffff0000u);
+          }
         }
         stage_put(stage_at(buf, lane, p), make_uint4(w[0], w[1], w[2], w[3]));
       }
@@ -817,8 +824,9 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const int limit = min(args.N, (t + 1) * few.width);
-      Epilogue<kMode> e{args, M, limit, lane, q * 32, q * 32 + lane, half, 0, -1,
-                        t * few.width + half * 128, buf, {}, 1.0f};
+      Epilogue<kMode, 4, kMode == kTrainGrad && kParts == 1 ? 2 : 1> e{
+          args, M, limit, lane, q * 32, q * 32 + lane, half, 0, -1, t * few.width + half * 128,
+          buf, {}, 1.0f};
       e.begin();
       float acc[128];
 #pragma unroll
@@ -905,13 +913,15 @@ __global__ void __launch_bounds__(256)
     const float4* from = args.slots + slot_index(slot_of(work.plan, s.all, t, 0), rank, half, c,
                                                  warp, q0 + lane);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int side = 0; side <= s.fold; ++side, from += slot_index(0, 1, 0, 0, 0, 0)) {
 #pragma unroll 8
-    for (int p = 0; p < ranges; ++p) {
-      const float4 o = __ldcg(from + p * (kSlotBytes / 16));
-      v.x += o.x;
-      v.y += o.y;
-      v.z += o.z;
-      v.w += o.w;
+      for (int p = 0; p < ranges; ++p) {
+        const float4 o = __ldcg(from + p * (kSlotBytes / 16));
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+      }
     }
     __syncthreads();
     *reinterpret_cast<float4*>(&tile[lane][4 * warp]) = v;
@@ -1018,10 +1028,9 @@ int train_operands(bool bf16, const TrainOperand& A, bool a_mn, const TrainOpera
   if (st == 0) st = encode(B, b_mn, b_rows ? b_rows : args->width / 2, maps->b);
   if (st != 0) return st;
   // Terms of split operands, small ones first: of 3 x 3 parts the six whose
-  // product is above 2^-24 of the whole, or A's three parts against one B.
-  const bool split = A.parts == 3;
-  args->terms = !split ? 1 : B.parts == 3 ? 6 : 3;
-  args->term_code = !split ? 0u : B.parts == 3 ? 0x041582u : 0x012u;
+  // product is above 2^-24 of the whole, or A's two or three parts against one B.
+  args->terms = B.parts == 3 ? 6 : A.parts;
+  args->term_code = B.parts == 3 ? 0x041582u : A.parts == 3 ? 0x012u : A.parts == 2 ? 0x01u : 0u;
   args->a_mn = a_mn;
   args->b_mn = b_mn;
   args->idesc = idesc_f16_f32acc(bf16, S::BM, args->width, a_mn, b_mn);

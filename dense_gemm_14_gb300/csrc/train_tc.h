@@ -192,6 +192,7 @@ struct SlotsOut {
   int64_t ld;
   int elem;
   int64_t out_rows;
+  int fold = 0;  // 1: row r's sums are those of rows r and r + 128 of its tile
 };
 // clusters: the launch's.
 cudaError_t launch_slots_out(const TrainArgs& args, const SlotsOut& s, int clusters,

@@ -388,8 +388,8 @@ int gemm14_linear_ce_forward(int dtype, int64_t T, int64_t V, int64_t D, const v
  * when their rows of H hold NaN; a target outside [0, V) makes its row of dH
  * and all of dW NaN. T == 0 sets dW to zero.
  * dH and dW must not overlap each other, H or W.
- * Rounding: 16-bit dtypes hold dZ in that type, relative to the largest
- * |dloss[t]|, for the two products, which accumulate in fp32; each gradient is
+ * Rounding: 16-bit dtypes hold dZ in that type (of up to 128 rows in two parts
+ * of it), relative to the largest |dloss[t]|, for the two products, which accumulate in fp32; each gradient is
  * rounded once to the type. fp32 dtypes hold dZ in fp32.
  * Arguments and workspace as for the forward call.
  */
