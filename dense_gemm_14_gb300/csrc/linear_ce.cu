@@ -456,19 +456,21 @@ struct CeLayout {
   int parts = 1;       // bf16 parts of an operand
   int dz_parts = 1;    // parts of dZ
   bool few = false;    // the logits come from the kernel for few rows
+  int width = 0;       // columns of the logits' tiles, the same for every piece
   bool gather = false; // rows in use are numbered and gathered first
   bool copy_w = false; // pieces of W are copied (unaligned) or split
   int64_t slot_count = 0, tail_count = 0;  // of dH, and of dW's split tiles
   int64_t rows = 0;    // T rounded up to whole tiles
+  int64_t stats = 0;   // entries of the statistics, of all pieces
   size_t state = 0, counts = 0, index = 0, position = 0, target = 0, lse = 0, coef = 0, h = 0,
          w = 0, part = 0, z = 0, slots = 0, tail = 0, total = 0;
 };
 
-// Parts of a row's statistics that c columns leave: two a tile.
-int64_t stat_parts(bool few, int64_t c, int sms) {
-  const int64_t w = few ? few_width(c, sms) : TrainShape::BN;
-  return 2 * ((c + w - 1) / w);
-}
+// Parts of a row's statistics that c columns leave: two a tile. Tiles of one
+// width for all pieces: a last, smaller piece of c columns would be spread
+// better by tiles of its own width (few_width(c), which may be narrower and make
+// more of them), but then its parts have no bound in those of the others.
+int64_t stat_parts(const CeLayout& l, int64_t c) { return 2 * ((c + l.width - 1) / l.width); }
 
 void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_t ldh,
                const void* W, int64_t ldw, bool backward, int sms, CeLayout* l) {
@@ -512,6 +514,7 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
     if (backward) per_row = l->rows * 2 * l->parts;
     if (l->copy_w) per_row = std::max(per_row, l->ldx * 2 * l->parts);
     l->C = piece_rows(V, per_row);
+    l->width = l->few ? few_width(l->C, sms) : TrainShape::BN;
     l->ldz = round_up(l->C, 64);
     if (l->gather) {
       l->counts = take(256);
@@ -532,8 +535,9 @@ void ce_layout(int dtype, int64_t T, int64_t V, int64_t D, const void* H, int64_
       l->slots = take(static_cast<size_t>(l->slot_count) * kSlotBytes);
       l->tail = take(static_cast<size_t>(l->tail_count) * kSlotBytes);
     } else {
-      l->part = take(static_cast<size_t>((V + l->C - 1) / l->C) * stat_parts(l->few, l->C, sms) *
-                     l->rows * sizeof(float2));
+      const int64_t full = (V - 1) / l->C;  // pieces before the last
+      l->stats = (full * stat_parts(*l, l->C) + stat_parts(*l, V - full * l->C)) * l->rows;
+      l->part = take(static_cast<size_t>(l->stats) * sizeof(float2));
       l->state = take(t4);
     }
     l->total = at;
@@ -694,17 +698,14 @@ struct CeCall {
                     "linear_ce product launch");
   }
 
-  int64_t parts_of(int64_t c) const { return stat_parts(l.few, c, ctx.sm_count); }
-
   // A product of few rows with c rows of W, its arguments in a.
   int run_few(int mode, const TrainOperand& w, TrainArgs a) {
     TrainMaps maps;
-    const int width = few_width(a.N, ctx.sm_count);
     const int st = train_operands(bf16(), h_operand(), false, w, false, &maps, &a, few_rows(T),
-                                  width);
+                                  l.width);
     if (st != GEMM14_OK) return st;
     ctx.fault = kFaultNone;
-    return launched(launch_train_few(mode, maps, a, bf16(), width, ctx.sm_count, stream),
+    return launched(launch_train_few(mode, maps, a, bf16(), l.width, ctx.sm_count, stream),
                     "linear_ce few rows launch");
   }
 
@@ -778,15 +779,15 @@ struct CeCall {
       a.v0 = static_cast<int>(v0);
       a.target = l.gather ? r.target : nullptr;
       a.target64 = targets;
-      a.part = at<float2>(l.part) + v0 / l.C * parts_of(l.C) * l.rows;
+      a.part = at<float2>(l.part) + parts * l.rows;
       a.part_ld = l.rows;
-      a.part_count = parts_of(c) * l.rows;
+      a.part_count = l.stats - parts * l.rows;
       a.target_logit = at<float>(l.state);
       const bool promote = D > TrainShape::STATS_CHUNK * TrainShape::BK;
       st = l.few ? run_few(kTrainStats, w, a)
                  : run(kTrainStats, promote, h_operand(), false, w, false, &a);
       if (st != GEMM14_OK) return st;
-      parts = v0 / l.C * parts_of(l.C) + parts_of(c);
+      parts += stat_parts(l, c);
     }
     return combine(at<float2>(l.part), l.rows, parts, at<float>(l.state),
                    l.gather ? r.position : nullptr, loss, lse);
