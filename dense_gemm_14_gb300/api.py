@@ -1,6 +1,8 @@
 """Tensor-level calls on top of the C ABI (argument marshalling only)."""
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import _lib
@@ -8,9 +10,18 @@ from . import _lib
 _CODE = {torch.float32: _lib.GEMM14_DTYPE_F32, torch.bfloat16: _lib.GEMM14_DTYPE_BF16,
          torch.float16: _lib.GEMM14_DTYPE_F16}
 
-# Stream-K workspaces, one per (device, stream): calls on one stream run in
-# order, so they may share it; calls on different streams must not.
+# Workspaces, one per (device, stream): calls on one stream run in order, so
+# they may share it; calls on different streams must not. The launches of a call
+# hand data on through it, so a host thread holds its lock while it makes them:
+# another thread's call on the stream comes before all of them or after.
 _workspaces: dict = {}
+_locks: dict = {}
+
+
+def _workspace_lock(device: torch.device, stream_handle: int):
+    key = (device.index, stream_handle)
+    lock = _locks.get(key)
+    return lock if lock is not None else _locks.setdefault(key, threading.RLock())
 
 
 def _workspace(device: torch.device, stream_handle: int, nbytes: int) -> torch.Tensor:
@@ -90,10 +101,17 @@ def gemm_into(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, alpha: float 
         nbytes = _lib.workspace_bytes_ex(code, ta, tb, M, N, K, a.data_ptr(), lda, b.data_ptr(),
                                          ldb, out.data_ptr(), max(out.stride(0), N, 1)) \
             if M and N and K else 0
-        ws = _workspace(a.device, int(stream or 0), nbytes) if nbytes else None
-        _lib.gemm_ex(code, ta, tb, M, N, K, float(alpha), a.data_ptr(), lda,
-                     b.data_ptr(), ldb, float(beta), out.data_ptr(), max(out.stride(0), N, 1),
-                     ws.data_ptr() if ws is not None else None, nbytes, stream)
+
+        def call(ws):
+            _lib.gemm_ex(code, ta, tb, M, N, K, float(alpha), a.data_ptr(), lda,
+                         b.data_ptr(), ldb, float(beta), out.data_ptr(), max(out.stride(0), N, 1),
+                         ws.data_ptr() if ws is not None else None, nbytes, stream)
+
+        if not nbytes:
+            call(None)
+        else:
+            with _workspace_lock(a.device, int(stream or 0)):
+                call(_workspace(a.device, int(stream or 0), nbytes))
     return out
 
 

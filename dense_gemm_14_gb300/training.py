@@ -6,7 +6,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import _CODE, _FP32_MODES, _workspace, _workspaces
+from .api import _CODE, _FP32_MODES, _workspace, _workspace_lock, _workspaces
 
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -40,18 +40,19 @@ def _in_workspace(device: torch.device, handle: int, call, need, where: str) -> 
     """call(workspace pointer, bytes) on the stream's workspace as it is; where
     it is refused, on one of need() bytes (asked for only then). A call that
     fails otherwise may have run in part, and is not repeated."""
-    ws = _workspaces.get((device.index, handle))
-    if ws is not None:
-        status = call(ws.data_ptr(), ws.numel())
-        if status == _lib.GEMM14_OK:
-            return
-        if status != _lib.GEMM14_ERR_INVALID_ARG:
+    with _workspace_lock(device, handle):
+        ws = _workspaces.get((device.index, handle))
+        if ws is not None:
+            status = call(ws.data_ptr(), ws.numel())
+            if status == _lib.GEMM14_OK:
+                return
+            if status != _lib.GEMM14_ERR_INVALID_ARG:
+                raise _lib.Gemm14Error(status, where)
+        n = need()
+        ws = _workspace(device, handle, n) if n else None
+        status = call(ws.data_ptr() if n else None, ws.numel() if n else 0)
+        if status:
             raise _lib.Gemm14Error(status, where)
-    n = need()
-    ws = _workspace(device, handle, n) if n else None
-    status = call(ws.data_ptr() if n else None, ws.numel() if n else 0)
-    if status:
-        raise _lib.Gemm14Error(status, where)
 
 
 def _matrix(x: torch.Tensor, name: str, device: int | None = None) -> int:

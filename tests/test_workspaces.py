@@ -1,0 +1,108 @@
+"""The workspaces that the tensor-level calls keep for each (device, stream):
+host threads that call on one stream at once."""
+import threading
+import time
+
+import pytest
+import torch
+
+import dense_gemm_14_gb300 as g14
+from dense_gemm_14_gb300 import api, training
+
+
+def in_threads(*bodies):
+    errors = []
+
+    def run(body):
+        try:
+            body()
+        except BaseException as e:  # noqa: BLE001 - reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(b,)) for b in bodies]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not errors, errors
+    assert not any(t.is_alive() for t in threads)
+
+
+def test_launches_of_two_threads_on_one_stream_do_not_interleave(monkeypatch):
+    """A call's launches hand data on through the stream's workspace: none of another
+    thread's call may come between them. Calls on two streams do not wait for each other."""
+    device = torch.device("cuda", 0)
+    monkeypatch.setattr(api, "_workspaces", {})
+    monkeypatch.setattr(training, "_workspaces", api._workspaces)
+    for handle in (7, 8):
+        api._workspaces[(0, handle)] = torch.empty(64, dtype=torch.uint8)
+    launches = []
+
+    def call_of(name):
+        def call(pointer, size):
+            for _ in range(4):
+                launches.append(name)
+                time.sleep(0.005)
+            return g14.GEMM14_OK
+        return call
+
+    def body(name, handle):
+        return lambda: [training._in_workspace(device, handle, call_of(name), lambda: 64, name)
+                        for _ in range(5)]
+
+    in_threads(body("a", 7), body("b", 7))
+    assert len(launches) == 40
+    for i in range(0, 40, 4):
+        assert len(set(launches[i:i + 4])) == 1, launches
+    # two streams: each of the two calls waits for the other to have begun
+    begun = {7: threading.Event(), 8: threading.Event()}
+
+    def meet(handle, other):
+        def call(pointer, size):
+            begun[handle].set()
+            return g14.GEMM14_OK if begun[other].wait(10) else g14.GEMM14_ERR_TIMEOUT
+        return lambda: training._in_workspace(device, handle, call, lambda: 64, "meeting")
+
+    in_threads(meet(7, 8), meet(8, 7))
+
+
+@pytest.mark.gpu
+def test_threads_on_one_stream_give_what_each_gives_alone():
+    def step(T, V, D, dtype, mode, seed):
+        g = torch.Generator().manual_seed(seed)
+        h = torch.randn(T, D, generator=g).to(dtype).cuda()
+        w = (torch.randn(V, D, generator=g) / D ** 0.5).to(dtype).cuda()
+        y = torch.randint(0, V, (T,), generator=g).cuda()
+        up = torch.full((T,), 1.0 / T, device="cuda")
+
+        def run():
+            loss, lse = g14.linear_cross_entropy(h, w, y, fp32_mode=mode)
+            return (loss, lse) + g14.linear_cross_entropy_backward(h, w, y, lse, up, fp32_mode=mode)
+        return run
+
+    def product():
+        g = torch.Generator().manual_seed(9)
+        a = torch.randn(515, 1001, generator=g).cuda()  # copied and split in the workspace
+        b = torch.randn(1001, 333, generator=g).cuda()
+        return lambda: (g14.gemm(a, b, fp32_mode="3xtf32"),)
+
+    def gradient():
+        g = torch.Generator().manual_seed(10)
+        c = g14.ckpt8_save(torch.randn(700, 520, generator=g).bfloat16().cuda())
+        dy = torch.randn(700, 264, generator=g).bfloat16().cuda()
+        return lambda: (g14.ckpt8_weight_grad(dy, c),)
+
+    work = [step(300, 3000, 136, torch.bfloat16, None, 1), step(700, 1031, 72, torch.float16, None, 2),
+            step(60, 2000, 65, torch.float32, "3xtf32", 3), product(), gradient()]
+    want = [run() for run in work]
+    torch.cuda.synchronize()
+    got = [[] for _ in work]
+    in_threads(*[lambda i=i, run=run: got[i].extend(run() for _ in range(30))
+                 for i, run in enumerate(work)])
+    torch.cuda.synchronize()
+    assert g14.check_device_error(torch.cuda.current_stream().cuda_stream) == 0
+    for a, rounds in zip(want, got):
+        assert len(rounds) == 30
+        for b in rounds:
+            for x, z in zip(a, b):
+                assert torch.equal(x, z)
