@@ -1,6 +1,7 @@
 """Tensor-level calls on top of the C ABI (argument marshalling only)."""
 from __future__ import annotations
 
+import contextlib
 import threading
 
 import torch
@@ -18,6 +19,13 @@ _workspaces: dict = {}
 _locks: dict = {}
 
 
+def _current(device: torch.device, stream_handle: int):
+    """A context with the stream current (the caller has `device` current)."""
+    if torch._C._cuda_getCurrentRawStream(device.index) == stream_handle:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, device=device))
+
+
 def _workspace_lock(device: torch.device, stream_handle: int):
     key = (device.index, stream_handle)
     lock = _locks.get(key)
@@ -28,8 +36,11 @@ def _workspace(device: torch.device, stream_handle: int, nbytes: int) -> torch.T
     key = (device.index, stream_handle)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        # zero-filled once: the library leaves only epochs of finished calls in it
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        # zero-filled once: the library leaves only epochs of finished calls in it.
+        # Made on the stream that uses it: the fill comes before the calls, and
+        # what the allocator makes of a smaller one's memory comes after them
+        with _current(device, stream_handle):
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
         _workspaces[key] = ws
     return ws
 

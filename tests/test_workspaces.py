@@ -1,5 +1,6 @@
 """The workspaces that the tensor-level calls keep for each (device, stream):
-host threads that call on one stream at once."""
+host threads that call on one stream at once, and the stream a workspace is made on."""
+import contextlib
 import threading
 import time
 
@@ -64,6 +65,56 @@ def test_launches_of_two_threads_on_one_stream_do_not_interleave(monkeypatch):
         return lambda: training._in_workspace(device, handle, call, lambda: 64, "meeting")
 
     in_threads(meet(7, 8), meet(8, 7))
+
+
+@pytest.mark.parametrize("current", [0, 7])
+def test_a_workspace_is_made_on_the_stream_that_uses_it(current, monkeypatch):
+    """Its zero fill would else run on the current stream, after calls on the other had begun."""
+    stack = [current]
+
+    @contextlib.contextmanager
+    def stream(handle):
+        stack.append(handle)
+        yield
+        stack.pop()
+
+    made = []
+
+    def zeros(n, dtype=None, device=None):
+        made.append((n, stack[-1]))
+        return torch.empty(n, dtype=dtype)
+
+    monkeypatch.setattr(api, "_workspaces", {})
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: stack[-1])
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch, "zeros", zeros)
+    device = torch.device("cuda", 0)
+    small = api._workspace(device, 7, 64)
+    assert api._workspace(device, 7, 32) is small
+    assert api._workspace(device, 7, 128).numel() == 128
+    assert made == [(64, 7), (128, 7)]
+
+
+@pytest.mark.gpu
+def test_a_product_on_a_given_stream_waits_for_nothing_on_the_current_one():
+    """gemm_into's first call on a stream of its own, with the current stream held up: the
+    stream's workspace is zero before the product's split tiles use it."""
+    a = torch.randn(2304, 4096, device="cuda").bfloat16()
+    b = torch.randn(4096, 2560, device="cuda").bfloat16()
+    want = g14.gemm(a, b)
+    side = torch.cuda.Stream()
+    got = torch.empty_like(want)
+    dirt = torch.full((64 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del dirt  # what the allocator hands out next holds no zeros
+    torch.cuda._sleep(1_000_000_000)  # about half a second
+    g14.gemm_into(a, b, got, stream=side)
+    side.synchronize()
+    busy = not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert g14.check_device_error(side.cuda_stream) == 0
+    assert busy and torch.equal(got, want)
 
 
 @pytest.mark.gpu
