@@ -45,6 +45,27 @@ def _workspace(device: torch.device, stream_handle: int, nbytes: int) -> torch.T
     return ws
 
 
+# Bytes at a workspace's start that hold the flags of split products (a 4-byte
+# word per SM): what has to be zero before its first use.
+_FLAG_BYTES = 4096
+
+
+def _capturing() -> bool:
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
+def _graph_workspace(device: torch.device, stream_handle: int, nbytes: int) -> torch.Tensor:
+    """Memory of the graph that is being captured, for one call of it (the
+    graph's pool hands it on to later nodes). A kept workspace would be shared by
+    all that the graph's replays run beside, and its memory given to others when
+    a larger one takes its place; one made during the capture is zero only once
+    the graph has run."""
+    with _current(device, stream_handle):
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:_FLAG_BYTES].zero_()
+    return ws
+
+
 def _check_matrix(x: torch.Tensor, name: str) -> None:
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(x.shape)}")
@@ -83,7 +104,8 @@ def gemm_into(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, alpha: float 
     either a row-major view or the transpose of one (e.g. ``x.t()``), which
     becomes the call's transa / transb; out: (M, N) float32, row-major. With
     beta == 0, out is not read. Uses a stream-K workspace cached per (device,
-    stream) when the product benefits from it. Runs on `stream` (default:
+    stream) when the product benefits from it (in a graph being captured, memory
+    of the graph's own). Runs on `stream` (default:
     torch's current stream) without synchronising. fp32_mode (float32 inputs
     only): "fp32" (default, FFMA), "tf32" or "3xtf32" (tensor cores).
     """
@@ -120,6 +142,8 @@ def gemm_into(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, alpha: float 
 
         if not nbytes:
             call(None)
+        elif _capturing():
+            call(_graph_workspace(a.device, int(stream or 0), nbytes))
         else:
             with _workspace_lock(a.device, int(stream or 0)):
                 call(_workspace(a.device, int(stream or 0), nbytes))

@@ -6,7 +6,8 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import _CODE, _FP32_MODES, _workspace, _workspace_lock, _workspaces
+from .api import (_CODE, _FP32_MODES, _capturing, _graph_workspace, _workspace, _workspace_lock,
+                  _workspaces)
 
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -39,7 +40,15 @@ def _on(stream, device: torch.device, body):
 def _in_workspace(device: torch.device, handle: int, call, need, where: str) -> None:
     """call(workspace pointer, bytes) on the stream's workspace as it is; where
     it is refused, on one of need() bytes (asked for only then). A call that
-    fails otherwise may have run in part, and is not repeated."""
+    fails otherwise may have run in part, and is not repeated. In a graph being
+    captured: on memory of the graph's own."""
+    if _capturing():
+        n = need()
+        ws = _graph_workspace(device, handle, n) if n else None
+        status = call(ws.data_ptr() if n else None, n)
+        if status:
+            raise _lib.Gemm14Error(status, where)
+        return
     with _workspace_lock(device, handle):
         ws = _workspaces.get((device.index, handle))
         if ws is not None:
@@ -104,8 +113,8 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     one GPU; targets: (T,) int64. loss, lse: (T,) float32, 0 for rows whose
     target is ignore_index; a target outside [0, V) gives NaN. Keep lse for
     linear_cross_entropy_backward. Runs on `stream` (default: torch's current
-    stream) without synchronising, with a workspace cached per (device, stream);
-    what it allocates belongs to that stream, and operands made on another are
+    stream) without synchronising, with a workspace cached per (device, stream)
+    (in a graph being captured, memory of the graph's own); what it allocates belongs to that stream, and operands made on another are
     the caller's to order and keep (wait_stream, record_stream).
     fp32_mode as for gemm_into."""
     code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)

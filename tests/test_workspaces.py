@@ -1,5 +1,5 @@
 """The workspaces that the tensor-level calls keep for each (device, stream):
-host threads that call on one stream at once, and the stream a workspace is made on."""
+host threads that call on one stream at once, the stream a workspace is made on, and graphs being captured."""
 import contextlib
 import threading
 import time
@@ -157,3 +157,85 @@ def test_threads_on_one_stream_give_what_each_gives_alone():
         for b in rounds:
             for x, z in zip(a, b):
                 assert torch.equal(x, z)
+
+
+def test_a_captured_call_takes_no_kept_workspace_and_keeps_none(monkeypatch):
+    """A graph holds its workspace's address: one kept for the stream may be replaced (and its
+    memory given away) before a replay, or be used beside it; one made during the capture is
+    zero-filled by the graph alone."""
+    device = torch.device("cpu")
+    kept = torch.full((256,), 0xff, dtype=torch.uint8)
+    monkeypatch.setattr(api, "_workspaces", {(None, 7): kept})
+    monkeypatch.setattr(training, "_workspaces", api._workspaces)
+    monkeypatch.setattr(api, "_current", lambda d, h: contextlib.nullcontext(), raising=False)
+    for module in (api, training):
+        monkeypatch.setattr(module, "_capturing", lambda: True, raising=False)
+    given = []
+
+    def call(pointer, size):
+        given.append((pointer, size))
+        return g14.GEMM14_OK if size >= 128 else g14.GEMM14_ERR_INVALID_ARG
+
+    for n in (128, 512):
+        training._in_workspace(device, 7, call, lambda: n, "a call")
+    assert [size for _, size in given] == [128, 512]
+    assert all(pointer != kept.data_ptr() for pointer, _ in given)
+    assert api._workspaces == {(None, 7): kept}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("warm", [False, True])
+def test_graphs_and_larger_calls_on_one_stream(warm):
+    """Two graphs captured on one stream, larger calls on it afterwards, and what the allocator
+    then makes of smaller workspaces' memory: replays of both graphs at once, on streams of
+    their own, give what the calls gave, and nothing else is written."""
+    def data(T, V, seed):
+        g = torch.Generator().manual_seed(seed)
+        return (torch.randn(T, 136, generator=g).bfloat16().cuda(),
+                (torch.randn(V, 136, generator=g) / 12.0).bfloat16().cuda(),
+                torch.randint(0, V, (T,), generator=g).cuda(), torch.full((T,), 1.0 / T, device="cuda"))
+
+    a = torch.randn(2304, 4096, device="cuda").bfloat16()
+    b = torch.randn(4096, 2560, device="cuda").bfloat16()
+
+    def calls(h, w, y, up):
+        loss, lse = g14.linear_cross_entropy(h, w, y)
+        return (loss, lse) + g14.linear_cross_entropy_backward(h, w, y, lse, up) + (g14.gemm(a, b),)
+
+    sets = [data(300, 3000, 1), data(500, 2500, 2)]
+    want = [calls(*x) for x in sets]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if warm:
+        with torch.cuda.stream(side):
+            calls(*sets[1])
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for x in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got.append(calls(*x))
+        graphs.append(graph)
+    with torch.cuda.stream(side):  # calls of the same stream, before any replay, and larger ones
+        again = calls(*sets[0])
+        large = calls(*data(2000, 30000, 3))
+        other = [torch.full((1 << 20,), 0x5a, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    for x, z in zip(want[0], again):
+        assert torch.equal(x, z)
+    assert all(bool(torch.isfinite(x).all()) for x in large)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                for x in got[i]:
+                    x.fill_(float("nan"))
+                graphs[i].replay()
+        with torch.cuda.stream(side):
+            again = calls(*sets[0])
+        torch.cuda.synchronize()
+        for w_, g_ in list(zip(want, got)) + [(want[0], again)]:
+            for x, z in zip(w_, g_):
+                assert torch.equal(x, z)
+    assert all(bool((o == 0x5a).all()) for o in other)
+    assert g14.check_device_error(side.cuda_stream) == 0
