@@ -709,6 +709,10 @@ struct CeCall {
                     "linear_ce few rows launch");
   }
 
+  // Whether the logits' sums over D are carried in fp32 registers: in both calls,
+  // so that dZ is formed from the logits that lse was.
+  bool long_logits() const { return D > TrainShape::LOGITS_CHUNK * TrainShape::BK; }
+
   // Whether sums over K are carried in fp32 registers: what is written in fp32
   // keeps fp32's accuracy; what is rounded to 16 bits loses nothing by TMEM's.
   bool long_sum(int64_t K) const { return K > TrainShape::CHUNK * TrainShape::BK; }
@@ -783,9 +787,8 @@ struct CeCall {
       a.part_ld = l.rows;
       a.part_count = l.stats - parts * l.rows;
       a.target_logit = at<float>(l.state);
-      const bool promote = D > TrainShape::STATS_CHUNK * TrainShape::BK;
       st = l.few ? run_few(kTrainStats, w, a)
-                 : run(kTrainStats, promote, h_operand(), false, w, false, &a);
+                 : run(kTrainStats, long_logits(), h_operand(), false, w, false, &a);
       if (st != GEMM14_OK) return st;
       parts += stat_parts(l, c);
     }
@@ -820,7 +823,7 @@ struct CeCall {
       a.out_rows = z_rows;
       a.out_cols = c;
       st = l.few ? run_few(kTrainGrad, w, a)
-                 : run(kTrainGrad, exact && long_sum(D), h_operand(), false, w, false, &a);
+                 : run(kTrainGrad, long_logits(), h_operand(), false, w, false, &a);
       if (st != GEMM14_OK) return st;
       // (rows past T's last block of 64 are zeros without being read)
       const TrainOperand dz{ws + l.z, round_up(T, 64), c, l.ldz, l.dz_parts, g_part};

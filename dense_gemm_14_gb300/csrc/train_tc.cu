@@ -431,7 +431,8 @@ struct Epilogue {
 template <int kMode, bool kPromote, int kWidth>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::THREADS, 1)
     train_tc_kernel(const __grid_constant__ TrainMaps maps, const TrainArgs args) {
-  constexpr int kChunk = kMode == kTrainStats ? S::STATS_CHUNK : S::CHUNK;
+  constexpr int kChunk =
+      kMode == kTrainStats || kMode == kTrainGrad ? S::LOGITS_CHUNK : S::CHUNK;
   constexpr int kHalf = kWidth / 2;  // a CTA's columns of B, and a warp's of D
   constexpr int kChunks = kHalf / 32;
   extern __shared__ uint8_t smem_raw[];

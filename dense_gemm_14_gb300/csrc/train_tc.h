@@ -44,12 +44,17 @@ struct TrainShape {
   // k-blocks, leave 6e-7. Half as many leave 3e-7 and cost 1 to 5 % (wgrad 8192 x
   // 4096 x 11008: 535 -> 563 us): the drains then wait for each other.
   static constexpr int CHUNK = 16;
-  // The same for the loss's statistics: truncation moves logits one way, a learnt
-  // row's target the furthest, and adds up in lse - z_y, which is small there. After
-  // 64 MMAs the losses of 600 such rows of fp16 over 1000 x 960 were 1.2e-6 off (an fp32
-  // product: 4e-7), after 32 they are 5e-7. 2047 x 50021 x 1000 fp16, both
-  // directions: 572 -> 579 us; 4096 x 65536 x 4096 bf16 the same within 0.5 %.
-  static constexpr int STATS_CHUNK = 8;
+  // The same for logits, in both directions. Truncation moves them one way, a
+  // learnt row's target the furthest, and adds up in lse - z_y, which is small
+  // there: after 64 MMAs the losses of 600 such rows of fp16 over 1000 x 960 were
+  // 1.2e-6 off (an fp32 product: 4e-7), after 32 they are 5e-7. dZ_y = exp(z_y -
+  // lse) - 1 is such a difference too, and wants the very sums that lse came
+  // from: with all of 4096 terms in one accumulator in the backward pass alone, dH of
+  // rows of p_y = 0.99 .. 0.9995 was up to 11 % (bf16) and 19 % (fp16) off,
+  // with 8192 terms 23 and 30 %; so it is 0.5 and 0.3 %, dZ's rounding or p_y's.
+  // A step of 4096 x 65536 x 4096 bf16 takes 5533 -> 5679 us for it, 2047 x 50021 x
+  // 1000 fp16 576 -> 591, 515 x 8191 x 769 fp32 256 -> 260.
+  static constexpr int LOGITS_CHUNK = 8;
 };
 
 struct TrainArgs {
