@@ -713,9 +713,17 @@ struct CeCall {
   // so that dZ is formed from the logits that lse was.
   bool long_logits() const { return D > TrainShape::LOGITS_CHUNK * TrainShape::BK; }
 
-  // Whether sums over K are carried in fp32 registers: what is written in fp32
-  // keeps fp32's accuracy; what is rounded to 16 bits loses nothing by TMEM's.
-  bool long_sum(int64_t K) const { return K > TrainShape::CHUNK * TrainShape::BK; }
+  // Whether a gradient's sums over K are carried in fp32 registers. Written in
+  // fp32 they keep fp32's accuracy. Rounded to 16 bits they may be off by a
+  // fraction of that rounding: 262144 terms in one truncating accumulator left
+  // dH of fp16 2.6 times its rounding off (its largest term came first), 700000
+  // of bf16 0.9 times, so 0.16 times is left for as many as may stay there.
+  bool long_sum(int64_t K) const {
+    const int64_t most = l.parts == 3 ? TrainShape::CHUNK * TrainShape::BK
+                         : bf16()     ? int64_t(131072)
+                                      : int64_t(16384);
+    return K > most;
+  }
 
   // ---- a handful of rows
 
@@ -839,7 +847,7 @@ struct CeCall {
         a.slots = at<float4>(l.slots);
         a.slot_count = l.slot_count;
         a.add = v0 > 0;
-        if ((st = run(kTrainSlots, exact && long_sum(c), both, false, w, true, &a)) != GEMM14_OK)
+        if ((st = run(kTrainSlots, long_sum(c), both, false, w, true, &a)) != GEMM14_OK)
           return st;
       }
       if (dW) {
@@ -855,7 +863,7 @@ struct CeCall {
         a.slot_count = l.tail_count;
         a.out_rows = c;
         a.out_cols = D;
-        if ((st = run(kTrainOut, exact && long_sum(T), dz, true, h_operand(), true, &a)) !=
+        if ((st = run(kTrainOut, long_sum(T), dz, true, h_operand(), true, &a)) !=
             GEMM14_OK)
           return st;
         if (may_split(a, clusters)) {

@@ -354,11 +354,11 @@ int gemm14_host_synchronize(void);
  * for gemm14_gemm_ex (F32, BF16, F16, TF32, F32_3XTF32). F32_3XTF32 here
  * splits each fp32 value into three bf16 parts (their sum is the value to 24
  * bits) and sums the six products of parts above 2^-24 of the whole: the fp32
- * bound, at tensor-core speed; an infinite input gives NaN. Sums whose result is
- * fp32 leave the tensor cores' accumulators every 1024 terms (fp32 gradients,
- * gemm14_ckpt8_wgrad), or every 512 or fewer (losses), and are carried in fp32
- * registers, as the accumulators add with truncation. Up to 32 rows of F32
- * or F32_3XTF32 run as fp32 FMAs on the CUDA cores.
+ * bound, at tensor-core speed; an infinite input gives NaN. As the tensor cores'
+ * accumulators add with truncation, sums leave them for fp32 registers: logits
+ * every 512 terms or fewer, fp32 gradients and gemm14_ckpt8_wgrad every 1024, and
+ * so 16-bit gradients of more than 16384 (F16) or 131072 (BF16) terms. Up to
+ * 32 rows of F32 or F32_3XTF32 run as fp32 FMAs on the CUDA cores.
  * loss and lse: T fp32.
  * targets: T int64 on the device. A row whose target is ignore_index takes no
  * part: its loss and lse are 0 and nothing its row of H holds is used. Any
