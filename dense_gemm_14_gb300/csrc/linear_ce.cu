@@ -441,10 +441,18 @@ int64_t piece_rows(int64_t V, int64_t per_row) {
 
 // Whether a handful of rows run on the CUDA cores (linear_ce_narrow.cu): fp32
 // ones, in the modes that keep the fp32 bound (and no wider than a grid's second
-// dimension reaches).
+// dimension reaches). The FFMA mode's other side is the library's products: 32 x
+// 32768 x 4096, loss and gradients, 1937 us here against 2281, 32 x 100000 x 900
+// 866 against 1836. The split mode's is the tensor cores on W's parts. Up to 16
+// rows are ahead here (16 x 32768 x 4096 817 us against 1312, 1 row 404 against 1310),
+// and 17 to 32 while shared memory holds them (32 x 65536 x 1024 587 against 619,
+// x 1536 946 against 934, 17 rows 909 against 933); wider ones are loaded again, in
+// slices, for each 32 rows of W, as many bytes as those: 17 x 65536 x 1600 1591
+// against 1000, 32 rows 2072 against 999.
 bool on_cuda_cores(int dtype, int64_t T, int64_t D) {
-  return (dtype == GEMM14_DTYPE_F32 || dtype == GEMM14_DTYPE_F32_3XTF32) && T <= kNarrowRows &&
-         D <= kNarrowMaxD;
+  if (T > kNarrowRows || D > kNarrowMaxD) return false;
+  return dtype == GEMM14_DTYPE_F32 ||
+         (dtype == GEMM14_DTYPE_F32_3XTF32 && (T <= 16 || narrow_in_one_slice(T, D)));
 }
 
 struct CeLayout {

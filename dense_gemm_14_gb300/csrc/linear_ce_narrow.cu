@@ -395,6 +395,12 @@ cudaError_t run(const NarrowArgs& a, bool backward, int sm_count, cudaStream_t s
 
 }  // namespace
 
+bool narrow_in_one_slice(int64_t T, int64_t D) {
+  int kT = 1;
+  while (kT < T) kT *= 2;
+  return slice_of(kT, D) >= D;
+}
+
 int narrow_blocks(int64_t V, int sm_count) {
   const int64_t most = (V + 31) / 32;  // (4 rows of W for each of 8 warps)
   return static_cast<int>(std::min<int64_t>(most, sm_count));

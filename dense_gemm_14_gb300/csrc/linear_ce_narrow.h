@@ -39,6 +39,7 @@ struct NarrowArgs {
   int64_t lddw;
 };
 
+bool narrow_in_one_slice(int64_t T, int64_t D);  // whether a block's shared memory holds H
 int narrow_blocks(int64_t V, int sm_count);            // of the logits' launch
 int narrow_splits(int T, int64_t V, int64_t D, int sm_count);  // of dH's sum over the vocabulary
 cudaError_t launch_narrow_stats(const NarrowArgs& a, int sm_count, cudaStream_t stream);

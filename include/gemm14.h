@@ -358,7 +358,8 @@ int gemm14_host_synchronize(void);
  * accumulators add with truncation, sums leave them for fp32 registers: logits
  * every 512 terms or fewer, fp32 gradients and gemm14_ckpt8_wgrad every 1024, and
  * so 16-bit gradients of more than 16384 (F16) or 131072 (BF16) terms. Up to
- * 32 rows of F32 or F32_3XTF32 run as fp32 FMAs on the CUDA cores.
+ * 32 rows of F32 run as fp32 FMAs on the CUDA cores, and so do up to 16 of
+ * F32_3XTF32, or 32 where D <= 1536.
  * loss and lse: T fp32.
  * targets: T int64 on the device. A row whose target is ignore_index takes no
  * part: its loss and lse are 0 and nothing its row of H holds is used. Any
@@ -528,8 +529,8 @@ int gemm14_set_pair_kernel(int enable);
  * The fp32 small-product kernel (plan kernel 6) synchronises only through
  * block and cluster barriers, with no mbarrier wait to expire: a call that
  * runs on it consumes the request and computes C as usual; so do
- * gemm14_linear_ce_* calls of up to 32 fp32 rows and gemm14_ckpt8_wgrad calls of up
- * to 16 rows. (gemm14_ckpt8_save and _restore wait for nothing and leave the
+ * gemm14_linear_ce_* calls of fp32 rows that run on the CUDA cores and
+ * gemm14_ckpt8_wgrad calls of up to 16 rows. (gemm14_ckpt8_save and _restore wait for nothing and leave the
  * request to the next call.)
  * Returns GEMM14_ERR_INVALID_ARG for an unknown mode.
  */

@@ -242,7 +242,28 @@ bool check(const Case& c) {
 }
 }  // namespace
 
+// Whether a forward call runs on the tensor cores.
+bool on_tensor_cores(int dtype, int64_t T, int64_t V, int64_t D) {
+  const size_t bytes =
+      gemm14_linear_ce_workspace_bytes(dtype, 0, T, V, D, kH, D, kW, D, kSms);
+  g_launches.clear();
+  if (gemm14_linear_ce_forward(dtype, T, V, D, kH, D, kW, D,
+                               reinterpret_cast<const int64_t*>(kOut + (1 << 30)), -100,
+                               reinterpret_cast<float*>(kOut), reinterpret_cast<float*>(kOut + 4096),
+                               kWorkspace, bytes, nullptr) != GEMM14_OK)
+    return false;
+  for (const Launch& l : g_launches)
+    if (l.name.find("train_") != std::string::npos) return true;
+  return false;
+}
+
 int main() {
+  // fp32 rows: on the CUDA cores up to 32, in split arithmetic while that is the faster side
+  for (int64_t T : {1, 8, 16, 17, 24, 32})
+    for (int64_t D : {64, 1536, 1537, 4096, 12000}) {
+      if (on_tensor_cores(GEMM14_DTYPE_F32, T, 5000, D)) return 3;
+      if (on_tensor_cores(GEMM14_DTYPE_F32_3XTF32, T, 5000, D) != (T > 16 && D > 1536)) return 4;
+    }
   long calls = 0, bad = 0;
   const auto run = [&](const Case& c) {
     ++calls;
