@@ -363,8 +363,11 @@ int gemm14_host_synchronize(void);
  * loss and lse: T fp32.
  * targets: T int64 on the device. A row whose target is ignore_index takes no
  * part: its loss and lse are 0 and nothing its row of H holds is used. Any
- * other target outside [0, V) gives a loss of NaN. A NaN or infinity among a
- * row's logits makes that row's results NaN and no other's.
+ * other target outside [0, V) gives a loss of NaN. A NaN or +infinity among a
+ * row's logits makes that row's results NaN and no other's. A logit of -infinity
+ * stands for a probability of 0: the target's gives a loss of +infinity, a row of
+ * nothing else an lse of -infinity and a loss of NaN. (Where W holds infinities,
+ * gradients multiply them, by 0 too, which is NaN.)
  * workspace: caller-owned, 16-byte aligned, zero-filled before its first use
  * (one kept for the *_ws calls serves, and the other way round),
  * gemm14_linear_ce_workspace_bytes(...) bytes at least; a smaller one is
