@@ -3,11 +3,12 @@
 // multiplies, so that the call is bound by reading W (and writing dW) however
 // plainly it multiplies, and what matters is to touch W once in each product.
 // The tensor-core path has to write W's three bf16 parts first and read them
-// back, 22 bytes a value against 4: 100000 x 900 from one row took 372 us
-// forward and 740 backward, here 85 and 235 (from 16 rows 146 and 379).
+// back, 22 bytes a value against 4: 100000 x 900 from one row takes 288 us
+// forward and 633 backward, here 80 and 204 (from 16 rows 145 and 344).
 //
-//   logits: a warp takes 4 rows of W, a lane 16 bytes of each at a time against every row of H, held in shared memory, a block's
-//     rows together through slices of D when H does not fit; the lanes' sums are
+//   logits: a warp takes 4 rows of W, a lane 16 bytes of each at a time against
+//     every row of H, held in shared memory, a block's rows together through
+//     slices of D when H does not fit; the lanes' sums are
 //     exchanged once a row (31 shuffles for 32 sums) and each lane keeps the
 //     statistics, or writes dZ, of its own pair of rows. From 16 rows on, reading H
 //     from shared memory bounds it (4 cycles for 16 multiplies a lane);

@@ -11,13 +11,13 @@
 // one row's 128 columns, so that a row's maximum and sum need no exchange
 // between threads.
 //
-// Measured (GB300): 4096 x 65536 x 4096 bf16 statistics 1130 us, 1.95 PFLOP/s alone;
-// a whole step of loss and gradients runs at 1.62, the power limit. About 9 us of
+// Measured (GB300): 4096 x 65536 x 4096 bf16 losses 1224 us, 1.80 PFLOP/s; a whole
+// step of loss and gradients runs at 1.55 to 1.60, the power limit. About 9 us of
 // each launch are its start and its last tile's epilogue.
 //
-// Long sums (kPromote): the accumulator is drained every CHUNK k-blocks into 128
-// fp32 registers a thread and starts again from zero while the MMAs go on in
-// the other one.
+// Long sums (kPromote): the accumulator is drained every CHUNK k-blocks (logits:
+// LOGITS_CHUNK) into 128 fp32 registers a thread and starts again from zero while
+// the MMAs go on in the other one.
 //
 // Every wait is bounded (ptx.cuh); a CTA that gives up raises its peer's abort
 // flag, and both meet at a cluster barrier before TMEM is freed.

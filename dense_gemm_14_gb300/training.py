@@ -1,6 +1,7 @@
 """Tensor-level calls of the training products: softmax cross entropy over a
 projection's outputs, and activations kept in 8 bits (argument marshalling
-only; every step runs in the library's CUDA kernels)."""
+only; every step runs in the library's CUDA kernels). None of them is recorded
+by autograd."""
 from __future__ import annotations
 
 import torch
@@ -115,7 +116,8 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     linear_cross_entropy_backward. Runs on `stream` (default: torch's current
     stream) without synchronising, with a workspace cached per (device, stream)
     (in a graph being captured, memory of the graph's own); what it allocates belongs to that stream, and operands made on another are
-    the caller's to order and keep (wait_stream, record_stream).
+    the caller's to order and keep (wait_stream, record_stream). Not recorded by
+    autograd: linear_cross_entropy_backward forms the gradients.
     fp32_mode as for gemm_into."""
     code, T, V, D, ldh, ldw = _ce_operands(h, w, targets, fp32_mode)
 

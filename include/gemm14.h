@@ -372,7 +372,8 @@ int gemm14_host_synchronize(void);
  * (one kept for the *_ws calls serves, and the other way round),
  * gemm14_linear_ce_workspace_bytes(...) bytes at least; a smaller one is
  * GEMM14_ERR_INVALID_ARG, and gemm14_last_error_string says how many are
- * needed. A call is several launches that hand data on through it: host
+ * needed. (A forward call keeps 8 bytes for each row and 128 columns, T V / 16 bytes
+ * of it; the rest is bounded by pieces of the vocabulary.) A call is several launches that hand data on through it: host
  * threads that share a workspace, on one stream too, make their calls one after
  * the other (a lock around the call; the work itself stays asynchronous).
  * Sizes: T >= 0 (0: nothing is done), V >= 1, D >= 1, each at most
