@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}  # 2^-p, p significant bits
 
 
-@pytest.mark.parametrize("T", [129, 300])
+@pytest.mark.parametrize("T", [32, 100, 129, 300])
 @pytest.mark.parametrize("D", [1024, 4096, 8192])
 @pytest.mark.parametrize("dtype,mode", [(torch.bfloat16, None), (torch.float16, None),
                                         (torch.float32, "3xtf32"), (torch.float32, "fp32")])
@@ -42,7 +42,6 @@ def test_gradients_of_learnt_rows(T, D, dtype, mode):
     dh = g14.linear_cross_entropy_backward(h, w, y, lse, up, need_dw=False, fp32_mode=mode)[0]
     off = (dh.double() - want).norm(dim=1) / want.norm(dim=1)
     allowed = 2.5 * U[dtype] + 1.5e-6 / rest
-    print(D, dtype, mode, float(off[learnt].max()), float((off / allowed)[learnt].max()))
     assert bool((off <= allowed)[learnt].all()), float((off / allowed)[learnt].max())
 
 
@@ -68,5 +67,4 @@ def test_sums_over_a_large_vocabulary(dtype, V, D):
     dh = g14.linear_cross_entropy_backward(h, w, y, lse, up, need_dw=False)[0]
     once = float((want.to(dtype).double() - want).norm())
     off = float((dh.double() - want).norm())
-    print(dtype, V, off / float(want.norm()), once / float(want.norm()), float(((dh.double() - want) * want.sign()).mean() / want.abs().mean()))
     assert off <= 1.1 * once + 1e-5 * float(want.norm()), (off, once)
