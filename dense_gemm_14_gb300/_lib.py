@@ -46,6 +46,7 @@ SIGNATURES = {
     "gemm14_plan_gemm": (_int, [_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int,
                                 ctypes.POINTER(_Plan)]),
     "gemm14_version": (_int, []),
+    "gemm14_capture_id": (ctypes.c_uint64, [_vp]),
     "gemm14_debug_inject": (_int, [_int, ctypes.c_uint64]),
     "gemm14_set_pair_kernel": (_int, [_int]),
     "gemm_f32_ws": (_int, _GEMM_ARGS[:9] + [_vp, ctypes.c_size_t, _vp]),
@@ -335,6 +336,11 @@ def debug_inject(fault: int, wait_limit_ns: int = 0) -> int:
     """Failure-detection hook: the next call on this thread runs with `fault`
     (1 = the producer never loads its first stage) and the given wait limit."""
     return int(load().gemm14_debug_inject(fault, wait_limit_ns))
+
+
+def capture_id(stream=None) -> int:
+    """The number of the graph capture that the stream is part of, 0: none."""
+    return int(load().gemm14_capture_id(stream))
 
 
 def set_pair_kernel(enable: bool) -> bool:

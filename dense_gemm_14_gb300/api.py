@@ -54,15 +54,24 @@ def _capturing() -> bool:
     return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
 
 
+# The workspace of the latest capture on a (device, stream), with its number.
+_graph_workspaces: dict = {}
+
+
 def _graph_workspace(device: torch.device, stream_handle: int, nbytes: int) -> torch.Tensor:
-    """Memory of the graph that is being captured, for one call of it (the
-    graph's pool hands it on to later nodes). A kept workspace would be shared by
-    all that the graph's replays run beside, and its memory given to others when
-    a larger one takes its place; one made during the capture is zero only once
-    the graph has run."""
-    with _current(device, stream_handle):
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        ws[:_FLAG_BYTES].zero_()
+    """Memory of the graph that is being captured, for its calls on the stream,
+    its flags zeroed in the graph (one node, of 2 to 4 us). A kept workspace would
+    be shared by all that the graph's replays run beside, and its memory given
+    to others when a larger one takes its place; and one made during a capture
+    is zero only once its graph has run."""
+    capture = _lib.capture_id(stream_handle)
+    key = (device.index, stream_handle)
+    last, ws = _graph_workspaces.get(key, (None, None))
+    if last != capture or ws.numel() < nbytes:
+        with _current(device, stream_handle):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            ws[:_FLAG_BYTES].zero_()
+        _graph_workspaces[key] = (capture, ws)
     return ws
 
 
@@ -142,11 +151,10 @@ def gemm_into(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, alpha: float 
 
         if not nbytes:
             call(None)
-        elif _capturing():
-            call(_graph_workspace(a.device, int(stream or 0), nbytes))
         else:
             with _workspace_lock(a.device, int(stream or 0)):
-                call(_workspace(a.device, int(stream or 0), nbytes))
+                make = _graph_workspace if _capturing() else _workspace
+                call(make(a.device, int(stream or 0), nbytes))
     return out
 
 

@@ -824,6 +824,16 @@ int gemm14_debug_inject(int fault, uint64_t wait_limit_ns) {
   return GEMM14_OK;
 }
 
+uint64_t gemm14_capture_id(void* stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 int gemm14_version(void) { return 210; }
 
 }  // extern "C"

@@ -43,15 +43,9 @@ def _in_workspace(device: torch.device, handle: int, call, need, where: str) -> 
     it is refused, on one of need() bytes (asked for only then). A call that
     fails otherwise may have run in part, and is not repeated. In a graph being
     captured: on memory of the graph's own."""
-    if _capturing():
-        n = need()
-        ws = _graph_workspace(device, handle, n) if n else None
-        status = call(ws.data_ptr() if n else None, n)
-        if status:
-            raise _lib.Gemm14Error(status, where)
-        return
     with _workspace_lock(device, handle):
-        ws = _workspaces.get((device.index, handle))
+        capturing = _capturing()
+        ws = None if capturing else _workspaces.get((device.index, handle))
         if ws is not None:
             status = call(ws.data_ptr(), ws.numel())
             if status == _lib.GEMM14_OK:
@@ -59,7 +53,8 @@ def _in_workspace(device: torch.device, handle: int, call, need, where: str) -> 
             if status != _lib.GEMM14_ERR_INVALID_ARG:
                 raise _lib.Gemm14Error(status, where)
         n = need()
-        ws = _workspace(device, handle, n) if n else None
+        make = _graph_workspace if capturing else _workspace
+        ws = make(device, handle, n) if n else None
         status = call(ws.data_ptr() if n else None, ws.numel() if n else 0)
         if status:
             raise _lib.Gemm14Error(status, where)

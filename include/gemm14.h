@@ -540,6 +540,14 @@ int gemm14_set_pair_kernel(int enable);
  */
 int gemm14_debug_inject(int fault, uint64_t wait_limit_ns);
 
+/*
+ * The number of the CUDA graph capture that `stream` is part of (distinct for
+ * every capture of the process), 0: it is not being captured. A workspace that
+ * is made during a capture, and zero-filled in the graph, serves the calls of
+ * that capture on that stream and no others: this tells them apart.
+ */
+uint64_t gemm14_capture_id(void* stream);
+
 /* Library version, major * 10000 + minor * 100 + patch. */
 int gemm14_version(void);
 

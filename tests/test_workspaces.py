@@ -168,6 +168,9 @@ def test_a_captured_call_takes_no_kept_workspace_and_keeps_none(monkeypatch):
     monkeypatch.setattr(api, "_workspaces", {(None, 7): kept})
     monkeypatch.setattr(training, "_workspaces", api._workspaces)
     monkeypatch.setattr(api, "_current", lambda d, h: contextlib.nullcontext(), raising=False)
+    monkeypatch.setattr(api, "_graph_workspaces", {}, raising=False)
+    captures = []
+    monkeypatch.setattr(api._lib, "capture_id", lambda stream: captures[-1], raising=False)
     for module in (api, training):
         monkeypatch.setattr(module, "_capturing", lambda: True, raising=False)
     given = []
@@ -176,9 +179,10 @@ def test_a_captured_call_takes_no_kept_workspace_and_keeps_none(monkeypatch):
         given.append((pointer, size))
         return g14.GEMM14_OK if size >= 128 else g14.GEMM14_ERR_INVALID_ARG
 
-    for n in (128, 512):
+    for capture, n in ((1, 256), (1, 128), (1, 512), (2, 128), (2, 128)):
+        captures.append(capture)
         training._in_workspace(device, 7, call, lambda: n, "a call")
-    assert [size for _, size in given] == [128, 512]
+    assert [size for _, size in given] == [256, 256, 512, 128, 128]  # one for a capture, while it is enough
     assert all(pointer != kept.data_ptr() for pointer, _ in given)
     assert api._workspaces == {(None, 7): kept}
 
