@@ -19,9 +19,12 @@ from ._lib import (GEMM14_DTYPE_BF16, GEMM14_DTYPE_F16, GEMM14_DTYPE_F32,
                    capture_id, check_device_error, debug_inject, gemm_bf16_f32acc, gemm_bf16_f32acc_ws,
                    gemm_bf16_f32acc_noalloc, gemm_ex, gemm_host, host_synchronize, host_wait, workspace_bytes_ex, gemm_f16_f32acc, gemm_f16_f32acc_ws, gemm_f32,
                    gemm_f32_3xtf32, gemm_f32_ws, gemm_tf32_f32acc, last_error_string, linear_ce_forward, linear_ce_backward,
-                   linear_ce_workspace_bytes, ckpt8_save_raw, ckpt8_restore_raw, ckpt8_wgrad, ckpt8_wgrad_workspace_bytes, lib_path, load, plan, plan_ex, set_pair_kernel, status_string, version, workspace_bytes)
+                   linear_ce_workspace_bytes, ckpt8_save_raw, ckpt8_restore_raw, ckpt8_wgrad, ckpt8_wgrad_workspace_bytes,
+                   TensorArg, embedding_backward_raw, embedding_backward_workspace_bytes, embedding_raw, grad_clip_raw,
+                   grad_norm_raw, grad_workspace_bytes, lib_path, load, plan, plan_ex, set_pair_kernel, status_string, version, workspace_bytes)
 from .api import HostGemm, gemm, gemm_async, gemm_into
-from .training import (Ckpt8, ckpt8_restore, ckpt8_save, ckpt8_weight_grad,
+from .training import (Ckpt8, GradList, ckpt8_restore, ckpt8_save, ckpt8_weight_grad,
+                       clip_grad_norm, embedding, embedding_backward, grad_norm,
                        linear_cross_entropy, linear_cross_entropy_backward)
 
 __all__ = [
@@ -33,6 +36,10 @@ __all__ = [
     "linear_ce_backward", "linear_ce_workspace_bytes",
     "Ckpt8", "ckpt8_save", "ckpt8_restore", "ckpt8_weight_grad", "ckpt8_save_raw",
     "ckpt8_restore_raw", "ckpt8_wgrad", "ckpt8_wgrad_workspace_bytes",
+    "embedding", "embedding_backward", "embedding_raw", "embedding_backward_raw",
+    "embedding_backward_workspace_bytes",
+    "GradList", "TensorArg", "grad_norm", "clip_grad_norm", "grad_norm_raw", "grad_clip_raw",
+    "grad_workspace_bytes",
     "last_error_string", "plan", "plan_ex", "Plan",
     "capture_id", "check_device_error", "debug_inject", "set_pair_kernel", "status_string", "version", "load", "lib_path", "Gemm14Error",
     "GEMM14_DTYPE_F32", "GEMM14_DTYPE_BF16", "GEMM14_DTYPE_F16", "GEMM14_DTYPE_TF32",

@@ -34,6 +34,13 @@ class _Plan(ctypes.Structure):
                 ("vec_store", _int), ("tiles", _i64), ("grid", _int)]
 
 
+class TensorArg(ctypes.Structure):
+    """gemm14_tensor: a gradient in a list of them."""
+    _fields_ = [("data", _vp), ("rows", _i64), ("cols", _i64), ("ld", _i64), ("dtype", _int)]
+
+
+_TENSORS = ctypes.POINTER(TensorArg)
+
 SIGNATURES = {
     "gemm_f32": (_int, _GEMM_ARGS),
     "gemm_bf16_f32acc": (_int, _GEMM_ARGS),
@@ -79,6 +86,17 @@ SIGNATURES = {
                                   _vp]),
     "gemm14_ckpt8_wgrad_workspace_bytes": (ctypes.c_size_t, [_int, _i64, _i64, _i64, _vp, _i64,
                                                              _vp, _i64, _int]),
+    "gemm14_embedding_forward": (_int, [_int, _int, _i64, _i64, _i64, _vp, _i64, _vp, _int, _i64,
+                                        ctypes.c_float, _vp, _i64, _vp]),
+    "gemm14_embedding_backward": (_int, [_int, _int, _i64, _i64, _i64, _vp, _i64, _vp, _int, _i64,
+                                         ctypes.c_float, ctypes.c_float, _vp, _i64, _vp,
+                                         ctypes.c_size_t, _vp]),
+    "gemm14_embedding_backward_workspace_bytes": (ctypes.c_size_t, [_int, _i64, _i64, _i64, _int]),
+    "gemm14_grad_norm": (_int, [_i64, _TENSORS, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t,
+                                _vp]),
+    "gemm14_grad_clip": (_int, [_i64, _TENSORS, _TENSORS, ctypes.c_float, ctypes.c_float, _vp, _vp,
+                                _vp, ctypes.c_size_t, _vp]),
+    "gemm14_grad_workspace_bytes": (ctypes.c_size_t, [_i64, _int]),
 }
 
 _lib = None
@@ -320,6 +338,58 @@ def ckpt8_wgrad_workspace_bytes(dtype: int, T, N, K, dY, lddy, dW, lddw,
     """C ABI gemm14_ckpt8_wgrad_workspace_bytes: workspace for these exact operands."""
     return int(load().gemm14_ckpt8_wgrad_workspace_bytes(dtype, T, N, K, dY, lddy, dW, lddw,
                                                          sm_count))
+
+
+def embedding_raw(dtype: int, dtype_out: int, T, V, D, W, ldw, tokens, token_bytes, ignore_index,
+                  scale, out, ldo, stream=None, check=True) -> int:
+    """C ABI gemm14_embedding_forward on raw device pointers (ints)."""
+    st = int(load().gemm14_embedding_forward(dtype, dtype_out, T, V, D, W, ldw, tokens, token_bytes,
+                                             ignore_index, scale, out, ldo, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_embedding_forward")
+    return st
+
+
+def embedding_backward_raw(dtype: int, dtype_out: int, T, V, D, dY, lddy, tokens, token_bytes,
+                           ignore_index, scale, beta, dW, lddw, workspace, workspace_bytes,
+                           stream=None, check=True) -> int:
+    """C ABI gemm14_embedding_backward on raw device pointers (ints)."""
+    st = int(load().gemm14_embedding_backward(dtype, dtype_out, T, V, D, dY, lddy, tokens,
+                                              token_bytes, ignore_index, scale, beta, dW, lddw,
+                                              workspace, workspace_bytes, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_embedding_backward")
+    return st
+
+
+def embedding_backward_workspace_bytes(dtype: int, T, V, D, sm_count: int = 0) -> int:
+    """C ABI gemm14_embedding_backward_workspace_bytes."""
+    return int(load().gemm14_embedding_backward_workspace_bytes(dtype, T, V, D, sm_count))
+
+
+def grad_norm_raw(n, grads, scale, norm, each, workspace, workspace_bytes, stream=None,
+                  check=True) -> int:
+    """C ABI gemm14_grad_norm; grads: a ctypes array of n TensorArg (or None)."""
+    st = int(load().gemm14_grad_norm(n, grads, scale, norm, each, workspace, workspace_bytes,
+                                     stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_grad_norm")
+    return st
+
+
+def grad_clip_raw(n, grads, out, scale, max_norm, norm, each, workspace, workspace_bytes,
+                  stream=None, check=True) -> int:
+    """C ABI gemm14_grad_clip; grads and out (None: in place): ctypes arrays of n TensorArg."""
+    st = int(load().gemm14_grad_clip(n, grads, out, scale, max_norm, norm, each, workspace,
+                                     workspace_bytes, stream))
+    if check and st:
+        raise Gemm14Error(st, "gemm14_grad_clip")
+    return st
+
+
+def grad_workspace_bytes(n, sm_count: int = 0) -> int:
+    """C ABI gemm14_grad_workspace_bytes: workspace of the two calls on n tensors."""
+    return int(load().gemm14_grad_workspace_bytes(n, sm_count))
 
 
 def last_error_string() -> str:

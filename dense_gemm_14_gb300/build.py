@@ -31,9 +31,9 @@ SOURCES = ["api.cu", "sgemm_simt.cu", "sgemm_small.cu", "hgemm_tc.cu", "hgemm_tc
            "sgemm_tc3.cu", "epilogue.cu", "host_path.cu", "copy.cu", "plan.cu",
            "train_tc.cu",
            "linear_ce.cu",
-           "linear_ce_narrow.cu", "ckpt8.cu"]
+           "linear_ce_narrow.cu", "ckpt8.cu", "embedding.cu", "grad_norm.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "streamk.cuh", "api_internal.h", "plan.h", "checks.h", "train_tc.h",
-           "unaligned.cuh",
+           "unaligned.cuh", "elements.cuh",
            "operand_copy.cuh",
            "linear_ce_narrow.h",
            "libgemm14.map"]

@@ -834,7 +834,7 @@ uint64_t gemm14_capture_id(void* stream) {
   return status == cudaStreamCaptureStatusActive ? id : 0;
 }
 
-int gemm14_version(void) { return 210; }
+int gemm14_version(void) { return 211; }
 
 }  // extern "C"
 

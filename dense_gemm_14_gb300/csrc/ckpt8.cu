@@ -18,6 +18,7 @@
 
 #include "../../include/gemm14.h"
 #include "api_internal.h"
+#include "elements.cuh"
 #include "kernels.h"
 #include "operand_copy.cuh"
 #include "plan.h"
@@ -29,20 +30,6 @@ namespace {
 
 constexpr int kBlock = 32;       // columns that share a scale
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
 // The scale byte of a block whose largest magnitude has these fp32 bits (a
 // NaN's bits, sign cleared, compare above every number's).

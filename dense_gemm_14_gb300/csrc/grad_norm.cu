@@ -1,0 +1,667 @@
+// grad_norm.cu -- the norm of many gradients taken together (and of each), and
+// the gradients scaled so that it stays within a limit:
+//     N = |scale| sqrt(sum over tensors and elements of g^2),
+//     f = scale min(1, max_norm / N),    out = f g.
+// One reading of the gradients for the norm, one reading and one writing for
+// the scaling: memory-bound, so the whole list goes in one launch a pass,
+// however many tensors it has, and the factor never leaves the device.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <memory>
+#include <new>
+
+#include "../../include/gemm14.h"
+#include "api_internal.h"
+#include "checks.h"
+#include "elements.cuh"
+#include "kernels.h"
+#include "plan.h"
+#include "ptx.cuh"
+
+namespace gemm14 {
+namespace {
+
+// A tensor of the list as the kernels see it: rows of `cols` elements (a dense
+// one is a single row). Its elements are numbered in units of kUnitBytes of the
+// source, which a warp takes at a time; the list's units are numbered through.
+struct Entry {
+  const void* src;
+  void* dst;
+  int64_t rows, cols, ld_src, ld_dst;
+  uint32_t first_unit;
+  uint16_t type, dst_type;  // gemm14 dtypes
+};
+// Passed by value: the kernels' parameters hold up to 32764 bytes.
+template <int kN>
+struct Table {
+  int n;
+  uint32_t units;
+  Entry e[kN];
+};
+constexpr int kMostEntries = 576;  // of a launch
+
+constexpr int kUnitBytes = 4096;
+constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 6;
+constexpr int kEach = 8;  // pieces of 16 bytes a lane has of a unit
+
+__host__ __device__ inline int type_bytes(int type) { return type == GEMM14_DTYPE_F32 ? 4 : 2; }
+__host__ __device__ inline int64_t unit_values(int type) { return kUnitBytes / type_bytes(type); }
+// Units of a row (its first may begin up to 7 elements before an aligned word),
+// and the rows that share a unit.
+__host__ __device__ inline int64_t row_units(int64_t cols, int type) {
+  return (cols + 7 + unit_values(type) - 1) / unit_values(type);
+}
+__host__ __device__ inline int64_t unit_rows(int64_t cols, int type) {
+  const int64_t r = unit_values(type) / (cols + 7);
+  return r > 1 ? r : 1;
+}
+__host__ inline int64_t entry_units(const Entry& e) {
+  const int64_t u = row_units(e.cols, e.type);
+  return u > 1 ? e.rows * u : (e.rows + unit_rows(e.cols, e.type) - 1) / unit_rows(e.cols, e.type);
+}
+
+// Warp w of `warps` takes the units [unit_at(w), unit_at(w + 1)); unit u is warp_of(u)'s.
+__device__ __forceinline__ uint32_t unit_at(uint32_t units, uint32_t w, uint32_t warps) {
+  return static_cast<uint32_t>(static_cast<uint64_t>(units) * w / warps);
+}
+__device__ __forceinline__ uint32_t warp_of(uint32_t units, uint32_t u, uint32_t warps) {
+  return static_cast<uint32_t>(((static_cast<uint64_t>(u) + 1) * warps - 1) / units);
+}
+
+// What a unit holds of its tensor: rows [row, row + rows) (more than one: whole
+// rows, side by side), and of each the part-th stretch of unit_values elements,
+// counted from the aligned word that holds the row's first element.
+struct Unit {
+  int64_t row, part;
+  int rows;
+};
+__device__ __forceinline__ Unit unit_of(const Entry& e, uint32_t u) {
+  const int64_t per = row_units(e.cols, e.type);
+  if (per > 1) {
+    if (e.rows == 1) return Unit{0, u, 1};
+    const int64_t row = u / per;
+    return Unit{row, u - row * per, 1};
+  }
+  const int64_t share = unit_rows(e.cols, e.type), row = u * share;
+  return Unit{row, 0, static_cast<int>(min(share, e.rows - row))};
+}
+// Lanes that share a row of a unit: all of them, or a power of two that its
+// pieces do not fill twice.
+__device__ __forceinline__ int lanes_along(const Unit& u, int64_t cols, int per) {
+  if (u.rows == 1) return 32;
+  int x = 1;
+  while (x < 32 && x * per < cols + 7) x *= 2;
+  return x;
+}
+
+// ---- sums of squares
+
+// A lane squares and adds the values of a unit in fp32 (at most 64 of them),
+// then adds that to its sum in fp64. Squares that leave what fp32 holds to 24
+// bits (a sum above 2^120, or below 2^-120 and not 0) are formed again in fp64,
+// from values read again: no value that the types have overflows or is lost, and
+// the fp64 units see one addition for 32 or 64 values.
+__device__ __forceinline__ float square_sum(float s, const Pack<float, 4>& p) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s = fmaf(p.x[j], p.x[j], s);
+  return s;
+}
+template <typename S>
+__device__ __forceinline__ float square_sum(float s, const Pack<S, 8>& p) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = to_f32(p.x[j]);
+    s = fmaf(x, x, s);
+  }
+  return s;
+}
+
+template <typename S>
+__device__ __forceinline__ void add_unit(double& sum, const Entry& e, const Unit& u, int lane) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
+  const int along = lanes_along(u, e.cols, kPer), lx = lane & (along - 1);
+  for (int r = lane / along; r < u.rows; r += 32 / along) {
+    const S* row = static_cast<const S*>(e.src) + (u.row + r) * e.ld_src;
+    const int before =
+        static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / static_cast<int>(sizeof(S));
+    const int64_t c0 = u.part * unit_values(e.type) - before + lx * kPer;
+    Pack<S, kPer> p[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) p[i] = load_pack<S, kPer, false>(row, c0 + i * along * kPer, e.cols, nullptr, nullptr);
+    float s[4] = {};
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) s[i & 3] = square_sum(s[i & 3], p[i]);
+    const float all = (s[0] + s[1]) + (s[2] + s[3]);
+    if (all <= 0x1p120f && all >= 0x1p-120f) {
+      sum += static_cast<double>(all);
+    } else {
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) any |= p[i].raw.x | p[i].raw.y | p[i].raw.z | p[i].raw.w;
+      if (any & (sizeof(S) == 4 ? 0x7fffffffu : 0x7fff7fffu)) {
+#pragma unroll 1
+        for (int i = 0; i < kEach; ++i) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int64_t c = c0 + i * along * kPer + j;
+            const double x = c >= 0 && c < e.cols ? static_cast<double>(to_f32(row[c])) : 0.0;
+            sum = fma(x, x, sum);
+          }
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Warp w's units, in order. What they hold of tensor i goes to slot w + i: where
+// a warp or a tensor ends, the next sum's slot is one further, so that a tensor's
+// slots lie side by side, in order. (Where both end at once a slot is left over,
+// and is set to 0.)
+template <int kN>
+__device__ __forceinline__ void sum_units(const Table<kN>& t, uint32_t w, uint32_t warps, int lane,
+                                          double* slots) {
+  const uint32_t u0 = unit_at(t.units, w, warps), u1 = unit_at(t.units, w + 1, warps);
+  int lo = 0, hi = t.n - 1;  // the tensor of u0
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.e[mid].first_unit <= u0) lo = mid; else hi = mid - 1;
+  }
+  int i = lo;
+  if (lane == 0 && w > 0 && i > 0 && t.e[i].first_unit == u0) slots[w + i - 1] = 0.0;
+  for (uint32_t u = u0; u < u1;) {
+    const Entry& e = t.e[i];
+    const uint32_t end = min(u1, i + 1 < t.n ? t.e[i + 1].first_unit : t.units);
+    double sum = 0.0;
+    for (; u < end; ++u) {
+      const Unit at = unit_of(e, u - e.first_unit);
+      if (e.type == GEMM14_DTYPE_BF16)
+        add_unit<__nv_bfloat16>(sum, e, at, lane);
+      else if (e.type == GEMM14_DTYPE_F16)
+        add_unit<__half>(sum, e, at, lane);
+      else
+        add_unit<float>(sum, e, at, lane);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) slots[w + i] = sum;
+    if (u < u1) ++i;
+  }
+}
+
+// ---- from the slots to the norms
+
+struct Finish {
+  const double* slots;
+  double* totals;      // of the launches so far
+  int launch;          // this one's number
+  bool last;
+  float scale, max_norm;
+  float* norm;         // written by the last launch
+  float* each;         // of this launch's tensors, or NULL
+  float* factor;       // for the scaling, or NULL
+};
+
+// The sum of v over the block's threads, to all of them; in an order of its own.
+__device__ __forceinline__ double block_sum(double v, double* smem) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  v = warp_sum(v);
+  __syncthreads();
+  if (lane == 0) smem[warp] = v;
+  __syncthreads();
+  return warp_sum(lane < warps ? smem[lane] : 0.0);
+}
+// Slots [a, b], every `step`-th from the `from`-th.
+__device__ __forceinline__ double slot_sum(const double* slots, uint32_t a, uint32_t b,
+                                           uint32_t from, uint32_t step) {
+  double s = 0.0;
+  for (uint32_t i0 = a + from; i0 <= b; i0 += 4 * step) {
+    double v[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) v[k] = i0 + k * step <= b ? __ldcg(slots + i0 + k * step) : 0.0;
+    s += (v[0] + v[1]) + (v[2] + v[3]);
+  }
+  return s;
+}
+
+// By one block of 1024 threads at most.
+template <int kN>
+__device__ __forceinline__ void finish(const Table<kN>& t, const Finish& f, uint32_t warps,
+                                       double* smem) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in_block = blockDim.x >> 5;
+  const uint32_t slots = warps + static_cast<uint32_t>(t.n) - 1u;
+  const double total =
+      block_sum(slot_sum(f.slots, 0u, slots - 1u, threadIdx.x, blockDim.x), smem);
+  if (threadIdx.x == 0) {
+    double all = total;
+    for (int l = 0; l < f.launch; ++l) all += f.totals[l];
+    f.totals[f.launch] = total;
+    if (f.last) {
+      const double norm = sqrt(all) * fabs(static_cast<double>(f.scale));
+      *f.norm = static_cast<float>(norm);
+      if (f.factor) {
+        const bool over = norm > static_cast<double>(f.max_norm) && norm - norm == 0.0;
+        *f.factor = over ? static_cast<float>(f.scale * (f.max_norm / norm)) : f.scale;
+      }
+    }
+  }
+  if (!f.each) return;
+  // a tensor of up to 32 slots a lane to a warp, longer ones to the block
+  constexpr uint32_t kLong = 1024;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int i = pass ? 0 : warp; i < t.n; i += pass ? 1 : in_block) {
+      const uint32_t first = t.e[i].first_unit;
+      const uint32_t end = i + 1 < t.n ? t.e[i + 1].first_unit : t.units;
+      const uint32_t a = warp_of(t.units, first, warps) + i, b = warp_of(t.units, end - 1, warps) + i;
+      if ((b - a >= kLong) != (pass == 1)) continue;
+      const double s = pass ? block_sum(slot_sum(f.slots, a, b, threadIdx.x, blockDim.x), smem)
+                            : warp_sum(slot_sum(f.slots, a, b, lane, 32u));
+      if (pass ? threadIdx.x == 0 : lane == 0)
+        f.each[i] = static_cast<float>(sqrt(s) * fabs(static_cast<double>(f.scale)));
+    }
+  }
+}
+
+// ---- scaling
+
+// kPer values from the source's word(s), to one or two words of the output: the
+// pieces are the aligned words of the output, the source's, where they lie
+// otherwise, are read as two words and a shift. Products are rounded to fp32 and
+// then to a 16-bit type: within half a step and 2^-24 of the value.
+template <typename S, typename O, bool kAny>
+__device__ __forceinline__ void scale_row(const S* src, O* dst, const S* begin, const S* end,
+                                          int64_t cols, int64_t c0, int step, float f) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(S)), kWord = 16 / static_cast<int>(sizeof(O));
+  Pack<S, kPer> p[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) p[i] = load_pack<S, kPer, kAny>(src, c0 + i * step, cols, begin, end);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t c = c0 + i * step;
+    if (c >= cols) break;
+    O y[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) y[j] = from_f32<O>(f * to_f32(p[i].x[j]));
+    if (c >= 0 && c + kPer <= cols) {
+#pragma unroll
+      for (int k = 0; k < kPer / kWord; ++k) {
+        Pack<O, kWord> w;
+#pragma unroll
+        for (int j = 0; j < kWord; ++j) w.x[j] = y[k * kWord + j];
+        *reinterpret_cast<uint4*>(dst + c + k * kWord) = w.raw;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (c + j >= 0 && c + j < cols) dst[c + j] = y[j];
+    }
+  }
+}
+
+template <typename S, typename O>
+__device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int lane, float f) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
+  const int along = lanes_along(u, e.cols, kPer), lx = lane & (along - 1);
+  const S* begin = static_cast<const S*>(e.src);
+  const S* end = begin + (e.rows - 1) * e.ld_src + e.cols;
+  for (int r = lane / along; r < u.rows; r += 32 / along) {
+    const S* src = begin + (u.row + r) * e.ld_src;
+    O* dst = static_cast<O*>(e.dst) + (u.row + r) * e.ld_dst;
+    const int before =
+        static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15u) / static_cast<int>(sizeof(O));
+    const int64_t c0 = u.part * unit_values(e.type) - before + lx * kPer;
+    if ((reinterpret_cast<uintptr_t>(src - before) & 15u) == 0)
+      scale_row<S, O, false>(src, dst, begin, end, e.cols, c0, along * kPer, f);
+    else
+      scale_row<S, O, true>(src, dst, begin, end, e.cols, c0, along * kPer, f);
+  }
+}
+
+// Warp w's units from the last to the first: what the norm's pass read last is in L2 still.
+template <int kN>
+__device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint32_t warps,
+                                            int lane, float f) {
+  const uint32_t u0 = unit_at(t.units, w, warps), u1 = unit_at(t.units, w + 1, warps);
+  int lo = 0, hi = t.n - 1;  // the tensor of u1 - 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.e[mid].first_unit <= u1 - 1u) lo = mid; else hi = mid - 1;
+  }
+  for (uint32_t u = u1, i = lo; u > u0; --i) {
+    const Entry& e = t.e[i];
+    const uint32_t begin = max(u0, e.first_unit);
+    if (e.src == e.dst && f == 1.0f) {  // nothing changes
+      u = begin;
+      continue;
+    }
+    for (; u > begin; --u) {
+      const Unit at = unit_of(e, u - 1u - e.first_unit);
+      if (e.type == GEMM14_DTYPE_BF16) {
+        if (e.dst_type == GEMM14_DTYPE_F32)
+          scale_unit<__nv_bfloat16, float>(e, at, lane, f);
+        else
+          scale_unit<__nv_bfloat16, __nv_bfloat16>(e, at, lane, f);
+      } else if (e.type == GEMM14_DTYPE_F16) {
+        if (e.dst_type == GEMM14_DTYPE_F32)
+          scale_unit<__half, float>(e, at, lane, f);
+        else
+          scale_unit<__half, __half>(e, at, lane, f);
+      } else {
+        scale_unit<float, float>(e, at, lane, f);
+      }
+    }
+  }
+}
+
+// ---- kernels
+
+template <int kN>
+__global__ void __launch_bounds__(kThreads)
+    grad_sum_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, double* slots) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (w < warps) sum_units(t, w, warps, threadIdx.x & 31, slots);
+}
+
+template <int kN>
+__global__ void __launch_bounds__(1024)
+    grad_finish_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, const Finish f) {
+  __shared__ double smem[32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  finish(t, f, warps, smem);
+}
+
+template <int kN>
+__global__ void __launch_bounds__(kThreads)
+    grad_scale_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, const float* factor) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (w < warps) scale_units(t, w, warps, threadIdx.x & 31, *factor);
+}
+
+// ---- the calls
+
+// Bytes of the workspace: the launches' totals, the factor, a launch's slots.
+struct Layout {
+  size_t totals = 0, factor = 0, slots = 0, total = 0;
+};
+uint32_t most_warps(int sms) { return static_cast<uint32_t>(sms) * kBlocksPerSm * (kThreads / 32); }
+void layout(int64_t n, int sms, Layout* l) {
+  const int64_t launches = (n + kMostEntries - 1) / kMostEntries;
+  l->totals = streamk_flag_bytes(sms);
+  l->factor = l->totals + round256(static_cast<size_t>(launches) * sizeof(double));
+  l->slots = l->factor + 256;
+  l->total = l->slots + round256((most_warps(sms) + static_cast<size_t>(kMostEntries)) * sizeof(double));
+}
+
+constexpr int64_t kMostTensors = int64_t(1) << 20;
+constexpr int64_t kMostSize = int64_t(1) << 40, kMostSpan = int64_t(1) << 43;
+
+bool dense(const gemm14_tensor& g) { return g.rows <= 1 || g.ld == g.cols; }
+bool empty(const gemm14_tensor& g) { return g.rows == 0 || g.cols == 0; }
+
+int validate_tensor(const gemm14_tensor& g) {
+  if (g.dtype != GEMM14_DTYPE_F32 && g.dtype != GEMM14_DTYPE_BF16 && g.dtype != GEMM14_DTYPE_F16)
+    return GEMM14_ERR_INVALID_ARG;
+  if (g.rows < 0 || g.cols < 0 || g.rows > kMostSize || g.cols > kMostSize || g.ld > kMostSize)
+    return GEMM14_ERR_INVALID_ARG;
+  if (empty(g)) return GEMM14_OK;
+  if (g.rows > 1 && (g.ld < g.cols || g.rows > kMostSpan / g.ld)) return GEMM14_ERR_INVALID_ARG;
+  if (!g.data || !aligned(g.data, type_bytes(g.dtype))) return GEMM14_ERR_INVALID_ARG;
+  return GEMM14_OK;
+}
+
+Entry entry_of(const gemm14_tensor& g, const gemm14_tensor* out) {
+  Entry e{};
+  e.type = static_cast<uint16_t>(g.dtype);
+  e.dst_type = static_cast<uint16_t>(out ? out->dtype : g.dtype);
+  e.rows = 1;  // an empty one is one unit with nothing in it
+  if (empty(g)) return e;
+  e.src = g.data;
+  e.dst = out ? out->data : g.data;
+  if (dense(g) && (!out || dense(*out))) {
+    e.cols = g.rows * g.cols;
+  } else {
+    e.rows = g.rows;
+    e.cols = g.cols;
+    e.ld_src = g.ld;
+    e.ld_dst = out ? out->ld : g.ld;
+  }
+  return e;
+}
+
+// ---- tensors that share memory
+
+struct Span {
+  uintptr_t begin, end;  // its first byte, and the byte after its last
+  const gemm14_tensor* g;
+  bool written;
+  int64_t i;
+};
+// Whether two tensors whose spans cross share an element: not where both are
+// columns of one matrix (rows of one pitch) and their columns lie apart.
+bool share_elements(const Span& a, const Span& b) {
+  const gemm14_tensor &x = *a.g, &y = *b.g;
+  const int size = type_bytes(x.dtype);
+  if (x.rows <= 1 || y.rows <= 1 || x.ld * size != y.ld * type_bytes(y.dtype)) return true;
+  const int64_t pitch = x.ld * size, wide_x = x.cols * size, wide_y = y.cols * type_bytes(y.dtype);
+  const int64_t off = static_cast<int64_t>(b.begin - a.begin) % pitch;  // b begins no earlier
+  return off < wide_x || off + wide_y > pitch;
+}
+// What is written may share no element with anything else of the lists, its own source aside.
+int check_apart(int64_t n, const gemm14_tensor* grads, const gemm14_tensor* outs) {
+  const int64_t most = outs ? 2 * n : n;
+  std::unique_ptr<Span[]> s(new (std::nothrow) Span[static_cast<size_t>(most > 0 ? most : 1)]);
+  if (!s) {
+    note_error("gemm14_grad_clip: no host memory for %lld tensors", static_cast<long long>(n));
+    return GEMM14_ERR_CUDA;
+  }
+  int64_t m = 0;
+  const auto add = [&](const gemm14_tensor& g, bool written, int64_t i) {
+    if (empty(g)) return;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(g.data);
+    const int64_t values = (g.rows > 1 ? (g.rows - 1) * g.ld : 0) + g.cols;
+    s[m++] = Span{b, b + static_cast<uintptr_t>(values * type_bytes(g.dtype)), &g, written, i};
+  };
+  for (int64_t i = 0; i < n; ++i) {
+    const bool in_place = outs && !empty(grads[i]) && outs[i].data == grads[i].data &&
+                          outs[i].dtype == grads[i].dtype &&
+                          ((dense(outs[i]) && dense(grads[i])) || outs[i].ld == grads[i].ld);
+    add(outs ? outs[i] : grads[i], true, i);
+    if (outs && !in_place) add(grads[i], false, i);
+  }
+  const auto before = [](const Span& a, const Span& b) {
+    return a.begin != b.begin ? a.begin < b.begin : a.i < b.i;
+  };
+  if (!std::is_sorted(s.get(), s.get() + m, before)) std::sort(s.get(), s.get() + m, before);
+  for (int64_t i = 0; i < m; ++i) {
+    for (int64_t j = i + 1; j < m && s[j].begin < s[i].end; ++j) {
+      if (!s[i].written && !s[j].written) continue;
+      if (!share_elements(s[i], s[j])) continue;
+      note_error("gemm14_grad_clip: tensors %lld and %lld share memory that is written",
+                 static_cast<long long>(s[i].i), static_cast<long long>(s[j].i));
+      return GEMM14_ERR_INVALID_ARG;
+    }
+  }
+  return GEMM14_OK;
+}
+
+struct Call {
+  int64_t n;
+  const gemm14_tensor* grads;
+  const gemm14_tensor* outs;  // NULL: none, or in place
+  bool clip;
+  float scale, max_norm;
+  float* norm;
+  float* each;
+  char* ws;
+  Layout l;
+  int sms;
+  cudaStream_t stream;
+};
+
+// One launch's tensors, [i0, i0 + t.n).
+template <int kN>
+void fill(const Call& c, int64_t i0, Table<kN>* t) {
+  t->n = static_cast<int>(std::min<int64_t>(kN, c.n - i0));
+  int64_t units = 0;
+  for (int i = 0; i < t->n; ++i) {
+    t->e[i] = entry_of(c.grads[i0 + i], c.outs ? c.outs + i0 + i : nullptr);
+    t->e[i].first_unit = static_cast<uint32_t>(units);
+    units += entry_units(t->e[i]);
+  }
+  t->units = static_cast<uint32_t>(units);
+}
+
+uint32_t warps_for(uint32_t units, int sms) { return std::min(units, most_warps(sms)); }
+dim3 blocks_for(uint32_t warps) { return dim3((warps + kThreads / 32 - 1) / (kThreads / 32)); }
+
+template <int kN>
+int sum_launch(const Call& c, int64_t i0, int launch) {
+  Table<kN> t;
+  fill(c, i0, &t);
+  const uint32_t warps = warps_for(t.units, c.sms);
+  double* slots = reinterpret_cast<double*>(c.ws + c.l.slots);
+  int st = finish_launch(launch_kernel(grad_sum_kernel<kN>, blocks_for(warps), dim3(kThreads), 0,
+                                       c.stream, t, warps, slots),
+                         "gradient norm launch", c.stream);
+  if (st != GEMM14_OK) return st;
+  Finish f{};
+  f.slots = slots;
+  f.totals = reinterpret_cast<double*>(c.ws + c.l.totals);
+  f.launch = launch;
+  f.last = i0 + t.n == c.n;
+  f.scale = c.scale;
+  f.max_norm = c.max_norm;
+  f.norm = c.norm;
+  f.each = c.each ? c.each + i0 : nullptr;
+  f.factor = c.clip ? reinterpret_cast<float*>(c.ws + c.l.factor) : nullptr;
+  return finish_launch(
+      launch_kernel(grad_finish_kernel<kN>, dim3(1), dim3(1024), 0, c.stream, t, warps, f),
+      "gradient norm launch", c.stream);
+}
+template <int kN>
+int scale_launch(const Call& c, int64_t i0) {
+  Table<kN> t;
+  fill(c, i0, &t);
+  const uint32_t warps = warps_for(t.units, c.sms);
+  return finish_launch(launch_kernel(grad_scale_kernel<kN>, blocks_for(warps), dim3(kThreads), 0,
+                                     c.stream, t, warps,
+                                     reinterpret_cast<const float*>(c.ws + c.l.factor)),
+                       "gradient scaling launch", c.stream);
+}
+
+// Tables of three sizes: a launch's parameters are copied with it.
+int run(const Call& c) {
+  int launch = 0;
+  for (int64_t i0 = 0; i0 < c.n; i0 += kMostEntries, ++launch) {
+    const int64_t m = c.n - i0;
+    const int st = m <= 16   ? sum_launch<16>(c, i0, launch)
+                   : m <= 72 ? sum_launch<72>(c, i0, launch)
+                             : sum_launch<kMostEntries>(c, i0, launch);
+    if (st != GEMM14_OK) return st;
+  }
+  if (!c.clip) return GEMM14_OK;
+  // from the last tensors to the first: what was read last is in L2 still
+  for (int64_t i0 = (c.n - 1) / kMostEntries * kMostEntries; i0 >= 0; i0 -= kMostEntries) {
+    const int64_t m = c.n - i0;
+    const int st = m <= 16   ? scale_launch<16>(c, i0)
+                   : m <= 72 ? scale_launch<72>(c, i0)
+                             : scale_launch<kMostEntries>(c, i0);
+    if (st != GEMM14_OK) return st;
+  }
+  return GEMM14_OK;
+}
+
+bool finite(float x) { return x - x == 0.0f; }
+
+int grad_call(Call c, size_t workspace_bytes, const char* where) {
+  if (c.n < 0 || c.n > kMostTensors || (c.n > 0 && !c.grads)) return GEMM14_ERR_INVALID_ARG;
+  if (!finite(c.scale) || !c.norm || !aligned(c.norm, 4) || !aligned(c.each, 4))
+    return GEMM14_ERR_INVALID_ARG;
+  if (c.clip && !(c.max_norm >= 0.0f)) return GEMM14_ERR_INVALID_ARG;
+  int64_t units = 0;
+  for (int64_t i = 0; i < c.n; ++i) {
+    const gemm14_tensor& g = c.grads[i];
+    int st = validate_tensor(g);
+    if (st != GEMM14_OK) return st;
+    if (c.outs) {
+      const gemm14_tensor& o = c.outs[i];
+      if ((st = validate_tensor(o)) != GEMM14_OK) return st;
+      if (o.rows != g.rows || o.cols != g.cols ||
+          (o.dtype != g.dtype && o.dtype != GEMM14_DTYPE_F32))
+        return GEMM14_ERR_INVALID_ARG;
+    }
+    units += entry_units(entry_of(g, c.outs ? c.outs + i : nullptr));
+    if (units > INT32_MAX) return GEMM14_ERR_INVALID_ARG;
+  }
+  if (c.ws && !aligned(c.ws, 16)) return GEMM14_ERR_INVALID_ARG;
+  int st = c.clip ? check_apart(c.n, c.grads, c.outs) : GEMM14_OK;
+  if (st != GEMM14_OK) return st;
+  if ((st = current_sm_count(&c.sms)) != GEMM14_OK) return st;
+  if (c.n == 0)
+    return finish_launch(cudaMemset2DAsync(c.norm, 4, 0, 4, 1, c.stream), "gradient norm", c.stream);
+  layout(c.n, c.sms, &c.l);
+  if (!c.ws || workspace_bytes < c.l.total) {
+    note_error("%s: %zu bytes of workspace given, %zu needed", where, workspace_bytes, c.l.total);
+    return GEMM14_ERR_INVALID_ARG;
+  }
+  return run(c);
+}
+
+}  // namespace
+}  // namespace gemm14
+
+using namespace gemm14;
+
+extern "C" {
+
+size_t gemm14_grad_workspace_bytes(int64_t n, int sm_count) {
+  if (n < 1 || n > kMostTensors) return 0;
+  if (sm_count <= 0 && current_sm_count(&sm_count) != GEMM14_OK) return 0;
+  Layout l;
+  layout(n, sm_count, &l);
+  return l.total;
+}
+
+int gemm14_grad_norm(int64_t n, const gemm14_tensor* grads, float scale, float* norm, float* each,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  Call c{};
+  c.n = n;
+  c.grads = grads;
+  c.scale = scale;
+  c.norm = norm;
+  c.each = each;
+  c.ws = static_cast<char*>(workspace);
+  c.stream = static_cast<cudaStream_t>(stream);
+  return grad_call(c, workspace_bytes, "gemm14_grad_norm");
+}
+
+int gemm14_grad_clip(int64_t n, const gemm14_tensor* grads, const gemm14_tensor* out, float scale,
+                     float max_norm, float* norm, float* each, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  Call c{};
+  c.n = n;
+  c.grads = grads;
+  c.outs = out;
+  c.clip = true;
+  c.scale = scale;
+  c.max_norm = max_norm;
+  c.norm = norm;
+  c.each = each;
+  c.ws = static_cast<char*>(workspace);
+  c.stream = static_cast<cudaStream_t>(stream);
+  return grad_call(c, workspace_bytes, "gemm14_grad_clip");
+}
+
+}  // extern "C"

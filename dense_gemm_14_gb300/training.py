@@ -1,8 +1,11 @@
 """Tensor-level calls of the training products: softmax cross entropy over a
-projection's outputs, and activations kept in 8 bits (argument marshalling
-only; every step runs in the library's CUDA kernels). None of them is recorded
-by autograd."""
+projection's outputs, activations kept in 8 bits, rows of a table looked up by
+token and their gradient, and the norm of many gradients and their clipping
+(argument marshalling only; every step runs in the library's CUDA kernels). None
+of them is recorded by autograd."""
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -281,3 +284,236 @@ def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = Non
         return dw
 
     return _on(stream, dy.device, body)
+
+
+def _tokens(tokens: torch.Tensor, device: int) -> int:
+    """The bytes of a token (a contiguous integer tensor on the device of this index)."""
+    if tokens.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"tokens must be int64 or int32, got {tokens.dtype}")
+    if tokens.get_device() != device or not tokens.is_contiguous():
+        raise ValueError("tokens must be contiguous, on the operands' device, got strides "
+                         f"{tokens.stride()} on {tokens.device}")
+    return tokens.element_size()
+
+
+def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
+              ignore_index: int = -100, dtype: torch.dtype | None = None,
+              stream=None) -> torch.Tensor:
+    """scale * table[tokens] (gemm14_embedding_forward), of shape (*tokens.shape, D).
+
+    table: (V, D) float32, bfloat16 or float16, a row-major view; tokens: int64 or
+    int32 of any shape, contiguous, on the same GPU. The row of a token that is
+    ignore_index is 0, that of another outside [0, V) NaN. dtype: the output's
+    (default: the table's). Stream, allocation and autograd as for
+    linear_cross_entropy; embedding_backward forms the gradient."""
+    dtype = table.dtype if dtype is None else dtype
+    if table.dtype not in _CODE or dtype not in _CODE:
+        raise TypeError(f"unsupported dtypes {table.dtype}, {dtype}")
+    ldw = _matrix(table, "table")
+    size = _tokens(tokens, table.get_device())
+    V, D = table.shape
+    if V < 1 or D < 1:
+        raise ValueError(f"table must not be empty, got shape {tuple(table.shape)}")
+    T = tokens.numel()
+
+    def body(handle):
+        out = torch.empty((*tokens.shape, D), dtype=dtype, device=table.device)
+        if T:
+            _lib.embedding_raw(_CODE[table.dtype], _CODE[dtype], T, V, D, table.data_ptr(), ldw,
+                               tokens.data_ptr(), size, int(ignore_index), float(scale),
+                               out.data_ptr(), D, handle)
+        return out
+
+    return _on(stream, table.device, body)
+
+
+def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None = None,
+                       out: torch.Tensor | None = None, scale: float = 1.0, beta: float = 0.0,
+                       ignore_index: int = -100, dtype: torch.dtype | None = None,
+                       stream=None) -> torch.Tensor:
+    """out = scale * (the rows of dy summed by token) + beta * out: the gradient of
+    embedding(table, tokens, scale) in its table (gemm14_embedding_backward).
+
+    dy: (*tokens.shape, D) float32, bfloat16 or float16; a row-major matrix view
+    where tokens has one dimension, else contiguous. out: (V, D), row-major, of
+    dy's dtype or float32; or rows = V, and it is allocated, in dtype (default:
+    dy's; beta is then 0). beta = 1 adds to the gradient that is there and leaves
+    rows without tokens as they are: the output projection's, where the two share
+    their weights. Tokens that are ignore_index or outside [0, V) add nothing. Sums
+    are fp32, in an order that repeats. Stream and workspace as for
+    linear_cross_entropy."""
+    if dy.dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {dy.dtype}")
+    if dy.dim() != tokens.dim() + 1 or dy.shape[:-1] != tokens.shape:
+        raise ValueError(f"dy {tuple(dy.shape)} must have a row for each of the tokens {tuple(tokens.shape)}")
+    if dy.dim() != 2:
+        if not dy.is_contiguous():
+            raise ValueError("dy must be contiguous where tokens is not one-dimensional")
+        dy = dy.view(tokens.numel(), dy.size(-1))
+    lddy = _matrix(dy, "dy")
+    size = _tokens(tokens, dy.get_device())
+    T, D = dy.shape
+    if out is None:
+        if rows is None or beta != 0.0:
+            raise ValueError("rows or out is needed, and out for beta != 0")
+        V, dtype = int(rows), dy.dtype if dtype is None else dtype
+    else:
+        if out.dim() != 2 or out.size(1) != D or (rows is not None and out.size(0) != rows) or \
+                dtype not in (None, out.dtype):
+            raise ValueError(f"out {out.dtype} {tuple(out.shape)} does not fit rows {rows}, "
+                             f"{D} columns and dtype {dtype}")
+        V, dtype = out.size(0), out.dtype
+    if dtype not in (dy.dtype, torch.float32):
+        raise TypeError(f"the gradient is formed in dy's dtype or float32, not {dtype}")
+    if V < 1 or D < 1:
+        raise ValueError(f"an empty table has no gradient: {V} rows of {D}")
+    code = _CODE[dy.dtype]
+
+    def body(handle):
+        dw = out if out is not None else torch.empty((V, D), dtype=dtype, device=dy.device)
+        lddw = _matrix(dw, "out", dy.get_device())
+        _in_workspace(
+            dy.device, handle,
+            lambda ws, n: _lib.embedding_backward_raw(code, _CODE[dtype], T, V, D, _ptr(dy), lddy,
+                                                      _ptr(tokens), size, int(ignore_index),
+                                                      float(scale), float(beta), dw.data_ptr(),
+                                                      lddw, ws, n, handle, check=False),
+            lambda: _lib.embedding_backward_workspace_bytes(code, T, V, D),
+            "gemm14_embedding_backward")
+        return dw
+
+    return _on(stream, dy.device, body)
+
+
+def _as_rows(x: torch.Tensor) -> tuple[int, int, int]:
+    """(rows, cols, pitch) of a tensor's elements: a row-major matrix as it is,
+    another in the order its elements lie in memory, one row where without gaps."""
+    if x.numel() == 0:
+        return 0, 0, 1
+    if x.dim() == 2 and (x.size(1) == 1 or x.stride(1) == 1) and \
+            (x.size(0) == 1 or x.stride(0) >= x.size(1)):
+        return x.size(0), x.size(1), max(x.stride(0), x.size(1))
+    if x.is_contiguous():
+        return 1, x.numel(), x.numel()
+    dims = sorted((s, n) for s, n in zip(x.stride(), x.shape) if n > 1)
+    cols, rows, ld = 1, 1, 1
+    while dims and dims[0][0] == cols:
+        cols *= dims.pop(0)[1]
+    if dims:
+        ld = dims[0][0]
+        for s, n in dims:
+            if s != ld * rows:
+                ld = 0
+                break
+            rows *= n
+    if ld < cols and rows > 1 or ld == 0:
+        raise ValueError(f"strides {x.stride()} of shape {tuple(x.shape)} are not rows of one pitch")
+    return rows, cols, max(ld, cols)
+
+
+class GradList:
+    """Tensors that grad_norm and clip_grad_norm take together: float32, bfloat16
+    and float16 CUDA tensors of one GPU, in any mixture, each without gaps or rows
+    of one pitch. A program that keeps its gradients keeps the list of them too:
+    making it costs a microsecond a tensor. It keeps the tensors, and reads what they
+    hold when a call runs."""
+
+    __slots__ = ("_tensors", "_args", "_device")
+
+    def __init__(self, tensors):
+        self._tensors = tuple(tensors)
+        self._args = (_lib.TensorArg * len(self._tensors))()
+        self._device = None
+        for i, (x, a) in enumerate(zip(self._tensors, self._args)):
+            if x.dtype not in _CODE:
+                raise TypeError(f"tensor {i}: unsupported dtype {x.dtype}")
+            if not x.is_cuda or (self._device is not None and x.device != self._device):
+                raise ValueError(f"tensor {i} must be a CUDA tensor on the others' device, is on {x.device}")
+            self._device = x.device
+            a.rows, a.cols, a.ld = _as_rows(x)
+            a.data, a.dtype = _ptr(x), _CODE[x.dtype]
+
+    @property
+    def tensors(self) -> tuple[torch.Tensor, ...]:
+        return self._tensors
+
+    def __len__(self) -> int:
+        return len(self._tensors)
+
+
+def _grad_call(grads, stream, call, where):
+    """(norm, each) of call(norm, each, workspace, bytes, stream handle)."""
+    device = grads._device or torch.device("cuda", torch.cuda.current_device())
+    n = len(grads)
+
+    def body(handle):
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        each = torch.empty(n, dtype=torch.float32, device=device)
+        try:
+            _in_workspace(device, handle, lambda ws, b: call(norm.data_ptr(), _ptr(each), ws, b, handle),
+                          lambda: _lib.grad_workspace_bytes(n), where)
+        except _lib.Gemm14Error as e:
+            if e.status == _lib.GEMM14_ERR_INVALID_ARG:
+                raise ValueError(f"{where}: {_lib.last_error_string()}") from e
+            raise
+        return norm, each
+
+    return _on(stream, device, body)
+
+
+def grad_norm(grads, scale: float = 1.0, each: bool = False, stream=None):
+    """|scale| * the square root of the sum of the squares of all elements of all of
+    grads (a GradList or a sequence of tensors), a 0-dimensional float32 tensor on
+    their GPU; with each, also the norm of each of them, a float32 vector
+    (gemm14_grad_norm). scale: 1 / the loss scale. Sums are held in fp64 and
+    repeat. Stream and workspace as for linear_cross_entropy."""
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    if not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
+    norm, norms = _grad_call(
+        grads, stream,
+        lambda norm, norms, ws, b, handle: _lib.grad_norm_raw(
+            len(grads), grads._args, float(scale), norm, norms if each else None, ws, b, handle,
+            check=False),
+        "gemm14_grad_norm")
+    return (norm, norms) if each else norm
+
+
+def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, out=None, each: bool = False,
+                   stream=None):
+    """Scales grads (a GradList or a sequence of tensors) by scale * min(1, max_norm
+    / norm), in place or into out (as many tensors of the same shapes and strides,
+    each of its gradient's dtype or float32), and returns the norm, as grad_norm
+    does, of before (gemm14_grad_clip). scale takes gradients out of a loss scale. A
+    norm that is infinite or NaN clips nothing: out = scale * grads, for the caller
+    to leave alone. No tensor that is written may share memory with another of the
+    lists. Nothing is copied to the host."""
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    if out is not None and not isinstance(out, GradList):
+        out = GradList(out)
+    if not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
+    if not max_norm >= 0.0:
+        raise ValueError(f"max_norm must not be negative, got {max_norm}")
+    if out is not None:
+        if len(out) != len(grads) or (len(out) and out._device != grads._device):
+            raise ValueError(f"{len(grads)} gradients and {len(out)} outputs, on one device each")
+        for i, (x, y) in enumerate(zip(grads._tensors, out._tensors)):
+            if x.shape != y.shape or y.dtype not in (x.dtype, torch.float32):
+                raise ValueError(f"output {i} ({y.dtype} {tuple(y.shape)}) does not fit its gradient "
+                                 f"({x.dtype} {tuple(x.shape)})")
+            a, b = grads._args[i], out._args[i]
+            if (a.rows, a.cols) != (b.rows, b.cols) or not (
+                    x.dim() == 2 or x.stride() == y.stride() or
+                    (x.is_contiguous() and y.is_contiguous())):
+                raise ValueError(f"output {i} lies otherwise than its gradient: strides "
+                                 f"{y.stride()}, {x.stride()}")
+    norm, norms = _grad_call(
+        grads, stream,
+        lambda norm, norms, ws, b, handle: _lib.grad_clip_raw(
+            len(grads), grads._args, None if out is None else out._args, float(scale),
+            float(max_norm), norm, norms if each else None, ws, b, handle, check=False),
+        "gemm14_grad_clip")
+    return (norm, norms) if each else norm

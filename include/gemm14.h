@@ -464,6 +464,92 @@ size_t gemm14_ckpt8_wgrad_workspace_bytes(int dtype, int64_t T, int64_t N, int64
                                           const void* dY, int64_t lddy, const float* dW,
                                           int64_t lddw, int sm_count);
 
+/*
+ * Rows of a table looked up by token: out[t] = scale * W[tokens[t]], t < T.
+ * W: V x D (pitch ldw) of dtype F32, BF16 or F16; out: T x D (pitch ldo) of
+ * dtype_out, any of the three; values are multiplied in fp32 and rounded once to
+ * dtype_out. tokens: T integers of token_bytes (4 or 8) bytes on the device. The
+ * row of a token that is ignore_index is 0 (so it is where that is a row of the
+ * table), of any other token outside [0, V) it is NaN.
+ * Bases and pitches of 16 bytes give the fastest accesses; any are allowed. out
+ * must not overlap W or the tokens. T == 0: nothing is done. Sizes at most
+ * 2^31 - 256, V and D at least 1; scale must be finite.
+ */
+int gemm14_embedding_forward(int dtype, int dtype_out, int64_t T, int64_t V, int64_t D,
+                             const void* W, int64_t ldw, const void* tokens, int token_bytes,
+                             int64_t ignore_index, float scale, void* out, int64_t ldo,
+                             void* stream);
+
+/*
+ * The gradient of a lookup in its table:
+ *     dW[v] = scale * sum over {t < T : tokens[t] == v} of dY[t]  +  beta * dW[v].
+ * dY: T x D (pitch lddy) of dtype F32, BF16 or F16; dW: V x D (pitch lddw) of
+ * dtype_out, dtype or F32. Places whose token is ignore_index or outside [0, V)
+ * add nothing, whatever their rows of dY hold. beta == 0: dW is not read, rows
+ * without tokens are set to 0. beta == 1 (the gradient that is there is added to,
+ * the output projection's where the two are tied, gemm14_linear_ce_backward):
+ * rows without tokens are neither read nor written.
+ * Sums are fp32, in an order that the tokens and the sizes fix (a call repeats
+ * bit for bit); each value of dW is rounded once.
+ * workspace: caller-owned, 16-byte aligned, of
+ * gemm14_embedding_backward_workspace_bytes(...) bytes at least (0: none needed);
+ * its contents do not matter, and one kept for other calls serves. A call is
+ * several launches that hand data on through it, as for the linear cross entropy.
+ * dW must not overlap dY or the tokens. T == 0: dW = beta * dW.
+ */
+int gemm14_embedding_backward(int dtype, int dtype_out, int64_t T, int64_t V, int64_t D,
+                              const void* dY, int64_t lddy, const void* tokens, int token_bytes,
+                              int64_t ignore_index, float scale, float beta, void* dW, int64_t lddw,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its workspace bytes (0: none needed, or invalid arguments); no CUDA call is made
+ * when sm_count > 0. */
+size_t gemm14_embedding_backward_workspace_bytes(int dtype, int64_t T, int64_t V, int64_t D,
+                                                 int sm_count);
+
+/* A gradient in a list of them: rows x cols elements of dtype F32, BF16 or F16 on
+ * the device, rows of pitch ld (not looked at where rows <= 1). rows or cols of 0:
+ * it holds nothing, and data may be NULL. */
+typedef struct gemm14_tensor {
+  void* data;
+  int64_t rows, cols, ld;
+  int dtype;
+} gemm14_tensor;
+
+/*
+ * The norm of n gradients taken together, N = |scale| sqrt(sum of g^2 over all
+ * elements of all of them), and, where each is not NULL, that of each: norm (one
+ * fp32) and each (n fp32) on the device; grads on the host, read before the call
+ * returns. scale: out of a loss scale, 1 / it. Squares are summed in fp32 over at
+ * most 64 values, those sums in fp64, and values whose squares fp32 does not hold
+ * are squared in fp64: values of any size add what they should. A call repeats bit
+ * for bit. Infinities give an infinite norm, NaN gives NaN. n == 0: *norm = 0.
+ * n at most 2^20; scale must be finite.
+ * workspace: caller-owned, 16-byte aligned, gemm14_grad_workspace_bytes(n, ...)
+ * bytes at least; its contents do not matter, and one kept for other calls serves.
+ */
+int gemm14_grad_norm(int64_t n, const gemm14_tensor* grads, float scale, float* norm, float* each,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same, and the gradients scaled so that their norm is at most max_norm:
+ *     out = f g,   f = scale * min(1, max_norm / N),
+ * written over them (out NULL) or into n tensors of the same sizes, each of its
+ * gradient's dtype or F32. The factor is worked out on the device, in fp64, and
+ * held in fp32; products are fp32, rounded to the output's type. A norm that is
+ * infinite or NaN clips nothing: f = scale, and *norm says so. f == 1 in place:
+ * nothing is written. max_norm >= 0 (infinity: only scale).
+ * What is written must share no element with any other tensor of the lists (the
+ * same tensor twice in a list is GEMM14_ERR_INVALID_ARG; an output may be its own
+ * gradient, with the same layout).
+ */
+int gemm14_grad_clip(int64_t n, const gemm14_tensor* grads, const gemm14_tensor* out, float scale,
+                     float max_norm, float* norm, float* each, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the two calls on n tensors (0: n is 0 or invalid). */
+size_t gemm14_grad_workspace_bytes(int64_t n, int sm_count);
+
 /* Launch plan chosen for a call (host-side only; no CUDA call is made). */
 typedef struct gemm14_plan {
   int kernel;     /* 1 = fp32 SIMT (FFMA), 2 = tcgen05 on one SM per tile,
