@@ -12,6 +12,7 @@
 // token that fills a tenth of the batch costs no more than others.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/gemm14.h"
@@ -49,7 +50,10 @@ __device__ __forceinline__ bool takes_part(const Tokens& k, int64_t token) {
 // (a second rounding, of a product that is right to 2^-24).
 // kAny: rows at any address; the pieces are then the aligned words of the
 // output's row, the table's are read as two words and a shift.
+// An output that L2 cannot hold is stored past it, so that the table's rows that
+// recur stay there.
 constexpr int kAhead = 4;
+constexpr double kStreamBytes = 64e6;
 
 template <typename S, typename O>
 __host__ __device__ constexpr int lookup_values() {
@@ -59,7 +63,7 @@ __host__ __device__ constexpr int lookup_values() {
 template <typename S, typename O, bool kAny>
 __global__ void __launch_bounds__(kThreads)
     embedding_kernel(const S* W, int64_t ldw, const Tokens k, O* out, int64_t ldo, int64_t D,
-                     float scale, int along) {
+                     float scale, int along, int stream_out) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int kPer = lookup_values<S, O>();
@@ -94,7 +98,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int j = 0; j < kPer; ++j) y.x[j] = from_f32<O>(real ? scale * to_f32(x[u].x[j]) : other);
         if (c >= 0 && c + kPer <= D) {
-          *reinterpret_cast<decltype(y.raw)*>(to + c) = y.raw;
+          if (stream_out)
+            __stcs(reinterpret_cast<decltype(y.raw)*>(to + c), y.raw);
+          else
+            *reinterpret_cast<decltype(y.raw)*>(to + c) = y.raw;
         } else {
 #pragma unroll
           for (int j = 0; j < kPer; ++j)
@@ -173,13 +180,14 @@ cudaError_t lookup_as(const void* W, int64_t ldw, const Tokens& k, void* out, in
                          dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along);
   }
   const int along = threads_along(k.T, (D + kPer - 1) / kPer + (words ? 0 : 1), kAhead, sms);
+  const int stream_out = static_cast<double>(k.T) * D * sizeof(O) > kStreamBytes;
   if constexpr (sizeof(S) == sizeof(O)) {
     if (!words)
       return launch_kernel(embedding_kernel<S, O, true>, dim3(grid_for(k.T * along, sms)),
-                           dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along);
+                           dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along, stream_out);
   }
   return launch_kernel(embedding_kernel<S, O, false>, dim3(grid_for(k.T * along, sms)),
-                       dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along);
+                       dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along, stream_out);
 }
 
 // ---- rows of the gradient that no token stands for
@@ -296,6 +304,10 @@ __device__ __forceinline__ void add_to(float (&sum)[kPer], const Pack<S, kPer>& 
 
 constexpr int kRowsAhead = 8;  // rows of dY in flight
 
+// Columns a thread has: one 16-byte word of the wider type.
+template <typename S, typename O>
+__host__ __device__ constexpr int sum_values() { return lookup_values<S, O>(); }
+
 template <typename S, typename O>
 struct GradArgs {
   const S* dY;
@@ -315,7 +327,7 @@ constexpr int kFewTokens = kThreads;
 template <typename S, typename O, bool kAny>
 __global__ void __launch_bounds__(kThreads)
     embedding_grad_few_kernel(const GradArgs<S, O> a, const Tokens k, int slices, int64_t share) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
+  constexpr int kPer = sum_values<S, O>();
   constexpr int kWarps = kThreads / 32, kMarked = 8192;
   __shared__ uint32_t marks[kMarked / 32];
   __shared__ int places[kFewTokens];
@@ -363,26 +375,33 @@ __global__ void __launch_bounds__(kThreads)
 
 // Radix sort, least significant digit first, of the places that take part, by
 // one cluster of kCtas CTAs whose barriers are the hardware's. In a pass every
-// warp has a range of the list: it counts its digits (places of one digit found
-// with match.any), the counts are summed over warps and CTAs (through
+// warp has a range of the list: it counts its digits (shared-memory atomics on
+// its own counts), the counts are summed over warps and CTAs (through
 // distributed shared memory) to each warp's first position for each digit, and
-// the warp goes through its range again and moves the places there, in order.
-// Two passes for up to 2^18 tokens; the list lies in L2. The first pass leaves
-// out what takes no part.
+// the warp goes through its range again and moves the places there, in order:
+// a ballot for each bit of the digit finds the lanes that have the same one.
+// Two passes for a vocabulary of up to 2^18; the first leaves out what takes no
+// part. Between passes the list lies in L2; in shared memory where one CTA does.
+// @SORT@
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSortAhead = 8;  // words in flight a lane
 
 struct SortArgs {
   Tokens k;
-  uint32_t* key[2];  // of the sorted places: their tokens ...
-  uint32_t* at[2];   // ... and which they are
-  uint32_t* count;   // how many take part
+  uint2* list[2];   // the sorted places: the token, and which place it is
+  uint32_t* count;  // how many take part, and (count[1], set to 0) long sums
   int bits, passes;  // digits of this many bits
   unsigned* err;
 };
 
-constexpr size_t kSortSmem = (static_cast<size_t>(kSortWarps) * kDigits + 2 * kDigits + 32) * 4;
+constexpr int kOneCta = kSortThreads * kSortAhead;  // places that one CTA sorts
+constexpr int kEightCtas = 2 * kOneCta;
+template <int kCtas>
+constexpr size_t sort_smem_bytes() {
+  return (static_cast<size_t>(kSortWarps) * kDigits + 2 * kDigits + 32) * 4 +
+         (kCtas == 1 ? static_cast<size_t>(kOneCta) * sizeof(uint2) : 0);
+}
 
 __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -398,6 +417,7 @@ __global__ void __launch_bounds__(kSortThreads)
   uint32_t* total = hist + kSortWarps * kDigits;  // of this CTA, read by the others
   uint32_t* base = total + kDigits;
   uint32_t* sums = base + kDigits;                // of a warp's digits in the scan
+  uint2* own = reinterpret_cast<uint2*>(sums + 32);  // kCtas == 1: the list between passes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = kCtas > 1 ? cluster_ctarank() : 0u;
   grid_dependency_wait();
@@ -406,10 +426,8 @@ __global__ void __launch_bounds__(kSortThreads)
   uint32_t n = T;
   uint32_t* my_hist = hist + warp * kDigits;
   for (int pass = 0; pass < a.passes; ++pass) {
-    const uint32_t* key_in = a.key[(pass + 1) & 1];
-    const uint32_t* at_in = a.at[(pass + 1) & 1];
-    uint32_t* key_out = a.key[pass & 1];
-    uint32_t* at_out = a.at[pass & 1];
+    const uint2* in = kCtas == 1 ? own : a.list[(pass + 1) & 1];
+    uint2* out = kCtas == 1 && pass + 1 < a.passes ? own : a.list[pass & 1];
     const int shift = pass * a.bits;
     const uint32_t mask = (1u << a.bits) - 1u;
     const uint32_t per_cta = (n + kCtas - 1) / kCtas;
@@ -421,35 +439,29 @@ __global__ void __launch_bounds__(kSortThreads)
       reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     // ~0u: takes no part (tokens are below 2^31)
-    uint32_t key[kSortAhead];
+    uint32_t key[kSortAhead], at[kSortAhead];
     const auto load = [&](uint32_t i0) {
 #pragma unroll
       for (int u = 0; u < kSortAhead; ++u) {
         const uint32_t i = i0 + u * 32u + lane;
         key[u] = ~0u;
+        at[u] = i;
         if (i >= end) continue;
         if (pass == 0) {
           const int64_t token = token_at(a.k, i);
           if (takes_part(a.k, token)) key[u] = static_cast<uint32_t>(token);
         } else {
-          key[u] = __ldcg(key_in + i);
+          const uint2 v = kCtas == 1 ? in[i] : __ldcg(in + i);
+          key[u] = v.x;
+          at[u] = v.y;
         }
       }
-    };
-    // lanes of this lane's digit, and those before it among them
-    const auto peers_of = [&](uint32_t k) {
-      return __match_any_sync(0xffffffffu, k == ~0u ? ~0u : (k >> shift) & mask);
     };
     for (uint32_t i0 = begin; i0 < end; i0 += kSortAhead * 32u) {
       load(i0);
 #pragma unroll
-      for (int u = 0; u < kSortAhead; ++u) {
-        if (i0 + u * 32u >= end) break;
-        const uint32_t peers = peers_of(key[u]);
-        if (key[u] != ~0u && lane == __ffs(peers) - 1)
-          my_hist[(key[u] >> shift) & mask] += __popc(peers);
-        __syncwarp();
-      }
+      for (int u = 0; u < kSortAhead; ++u)
+        if (key[u] != ~0u) atomicAdd(&my_hist[(key[u] >> shift) & mask], 1u);
     }
     __syncthreads();
     if (tid < kDigits) {
@@ -470,11 +482,11 @@ __global__ void __launch_bounds__(kSortThreads)
     uint32_t all = 0, before = 0;
     if (tid < kDigits) {
 #pragma unroll
-      for (uint32_t c = 0; c < kCtas; ++c) {
+      for (int c = 0; c < kCtas; ++c) {
         const uint32_t v =
             kCtas > 1 ? load_cluster_u32(mapa_shared(smem_u32(total + tid), c)) : total[tid];
         all += v;
-        if (c < rank) before += v;
+        if (c < static_cast<int>(rank)) before += v;
       }
     }
     uint32_t upto = all;  // of the warp's digits up to this one
@@ -496,18 +508,17 @@ __global__ void __launch_bounds__(kSortThreads)
     const bool kept = end - begin <= kSortAhead * 32u;  // the keys are still in registers
     for (uint32_t i0 = begin; i0 < end; i0 += kSortAhead * 32u) {
       if (!kept) load(i0);
-      uint32_t at[kSortAhead];
-#pragma unroll
-      for (int u = 0; u < kSortAhead; ++u) {
-        const uint32_t i = i0 + u * 32u + lane;
-        at[u] = pass == 0 ? i : i < end ? __ldcg(at_in + i) : 0u;
-      }
 #pragma unroll
       for (int u = 0; u < kSortAhead; ++u) {
         if (i0 + u * 32u >= end) break;
-        const uint32_t peers = peers_of(key[u]);
         const uint32_t digit = (key[u] >> shift) & mask;
         const bool on = key[u] != ~0u;
+        uint32_t peers = __ballot_sync(0xffffffffu, on);  // lanes of this lane's digit
+#pragma unroll
+        for (int b = 0; b < kDigitBits; ++b) {
+          const uint32_t set = __ballot_sync(0xffffffffu, digit >> b & 1u);
+          peers &= digit >> b & 1u ? set : ~set;
+        }
         uint32_t first = 0;
         if (on) first = base[digit] + my_hist[digit];
         __syncwarp();
@@ -515,10 +526,7 @@ __global__ void __launch_bounds__(kSortThreads)
         __syncwarp();
         if (on) {
           const uint32_t to = first + __popc(peers & ((1u << lane) - 1u));
-          if (dev_check(index_ok(to, T), a.err)) {
-            key_out[to] = key[u];
-            at_out[to] = at[u];
-          }
+          if (dev_check(index_ok(to, T), a.err)) out[to] = make_uint2(key[u], at[u]);
         }
       }
     }
@@ -529,37 +537,84 @@ __global__ void __launch_bounds__(kSortThreads)
     else
       __syncthreads();
   }
-  if (rank == 0 && tid == 0) *a.count = n;
+  if (rank == 0 && tid < 2) a.count[tid] = tid == 0 ? n : 0u;
 }
 
 // ---- sums over ranges of the sorted places
 
 // A group of `along` threads takes one range of the sorted places and a slice of
 // the columns, kPer of them a thread (16 bytes of dY's type), kRowsAhead rows in
-// flight. Each token's sum that begins and ends in the range goes to dW; what a
-// range holds of a sum that began before it, or goes on behind it, goes to the
-// range's first or second slot, for the join.
+// flight. A token of up to kWhole places is one range's, the one where it begins;
+// the sum of a longer one may lie in several: what a range holds of a sum that
+// began before it, or goes on behind it, goes to the range's first or second slot,
+// and the range where it began goes on a list for the join.
 struct Ranges {
-  const uint32_t* key;
-  const uint32_t* at;
-  const uint32_t* count;
-  float* slots;       // two rows of slot_ld floats a range
+  const uint2* place;  // sorted: token, place
+  uint32_t* count;     // places, and long sums
+  uint32_t* list;      // of the ranges where a sum begins that goes on behind them
+  float* slots;        // two rows of slot_ld floats a range
   int64_t slot_ld;
   int64_t ranges;
   int along, slices;
 };
-constexpr uint32_t kLeastRange = 8;
+constexpr uint32_t kLeastRange = 8, kWhole = 16;
 
-// Places of a range: all ranges but the last hold as many.
+// Places of a range: all ranges but the last hold as many, before their ends move.
 __device__ __forceinline__ uint32_t range_length(uint32_t n, int64_t ranges) {
   const uint32_t even = static_cast<uint32_t>((n + ranges - 1) / ranges);
   return max(kLeastRange, even);
 }
+// Where a range that should begin at p does, from which of the places p - 16 ..
+// p + 15 have p's token: at p, or behind the token that has places on both sides
+// of p, if it has no more than kWhole.
+__device__ __forceinline__ uint32_t moved(uint32_t p, uint32_t same) {
+  const uint32_t before = static_cast<uint32_t>(__clz(static_cast<int>(~(same << 16))));  // <= 16
+  const uint32_t after = static_cast<uint32_t>(__ffs(static_cast<int>(~(same >> 16))) - 1);
+  return before == 0 || before + after > kWhole ? p : p + after;
+}
+// The range's places [p0, p1).
+__device__ __forceinline__ void range_ends(const Ranges& r, int64_t range, uint32_t n,
+                                           uint32_t& p0, uint32_t& p1) {
+  const uint32_t length = range_length(n, r.ranges);
+  const uint32_t q[2] = {
+      static_cast<uint32_t>(min(static_cast<int64_t>(n), range * length)),
+      static_cast<uint32_t>(min(static_cast<int64_t>(n), (range + 1) * length))};
+  uint32_t same[2] = {0u, 0u};
+  if (r.along >= 32) {  // a warp's range: its lanes look at a place each
+    uint32_t token[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t i = static_cast<int64_t>(q[e]) - 16 + (threadIdx.x & 31);
+      token[e] = i >= 0 && i < n ? r.place[i].x : ~0u;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      same[e] = __ballot_sync(0xffffffffu, token[e] == __shfl_sync(0xffffffffu, token[e], 16) &&
+                                               token[e] != ~0u);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t token = q[e] < n ? r.place[q[e]].x : ~0u;
+#pragma unroll 8
+      for (int u = 0; u < 32; ++u) {
+        const int64_t i = static_cast<int64_t>(q[e]) - 16 + u;
+        if (i >= 0 && i < n && r.place[i].x == token) same[e] |= 1u << u;
+      }
+    }
+  }
+  p0 = q[0] < n ? moved(q[0], same[0]) : n;
+  p1 = q[1] < n ? moved(q[1], same[1]) : n;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 template <typename S, typename O, bool kAny>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     embedding_sum_kernel(const GradArgs<S, O> a, const Ranges r, int64_t T, int64_t V) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
+  constexpr int kPer = sum_values<S, O>();
+  constexpr uint32_t kFlag = 0x80000000u;  // beside a token or a place, below 2^31
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t n = *r.count;
@@ -567,93 +622,141 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t part = blockIdx.x / r.slices;
   const int slice = static_cast<int>(blockIdx.x - part * r.slices);
   const int64_t range = part * (kThreads / r.along) + group;
-  const uint32_t length = range_length(n, r.ranges);
   const int64_t c = (static_cast<int64_t>(slice) * r.along + tx) * kPer;
-  if (range >= r.ranges || range * length >= n || c >= a.D) return;
-  const uint32_t p0 = static_cast<uint32_t>(range) * length, p1 = min(n, p0 + length);
+  uint32_t p0 = n, p1 = n;
+  if (range < r.ranges) range_ends(r, range, n, p0, p1);
+  const uint32_t most = __reduce_max_sync(0xffffffffu, p1 - p0);  // of the warp's ranges
+  const bool live = c < a.D;
   const S* end = a.dY + (T - 1) * a.lddy + a.D;
+  // a stage of the range's places, one a lane: the token (kFlag: its sum goes on
+  // behind the range) and the place (kFlag: the last of its sum here)
+  const int stage = min(r.along, 32), in_stage = threadIdx.x & (stage - 1);
+  const auto places = [&](uint32_t q) {
+    const uint32_t p = p0 + q + in_stage;
+    if (p >= p1) return make_uint2(0u, 0u);
+    uint2 v = r.place[p];
+    const bool same = p + 1 < n && r.place[p + 1].x == v.x;
+    if (p + 1 == p1 && same) v.x |= kFlag;
+    if (p + 1 == p1 || !same) v.y |= kFlag;
+    return v;
+  };
   float sum[kPer] = {};
-  uint32_t token = r.key[p0];
-  bool began_before = p0 > 0 && r.key[p0 - 1] == token;
+  bool began_before = p0 > 0 && p0 < p1 && r.place[p0 - 1].x == r.place[p0].x;
   const auto to_slot = [&](int which) {
     float* slot = r.slots + (2 * range + which) * r.slot_ld + c;
 #pragma unroll
     for (int j = 0; j < kPer; j += 4)
       *reinterpret_cast<float4*>(slot + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
   };
-  const auto to_row = [&]() {
-    if (dev_check(index_ok(token, V), a.err))
-      put_sums<O, kPer>(a.dW + token * a.lddw, c, a.D, sum, a.scale, a.beta, a.words != 0);
-  };
-  for (uint32_t p = p0; p < p1; p += kRowsAhead) {
-    uint32_t key[kRowsAhead];
-    Pack<S, kPer> x[kRowsAhead];
+  uint2 next = places(0);
+  for (uint32_t q = 0; q < most; q += stage) {
+    const uint2 now = next;
+    next = places(q + stage);
+    for (int u0 = 0; u0 < stage && q + u0 < most; u0 += kRowsAhead) {
+      Pack<S, kPer> x[kRowsAhead];
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      if (p + u >= p1) continue;
-      key[u] = r.key[p + u];
-      x[u] = load_pack<S, kPer, kAny>(a.dY + static_cast<int64_t>(r.at[p + u]) * a.lddy, c, a.D,
-                                      a.dY, end);
-    }
+      for (int u = 0; u < kRowsAhead; ++u) {
+        const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage) & ~kFlag;
+        if (live && p0 + q + u0 + u < p1)
+          x[u] = load_pack<S, kPer, kAny>(a.dY + static_cast<int64_t>(at) * a.lddy, c, a.D, a.dY, end);
+      }
+      // the old rows that these places' sums will be added to
+      if (a.beta != 0.0f) {
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      if (p + u >= p1) continue;
-      if (key[u] != token) {
-        if (began_before)
+        for (int u = 0; u < kRowsAhead; ++u) {
+          const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage);
+          const uint32_t token = __shfl_sync(0xffffffffu, now.x, u0 + u, stage) & ~kFlag;
+          if (live && p0 + q + u0 + u < p1 && (at & kFlag) && index_ok(token, V))
+            prefetch_l2(a.dW + token * a.lddw + c);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRowsAhead; ++u) {
+        const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage);
+        const uint32_t token = __shfl_sync(0xffffffffu, now.x, u0 + u, stage);
+        if (!live || p0 + q + u0 + u >= p1) continue;
+        add_to<S, kPer>(sum, x[u]);
+        if (!(at & kFlag)) continue;
+        if (began_before) {
           to_slot(0);
-        else
-          to_row();
+        } else if (token & kFlag) {
+          to_slot(1);
+          if (c == 0) r.list[atomicAdd(r.count + 1, 1u)] = static_cast<uint32_t>(range);
+        } else if (dev_check(index_ok(token, V), a.err)) {
+          put_sums<O, kPer>(a.dW + token * a.lddw, c, a.D, sum, a.scale, a.beta, a.words != 0);
+        }
         began_before = false;
-        token = key[u];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) sum[j] = 0.0f;
       }
-      add_to<S, kPer>(sum, x[u]);
     }
   }
-  if (began_before)
-    to_slot(0);
-  else if (p1 < n && r.key[p1] == token)
-    to_slot(1);
-  else
-    to_row();
 }
 
-// The sums that lie in several ranges: the group of the range where one begins
-// adds what the later ranges hold of it, in order.
-template <typename S, typename O>
+// The sums that lie in several ranges, 128 columns of one by a block at a time:
+// its warps add the ranges' slots in turn, every eighth each, and the warps' sums
+// are added in order. (The list's order, which varies, decides nothing but which
+// block that is.)
+template <typename O>
 __global__ void __launch_bounds__(kThreads)
-    embedding_join_kernel(const GradArgs<S, O> a, const Ranges r, int64_t V) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
+    embedding_join_kernel(O* dW, int64_t lddw, int64_t D, float scale, float beta, const Ranges r,
+                          int64_t V, unsigned* err) {
+  constexpr int kWarps = kThreads / 32, kEach = 4;
+  __shared__ float4 sums[kWarps][32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const uint32_t n = *r.count;
-  const int tx = threadIdx.x & (r.along - 1), group = threadIdx.x / r.along;
-  const int64_t part = blockIdx.x / r.slices;
-  const int slice = static_cast<int>(blockIdx.x - part * r.slices);
-  const int64_t range = part * (kThreads / r.along) + group;
+  const uint32_t n = r.count[0], listed = r.count[1];
   const uint32_t length = range_length(n, r.ranges);
-  const int64_t c = (static_cast<int64_t>(slice) * r.along + tx) * kPer;
-  if (range >= r.ranges || (range + 1) * length >= n || c >= a.D) return;
-  const uint32_t p0 = static_cast<uint32_t>(range) * length, p1 = p0 + length;
-  const uint32_t token = r.key[p1];
-  if (r.key[p1 - 1] != token || (r.key[p0] == token && p0 > 0 && r.key[p0 - 1] == token)) return;
-  float sum[kPer];
-  const auto add_slot = [&](int64_t i, bool first) {
-    const float* slot = r.slots + i * r.slot_ld + c;
-#pragma unroll
-    for (int j = 0; j < kPer; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(slot + j);
-      sum[j] = first ? v.x : sum[j] + v.x;
-      sum[j + 1] = first ? v.y : sum[j + 1] + v.y;
-      sum[j + 2] = first ? v.z : sum[j + 2] + v.z;
-      sum[j + 3] = first ? v.w : sum[j + 3] + v.w;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t slices = (D + 127) / 128;
+  for (int64_t item = blockIdx.x; item < listed * slices; item += gridDim.x) {
+    const int64_t range = r.list[item / slices];
+    const int64_t c = (item % slices) * 128 + lane * 4;
+    const uint32_t token = r.place[(range + 1) * length].x;
+    // the ranges behind it that begin within the sum
+    int64_t last = range;
+    for (bool more = true; more; last += more ? 32 : 0) {
+      const int64_t i = last + 1 + lane;
+      const uint32_t in = __ballot_sync(0xffffffffu, i * length < n && r.place[i * length].x == token);
+      more = in == 0xffffffffu;
+      if (!more) last += __popc(in);
     }
-  };
-  add_slot(2 * range + 1, true);
-  for (int64_t i = range + 1; i * length < n && r.key[i * length] == token; ++i) add_slot(2 * i, false);
-  if (dev_check(index_ok(token, V), a.err))
-    put_sums<O, kPer>(a.dW + token * a.lddw, c, a.D, sum, a.scale, a.beta, a.words != 0);
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // slot 0 of this loop is the range's own second one, slot k the first of the k-th behind it
+    for (int64_t k0 = warp; k0 <= last - range; k0 += kWarps * kEach) {
+      float4 v[kEach];
+#pragma unroll
+      for (int u = 0; u < kEach; ++u) {
+        const int64_t k = k0 + u * kWarps;
+        v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k <= last - range && c < r.slot_ld)
+          v[u] = *reinterpret_cast<const float4*>(r.slots + (2 * (range + k) + (k == 0)) * r.slot_ld + c);
+      }
+#pragma unroll
+      for (int u = 0; u < kEach; ++u) {
+        s.x += v[u].x;
+        s.y += v[u].y;
+        s.z += v[u].z;
+        s.w += v[u].w;
+      }
+    }
+    __syncthreads();
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < D) {
+      float all[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 v = sums[w][lane];
+        all[0] += v.x;
+        all[1] += v.y;
+        all[2] += v.z;
+        all[3] += v.w;
+      }
+      if (dev_check(index_ok(token, V), err))
+        put_sums<O, 4>(dW + token * lddw, c, D, all, scale, beta, false);
+    }
+  }
 }
 
 // ---- the call's plan
@@ -663,11 +766,11 @@ struct GradPlan {
   int along = 8, slices = 1, ctas = 1;
   int bits = 1, passes = 1;
   int64_t ranges = 1, slot_ld = 0, blocks = 1;
-  size_t key_off[2] = {}, at_off[2] = {}, count_off = 0, slots_off = 0, total = 0;
+  size_t place_off[2] = {}, count_off = 0, list_off = 0, slots_off = 0, total = 0;
 };
 
-void grad_plan(int dtype, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g) {
-  const int per = 16 / elem_bytes_of(dtype);
+void grad_plan(int dtype, int dtype_out, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g) {
+  const int wider = std::max(elem_bytes_of(dtype), elem_bytes_of(dtype_out)), per = 16 / wider;
   const int64_t pieces = (D + per - 1) / per;
   if (T <= kFewTokens) {
     g->few = true;
@@ -688,42 +791,66 @@ void grad_plan(int dtype, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g)
   while (width < 31 && (V - 1) >> width) ++width;
   g->passes = (width + kDigitBits - 1) / kDigitBits;
   g->bits = (width + g->passes - 1) / g->passes;
-  g->ctas = T <= 2048 ? 1 : 8;
+  g->ctas = T <= kOneCta ? 1 : T <= kEightCtas ? 8 : 16;
   size_t at = streamk_flag_bytes(sms);
   const auto take = [&](size_t bytes) {
     const size_t o = at;
     at += round256(bytes);
     return o;
   };
-  g->count_off = take(4);
-  for (int i = 0; i < 2; ++i) {
-    g->key_off[i] = take(static_cast<size_t>(T) * 4);
-    g->at_off[i] = take(static_cast<size_t>(T) * 4);
-  }
+  g->count_off = take(8);
+  g->list_off = take(static_cast<size_t>(g->ranges) * 4);
+  for (int i = 0; i < 2; ++i) g->place_off[i] = take(static_cast<size_t>(T) * sizeof(uint2));
   g->slots_off = take(static_cast<size_t>(g->ranges) * 2 * g->slot_ld * 4);
   g->total = at;
 }
 
+// Clusters of 16 are not portable: whether this device runs one, else 8 do.
 template <int kCtas>
-cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
+cudaError_t sort_config(cudaStream_t stream, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr) {
   static DeviceOnce configured;
-  const cudaError_t e = set_smem_once(configured, embedding_sort_kernel<kCtas>, kSortSmem);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = kCtas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
+  cfg->gridDim = dim3(kCtas);
+  cfg->blockDim = dim3(kSortThreads);
+  cfg->dynamicSmemBytes = sort_smem_bytes<kCtas>();
+  cfg->stream = stream;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+  return static_cast<cudaError_t>(configured.get(
+      dev,
+      [&] {
+        cudaError_t r = cudaFuncSetAttribute(embedding_sort_kernel<kCtas>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(cfg->dynamicSmemBytes));
+        if (r == cudaSuccess && kCtas > 8)
+          r = cudaFuncSetAttribute(embedding_sort_kernel<kCtas>,
+                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        int clusters = 1;
+        if (r == cudaSuccess && kCtas > 8)
+          r = cudaOccupancyMaxActiveClusters(&clusters, embedding_sort_kernel<kCtas>, cfg);
+        if (r == cudaSuccess && clusters < 1) r = cudaErrorInvalidConfiguration;
+        return static_cast<int>(r);
+      },
+      [](int r) { return r == static_cast<int>(cudaSuccess) ||
+                       r == static_cast<int>(cudaErrorInvalidConfiguration); }));
+}
+template <int kCtas>
+cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCtas);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = kSortSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<kCtas>, s);
+  const cudaError_t e = sort_config<kCtas>(stream, &cfg, attr);
+  if (e == cudaSuccess) return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<kCtas>, s);
+  if (kCtas <= 8) return e;
+  cudaGetLastError();
+  return launch_sort<(kCtas > 8 ? 8 : kCtas)>(s, stream);
 }
 
 template <typename S, typename O>
@@ -733,11 +860,12 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   const int sms = ctx.sm_count;
   const GradArgs<S, O> a{static_cast<const S*>(dY), lddy,  static_cast<O*>(dW), lddw, D, scale, beta,
                          rows_on(dW, lddw, sizeof(O), 16), ctx.err};
-  const bool any = !rows_on(dY, lddy, sizeof(S), 16);
-  // the rows without tokens: about 32 KB a block at least, four blocks an SM at most
+  const bool any = !rows_on(dY, lddy, sizeof(S), sum_values<S, O>() * sizeof(S));
+  // the rows without tokens: about 32 KB a block at least, two blocks an SM at most
+  // (each looks at all tokens)
   const int64_t row_bytes = D * static_cast<int64_t>(sizeof(O));
   int64_t share = (32768 + row_bytes - 1) / row_bytes;
-  const int64_t even = (k.V + static_cast<int64_t>(sms) * 4 - 1) / (static_cast<int64_t>(sms) * 4);
+  const int64_t even = (k.V + static_cast<int64_t>(sms) * 2 - 1) / (static_cast<int64_t>(sms) * 2);
   if (share < even) share = even;
   const int64_t rest = beta == 1.0f ? 0 : (k.V + share - 1) / share;
   if (g.few) {
@@ -752,15 +880,14 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   }
   SortArgs s{};
   s.k = k;
-  for (int i = 0; i < 2; ++i) {
-    s.key[i] = reinterpret_cast<uint32_t*>(ws + g.key_off[i]);
-    s.at[i] = reinterpret_cast<uint32_t*>(ws + g.at_off[i]);
-  }
+  for (int i = 0; i < 2; ++i) s.list[i] = reinterpret_cast<uint2*>(ws + g.place_off[i]);
   s.count = reinterpret_cast<uint32_t*>(ws + g.count_off);
   s.bits = g.bits;
   s.passes = g.passes;
   s.err = ctx.err;
-  int st = finish_launch(g.ctas == 1 ? launch_sort<1>(s, stream) : launch_sort<8>(s, stream),
+  int st = finish_launch(g.ctas == 1   ? launch_sort<1>(s, stream)
+                         : g.ctas == 8 ? launch_sort<8>(s, stream)
+                                       : launch_sort<16>(s, stream),
                          "embedding sort launch", stream);
   if (st != GEMM14_OK) return st;
   if (rest) {
@@ -771,17 +898,19 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
     if (st != GEMM14_OK) return st;
   }
   const int last = (g.passes - 1) & 1;
-  const Ranges r{s.key[last],   s.at[last], s.count, reinterpret_cast<float*>(ws + g.slots_off),
-                 g.slot_ld,     g.ranges,   g.along, g.slices};
+  const Ranges r{s.list[last], s.count, reinterpret_cast<uint32_t*>(ws + g.list_off),
+                 reinterpret_cast<float*>(ws + g.slots_off), g.slot_ld, g.ranges, g.along, g.slices};
   const auto sum = any ? embedding_sum_kernel<S, O, true> : embedding_sum_kernel<S, O, false>;
   st = finish_launch(launch_kernel(sum, dim3(static_cast<unsigned>(g.blocks)), dim3(kThreads), 0,
                                    stream, a, r, k.T, k.V),
                      "embedding gradient launch", stream);
   if (st != GEMM14_OK) return st;
-  return finish_launch(launch_kernel(embedding_join_kernel<S, O>,
-                                     dim3(static_cast<unsigned>(g.blocks)), dim3(kThreads), 0,
-                                     stream, a, r, k.V),
-                       "embedding gradient launch", stream);
+  if (g.ranges == 1) return GEMM14_OK;
+  const int64_t items = g.ranges * ((D + 127) / 128), most = static_cast<int64_t>(sms) * 4;
+  return finish_launch(
+      launch_kernel(embedding_join_kernel<O>, dim3(static_cast<unsigned>(items < most ? items : most)),
+                    dim3(kThreads), 0, stream, a.dW, lddw, D, scale, beta, r, k.V, ctx.err),
+      "embedding gradient launch", stream);
 }
 
 bool element_type(int dtype) {
@@ -845,14 +974,14 @@ int gemm14_embedding_forward(int dtype, int dtype_out, int64_t T, int64_t V, int
   return finish_launch(e, "embedding launch", stream);
 }
 
-size_t gemm14_embedding_backward_workspace_bytes(int dtype, int64_t T, int64_t V, int64_t D,
-                                                 int sm_count) {
+size_t gemm14_embedding_backward_workspace_bytes(int dtype, int dtype_out, int64_t T, int64_t V,
+                                                 int64_t D, int sm_count) {
   if (sm_count <= 0 && current_sm_count(&sm_count) != GEMM14_OK) return 0;
-  if (!element_type(dtype) || T < 0 || T > kTrainMaxSize || V < 1 || V > kTrainMaxSize || D < 1 ||
+  if (!element_type(dtype) || !element_type(dtype_out) || T < 0 || T > kTrainMaxSize || V < 1 || V > kTrainMaxSize || D < 1 ||
       D > kTrainMaxSize)
     return 0;
   GradPlan g;
-  grad_plan(dtype, T, V, D, sm_count, &g);
+  grad_plan(dtype, dtype_out, T, V, D, sm_count, &g);
   return g.total;
 }
 
@@ -868,7 +997,7 @@ int gemm14_embedding_backward(int dtype, int dtype_out, int64_t T, int64_t V, in
   CallContext ctx;
   if ((st = call_device(&ctx)) != GEMM14_OK) return st;
   GradPlan g;
-  grad_plan(dtype, T, V, D, ctx.sm_count, &g);
+  grad_plan(dtype, dtype_out, T, V, D, ctx.sm_count, &g);
   if (g.total && (!workspace || workspace_bytes < g.total)) {
     note_error("gemm14_embedding_backward: %zu bytes of workspace given, %zu needed",
                workspace_bytes, g.total);

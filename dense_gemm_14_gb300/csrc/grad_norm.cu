@@ -44,7 +44,7 @@ constexpr int kMostEntries = 576;  // of a launch
 
 constexpr int kUnitBytes = 4096;
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 6;
+constexpr int kBlocksPerSm = 4;  // resident: 64 registers a thread
 constexpr int kEach = 8;  // pieces of 16 bytes a lane has of a unit
 
 __host__ __device__ inline int type_bytes(int type) { return type == GEMM14_DTYPE_F32 ? 4 : 2; }
@@ -67,9 +67,17 @@ __host__ inline int64_t entry_units(const Entry& e) {
 __device__ __forceinline__ uint32_t unit_at(uint32_t units, uint32_t w, uint32_t warps) {
   return static_cast<uint32_t>(static_cast<uint64_t>(units) * w / warps);
 }
-__device__ __forceinline__ uint32_t warp_of(uint32_t units, uint32_t u, uint32_t warps) {
+__host__ inline uint32_t warp_of(uint32_t units, uint32_t u, uint32_t warps) {
   return static_cast<uint32_t>(((static_cast<uint64_t>(u) + 1) * warps - 1) / units);
 }
+
+// Where the sums of the list's tensors lie among the slots (sum_units below):
+// tensor i's are [first[i], first[i + 1]).
+template <int kN>
+struct Parts {
+  int n;
+  uint32_t first[kN + 1];
+};
 
 // What a unit holds of its tensor: rows [row, row + rows) (more than one: whole
 // rows, side by side), and of each the part-th stretch of unit_values elements,
@@ -119,40 +127,68 @@ __device__ __forceinline__ float square_sum(float s, const Pack<S, 8>& p) {
   return s;
 }
 
+// s, the squares of the values c0, c0 + 1, .. (kPer of them), those `step`
+// further, and so on before c1, to the lane's sum; bits: what is set in any value.
+template <typename S>
+__device__ __forceinline__ void add_squares(double& sum, float s, uint32_t bits, const S* row,
+                                            int64_t c0, int step, int64_t c1) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
+  if (s <= 0x1p120f && s >= 0x1p-120f) {
+    sum += static_cast<double>(s);
+  } else if (bits & (sizeof(S) == 4 ? 0x7fffffffu : 0x7fff7fffu)) {
+#pragma unroll 1
+    for (int64_t c = c0; c < c1; c += step) {
+#pragma unroll 1
+      for (int64_t j = max(c, int64_t(0)); j < min(c + kPer, c1); ++j) {
+        const double x = static_cast<double>(to_f32(row[j]));
+        sum = fma(x, x, sum);
+      }
+    }
+  }
+}
+__device__ __forceinline__ uint32_t bits_of(const uint4& v) { return v.x | v.y | v.z | v.w; }
+
 template <typename S>
 __device__ __forceinline__ void add_unit(double& sum, const Entry& e, const Unit& u, int lane) {
   constexpr int kPer = 16 / static_cast<int>(sizeof(S));
-  const int along = lanes_along(u, e.cols, kPer), lx = lane & (along - 1);
-  for (int r = lane / along; r < u.rows; r += 32 / along) {
-    const S* row = static_cast<const S*>(e.src) + (u.row + r) * e.ld_src;
+  const S* row = static_cast<const S*>(e.src) + u.row * e.ld_src;
+  if (u.rows == 1) {
     const int before =
         static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / static_cast<int>(sizeof(S));
-    const int64_t c0 = u.part * unit_values(e.type) - before + lx * kPer;
-    Pack<S, kPer> p[kEach];
+    const int64_t from = u.part * unit_values(e.type) - before;
+    if (from >= 0 && from + unit_values(e.type) <= e.cols) {  // a whole unit
+      const uint4* at = reinterpret_cast<const uint4*>(row + from) + lane;
+      Pack<S, kPer> p[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) p[i] = load_pack<S, kPer, false>(row, c0 + i * along * kPer, e.cols, nullptr, nullptr);
-    float s[4] = {};
+      for (int i = 0; i < kEach; ++i) p[i].raw = at[32 * i];
+      float s[4] = {};
+      uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) s[i & 3] = square_sum(s[i & 3], p[i]);
-    const float all = (s[0] + s[1]) + (s[2] + s[3]);
-    if (all <= 0x1p120f && all >= 0x1p-120f) {
-      sum += static_cast<double>(all);
-    } else {
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) any |= p[i].raw.x | p[i].raw.y | p[i].raw.z | p[i].raw.w;
-      if (any & (sizeof(S) == 4 ? 0x7fffffffu : 0x7fff7fffu)) {
-#pragma unroll 1
-        for (int i = 0; i < kEach; ++i) {
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const int64_t c = c0 + i * along * kPer + j;
-            const double x = c >= 0 && c < e.cols ? static_cast<double>(to_f32(row[c])) : 0.0;
-            sum = fma(x, x, sum);
-          }
-        }
+      for (int i = 0; i < kEach; ++i) {
+        s[i & 3] = square_sum(s[i & 3], p[i]);
+        bits |= bits_of(p[i].raw);
       }
+      add_squares(sum, (s[0] + s[1]) + (s[2] + s[3]), bits, row, from + lane * kPer, 32 * kPer,
+                  from + unit_values(e.type));
+      return;
     }
+  }
+  const int along = lanes_along(u, e.cols, kPer), lx = lane & (along - 1);
+  for (int r = lane / along; r < u.rows; r += 32 / along) {
+    const S* at = row + r * e.ld_src;
+    const int before =
+        static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u) / static_cast<int>(sizeof(S));
+    const int64_t from = u.part * unit_values(e.type) - before;
+    const int64_t c0 = from + lx * kPer, c1 = min(from + unit_values(e.type), e.cols);
+    float s = 0.0f;
+    uint32_t bits = 0;
+#pragma unroll 2
+    for (int64_t c = c0; c < c1; c += along * kPer) {
+      const Pack<S, kPer> p = load_pack<S, kPer, false>(at, c, c1, nullptr, nullptr);
+      s += square_sum(0.0f, p);
+      bits |= bits_of(p.raw);
+    }
+    add_squares(sum, s, bits, at, c0, along * kPer, c1);
   }
 }
 
@@ -218,109 +254,144 @@ __device__ __forceinline__ double block_sum(double v, double* smem) {
   __syncthreads();
   return warp_sum(lane < warps ? smem[lane] : 0.0);
 }
-// Slots [a, b], every `step`-th from the `from`-th.
+// Slots [a, b), every `step`-th from the `from`-th.
 __device__ __forceinline__ double slot_sum(const double* slots, uint32_t a, uint32_t b,
                                            uint32_t from, uint32_t step) {
   double s = 0.0;
-  for (uint32_t i0 = a + from; i0 <= b; i0 += 4 * step) {
-    double v[4];
+  for (uint32_t i0 = a + from; i0 < b; i0 += 8 * step) {
+    double v[8];
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) v[k] = i0 + k * step <= b ? __ldcg(slots + i0 + k * step) : 0.0;
-    s += (v[0] + v[1]) + (v[2] + v[3]);
+    for (uint32_t k = 0; k < 8; ++k) v[k] = i0 + k * step < b ? __ldcg(slots + i0 + k * step) : 0.0;
+    s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
   }
   return s;
 }
 
-// By one block of 1024 threads at most.
-template <int kN>
-__device__ __forceinline__ void finish(const Table<kN>& t, const Finish& f, uint32_t warps,
-                                       double* smem) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in_block = blockDim.x >> 5;
-  const uint32_t slots = warps + static_cast<uint32_t>(t.n) - 1u;
-  const double total =
-      block_sum(slot_sum(f.slots, 0u, slots - 1u, threadIdx.x, blockDim.x), smem);
-  if (threadIdx.x == 0) {
-    double all = total;
-    for (int l = 0; l < f.launch; ++l) all += f.totals[l];
-    f.totals[f.launch] = total;
-    if (f.last) {
-      const double norm = sqrt(all) * fabs(static_cast<double>(f.scale));
-      *f.norm = static_cast<float>(norm);
-      if (f.factor) {
-        const bool over = norm > static_cast<double>(f.max_norm) && norm - norm == 0.0;
-        *f.factor = over ? static_cast<float>(f.scale * (f.max_norm / norm)) : f.scale;
-      }
-    }
-  }
-  if (!f.each) return;
-  // a tensor of up to 32 slots a lane to a warp, longer ones to the block
-  constexpr uint32_t kLong = 1024;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int i = pass ? 0 : warp; i < t.n; i += pass ? 1 : in_block) {
-      const uint32_t first = t.e[i].first_unit;
-      const uint32_t end = i + 1 < t.n ? t.e[i + 1].first_unit : t.units;
-      const uint32_t a = warp_of(t.units, first, warps) + i, b = warp_of(t.units, end - 1, warps) + i;
-      if ((b - a >= kLong) != (pass == 1)) continue;
-      const double s = pass ? block_sum(slot_sum(f.slots, a, b, threadIdx.x, blockDim.x), smem)
-                            : warp_sum(slot_sum(f.slots, a, b, lane, 32u));
-      if (pass ? threadIdx.x == 0 : lane == 0)
-        f.each[i] = static_cast<float>(sqrt(s) * fabs(static_cast<double>(f.scale)));
-    }
+// The norm and the factor, by one block.
+__device__ __forceinline__ void finish_total(const Finish& f, uint32_t slots, double* smem) {
+  const double total = block_sum(slot_sum(f.slots, 0u, slots, threadIdx.x, blockDim.x), smem);
+  if (threadIdx.x != 0) return;
+  double all = total;
+  for (int l = 0; l < f.launch; ++l) all += f.totals[l];
+  f.totals[f.launch] = total;
+  if (!f.last) return;
+  const double norm = sqrt(all) * fabs(static_cast<double>(f.scale));
+  *f.norm = static_cast<float>(norm);
+  if (f.factor) {
+    const bool over = norm > static_cast<double>(f.max_norm) && norm - norm == 0.0;
+    *f.factor = over ? static_cast<float>(f.scale * (f.max_norm / norm)) : f.scale;
   }
 }
+// The norms of the tensors block, block + blocks, ..: a warp each, the block for
+// one of many slots. (All of them by one block took 35 us for 109 tensors: an SM
+// does two fp64 operations a cycle, and a root is some thirty of a warp's.)
+template <int kN>
+__device__ __forceinline__ void finish_each(const Parts<kN>& t, const Finish& f, int block,
+                                            int blocks, double* smem) {
+  constexpr uint32_t kLong = 1024;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  for (int i = block + warp * blocks; i < t.n; i += warps * blocks) {
+    if (t.first[i + 1] - t.first[i] > kLong) continue;
+    const double s = warp_sum(slot_sum(f.slots, t.first[i], t.first[i + 1], lane, 32u));
+    if (lane == 0) f.each[i] = static_cast<float>(sqrt(s) * fabs(static_cast<double>(f.scale)));
+  }
+  for (int i = block; i < t.n; i += blocks) {
+    if (t.first[i + 1] - t.first[i] <= kLong) continue;
+    const double s =
+        block_sum(slot_sum(f.slots, t.first[i], t.first[i + 1], threadIdx.x, blockDim.x), smem);
+    if (threadIdx.x == 0)
+      f.each[i] = static_cast<float>(sqrt(s) * fabs(static_cast<double>(f.scale)));
+  }
+}
+// Blocks that share finish_each.
+constexpr int kEachBlocks = 64;
 
 // ---- scaling
 
-// kPer values from the source's word(s), to one or two words of the output: the
-// pieces are the aligned words of the output, the source's, where they lie
-// otherwise, are read as two words and a shift. Products are rounded to fp32 and
-// then to a 16-bit type: within half a step and 2^-24 of the value.
+// A lane's pieces of a unit: kPer values each, one 16-byte word of the output (so
+// a warp's stores lie side by side); the source's word, where it does not start
+// on its own size, is read as two and a shift. kEach of them are in flight.
+// Products are rounded to fp32 and then to a 16-bit type: within half a step and
+// 2^-24 of the value.
+template <typename S, typename O, int kPer>
+__device__ __forceinline__ Pack<O, kPer> scaled(const Pack<S, kPer>& p, float f) {
+  Pack<O, kPer> y;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) y.x[j] = from_f32<O>(f * to_f32(p.x[j]));
+  return y;
+}
+
 template <typename S, typename O, bool kAny>
-__device__ __forceinline__ void scale_row(const S* src, O* dst, const S* begin, const S* end,
-                                          int64_t cols, int64_t c0, int step, float f) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(S)), kWord = 16 / static_cast<int>(sizeof(O));
-  Pack<S, kPer> p[kEach];
+__device__ __forceinline__ void scale_whole(const S* src, O* dst, int lane, float f) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(O));
+  constexpr int kPieces = kUnitBytes / static_cast<int>(sizeof(S)) / kPer / 32;  // a lane's
+  using W = decltype(Pack<S, kPer>().raw);
+  src += lane * kPer;
+  dst += lane * kPer;
+#pragma unroll 1
+  for (int b = 0; b < kPieces; b += kEach) {
+    Pack<S, kPer> p[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) p[i] = load_pack<S, kPer, kAny>(src, c0 + i * step, cols, begin, end);
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int64_t c = c0 + i * step;
-    if (c >= cols) break;
-    O y[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) y[j] = from_f32<O>(f * to_f32(p[i].x[j]));
-    if (c >= 0 && c + kPer <= cols) {
-#pragma unroll
-      for (int k = 0; k < kPer / kWord; ++k) {
-        Pack<O, kWord> w;
-#pragma unroll
-        for (int j = 0; j < kWord; ++j) w.x[j] = y[k * kWord + j];
-        *reinterpret_cast<uint4*>(dst + c + k * kWord) = w.raw;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (c + j >= 0 && c + j < cols) dst[c + j] = y[j];
+    for (int i = 0; i < kEach; ++i) {
+      if constexpr (kAny)
+        p[i].raw = load_word_any(src + i * 32 * kPer, W());
+      else
+        p[i].raw = *reinterpret_cast<const W*>(src + i * 32 * kPer);
     }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      *reinterpret_cast<uint4*>(dst + i * 32 * kPer) = scaled<S, O, kPer>(p[i], f).raw;
+    src += kEach * 32 * kPer;
+    dst += kEach * 32 * kPer;
   }
 }
 
 template <typename S, typename O>
 __device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int lane, float f) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
-  const int along = lanes_along(u, e.cols, kPer), lx = lane & (along - 1);
+  constexpr int kPer = 16 / static_cast<int>(sizeof(O));
+  constexpr int kSourceBytes = kPer * static_cast<int>(sizeof(S));
   const S* begin = static_cast<const S*>(e.src);
   const S* end = begin + (e.rows - 1) * e.ld_src + e.cols;
-  for (int r = lane / along; r < u.rows; r += 32 / along) {
-    const S* src = begin + (u.row + r) * e.ld_src;
-    O* dst = static_cast<O*>(e.dst) + (u.row + r) * e.ld_dst;
+  const S* src = begin + u.row * e.ld_src;
+  O* dst = static_cast<O*>(e.dst) + u.row * e.ld_dst;
+  if (u.rows == 1) {
     const int before =
         static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15u) / static_cast<int>(sizeof(O));
-    const int64_t c0 = u.part * unit_values(e.type) - before + lx * kPer;
-    if ((reinterpret_cast<uintptr_t>(src - before) & 15u) == 0)
-      scale_row<S, O, false>(src, dst, begin, end, e.cols, c0, along * kPer, f);
-    else
-      scale_row<S, O, true>(src, dst, begin, end, e.cols, c0, along * kPer, f);
+    const int64_t from = u.part * unit_values(e.type) - before;
+    if (from >= 0 && from + unit_values(e.type) <= e.cols) {
+      if ((reinterpret_cast<uintptr_t>(src + from) & (kSourceBytes - 1)) == 0) {
+        scale_whole<S, O, false>(src + from, dst + from, lane, f);
+        return;
+      }
+      if (words_inside(src + from, kSourceBytes, begin, end) &&
+          words_inside(src + from + unit_values(e.type) - kPer, kSourceBytes, begin, end)) {
+        scale_whole<S, O, true>(src + from, dst + from, lane, f);
+        return;
+      }
+    }
+  }
+  const int along = lanes_along(u, e.cols, kPer), lx = lane & (along - 1);
+  for (int r = lane / along; r < u.rows; r += 32 / along) {
+    const S* x = src + r * e.ld_src;
+    O* y = dst + r * e.ld_dst;
+    const int before =
+        static_cast<int>(reinterpret_cast<uintptr_t>(y) & 15u) / static_cast<int>(sizeof(O));
+    const int64_t from = u.part * unit_values(e.type) - before;
+    const int64_t c1 = min(from + unit_values(e.type), e.cols);
+    const bool words = (reinterpret_cast<uintptr_t>(x + from) & (kSourceBytes - 1)) == 0;
+#pragma unroll 2
+    for (int64_t c = from + lx * kPer; c < c1; c += along * kPer) {
+      const Pack<S, kPer> p = words ? load_pack<S, kPer, false>(x, c, e.cols, begin, end)
+                                    : load_pack<S, kPer, true>(x, c, e.cols, begin, end);
+      const Pack<O, kPer> q = scaled<S, O, kPer>(p, f);
+      if (c >= 0 && c + kPer <= e.cols) {
+        *reinterpret_cast<uint4*>(y + c) = q.raw;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (c + j >= 0 && c + j < e.cols) y[c + j] = q.x[j];
+      }
+    }
   }
 }
 
@@ -363,7 +434,7 @@ __device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint
 // ---- kernels
 
 template <int kN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_sum_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, double* slots) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -373,20 +444,44 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int kN>
 __global__ void __launch_bounds__(1024)
-    grad_finish_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, const Finish f) {
+    grad_finish_kernel(const __grid_constant__ Parts<kN> t, const Finish f) {
   __shared__ double smem[32];
   grid_dependency_wait();
   grid_launch_dependents();
-  finish(t, f, warps, smem);
+  if (blockIdx.x == 0)
+    finish_total(f, t.first[t.n], smem);
+  else
+    finish_each(t, f, blockIdx.x - 1, gridDim.x - 1, smem);
 }
 
 template <int kN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_scale_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, const float* factor) {
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (w < warps) scale_units(t, w, warps, threadIdx.x & 31, *factor);
+}
+
+// A short list: one cluster of kSmallCtas CTAs does all of it in one launch, its
+// barriers between the passes.
+constexpr int kSmallCtas = 8, kSmallThreads = 1024, kSmallEntries = 72;
+constexpr int64_t kSmallUnits = 1024;  // 4 MB
+template <int kN>
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    grad_small_kernel(const __grid_constant__ Table<kN> t, const __grid_constant__ Parts<kN> parts,
+                      uint32_t warps, double* slots, const Finish f) {
+  __shared__ double smem[32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t w = blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
+  if (w < warps) sum_units(t, w, warps, threadIdx.x & 31, slots);
+  cluster_sync();
+  if (blockIdx.x == 0) finish_total(f, parts.first[parts.n], smem);
+  if (f.each) finish_each(parts, f, blockIdx.x, kSmallCtas, smem);
+  if (!f.factor) return;
+  cluster_sync();
+  if (w < warps) scale_units(t, w, warps, threadIdx.x & 31, __ldcg(f.factor));
 }
 
 // ---- the calls
@@ -527,28 +622,66 @@ uint32_t warps_for(uint32_t units, int sms) { return std::min(units, most_warps(
 dim3 blocks_for(uint32_t warps) { return dim3((warps + kThreads / 32 - 1) / (kThreads / 32)); }
 
 template <int kN>
-int sum_launch(const Call& c, int64_t i0, int launch) {
-  Table<kN> t;
-  fill(c, i0, &t);
-  const uint32_t warps = warps_for(t.units, c.sms);
-  double* slots = reinterpret_cast<double*>(c.ws + c.l.slots);
-  int st = finish_launch(launch_kernel(grad_sum_kernel<kN>, blocks_for(warps), dim3(kThreads), 0,
-                                       c.stream, t, warps, slots),
-                         "gradient norm launch", c.stream);
-  if (st != GEMM14_OK) return st;
+Parts<kN> parts_of(const Table<kN>& t, uint32_t warps) {
+  Parts<kN> p;
+  p.n = t.n;
+  for (int i = 0; i < t.n; ++i) p.first[i] = warp_of(t.units, t.e[i].first_unit, warps) + i;
+  p.first[t.n] = warps + static_cast<uint32_t>(t.n) - 1u;
+  return p;
+}
+
+Finish finish_of(const Call& c, int64_t i0, int n, int launch) {
   Finish f{};
-  f.slots = slots;
+  f.slots = reinterpret_cast<double*>(c.ws + c.l.slots);
   f.totals = reinterpret_cast<double*>(c.ws + c.l.totals);
   f.launch = launch;
-  f.last = i0 + t.n == c.n;
+  f.last = i0 + n == c.n;
   f.scale = c.scale;
   f.max_norm = c.max_norm;
   f.norm = c.norm;
   f.each = c.each ? c.each + i0 : nullptr;
   f.factor = c.clip ? reinterpret_cast<float*>(c.ws + c.l.factor) : nullptr;
+  return f;
+}
+
+template <int kN>
+int small_call(const Call& c) {
+  Table<kN> t;
+  fill(c, 0, &t);
+  const uint32_t warps = std::min<uint32_t>(t.units, kSmallCtas * kSmallThreads / 32);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kSmallCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kSmallCtas);
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return finish_launch(
-      launch_kernel(grad_finish_kernel<kN>, dim3(1), dim3(1024), 0, c.stream, t, warps, f),
+      cudaLaunchKernelEx(&cfg, grad_small_kernel<kN>, t, parts_of(t, warps), warps,
+                         reinterpret_cast<double*>(c.ws + c.l.slots), finish_of(c, 0, t.n, 0)),
       "gradient norm launch", c.stream);
+}
+
+template <int kN>
+int sum_launch(const Call& c, int64_t i0, int launch) {
+  Table<kN> t;
+  fill(c, i0, &t);
+  const uint32_t warps = warps_for(t.units, c.sms);
+  const int st = finish_launch(
+      launch_kernel(grad_sum_kernel<kN>, blocks_for(warps), dim3(kThreads), 0, c.stream, t, warps,
+                    reinterpret_cast<double*>(c.ws + c.l.slots)),
+      "gradient norm launch", c.stream);
+  if (st != GEMM14_OK) return st;
+  const int blocks = 1 + (c.each ? std::min(t.n, kEachBlocks) : 0);
+  return finish_launch(launch_kernel(grad_finish_kernel<kN>, dim3(blocks), dim3(1024), 0, c.stream,
+                                     parts_of(t, warps), finish_of(c, i0, t.n, launch)),
+                       "gradient norm launch", c.stream);
 }
 template <int kN>
 int scale_launch(const Call& c, int64_t i0) {
@@ -562,7 +695,9 @@ int scale_launch(const Call& c, int64_t i0) {
 }
 
 // Tables of three sizes: a launch's parameters are copied with it.
-int run(const Call& c) {
+int run(const Call& c, int64_t units) {
+  if (c.n <= kSmallEntries && units <= kSmallUnits)
+    return c.n <= 16 ? small_call<16>(c) : small_call<kSmallEntries>(c);
   int launch = 0;
   for (int64_t i0 = 0; i0 < c.n; i0 += kMostEntries, ++launch) {
     const int64_t m = c.n - i0;
@@ -616,7 +751,7 @@ int grad_call(Call c, size_t workspace_bytes, const char* where) {
     note_error("%s: %zu bytes of workspace given, %zu needed", where, workspace_bytes, c.l.total);
     return GEMM14_ERR_INVALID_ARG;
   }
-  return run(c);
+  return run(c, units);
 }
 
 }  // namespace

@@ -406,9 +406,9 @@ def test_gradient_refusals(bad):
 
 def test_workspace_sizes():
     need = g14.embedding_backward_workspace_bytes
-    assert need(1, 256, 1000, 64, 152) == 0 and need(1, 257, 1000, 64, 152) > 257 * 16
-    assert need(9, 1000, 10, 64, 152) == 0 and need(1, 1000, 0, 64, 152) == 0 and need(1, -1, 10, 64, 152) == 0
-    big = need(1, 1 << 20, 1 << 20, 4096, 152)
+    assert need(1, 1, 256, 1000, 64, 152) == 0 and need(1, 0, 257, 1000, 64, 152) > 257 * 16
+    assert need(9, 0, 1000, 10, 64, 152) == 0 and need(1, 1, 1000, 0, 64, 152) == 0 and need(1, 1, -1, 10, 64, 152) == 0
+    big = need(1, 1, 1 << 20, 1 << 20, 4096, 152)
     assert (1 << 24) < big < (1 << 24) + (32 << 20)  # sixteen bytes a place, and slots that do not grow
 
 
@@ -416,7 +416,7 @@ def test_workspace_sizes():
 def test_small_workspace_is_refused():
     dy, t = torch.randn(1000, 64, device="cuda"), torch.zeros(1000, dtype=torch.int64, device="cuda")
     dw = torch.zeros(8, 64, device="cuda")
-    need = g14.embedding_backward_workspace_bytes(0, 1000, 8, 64)
+    need = g14.embedding_backward_workspace_bytes(0, 0, 1000, 8, 64)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     for ptr, n in ((ws.data_ptr(), need - 1), (None, 0)):
         assert g14.embedding_backward_raw(0, 0, 1000, 8, 64, dy.data_ptr(), 64, t.data_ptr(), 8, -100, 1.0, 0.0,
