@@ -606,14 +606,25 @@ __device__ __forceinline__ void range_ends(const Ranges& r, int64_t range, uint3
   p1 = q[1] < n ? moved(q[1], same[1]) : n;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
+// A thread's columns of a row of dW.
+template <typename O, int kPer>
+struct alignas(kPer * sizeof(O)) Columns {
+  O x[kPer];
+};
 
-template <typename S, typename O, bool kAny>
-__global__ void __launch_bounds__(kThreads, 4)
+// kMode kWordsAdd: sums are added to rows that are there (beta != 0). The old words
+// of the sums that end among the rows in flight are loaded with them, so that no
+// sum waits for its own (65536 places of 2048 columns, bf16 added to fp32: 225 us
+// with a load at each sum's end, @SUMADD@ so). kAnywhere: rows of dY or dW at any
+// address (dW's values are then moved one by one).
+enum SumMode { kWordsSet, kWordsAdd, kAnywhere };
+constexpr int kSumBlocks = 4;  // resident of an SM
+template <typename S, typename O, int kMode>
+__global__ void __launch_bounds__(kThreads, kSumBlocks)
     embedding_sum_kernel(const GradArgs<S, O> a, const Ranges r, int64_t T, int64_t V) {
   constexpr int kPer = sum_values<S, O>();
+  constexpr bool kAny = kMode == kAnywhere, kAdd = kMode == kWordsAdd;
+  constexpr int kRows = kAdd ? 4 : kRowsAhead;
   constexpr uint32_t kFlag = 0x80000000u;  // beside a token or a place, below 2^31
   grid_dependency_wait();
   grid_launch_dependents();
@@ -626,8 +637,11 @@ __global__ void __launch_bounds__(kThreads, 4)
   uint32_t p0 = n, p1 = n;
   if (range < r.ranges) range_ends(r, range, n, p0, p1);
   const uint32_t most = __reduce_max_sync(0xffffffffu, p1 - p0);  // of the warp's ranges
-  const bool live = c < a.D;
-  const S* end = a.dY + (T - 1) * a.lddy + a.D;
+  const bool live = c < a.D, whole = c + kPer <= a.D;
+  const uint32_t length = live ? p1 - p0 : 0u;
+  const S* from = a.dY + (kAny ? 0 : c);
+  O* to = a.dW + c;
+  float* slot = r.slots + 2 * range * r.slot_ld + c;
   // a stage of the range's places, one a lane: the token (kFlag: its sum goes on
   // behind the range) and the place (kFlag: the last of its sum here)
   const int stage = min(r.along, 32), in_stage = threadIdx.x & (stage - 1);
@@ -642,48 +656,68 @@ __global__ void __launch_bounds__(kThreads, 4)
   };
   float sum[kPer] = {};
   bool began_before = p0 > 0 && p0 < p1 && r.place[p0 - 1].x == r.place[p0].x;
-  const auto to_slot = [&](int which) {
-    float* slot = r.slots + (2 * range + which) * r.slot_ld + c;
-#pragma unroll
-    for (int j = 0; j < kPer; j += 4)
-      *reinterpret_cast<float4*>(slot + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
-  };
   uint2 next = places(0);
   for (uint32_t q = 0; q < most; q += stage) {
     const uint2 now = next;
     next = places(q + stage);
-    for (int u0 = 0; u0 < stage && q + u0 < most; u0 += kRowsAhead) {
-      Pack<S, kPer> x[kRowsAhead];
+    for (int u0 = 0; u0 < stage && q + u0 < most; u0 += kRows) {
+      Pack<S, kPer> x[kRows];
+      Columns<O, kPer> old[kAdd ? kRows : 1];
 #pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u) {
-        const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage) & ~kFlag;
-        if (live && p0 + q + u0 + u < p1)
-          x[u] = load_pack<S, kPer, kAny>(a.dY + static_cast<int64_t>(at) * a.lddy, c, a.D, a.dY, end);
-      }
-      // the old rows that these places' sums will be added to
-      if (a.beta != 0.0f) {
+      for (int u = 0; u < kRows; ++u) {
+        const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage);
+        const bool on = q + u0 + u < length;
+        const S* row = from + static_cast<int64_t>(at & ~kFlag) * a.lddy;
+        if constexpr (kAny) {
+          if (on)
+            x[u] = load_pack<S, kPer, true>(row, c, a.D, a.dY, a.dY + (T - 1) * a.lddy + a.D);
+        } else if (on && whole) {
+          x[u].raw = *reinterpret_cast<const decltype(x[u].raw)*>(row);
+        } else if (on) {
 #pragma unroll
-        for (int u = 0; u < kRowsAhead; ++u) {
-          const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage);
-          const uint32_t token = __shfl_sync(0xffffffffu, now.x, u0 + u, stage) & ~kFlag;
-          if (live && p0 + q + u0 + u < p1 && (at & kFlag) && index_ok(token, V))
-            prefetch_l2(a.dW + token * a.lddw + c);
+          for (int j = 0; j < kPer; ++j) x[u].x[j] = c + j < a.D ? row[j] : from_f32<S>(0.0f);
+        }
+        if constexpr (kAdd) {
+          const uint32_t token = __shfl_sync(0xffffffffu, now.x, u0 + u, stage);
+          if (on && whole && (at & kFlag) && !(token & kFlag) && dev_check(index_ok(token, V), a.err))
+            old[u] = *reinterpret_cast<const Columns<O, kPer>*>(to + token * a.lddw);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage);
         const uint32_t token = __shfl_sync(0xffffffffu, now.x, u0 + u, stage);
-        if (!live || p0 + q + u0 + u >= p1) continue;
+        if (q + u0 + u >= length) continue;
         add_to<S, kPer>(sum, x[u]);
         if (!(at & kFlag)) continue;
-        if (began_before) {
-          to_slot(0);
-        } else if (token & kFlag) {
-          to_slot(1);
-          if (c == 0) r.list[atomicAdd(r.count + 1, 1u)] = static_cast<uint32_t>(range);
+        if (began_before || (token & kFlag)) {
+          float* s = began_before ? slot : slot + r.slot_ld;
+#pragma unroll
+          for (int j = 0; j < kPer; j += 4)
+            *reinterpret_cast<float4*>(s + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+          if (c == 0 && !began_before)
+            r.list[atomicAdd(r.count + 1, 1u)] = static_cast<uint32_t>(range);
         } else if (dev_check(index_ok(token, V), a.err)) {
-          put_sums<O, kPer>(a.dW + token * a.lddw, c, a.D, sum, a.scale, a.beta, a.words != 0);
+          O* row = to + token * a.lddw;
+          if (!kAny && whole) {
+            Columns<O, kPer> y;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              const float s = a.scale * sum[j];
+              y.x[j] = from_f32<O>(kAdd ? fmaf(a.beta, to_f32(old[kAdd ? u : 0].x[j]), s) : s);
+            }
+            *reinterpret_cast<Columns<O, kPer>*>(row) = y;
+          } else {
+            float y[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+              y[j] = a.beta != 0.0f && c + j < a.D ? to_f32(row[j]) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+              if (c + j < a.D)
+                row[j] = from_f32<O>(a.beta != 0.0f ? fmaf(a.beta, y[j], a.scale * sum[j])
+                                                    : a.scale * sum[j]);
+          }
         }
         began_before = false;
 #pragma unroll
@@ -780,9 +814,9 @@ void grad_plan(int dtype, int dtype_out, int64_t T, int64_t V, int64_t D, int sm
   while (g->along < kThreads && g->along < pieces) g->along *= 2;
   g->slices = static_cast<int>((pieces + g->along - 1) / g->along);
   const int groups = kThreads / g->along;
-  // as many ranges as are resident at once (4 blocks an SM), of 8 places at least
+  // as many ranges as are resident at once, of 8 places at least
   const int64_t most = (T + kLeastRange - 1) / kLeastRange;
-  g->ranges = static_cast<int64_t>(sms) * 4 * groups / g->slices;
+  g->ranges = static_cast<int64_t>(sms) * kSumBlocks * groups / g->slices;
   if (g->ranges < 1) g->ranges = 1;
   if (g->ranges > most) g->ranges = most;
   g->blocks = (g->ranges + groups - 1) / groups * g->slices;
@@ -900,7 +934,9 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   const int last = (g.passes - 1) & 1;
   const Ranges r{s.list[last], s.count, reinterpret_cast<uint32_t*>(ws + g.list_off),
                  reinterpret_cast<float*>(ws + g.slots_off), g.slot_ld, g.ranges, g.along, g.slices};
-  const auto sum = any ? embedding_sum_kernel<S, O, true> : embedding_sum_kernel<S, O, false>;
+  const auto sum = any || !a.words ? embedding_sum_kernel<S, O, kAnywhere>
+                   : beta == 0.0f  ? embedding_sum_kernel<S, O, kWordsSet>
+                                   : embedding_sum_kernel<S, O, kWordsAdd>;
   st = finish_launch(launch_kernel(sum, dim3(static_cast<unsigned>(g.blocks)), dim3(kThreads), 0,
                                    stream, a, r, k.T, k.V),
                      "embedding gradient launch", stream);
