@@ -91,8 +91,7 @@ SIGNATURES = {
     "gemm14_embedding_backward": (_int, [_int, _int, _i64, _i64, _i64, _vp, _i64, _vp, _int, _i64,
                                          ctypes.c_float, ctypes.c_float, _vp, _i64, _vp,
                                          ctypes.c_size_t, _vp]),
-    "gemm14_embedding_backward_workspace_bytes": (ctypes.c_size_t, [_int, _int, _i64, _i64, _i64,
-                                                                    _int]),
+    "gemm14_embedding_backward_workspace_bytes": (ctypes.c_size_t, [_int, _i64, _i64, _i64, _int]),
     "gemm14_grad_norm": (_int, [_i64, _TENSORS, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t,
                                 _vp]),
     "gemm14_grad_clip": (_int, [_i64, _TENSORS, _TENSORS, ctypes.c_float, ctypes.c_float, _vp, _vp,
@@ -363,11 +362,9 @@ def embedding_backward_raw(dtype: int, dtype_out: int, T, V, D, dY, lddy, tokens
     return st
 
 
-def embedding_backward_workspace_bytes(dtype: int, dtype_out: int, T, V, D,
-                                       sm_count: int = 0) -> int:
+def embedding_backward_workspace_bytes(dtype: int, T, V, D, sm_count: int = 0) -> int:
     """C ABI gemm14_embedding_backward_workspace_bytes."""
-    return int(load().gemm14_embedding_backward_workspace_bytes(dtype, dtype_out, T, V, D,
-                                                                sm_count))
+    return int(load().gemm14_embedding_backward_workspace_bytes(dtype, T, V, D, sm_count))
 
 
 def grad_norm_raw(n, grads, scale, norm, each, workspace, workspace_bytes, stream=None,

@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/gemm14.h"
 #include "api_internal.h"
@@ -47,13 +48,16 @@ __device__ __forceinline__ bool takes_part(const Tokens& k, int64_t token) {
 // kAhead of them in flight; `along` threads (a power of two) share a row, the
 // block's others take other rows, and the next row's token is read while a row
 // is moved. A value is multiplied in fp32 and rounded to the output's type
-// (a second rounding, of a product that is right to 2^-24).
+// (a second rounding, of a product that is right to 2^-24); where nothing
+// changes, words are moved as they are.
 // kAny: rows at any address; the pieces are then the aligned words of the
-// output's row, the table's are read as two words and a shift.
+// output's row, the table's are read as two words and a shift, and the elements
+// before and behind them go one by one.
 // An output that L2 cannot hold is stored past it, so that the table's rows that
 // recur stay there.
 constexpr int kAhead = 4;
 constexpr double kStreamBytes = 64e6;
+enum : int { kStreamOut = 1, kCopy = 2 };  // flags of a lookup
 
 template <typename S, typename O>
 __host__ __device__ constexpr int lookup_values() {
@@ -63,10 +67,12 @@ __host__ __device__ constexpr int lookup_values() {
 template <typename S, typename O, bool kAny>
 __global__ void __launch_bounds__(kThreads)
     embedding_kernel(const S* W, int64_t ldw, const Tokens k, O* out, int64_t ldo, int64_t D,
-                     float scale, int along, int stream_out) {
+                     float scale, int along, int flags) {
+  constexpr int kPer = lookup_values<S, O>();
+  using WordS = decltype(Pack<S, kPer>().raw);
+  using WordO = decltype(Pack<O, kPer>().raw);
   grid_dependency_wait();
   grid_launch_dependents();
-  constexpr int kPer = lookup_values<S, O>();
   const int tx = threadIdx.x & (along - 1), ty = threadIdx.x / along;
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * (kThreads / along);
   int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / along) + ty;
@@ -79,71 +85,60 @@ __global__ void __launch_bounds__(kThreads)
     const float other = token == k.ignore ? 0.0f : __uint_as_float(0x7fc00000u);
     const S* from = W + (real ? token : 0) * ldw;
     O* to = out + t * ldo;
-    const int before =
-        kAny ? static_cast<int>(reinterpret_cast<uintptr_t>(to) & (kPer * sizeof(O) - 1)) /
-                   static_cast<int>(sizeof(O))
-             : 0;
-    for (int64_t c0 = static_cast<int64_t>(tx) * kPer - before; c0 < D;
-         c0 += static_cast<int64_t>(along) * kAhead * kPer) {
-      Pack<S, kPer> x[kAhead];
+    const auto one = [&](int64_t c) { to[c] = from_f32<O>(real ? scale * to_f32(from[c]) : other); };
+    int lead = 0;  // elements before the row's first aligned word
+    if (kAny) {
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(to) & (kPer * sizeof(O) - 1)) /
+                      static_cast<int>(sizeof(O));
+      lead = static_cast<int>(min(D, static_cast<int64_t>((kPer - off) & (kPer - 1))));
+    }
+    const int64_t words = (D - lead) / kPer;
+    const int tail = static_cast<int>(D - lead - words * kPer);
+    for (int64_t i0 = tx; i0 < words; i0 += static_cast<int64_t>(along) * kAhead) {
+      const S* x = from + lead + i0 * kPer;
+      O* y = to + lead + i0 * kPer;
+      const int step = along * kPer;
+      const int64_t here = words - i0;
+      Pack<S, kPer> p[kAhead];
+      bool in[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int64_t c = c0 + static_cast<int64_t>(u) * along * kPer;
-        if (real) x[u] = load_pack<S, kPer, kAny>(from, c, D, W, end);
+        in[u] = u * along < here && real && (!kAny || words_inside(x + u * step, sizeof(WordS), W, end));
+        if (!in[u]) continue;
+        if constexpr (kAny)
+          p[u].raw = load_word_any(x + u * step, WordS());
+        else
+          p[u].raw = *reinterpret_cast<const WordS*>(x + u * step);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int64_t c = c0 + static_cast<int64_t>(u) * along * kPer;
-        Pack<O, kPer> y;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) y.x[j] = from_f32<O>(real ? scale * to_f32(x[u].x[j]) : other);
-        if (c >= 0 && c + kPer <= D) {
-          if (stream_out)
-            __stcs(reinterpret_cast<decltype(y.raw)*>(to + c), y.raw);
-          else
-            *reinterpret_cast<decltype(y.raw)*>(to + c) = y.raw;
-        } else {
+        if (u * along >= here) break;
+        if (kAny && real && !in[u]) {  // a word at the table's end
+#pragma unroll 1
+          for (int j = 0; j < kPer; ++j) one(lead + (i0 + u * along) * kPer + j);
+          continue;
+        }
+        Pack<O, kPer> q;
+        bool copied = false;
+        if constexpr (sizeof(S) == sizeof(O)) {
+          if ((flags & kCopy) && real) {
+            q.raw = p[u].raw;
+            copied = true;
+          }
+        }
+        if (!copied) {
 #pragma unroll
           for (int j = 0; j < kPer; ++j)
-            if (c + j >= 0 && c + j < D) to[c + j] = y.x[j];
+            q.x[j] = from_f32<O>(real ? scale * to_f32(p[u].x[j]) : other);
         }
+        if (flags & kStreamOut)
+          __stcs(reinterpret_cast<WordO*>(y + u * step), q.raw);
+        else
+          *reinterpret_cast<WordO*>(y + u * step) = q.raw;
       }
     }
-  }
-}
-
-// Rows at any address between types of different widths: a lane an element.
-template <typename S, typename O>
-__global__ void __launch_bounds__(kThreads)
-    embedding_elements_kernel(const S* W, int64_t ldw, const Tokens k, O* out, int64_t ldo,
-                              int64_t D, float scale, int along) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  constexpr int kEach = 8;
-  const int tx = threadIdx.x & (along - 1), ty = threadIdx.x / along;
-  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (kThreads / along);
-  int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / along) + ty;
-  int64_t next = t < k.T ? token_at(k, t) : 0;
-  for (; t < k.T; t += row_step) {
-    const int64_t token = next;
-    if (t + row_step < k.T) next = token_at(k, t + row_step);
-    const bool real = takes_part(k, token);
-    const float other = token == k.ignore ? 0.0f : __uint_as_float(0x7fc00000u);
-    const S* from = W + (real ? token : 0) * ldw;
-    O* to = out + t * ldo;
-    for (int64_t c0 = tx; c0 < D; c0 += static_cast<int64_t>(along) * kEach) {
-      float x[kEach];
-#pragma unroll
-      for (int u = 0; u < kEach; ++u) {
-        const int64_t c = c0 + static_cast<int64_t>(u) * along;
-        x[u] = real && c < D ? to_f32(from[c]) : 0.0f;
-      }
-#pragma unroll
-      for (int u = 0; u < kEach; ++u) {
-        const int64_t c = c0 + static_cast<int64_t>(u) * along;
-        if (c < D) to[c] = from_f32<O>(real ? scale * x[u] : other);
-      }
-    }
+    if (tx < lead) one(tx);
+    if (tx < tail) one(D - tail + tx);
   }
 }
 
@@ -152,7 +147,7 @@ __global__ void __launch_bounds__(kThreads)
 int threads_along(int64_t rows, int64_t items, int ahead, int sms) {
   int x = 8;
   while (x < kThreads && static_cast<int64_t>(x) * ahead < items) x *= 2;
-  while (x < kThreads && x < items && rows * x < static_cast<int64_t>(sms) * 1024) x *= 2;
+  while (x < kThreads && x < items && rows * x < static_cast<int64_t>(sms) * 512) x *= 2;
   return x;
 }
 
@@ -170,24 +165,15 @@ template <typename S, typename O>
 cudaError_t lookup_as(const void* W, int64_t ldw, const Tokens& k, void* out, int64_t ldo,
                       int64_t D, float scale, int sms, cudaStream_t stream) {
   constexpr int kPer = lookup_values<S, O>();
-  const S* w = static_cast<const S*>(W);
-  O* o = static_cast<O*>(out);
   const bool words = rows_on(W, ldw, sizeof(S), kPer * sizeof(S)) &&
                      rows_on(out, ldo, sizeof(O), kPer * sizeof(O));
-  if (!words && sizeof(S) != sizeof(O)) {
-    const int along = threads_along(k.T, D, 8, sms);
-    return launch_kernel(embedding_elements_kernel<S, O>, dim3(grid_for(k.T * along, sms)),
-                         dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along);
-  }
-  const int along = threads_along(k.T, (D + kPer - 1) / kPer + (words ? 0 : 1), kAhead, sms);
-  const int stream_out = static_cast<double>(k.T) * D * sizeof(O) > kStreamBytes;
-  if constexpr (sizeof(S) == sizeof(O)) {
-    if (!words)
-      return launch_kernel(embedding_kernel<S, O, true>, dim3(grid_for(k.T * along, sms)),
-                           dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along, stream_out);
-  }
-  return launch_kernel(embedding_kernel<S, O, false>, dim3(grid_for(k.T * along, sms)),
-                       dim3(kThreads), 0, stream, w, ldw, k, o, ldo, D, scale, along, stream_out);
+  const int along = threads_along(k.T, (D + kPer - 1) / kPer, kAhead, sms);
+  int flags = static_cast<double>(k.T) * D * sizeof(O) > kStreamBytes ? kStreamOut : 0;
+  if (std::is_same<S, O>::value && scale == 1.0f) flags |= kCopy;
+  return launch_kernel(words ? embedding_kernel<S, O, false> : embedding_kernel<S, O, true>,
+                       dim3(grid_for(k.T * along, sms)), dim3(kThreads), 0, stream,
+                       static_cast<const S*>(W), ldw, k, static_cast<O*>(out), ldo, D, scale, along,
+                       flags);
 }
 
 // ---- rows of the gradient that no token stands for
@@ -287,12 +273,13 @@ __device__ __forceinline__ void put_sums(O* row, int64_t c, int64_t D, const flo
       *at = p.raw;
     }
   } else {
+    float old[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (c + j >= D) break;
-      const float s = scale * sum[j];
-      row[c + j] = from_f32<O>(beta != 0.0f ? fmaf(beta, to_f32(row[c + j]), s) : s);
-    }
+    for (int j = 0; j < kPer; ++j) old[j] = beta != 0.0f && c + j < D ? to_f32(row[c + j]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (c + j < D)
+        row[c + j] = from_f32<O>(beta != 0.0f ? fmaf(beta, old[j], scale * sum[j]) : scale * sum[j]);
   }
 }
 
@@ -304,9 +291,9 @@ __device__ __forceinline__ void add_to(float (&sum)[kPer], const Pack<S, kPer>& 
 
 constexpr int kRowsAhead = 8;  // rows of dY in flight
 
-// Columns a thread has: one 16-byte word of the wider type.
-template <typename S, typename O>
-__host__ __device__ constexpr int sum_values() { return lookup_values<S, O>(); }
+// Columns a thread has: 16 bytes of dY's.
+template <typename S>
+__host__ __device__ constexpr int sum_values() { return 16 / static_cast<int>(sizeof(S)); }
 
 template <typename S, typename O>
 struct GradArgs {
@@ -319,22 +306,26 @@ struct GradArgs {
   unsigned* err;
 };
 
-// A few tokens: a block a token and a slice of the columns. The block of a
-// token's first place sums all its places, in order; the blocks past them write
-// the rows without tokens. One launch, no workspace.
-constexpr int kFewTokens = kThreads;
+// A few tokens: a block a place and a slice of the columns. The block of a token's
+// first place lists all its places, in order, and sums their rows, groups of
+// `along` threads a part of the list each (parts of 8 rows at least), the groups'
+// sums added in order; the other places' blocks end at once. The blocks behind
+// them write the rows without tokens. One launch, no workspace.
+constexpr int kFewTokens = 1024;
 
 template <typename S, typename O, bool kAny>
 __global__ void __launch_bounds__(kThreads)
-    embedding_grad_few_kernel(const GradArgs<S, O> a, const Tokens k, int slices, int64_t share) {
-  constexpr int kPer = sum_values<S, O>();
+    embedding_grad_few_kernel(const GradArgs<S, O> a, const Tokens k, int along, int slices,
+                              int64_t share) {
+  constexpr int kPer = sum_values<S>(), kEach = kFewTokens / kThreads;
   constexpr int kWarps = kThreads / 32, kMarked = 8192;
   __shared__ uint32_t marks[kMarked / 32];
   __shared__ int places[kFewTokens];
-  __shared__ int counts[kWarps];
+  __shared__ int counts[kEach * kWarps];
+  __shared__ float parts[kThreads * kPer];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int T = static_cast<int>(k.T), tid = threadIdx.x;
+  const int T = static_cast<int>(k.T), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (static_cast<int64_t>(blockIdx.x) >= static_cast<int64_t>(T) * slices) {
     const int64_t v0 = (blockIdx.x - static_cast<int64_t>(T) * slices) * share;
     write_rest(Rest<O>{a.dW, a.lddw, a.D, a.beta}, k, v0, min(k.V, v0 + share), marks, kMarked);
@@ -342,36 +333,129 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int t = blockIdx.x / slices, slice = blockIdx.x - t * slices;
   const int64_t token = token_at(k, t);
-  const bool same = tid < T && token_at(k, tid) == token;
-  if (__syncthreads_or(same && tid < t) || !takes_part(k, token)) return;
-  const uint32_t mine = __ballot_sync(0xffffffffu, same);
-  if ((tid & 31) == 0) counts[tid >> 5] = __popc(mine);
-  __syncthreads();
-  int at = __popc(mine & ((1u << (tid & 31)) - 1u)), n = 0;
+  bool same[kEach], earlier = false;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < tid >> 5) at += counts[w];
-    n += counts[w];
+  for (int e = 0; e < kEach; ++e) {
+    const int i = e * kThreads + tid;
+    same[e] = i < T && token_at(k, i) == token;
+    earlier = earlier || (same[e] && i < t);
   }
-  if (same) places[at] = tid;
+  if (__syncthreads_or(earlier) || !takes_part(k, token)) return;
+  uint32_t mine[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    mine[e] = __ballot_sync(0xffffffffu, same[e]);
+    if (lane == 0) counts[e * kWarps + warp] = __popc(mine[e]);
+  }
   __syncthreads();
-  const int64_t c = (static_cast<int64_t>(slice) * kThreads + tid) * kPer;
-  if (c >= a.D) return;
-  const S* end = a.dY + (k.T - 1) * a.lddy + a.D;
+  // the counts before this warp's, and of all: a lane a count
+  int before = lane < kEach * kWarps ? counts[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  const int n = __shfl_sync(0xffffffffu, before, 31);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int at = e * kWarps + warp, base = __shfl_sync(0xffffffffu, before, at) - __popc(mine[e]);
+    if (same[e]) places[base + __popc(mine[e] & ((1u << lane) - 1u))] = e * kThreads + tid;
+  }
+  __syncthreads();
+  const int tx = tid & (along - 1), group = tid / along;
+  const int64_t c = (static_cast<int64_t>(slice) * along + tx) * kPer;
+  const int groups = min(kThreads / along, (n + kRowsAhead - 1) / kRowsAhead);
+  const int share_of = (n + groups - 1) / groups;
+  const int end = group < groups ? min(n, (group + 1) * share_of) : 0;
+  const S* last = a.dY + (k.T - 1) * a.lddy + a.D;
   float sum[kPer] = {};
-  for (int i = 0; i < n; i += kRowsAhead) {
-    Pack<S, kPer> x[kRowsAhead];
+  if (c < a.D) {
+    for (int i = group * share_of; i < end; i += kRowsAhead) {
+      Pack<S, kPer> x[kRowsAhead];
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u)
-      if (i + u < n) x[u] = load_pack<S, kPer, kAny>(a.dY + places[i + u] * a.lddy, c, a.D, a.dY, end);
+      for (int u = 0; u < kRowsAhead; ++u)
+        if (i + u < end)
+          x[u] = load_pack<S, kPer, kAny>(a.dY + places[i + u] * a.lddy, c, a.D, a.dY, last);
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u)
-      if (i + u < n) add_to<S, kPer>(sum, x[u]);
+      for (int u = 0; u < kRowsAhead; ++u)
+        if (i + u < end) add_to<S, kPer>(sum, x[u]);
+    }
   }
-  put_sums<O, kPer>(a.dW + token * a.lddw, c, a.D, sum, a.scale, a.beta, a.words != 0);
+  if (groups > 1) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) parts[j * kThreads + tid] = sum[j];
+    __syncthreads();
+    for (int g = 1; g < groups && group == 0; ++g)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) sum[j] += parts[j * kThreads + g * along + tx];
+  }
+  if (group == 0 && c < a.D)
+    put_sums<O, kPer>(a.dW + token * a.lddw, c, a.D, sum, a.scale, a.beta, a.words != 0);
 }
 
 // ---- the places sorted by token
+
+// Up to kRanked places: each place's position is counted, the places of a lower
+// token and the earlier ones of its own, T^2 comparisons over all SMs with no
+// exchange between them. A block has 32 places, a lane each, and a warp every
+// 32nd chunk of 32 tokens to compare them with. (A radix sort by one SM took
+// 7.5 us for 300 places and 18 for 8192, @RANK@.)
+constexpr int kRankThreads = 1024, kRanked = 8192;
+
+__global__ void __launch_bounds__(kRankThreads)
+    embedding_rank_kernel(const Tokens k, uint2* list, uint32_t* count) {
+  __shared__ __align__(16) uint32_t tokens[kRanked];
+  __shared__ uint32_t counts[kRankThreads];
+  __shared__ uint32_t total;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int T = static_cast<int>(k.T), chunks = (T + 31) / 32;
+  if (tid == 0) total = 0u;
+  __syncthreads();
+  uint32_t valid = 0;
+  for (int i = tid; i < chunks * 32; i += kRankThreads) {
+    uint32_t v = ~0u;  // takes no part: above every token
+    if (i < T) {
+      const int64_t token = token_at(k, i);
+      if (takes_part(k, token)) v = static_cast<uint32_t>(token);
+    }
+    tokens[i] = v;
+    valid += v != ~0u;
+  }
+  valid = __reduce_add_sync(0xffffffffu, valid);
+  if (lane == 0 && blockIdx.x == 0) atomicAdd(&total, valid);
+  __syncthreads();
+  const int own = blockIdx.x;
+  const uint32_t mine = tokens[own * 32 + lane];
+  uint32_t lower = 0;
+  for (int chunk = warp; chunk < chunks; chunk += kRankThreads / 32) {
+    const uint4* at = reinterpret_cast<const uint4*>(tokens + chunk * 32);
+    if (chunk == own) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t v = tokens[chunk * 32 + j];
+        lower += v < mine || (v == mine && j < lane);
+      }
+    } else {
+      const uint32_t below = mine + (chunk < own ? 1u : 0u);  // (for ~0u no position is used)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 v = at[j];
+        lower += (v.x < below) + (v.y < below) + (v.z < below) + (v.w < below);
+      }
+    }
+  }
+  counts[tid] = lower;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t to = 0;
+#pragma unroll
+    for (int w = 0; w < kRankThreads / 32; ++w) to += counts[w * 32 + lane];
+    if (mine != ~0u) list[to] = make_uint2(mine, static_cast<uint32_t>(own * 32 + lane));
+  }
+  if (blockIdx.x == 0 && tid < 2) count[tid] = tid == 0 ? total : 0u;
+}
 
 // Radix sort, least significant digit first, of the places that take part, by
 // one cluster of kCtas CTAs whose barriers are the hardware's. In a pass every
@@ -381,7 +465,7 @@ __global__ void __launch_bounds__(kThreads)
 // the warp goes through its range again and moves the places there, in order:
 // a ballot for each bit of the digit finds the lanes that have the same one.
 // Two passes for a vocabulary of up to 2^18; the first leaves out what takes no
-// part. Between passes the list lies in L2; in shared memory where one CTA does.
+// part. Between passes the list lies in L2.
 // @SORT@
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
@@ -395,13 +479,8 @@ struct SortArgs {
   unsigned* err;
 };
 
-constexpr int kOneCta = kSortThreads * kSortAhead;  // places that one CTA sorts
-constexpr int kEightCtas = 2 * kOneCta;
-template <int kCtas>
-constexpr size_t sort_smem_bytes() {
-  return (static_cast<size_t>(kSortWarps) * kDigits + 2 * kDigits + 32) * 4 +
-         (kCtas == 1 ? static_cast<size_t>(kOneCta) * sizeof(uint2) : 0);
-}
+constexpr int kEightCtas = 16384;  // places that a cluster of 8 sorts, 16 where there are more
+constexpr size_t kSortSmem = (static_cast<size_t>(kSortWarps) * kDigits + 2 * kDigits + 32) * 4;
 
 __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -417,17 +496,16 @@ __global__ void __launch_bounds__(kSortThreads)
   uint32_t* total = hist + kSortWarps * kDigits;  // of this CTA, read by the others
   uint32_t* base = total + kDigits;
   uint32_t* sums = base + kDigits;                // of a warp's digits in the scan
-  uint2* own = reinterpret_cast<uint2*>(sums + 32);  // kCtas == 1: the list between passes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = kCtas > 1 ? cluster_ctarank() : 0u;
+  const uint32_t rank = cluster_ctarank();
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t T = static_cast<uint32_t>(a.k.T);
   uint32_t n = T;
   uint32_t* my_hist = hist + warp * kDigits;
   for (int pass = 0; pass < a.passes; ++pass) {
-    const uint2* in = kCtas == 1 ? own : a.list[(pass + 1) & 1];
-    uint2* out = kCtas == 1 && pass + 1 < a.passes ? own : a.list[pass & 1];
+    const uint2* in = a.list[(pass + 1) & 1];
+    uint2* out = a.list[pass & 1];
     const int shift = pass * a.bits;
     const uint32_t mask = (1u << a.bits) - 1u;
     const uint32_t per_cta = (n + kCtas - 1) / kCtas;
@@ -451,7 +529,7 @@ __global__ void __launch_bounds__(kSortThreads)
           const int64_t token = token_at(a.k, i);
           if (takes_part(a.k, token)) key[u] = static_cast<uint32_t>(token);
         } else {
-          const uint2 v = kCtas == 1 ? in[i] : __ldcg(in + i);
+          const uint2 v = __ldcg(in + i);
           key[u] = v.x;
           at[u] = v.y;
         }
@@ -475,16 +553,12 @@ __global__ void __launch_bounds__(kSortThreads)
       }
       total[tid] = s;
     }
-    if (kCtas > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    cluster_sync();
     uint32_t all = 0, before = 0;
     if (tid < kDigits) {
 #pragma unroll
       for (int c = 0; c < kCtas; ++c) {
-        const uint32_t v =
-            kCtas > 1 ? load_cluster_u32(mapa_shared(smem_u32(total + tid), c)) : total[tid];
+        const uint32_t v = load_cluster_u32(mapa_shared(smem_u32(total + tid), c));
         all += v;
         if (c < static_cast<int>(rank)) before += v;
       }
@@ -532,10 +606,7 @@ __global__ void __launch_bounds__(kSortThreads)
     }
     n = found;
     // the next pass reads what the others wrote, and writes what they read
-    if (kCtas > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    cluster_sync();
   }
   if (rank == 0 && tid < 2) a.count[tid] = tid == 0 ? n : 0u;
 }
@@ -554,15 +625,14 @@ struct Ranges {
   uint32_t* list;      // of the ranges where a sum begins that goes on behind them
   float* slots;        // two rows of slot_ld floats a range
   int64_t slot_ld;
-  int64_t ranges;
+  uint32_t ranges;
   int along, slices;
 };
 constexpr uint32_t kLeastRange = 8, kWhole = 16;
 
 // Places of a range: all ranges but the last hold as many, before their ends move.
-__device__ __forceinline__ uint32_t range_length(uint32_t n, int64_t ranges) {
-  const uint32_t even = static_cast<uint32_t>((n + ranges - 1) / ranges);
-  return max(kLeastRange, even);
+__device__ __forceinline__ uint32_t range_length(uint32_t n, uint32_t ranges) {
+  return max(kLeastRange, (n + ranges - 1u) / ranges);
 }
 // Where a range that should begin at p does, from which of the places p - 16 ..
 // p + 15 have p's token: at p, or behind the token that has places on both sides
@@ -572,152 +642,248 @@ __device__ __forceinline__ uint32_t moved(uint32_t p, uint32_t same) {
   const uint32_t after = static_cast<uint32_t>(__ffs(static_cast<int>(~(same >> 16))) - 1);
   return before == 0 || before + after > kWhole ? p : p + after;
 }
-// The range's places [p0, p1).
-__device__ __forceinline__ void range_ends(const Ranges& r, int64_t range, uint32_t n,
-                                           uint32_t& p0, uint32_t& p1) {
+
+// A thread's group of `along` threads, the places [p0, p1) of its range, its slice
+// of the columns and its place there. All of a warp's lanes look for the ends of
+// its groups' ranges, a place each.
+struct Group {
+  uint32_t range, p0, p1, most;  // most: places of the longest range of the warp's
+  int slice, tx;
+  bool began_before;  // the first sum, before the range
+};
+__device__ __forceinline__ Group group_of(const Ranges& r, uint32_t n) {
+  Group g;
+  const int lane = threadIdx.x & 31;
+  const uint32_t part = blockIdx.x / static_cast<uint32_t>(r.slices);
+  g.slice = static_cast<int>(blockIdx.x - part * r.slices);
+  g.tx = threadIdx.x & (r.along - 1);
+  g.range = part * (kThreads / r.along) + threadIdx.x / r.along;
   const uint32_t length = range_length(n, r.ranges);
-  const uint32_t q[2] = {
-      static_cast<uint32_t>(min(static_cast<int64_t>(n), range * length)),
-      static_cast<uint32_t>(min(static_cast<int64_t>(n), (range + 1) * length))};
-  uint32_t same[2] = {0u, 0u};
-  if (r.along >= 32) {  // a warp's range: its lanes look at a place each
-    uint32_t token[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int64_t i = static_cast<int64_t>(q[e]) - 16 + (threadIdx.x & 31);
-      token[e] = i >= 0 && i < n ? r.place[i].x : ~0u;
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      same[e] = __ballot_sync(0xffffffffu, token[e] == __shfl_sync(0xffffffffu, token[e], 16) &&
-                                               token[e] != ~0u);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t token = q[e] < n ? r.place[q[e]].x : ~0u;
-#pragma unroll 8
-      for (int u = 0; u < 32; ++u) {
-        const int64_t i = static_cast<int64_t>(q[e]) - 16 + u;
-        if (i >= 0 && i < n && r.place[i].x == token) same[e] |= 1u << u;
-      }
-    }
+  const uint32_t q0 = g.range < r.ranges ? min(n, g.range * length) : n;
+  const uint32_t q1 = g.range < r.ranges ? min(n, g.range * length + length) : n;
+  g.p0 = g.p1 = n;
+  g.began_before = false;
+  for (int from = 0; from < 32; from += r.along) {
+    const uint32_t a0 = __shfl_sync(0xffffffffu, q0, from), a1 = __shfl_sync(0xffffffffu, q1, from);
+    const int64_t i0 = static_cast<int64_t>(a0) - 16 + lane, i1 = static_cast<int64_t>(a1) - 16 + lane;
+    const uint32_t t0 = i0 >= 0 && i0 < n ? r.place[i0].x : ~0u;
+    const uint32_t t1 = i1 >= 0 && i1 < n ? r.place[i1].x : ~0u;
+    const uint32_t s0 = __ballot_sync(0xffffffffu, t0 == __shfl_sync(0xffffffffu, t0, 16));
+    const uint32_t s1 = __ballot_sync(0xffffffffu, t1 == __shfl_sync(0xffffffffu, t1, 16));
+    if (r.along < 32 && (lane & ~(r.along - 1)) != from) continue;
+    g.p0 = a0 < n ? moved(a0, a0 ? s0 : s0 & ~0xffffu) : n;
+    g.p1 = a1 < n ? moved(a1, s1) : n;
+    // a sum that goes on here is a long one, whose ranges' ends do not move
+    g.began_before = g.p0 < g.p1 && g.p0 == a0 && (s0 >> 15 & 1u) && a0 > 0;
   }
-  p0 = q[0] < n ? moved(q[0], same[0]) : n;
-  p1 = q[1] < n ? moved(q[1], same[1]) : n;
+  g.most = __reduce_max_sync(0xffffffffu, g.p1 - g.p0);
+  return g;
 }
 
-// A thread's columns of a row of dW.
-template <typename O, int kPer>
-struct alignas(kPer * sizeof(O)) Columns {
-  O x[kPer];
-};
+// A stage of a range's places, one a lane (of each 32, or of the group's lanes):
+// the token (kFlag: its sum goes on behind the range) and the place (kFlag: the
+// last of its sum here).
+constexpr uint32_t kFlag = 0x80000000u;
+__device__ __forceinline__ uint2 places_of(const Ranges& r, const Group& g, uint32_t n, uint32_t q,
+                                           int stage) {
+  const uint32_t p = g.p0 + q + (threadIdx.x & (stage - 1));
+  if (p >= g.p1) return make_uint2(0u, 0u);
+  uint2 v = r.place[p];
+  const bool same = p + 1 < n && r.place[p + 1].x == v.x;
+  if (p + 1 == g.p1 && same) v.x |= kFlag;
+  if (p + 1 == g.p1 || !same) v.y |= kFlag;
+  return v;
+}
+__device__ __forceinline__ uint2 from_lane(const uint2& v, int lane, int stage) {
+  return make_uint2(__shfl_sync(0xffffffffu, v.x, lane, stage),
+                    __shfl_sync(0xffffffffu, v.y, lane, stage));
+}
 
-// kMode kWordsAdd: sums are added to rows that are there (beta != 0). The old words
-// of the sums that end among the rows in flight are loaded with them, so that no
-// sum waits for its own (65536 places of 2048 columns, bf16 added to fp32: 225 us
-// with a load at each sum's end, @SUMADD@ so). kAnywhere: rows of dY or dW at any
-// address (dW's values are then moved one by one).
-enum SumMode { kWordsSet, kWordsAdd, kAnywhere };
+// bytes (at most 8 or 16) of kBytes from global to shared memory, zeros behind them.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 constexpr int kSumBlocks = 4;  // resident of an SM
-template <typename S, typename O, int kMode>
+
+// Rows that start on 16 bytes. What bounds it is how much is in flight: a row's
+// words go to shared memory by asynchronous copies, kDepth rows ahead, each
+// thread's to a place of its own, so that it waits for nothing but its own copies;
+// and where sums are added to rows that are there (kAdd), the old words of a sum
+// that ends come with the row that ends it. (With the words in registers, 4 or 8
+// rows loaded and then added, 65536 places of 2048 columns, bf16 added to fp32,
+// took 165 us for 597 MB; @SUMADD@ so.)
+template <typename S, typename O, bool kAdd>
+struct SumShape {
+  static constexpr int kWords = static_cast<int>(sizeof(O) / sizeof(S));  // of a thread
+  static constexpr int kCols = sum_values<S>() / kWords;  // of a word: 16 bytes of dW's
+  static constexpr int kRowBytes = kCols * static_cast<int>(sizeof(S));
+  static constexpr int kDepth = !kAdd ? 8 : kWords == 1 ? 6 : 4;
+  static constexpr int kSmem = kDepth * kThreads * kWords * (kRowBytes + (kAdd ? 16 : 0));
+};
+template <typename S, typename O, bool kAdd>
 __global__ void __launch_bounds__(kThreads, kSumBlocks)
-    embedding_sum_kernel(const GradArgs<S, O> a, const Ranges r, int64_t T, int64_t V) {
-  constexpr int kPer = sum_values<S, O>();
-  constexpr bool kAny = kMode == kAnywhere, kAdd = kMode == kWordsAdd;
-  constexpr int kRows = kAdd ? 4 : kRowsAhead;
-  constexpr uint32_t kFlag = 0x80000000u;  // beside a token or a place, below 2^31
+    embedding_sum_kernel(const GradArgs<S, O> a, const Ranges r, int64_t V) {
+  using Q = SumShape<S, O, kAdd>;
+  constexpr int kWords = Q::kWords, kCols = Q::kCols, kDepth = Q::kDepth;
+  extern __shared__ __align__(16) unsigned char sum_smem[];
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t n = *r.count;
-  const int tx = threadIdx.x & (r.along - 1), group = threadIdx.x / r.along;
-  const int64_t part = blockIdx.x / r.slices;
-  const int slice = static_cast<int>(blockIdx.x - part * r.slices);
-  const int64_t range = part * (kThreads / r.along) + group;
-  const int64_t c = (static_cast<int64_t>(slice) * r.along + tx) * kPer;
-  uint32_t p0 = n, p1 = n;
-  if (range < r.ranges) range_ends(r, range, n, p0, p1);
-  const uint32_t most = __reduce_max_sync(0xffffffffu, p1 - p0);  // of the warp's ranges
-  const bool live = c < a.D, whole = c + kPer <= a.D;
-  const uint32_t length = live ? p1 - p0 : 0u;
-  const S* from = a.dY + (kAny ? 0 : c);
+  const Group g = group_of(r, n);
+  // the thread's words, `along` words apart
+  const int64_t c = (static_cast<int64_t>(g.slice) * r.along * kWords + g.tx) * kCols;
+  const int apart = r.along * kCols;
+  const uint32_t length = c < a.D ? g.p1 - g.p0 : 0u;
+  const S* from = a.dY + c;
   O* to = a.dW + c;
-  float* slot = r.slots + 2 * range * r.slot_ld + c;
-  // a stage of the range's places, one a lane: the token (kFlag: its sum goes on
-  // behind the range) and the place (kFlag: the last of its sum here)
-  const int stage = min(r.along, 32), in_stage = threadIdx.x & (stage - 1);
-  const auto places = [&](uint32_t q) {
-    const uint32_t p = p0 + q + in_stage;
-    if (p >= p1) return make_uint2(0u, 0u);
-    uint2 v = r.place[p];
-    const bool same = p + 1 < n && r.place[p + 1].x == v.x;
-    if (p + 1 == p1 && same) v.x |= kFlag;
-    if (p + 1 == p1 || !same) v.y |= kFlag;
-    return v;
+  float* slot = r.slots + 2 * static_cast<int64_t>(g.range) * r.slot_ld + c;
+  unsigned char* rows = sum_smem + threadIdx.x * Q::kRowBytes;
+  unsigned char* olds = sum_smem + kDepth * kWords * kThreads * Q::kRowBytes + threadIdx.x * 16;
+  int left[kWords];  // columns of a word that there are
+#pragma unroll
+  for (int w = 0; w < kWords; ++w)
+    left[w] = static_cast<int>(max(int64_t(0), min(int64_t(kCols), a.D - c - w * apart)));
+  const auto fetch = [&](uint32_t i, const uint2& v, int at) {
+    if (i < length) {
+      const S* row = from + static_cast<int64_t>(v.y & ~kFlag) * a.lddy;
+      const bool ends = kAdd && (v.y & kFlag) && !(v.x & kFlag) && dev_check(index_ok(v.x, V), a.err);
+      const O* old = to + (ends ? v.x * a.lddw : 0);
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        if (left[w] == 0) break;
+        copy_async<Q::kRowBytes>(smem_u32(rows + (at * kWords + w) * kThreads * Q::kRowBytes),
+                                 row + w * apart, left[w] * static_cast<int>(sizeof(S)));
+        if (ends)
+          copy_async<16>(smem_u32(olds + (at * kWords + w) * kThreads * 16), old + w * apart,
+                         left[w] * static_cast<int>(sizeof(O)));
+      }
+    }
+    copy_commit();
   };
+  const int stage = min(r.along, 32);
+  uint2 now = places_of(r, g, n, 0, stage), next = places_of(r, g, n, stage, stage);
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i) fetch(i, from_lane(now, i, stage), i);
+  float sum[kWords][kCols] = {};
+  bool began_before = g.began_before;
+  int at = 0, j = 0;  // the ring's place, the stage's
+#pragma unroll 1
+  for (uint32_t i = 0; i < g.most; ++i) {
+    copy_wait<kDepth - 1>();
+    const uint2 v = from_lane(now, j, stage);
+    if (i < length) {
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        Pack<S, kCols> x;
+        x.raw = *reinterpret_cast<const decltype(x.raw)*>(rows + (at * kWords + w) * kThreads *
+                                                                     Q::kRowBytes);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) sum[w][k] += to_f32(x.x[k]);
+      }
+      if (v.y & kFlag) {
+        const bool part = began_before || (v.x & kFlag);
+        float* s = began_before ? slot : slot + r.slot_ld;
+        if (c == 0 && part && !began_before) r.list[atomicAdd(r.count + 1, 1u)] = g.range;
+        const bool mine = !part && dev_check(index_ok(v.x, V), a.err);
+        O* row = to + (mine ? v.x * a.lddw : 0);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          if (left[w] == 0) break;
+          if (part) {
+#pragma unroll
+            for (int k = 0; k < kCols; k += 4)
+              *reinterpret_cast<float4*>(s + w * apart + k) =
+                  make_float4(sum[w][k], sum[w][k + 1], sum[w][k + 2], sum[w][k + 3]);
+          } else if (mine) {
+            Pack<O, kCols> y, old;
+            if (kAdd)
+              old.raw = *reinterpret_cast<const decltype(old.raw)*>(olds + (at * kWords + w) *
+                                                                               kThreads * 16);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) {
+              const float p = a.scale * sum[w][k];
+              y.x[k] = from_f32<O>(kAdd ? fmaf(a.beta, to_f32(old.x[k]), p) : p);
+            }
+            if (left[w] == kCols) {
+              *reinterpret_cast<decltype(y.raw)*>(row + w * apart) = y.raw;
+            } else {
+#pragma unroll
+              for (int k = 0; k < kCols; ++k)
+                if (k < left[w]) row[w * apart + k] = y.x[k];
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) sum[w][k] = 0.0f;
+        }
+        began_before = false;
+      }
+    }
+    const int ahead = j + kDepth;
+    fetch(i + kDepth, ahead < stage ? from_lane(now, ahead, stage) : from_lane(next, ahead - stage, stage), at);
+    at = at + 1 == kDepth ? 0 : at + 1;
+    if (++j == stage) {
+      j = 0;
+      now = next;
+      next = places_of(r, g, n, i + 1 + stage, stage);
+    }
+  }
+}
+
+// Rows of dY or dW at any address: words read as two and a shift, kRowsAhead rows at
+// a time in registers, dW's values moved one by one.
+template <typename S, typename O>
+__global__ void __launch_bounds__(kThreads, kSumBlocks)
+    embedding_sum_any_kernel(const GradArgs<S, O> a, const Ranges r, int64_t T, int64_t V) {
+  constexpr int kPer = sum_values<S>();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t n = *r.count;
+  const Group g = group_of(r, n);
+  const int64_t c = (static_cast<int64_t>(g.slice) * r.along + g.tx) * kPer;
+  const uint32_t length = c < a.D ? g.p1 - g.p0 : 0u;
+  const S* end = a.dY + (T - 1) * a.lddy + a.D;
+  float* slot = r.slots + 2 * static_cast<int64_t>(g.range) * r.slot_ld + c;
+  const int stage = min(r.along, 32);
   float sum[kPer] = {};
-  bool began_before = p0 > 0 && p0 < p1 && r.place[p0 - 1].x == r.place[p0].x;
-  uint2 next = places(0);
-  for (uint32_t q = 0; q < most; q += stage) {
+  bool began_before = g.began_before;
+  uint2 next = places_of(r, g, n, 0, stage);
+  for (uint32_t q = 0; q < g.most; q += stage) {
     const uint2 now = next;
-    next = places(q + stage);
-    for (int u0 = 0; u0 < stage && q + u0 < most; u0 += kRows) {
-      Pack<S, kPer> x[kRows];
-      Columns<O, kPer> old[kAdd ? kRows : 1];
+    next = places_of(r, g, n, q + stage, stage);
+    for (int u0 = 0; u0 < stage && q + u0 < g.most; u0 += kRowsAhead) {
+      Pack<S, kPer> x[kRowsAhead];
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage);
-        const bool on = q + u0 + u < length;
-        const S* row = from + static_cast<int64_t>(at & ~kFlag) * a.lddy;
-        if constexpr (kAny) {
-          if (on)
-            x[u] = load_pack<S, kPer, true>(row, c, a.D, a.dY, a.dY + (T - 1) * a.lddy + a.D);
-        } else if (on && whole) {
-          x[u].raw = *reinterpret_cast<const decltype(x[u].raw)*>(row);
-        } else if (on) {
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) x[u].x[j] = c + j < a.D ? row[j] : from_f32<S>(0.0f);
-        }
-        if constexpr (kAdd) {
-          const uint32_t token = __shfl_sync(0xffffffffu, now.x, u0 + u, stage);
-          if (on && whole && (at & kFlag) && !(token & kFlag) && dev_check(index_ok(token, V), a.err))
-            old[u] = *reinterpret_cast<const Columns<O, kPer>*>(to + token * a.lddw);
-        }
+      for (int u = 0; u < kRowsAhead; ++u) {
+        const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage) & ~kFlag;
+        if (q + u0 + u < length)
+          x[u] = load_pack<S, kPer, true>(a.dY + static_cast<int64_t>(at) * a.lddy, c, a.D, a.dY, end);
       }
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        const uint32_t at = __shfl_sync(0xffffffffu, now.y, u0 + u, stage);
-        const uint32_t token = __shfl_sync(0xffffffffu, now.x, u0 + u, stage);
+      for (int u = 0; u < kRowsAhead; ++u) {
+        const uint2 v = from_lane(now, u0 + u, stage);
         if (q + u0 + u >= length) continue;
         add_to<S, kPer>(sum, x[u]);
-        if (!(at & kFlag)) continue;
-        if (began_before || (token & kFlag)) {
+        if (!(v.y & kFlag)) continue;
+        if (began_before || (v.x & kFlag)) {
           float* s = began_before ? slot : slot + r.slot_ld;
 #pragma unroll
           for (int j = 0; j < kPer; j += 4)
             *reinterpret_cast<float4*>(s + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
-          if (c == 0 && !began_before)
-            r.list[atomicAdd(r.count + 1, 1u)] = static_cast<uint32_t>(range);
-        } else if (dev_check(index_ok(token, V), a.err)) {
-          O* row = to + token * a.lddw;
-          if (!kAny && whole) {
-            Columns<O, kPer> y;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-              const float s = a.scale * sum[j];
-              y.x[j] = from_f32<O>(kAdd ? fmaf(a.beta, to_f32(old[kAdd ? u : 0].x[j]), s) : s);
-            }
-            *reinterpret_cast<Columns<O, kPer>*>(row) = y;
-          } else {
-            float y[kPer];
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-              y[j] = a.beta != 0.0f && c + j < a.D ? to_f32(row[j]) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-              if (c + j < a.D)
-                row[j] = from_f32<O>(a.beta != 0.0f ? fmaf(a.beta, y[j], a.scale * sum[j])
-                                                    : a.scale * sum[j]);
-          }
+          if (c == 0 && !began_before) r.list[atomicAdd(r.count + 1, 1u)] = g.range;
+        } else if (dev_check(index_ok(v.x, V), a.err)) {
+          put_sums<O, kPer>(a.dW + v.x * a.lddw, c, a.D, sum, a.scale, a.beta, false);
         }
         began_before = false;
 #pragma unroll
@@ -727,69 +893,106 @@ __global__ void __launch_bounds__(kThreads, kSumBlocks)
   }
 }
 
-// The sums that lie in several ranges, 128 columns of one by a block at a time:
-// its warps add the ranges' slots in turn, every eighth each, and the warps' sums
-// are added in order. (The list's order, which varies, decides nothing but which
-// block that is.)
+// The sums that lie in several ranges, 128 columns of one an item (a block's items
+// are of different sums). A warp adds an item's slots; those of many are the block's, whose warps add every eighth each,
+// and then the warps' sums in order. (The list's order, which varies, decides
+// nothing but who that is.)
+constexpr uint32_t kManySlots = 48;
+
+// Every `each`-th of slots 0 .. behind from the `from`-th; slot 0 is the first
+// range's second one, slot k the first of the k-th range behind it. (The loads are
+// unconditional, so that they are all in flight before the first is added.)
+__device__ __forceinline__ float4 add_slots(const float* slots, int64_t ld, uint32_t behind,
+                                            uint32_t from, uint32_t each) {
+  constexpr int kEach = 8;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (uint32_t k0 = from; k0 <= behind; k0 += each * kEach) {
+    float4 v[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const uint32_t k = min(k0 + u * each, behind);
+      v[u] = *reinterpret_cast<const float4*>(slots + (2 * static_cast<int64_t>(k) + (k == 0)) * ld);
+    }
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const bool on = k0 + u * each <= behind;
+      s.x += on ? v[u].x : 0.0f;
+      s.y += on ? v[u].y : 0.0f;
+      s.z += on ? v[u].z : 0.0f;
+      s.w += on ? v[u].w : 0.0f;
+    }
+  }
+  return s;
+}
+
 template <typename O>
 __global__ void __launch_bounds__(kThreads)
     embedding_join_kernel(O* dW, int64_t lddw, int64_t D, float scale, float beta, const Ranges r,
                           int64_t V, unsigned* err) {
-  constexpr int kWarps = kThreads / 32, kEach = 4;
+  constexpr int kWarps = kThreads / 32, kTests = 4;
   __shared__ float4 sums[kWarps][32];
+  __shared__ uint32_t many[kWarps];  // ranges behind the warp's item, 0: it is done
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t n = r.count[0], listed = r.count[1];
   const uint32_t length = range_length(n, r.ranges);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t slices = (D + 127) / 128;
-  for (int64_t item = blockIdx.x; item < listed * slices; item += gridDim.x) {
-    const int64_t range = r.list[item / slices];
-    const int64_t c = (item % slices) * 128 + lane * 4;
-    const uint32_t token = r.place[(range + 1) * length].x;
-    // the ranges behind it that begin within the sum
-    int64_t last = range;
-    for (bool more = true; more; last += more ? 32 : 0) {
-      const int64_t i = last + 1 + lane;
-      const uint32_t in = __ballot_sync(0xffffffffu, i * length < n && r.place[i * length].x == token);
-      more = in == 0xffffffffu;
-      if (!more) last += __popc(in);
+  const int64_t slices = (D + 127) / 128, items = listed * slices;
+  const auto put = [&](uint32_t token, int64_t c, const float4& s) {
+    const float all[4] = {s.x, s.y, s.z, s.w};
+    if (c < D && dev_check(index_ok(token, V), err))
+      put_sums<O, 4>(dW + token * lddw, c, D, all, scale, beta, false);
+  };
+  const auto slots_of = [&](uint32_t range, int64_t c) {
+    return r.slots + 2 * static_cast<int64_t>(range) * r.slot_ld + (c < r.slot_ld ? c : 0);
+  };
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kWarps; base < items;
+       base += static_cast<int64_t>(gridDim.x) * kWarps) {
+    uint32_t behind = 0;  // ranges behind the item's that begin within the sum
+    if (base + warp < items) {
+      const int64_t slice = (base + warp) / listed, entry = base + warp - slice * listed;
+      const int64_t c = slice * 128 + lane * 4;
+      const uint32_t range = r.list[entry], token = r.place[(range + 1) * length].x;
+      for (bool more = true; more;) {
+        uint32_t in[kTests];
+#pragma unroll
+        for (int u = 0; u < kTests; ++u) {
+          const int64_t i = static_cast<int64_t>(range + 1 + behind + 32 * u + lane) * length;
+          in[u] = __ballot_sync(0xffffffffu, i < n && r.place[i].x == token);
+        }
+#pragma unroll
+        for (int u = 0; u < kTests; ++u) {
+          if (more) behind += __popc(in[u]);
+          more = more && in[u] == ~0u;
+        }
+      }
+      if (behind < kManySlots)
+        put(token, c, add_slots(slots_of(range, c), r.slot_ld, behind, 0u, 1u));
     }
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    // slot 0 of this loop is the range's own second one, slot k the first of the k-th behind it
-    for (int64_t k0 = warp; k0 <= last - range; k0 += kWarps * kEach) {
-      float4 v[kEach];
+    if (lane == 0) many[warp] = behind < kManySlots ? 0u : behind;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      if (many[w] == 0u) continue;
+      const int64_t slice = (base + w) / listed, entry = base + w - slice * listed;
+      const int64_t c = slice * 128 + lane * 4;
+      const uint32_t range = r.list[entry];
+      sums[warp][lane] = add_slots(slots_of(range, c), r.slot_ld, many[w], warp, kWarps);
+      __syncthreads();
+      if (warp == 0) {
+        float4 s = sums[0][lane];
 #pragma unroll
-      for (int u = 0; u < kEach; ++u) {
-        const int64_t k = k0 + u * kWarps;
-        v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (k <= last - range && c < r.slot_ld)
-          v[u] = *reinterpret_cast<const float4*>(r.slots + (2 * (range + k) + (k == 0)) * r.slot_ld + c);
+        for (int k = 1; k < kWarps; ++k) {
+          const float4 v = sums[k][lane];
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+        put(r.place[(range + 1) * length].x, c, s);
       }
-#pragma unroll
-      for (int u = 0; u < kEach; ++u) {
-        s.x += v[u].x;
-        s.y += v[u].y;
-        s.z += v[u].z;
-        s.w += v[u].w;
-      }
+      __syncthreads();
     }
     __syncthreads();
-    sums[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < D) {
-      float all[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 v = sums[w][lane];
-        all[0] += v.x;
-        all[1] += v.y;
-        all[2] += v.z;
-        all[3] += v.w;
-      }
-      if (dev_check(index_ok(token, V), err))
-        put_sums<O, 4>(dW + token * lddw, c, D, all, scale, beta, false);
-    }
   }
 }
 
@@ -797,22 +1000,21 @@ __global__ void __launch_bounds__(kThreads)
 
 struct GradPlan {
   bool few = false;        // one launch, no workspace
-  int along = 8, slices = 1, ctas = 1;
+  int along = 8, slices = 1, ctas = 0;  // ctas of the sort (0: the places are ranked)
   int bits = 1, passes = 1;
   int64_t ranges = 1, slot_ld = 0, blocks = 1;
   size_t place_off[2] = {}, count_off = 0, list_off = 0, slots_off = 0, total = 0;
 };
 
-void grad_plan(int dtype, int dtype_out, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g) {
-  const int wider = std::max(elem_bytes_of(dtype), elem_bytes_of(dtype_out)), per = 16 / wider;
+void grad_plan(int dtype, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g) {
+  const int per = 16 / elem_bytes_of(dtype);
   const int64_t pieces = (D + per - 1) / per;
-  if (T <= kFewTokens) {
-    g->few = true;
-    g->slices = static_cast<int>((pieces + kThreads - 1) / kThreads);
-    return;
-  }
-  while (g->along < kThreads && g->along < pieces) g->along *= 2;
+  g->few = T <= kFewTokens;
+  // groups of a quarter of a block, where a token may have many places
+  const int widest = g->few && T > kThreads ? kThreads / 4 : kThreads;
+  while (g->along < widest && g->along < pieces) g->along *= 2;
   g->slices = static_cast<int>((pieces + g->along - 1) / g->along);
+  if (g->few) return;
   const int groups = kThreads / g->along;
   // as many ranges as are resident at once, of 8 places at least
   const int64_t most = (T + kLeastRange - 1) / kLeastRange;
@@ -823,9 +1025,9 @@ void grad_plan(int dtype, int dtype_out, int64_t T, int64_t V, int64_t D, int sm
   g->slot_ld = pieces * per;
   int width = 1;
   while (width < 31 && (V - 1) >> width) ++width;
-  g->passes = (width + kDigitBits - 1) / kDigitBits;
+  g->ctas = T <= kRanked ? 0 : T <= kEightCtas ? 8 : 16;
+  g->passes = g->ctas ? (width + kDigitBits - 1) / kDigitBits : 1;
   g->bits = (width + g->passes - 1) / g->passes;
-  g->ctas = T <= kOneCta ? 1 : T <= kEightCtas ? 8 : 16;
   size_t at = streamk_flag_bytes(sms);
   const auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -854,7 +1056,7 @@ cudaError_t sort_config(cudaStream_t stream, cudaLaunchConfig_t* cfg, cudaLaunch
   attr[1].val.clusterDim.z = 1;
   cfg->gridDim = dim3(kCtas);
   cfg->blockDim = dim3(kSortThreads);
-  cfg->dynamicSmemBytes = sort_smem_bytes<kCtas>();
+  cfg->dynamicSmemBytes = kSortSmem;
   cfg->stream = stream;
   cfg->attrs = attr;
   cfg->numAttrs = 2;
@@ -887,6 +1089,17 @@ cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
   return launch_sort<(kCtas > 8 ? 8 : kCtas)>(s, stream);
 }
 
+template <typename S, typename O, bool kAdd>
+cudaError_t launch_sum(const GradArgs<S, O>& a, const Ranges& r, int64_t V, dim3 blocks,
+                       cudaStream_t stream) {
+  static DeviceOnce configured;
+  constexpr int kSmem = SumShape<S, O, kAdd>::kSmem;
+  const cudaError_t e = set_smem_once(configured, embedding_sum_kernel<S, O, kAdd>, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(embedding_sum_kernel<S, O, kAdd>, blocks, dim3(kThreads), kSmem, stream, a,
+                       r, V);
+}
+
 template <typename S, typename O>
 int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, int64_t lddw,
             float scale, float beta, const GradPlan& g, char* ws, const CallContext& ctx,
@@ -894,7 +1107,7 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   const int sms = ctx.sm_count;
   const GradArgs<S, O> a{static_cast<const S*>(dY), lddy,  static_cast<O*>(dW), lddw, D, scale, beta,
                          rows_on(dW, lddw, sizeof(O), 16), ctx.err};
-  const bool any = !rows_on(dY, lddy, sizeof(S), sum_values<S, O>() * sizeof(S));
+  const bool any = !rows_on(dY, lddy, sizeof(S), 16);
   // the rows without tokens: about 32 KB a block at least, two blocks an SM at most
   // (each looks at all tokens)
   const int64_t row_bytes = D * static_cast<int64_t>(sizeof(O));
@@ -909,7 +1122,7 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
     const auto kernel =
         any ? embedding_grad_few_kernel<S, O, true> : embedding_grad_few_kernel<S, O, false>;
     return finish_launch(launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
-                                       0, stream, a, k, g.slices, share),
+                                       0, stream, a, k, g.along, g.slices, share),
                          "embedding gradient launch", stream);
   }
   SortArgs s{};
@@ -919,10 +1132,12 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   s.bits = g.bits;
   s.passes = g.passes;
   s.err = ctx.err;
-  int st = finish_launch(g.ctas == 1   ? launch_sort<1>(s, stream)
-                         : g.ctas == 8 ? launch_sort<8>(s, stream)
-                                       : launch_sort<16>(s, stream),
-                         "embedding sort launch", stream);
+  const cudaError_t e =
+      g.ctas == 0 ? launch_kernel(embedding_rank_kernel, dim3(static_cast<unsigned>((k.T + 31) / 32)),
+                                  dim3(kRankThreads), 0, stream, k, s.list[0], s.count)
+      : g.ctas == 8 ? launch_sort<8>(s, stream)
+                    : launch_sort<16>(s, stream);
+  int st = finish_launch(e, "embedding sort launch", stream);
   if (st != GEMM14_OK) return st;
   if (rest) {
     st = finish_launch(
@@ -933,13 +1148,15 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   }
   const int last = (g.passes - 1) & 1;
   const Ranges r{s.list[last], s.count, reinterpret_cast<uint32_t*>(ws + g.list_off),
-                 reinterpret_cast<float*>(ws + g.slots_off), g.slot_ld, g.ranges, g.along, g.slices};
-  const auto sum = any || !a.words ? embedding_sum_kernel<S, O, kAnywhere>
-                   : beta == 0.0f  ? embedding_sum_kernel<S, O, kWordsSet>
-                                   : embedding_sum_kernel<S, O, kWordsAdd>;
-  st = finish_launch(launch_kernel(sum, dim3(static_cast<unsigned>(g.blocks)), dim3(kThreads), 0,
-                                   stream, a, r, k.T, k.V),
-                     "embedding gradient launch", stream);
+                 reinterpret_cast<float*>(ws + g.slots_off), g.slot_ld,
+                 static_cast<uint32_t>(g.ranges), g.along, g.slices};
+  const dim3 blocks(static_cast<unsigned>(g.blocks));
+  const cudaError_t summed =
+      any || !a.words ? launch_kernel(embedding_sum_any_kernel<S, O>, blocks, dim3(kThreads), 0,
+                                      stream, a, r, k.T, k.V)
+      : beta == 0.0f  ? launch_sum<S, O, false>(a, r, k.V, blocks, stream)
+                      : launch_sum<S, O, true>(a, r, k.V, blocks, stream);
+  st = finish_launch(summed, "embedding gradient launch", stream);
   if (st != GEMM14_OK) return st;
   if (g.ranges == 1) return GEMM14_OK;
   const int64_t items = g.ranges * ((D + 127) / 128), most = static_cast<int64_t>(sms) * 4;
@@ -1010,14 +1227,14 @@ int gemm14_embedding_forward(int dtype, int dtype_out, int64_t T, int64_t V, int
   return finish_launch(e, "embedding launch", stream);
 }
 
-size_t gemm14_embedding_backward_workspace_bytes(int dtype, int dtype_out, int64_t T, int64_t V,
-                                                 int64_t D, int sm_count) {
+size_t gemm14_embedding_backward_workspace_bytes(int dtype, int64_t T, int64_t V, int64_t D,
+                                                 int sm_count) {
   if (sm_count <= 0 && current_sm_count(&sm_count) != GEMM14_OK) return 0;
-  if (!element_type(dtype) || !element_type(dtype_out) || T < 0 || T > kTrainMaxSize || V < 1 || V > kTrainMaxSize || D < 1 ||
+  if (!element_type(dtype) || T < 0 || T > kTrainMaxSize || V < 1 || V > kTrainMaxSize || D < 1 ||
       D > kTrainMaxSize)
     return 0;
   GradPlan g;
-  grad_plan(dtype, dtype_out, T, V, D, sm_count, &g);
+  grad_plan(dtype, T, V, D, sm_count, &g);
   return g.total;
 }
 
@@ -1033,7 +1250,7 @@ int gemm14_embedding_backward(int dtype, int dtype_out, int64_t T, int64_t V, in
   CallContext ctx;
   if ((st = call_device(&ctx)) != GEMM14_OK) return st;
   GradPlan g;
-  grad_plan(dtype, dtype_out, T, V, D, ctx.sm_count, &g);
+  grad_plan(dtype, T, V, D, ctx.sm_count, &g);
   if (g.total && (!workspace || workspace_bytes < g.total)) {
     note_error("gemm14_embedding_backward: %zu bytes of workspace given, %zu needed",
                workspace_bytes, g.total);

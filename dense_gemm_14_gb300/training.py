@@ -378,7 +378,7 @@ def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None 
                                                       _ptr(tokens), size, int(ignore_index),
                                                       float(scale), float(beta), dw.data_ptr(),
                                                       lddw, ws, n, handle, check=False),
-            lambda: _lib.embedding_backward_workspace_bytes(code, _CODE[dtype], T, V, D),
+            lambda: _lib.embedding_backward_workspace_bytes(code, T, V, D),
             "gemm14_embedding_backward")
         return dw
 

@@ -504,8 +504,8 @@ int gemm14_embedding_backward(int dtype, int dtype_out, int64_t T, int64_t V, in
 
 /* Its workspace bytes (0: none needed, or invalid arguments); no CUDA call is made
  * when sm_count > 0. */
-size_t gemm14_embedding_backward_workspace_bytes(int dtype, int dtype_out, int64_t T, int64_t V,
-                                                 int64_t D, int sm_count);
+size_t gemm14_embedding_backward_workspace_bytes(int dtype, int64_t T, int64_t V, int64_t D,
+                                                 int sm_count);
 
 /* A gradient in a list of them: rows x cols elements of dtype F32, BF16 or F16 on
  * the device, rows of pitch ld (not looked at where rows <= 1). rows or cols of 0:

@@ -186,7 +186,8 @@ def gradient_case(T, V, D, dtype, out, kind, seed=0):
 @pytest.mark.parametrize("dtype,out", PAIRS)
 @pytest.mark.parametrize("T,V,D", [(1, 1, 1), (2, 3, 8), (31, 5, 33), (255, 1000, 64), (256, 77, 769),
                                    (257, 77, 769), (2048, 300, 16), (2049, 4000, 40), (5000, 513, 200),
-                                   (700, 900, 2056), (20000, 700, 24)])
+                                   (700, 900, 2056), (1024, 60, 1032), (1025, 60, 1032), (8192, 900, 72), (8193, 900, 72),
+                                   (20000, 700, 24), (3000, 37, 264)])
 def test_gradient(T, V, D, dtype, out, kind):
     dy, tokens, dw0 = gradient_case(T, V, D, dtype, out, kind)
     dy_, t_ = dy.cuda(), tokens.cuda()
@@ -203,7 +204,7 @@ def test_gradient(T, V, D, dtype, out, kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,out", PAIRS)
-@pytest.mark.parametrize("T", [40, 900])
+@pytest.mark.parametrize("T", [40, 900, 2500])
 @pytest.mark.parametrize("D,pad,offset,opad,ooffset", [(64, 1, 0, 0, 0), (64, 0, 1, 0, 0), (64, 0, 0, 1, 0),
                                                        (64, 0, 0, 0, 1), (130, 3, 5, 2, 7), (7, 1, 1, 1, 1),
                                                        (1001, 0, 0, 0, 0), (1000, 8, 8, 8, 8)])
@@ -244,7 +245,7 @@ def test_many_tokens_and_large_vocabularies(T, V, D, kind):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [0, 1, 200, 3000])
+@pytest.mark.parametrize("T", [0, 1, 200, 3000, 10000])
 @pytest.mark.parametrize("beta", [0.0, 1.0, 0.5])
 def test_no_token_takes_part(T, beta):
     dw0 = torch.randn(90, 40, device="cuda")
@@ -257,7 +258,7 @@ def test_no_token_takes_part(T, beta):
 
 @pytest.mark.gpu
 def test_infinities_and_nan_stay_in_their_rows():
-    for T in (100, 1000):
+    for T in (100, 1000, 4000):
         dy = torch.randn(T, 48, device="cuda")
         tokens = torch.arange(T, device="cuda") % 20
         dy[3, 5], dy[4, 6], dy[24, 6], dy[7, 7] = math.inf, math.inf, -math.inf, math.nan
@@ -284,7 +285,7 @@ def test_shapes_of_a_batch():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [64, 1500])
+@pytest.mark.parametrize("T", [64, 900, 1500])
 def test_gradient_against_differences(T):
     """L = sum(r * embedding(W, tokens)) is linear in W: its derivative along a direction
     is the difference of two values, formed here from looked-up rows in 64 bits."""
@@ -323,7 +324,7 @@ def test_offsets_beyond_32_bits():
 # ---- streams, captures, threads
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [100, 4000])
+@pytest.mark.parametrize("T", [100, 4000, 20000])
 def test_on_another_stream_and_repeated(T):
     dy, tokens, _ = gradient_case(T, 500, 264, "bf16", "bf16", "text")
     dy, tokens = dy.cuda(), tokens.cuda()
@@ -349,7 +350,7 @@ def test_back_to_back_calls_share_the_workspace():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [120, 3000])
+@pytest.mark.parametrize("T", [120, 3000, 10000])
 @pytest.mark.parametrize("beta", [0.0, 1.0])
 def test_captured_and_replayed_on_other_tokens(T, beta):
     V, D = 300, 136
@@ -406,20 +407,21 @@ def test_gradient_refusals(bad):
 
 def test_workspace_sizes():
     need = g14.embedding_backward_workspace_bytes
-    assert need(1, 1, 256, 1000, 64, 152) == 0 and need(1, 0, 257, 1000, 64, 152) > 257 * 16
-    assert need(9, 0, 1000, 10, 64, 152) == 0 and need(1, 1, 1000, 0, 64, 152) == 0 and need(1, 1, -1, 10, 64, 152) == 0
-    big = need(1, 1, 1 << 20, 1 << 20, 4096, 152)
+    assert need(1, 100, 1000, 64, 152) == 0 and need(1, 5000, 1000, 64, 152) > 5000 * 16
+    assert need(9, 5000, 10, 64, 152) == 0 and need(1, 5000, 0, 64, 152) == 0 and need(1, -1, 10, 64, 152) == 0
+    big = need(1, 1 << 20, 1 << 20, 4096, 152)
     assert (1 << 24) < big < (1 << 24) + (32 << 20)  # sixteen bytes a place, and slots that do not grow
 
 
 @pytest.mark.gpu
 def test_small_workspace_is_refused():
-    dy, t = torch.randn(1000, 64, device="cuda"), torch.zeros(1000, dtype=torch.int64, device="cuda")
+    T = 5000
+    dy, t = torch.randn(T, 64, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
     dw = torch.zeros(8, 64, device="cuda")
-    need = g14.embedding_backward_workspace_bytes(0, 0, 1000, 8, 64)
+    need = g14.embedding_backward_workspace_bytes(0, T, 8, 64)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     for ptr, n in ((ws.data_ptr(), need - 1), (None, 0)):
-        assert g14.embedding_backward_raw(0, 0, 1000, 8, 64, dy.data_ptr(), 64, t.data_ptr(), 8, -100, 1.0, 0.0,
+        assert g14.embedding_backward_raw(0, 0, T, 8, 64, dy.data_ptr(), 64, t.data_ptr(), 8, -100, 1.0, 0.0,
                                           dw.data_ptr(), 64, ptr, n, check=False) == g14.GEMM14_ERR_INVALID_ARG
         assert str(need) in g14.last_error_string()
 
