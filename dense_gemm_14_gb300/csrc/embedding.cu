@@ -208,7 +208,8 @@ __device__ __forceinline__ void write_rest(const Rest<O>& r, const Tokens& k, in
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (takes_part(k, token[u]) && token[u] >= begin && token[u] < begin + rows)
+        if (static_cast<uint64_t>(token[u] - begin) < static_cast<uint64_t>(rows) &&
+            token[u] != k.ignore)
           atomicOr(&marks[(token[u] - begin) >> 5], 1u << ((token[u] - begin) & 31));
     }
     __syncthreads();
@@ -724,18 +725,21 @@ constexpr int kSumBlocks = 4;  // resident of an SM
 // that ends come with the row that ends it. (With the words in registers, 4 or 8
 // rows loaded and then added, 65536 places of 2048 columns, bf16 added to fp32,
 // took 165 us for 597 MB; @SUMADD@ so.)
-template <typename S, typename O, bool kAdd>
+// kPieces: 16 bytes of dY's columns that a thread has; two where a row has enough
+// for a warp, as a row costs a thread some forty instructions whatever it moves.
+template <typename S, typename O, bool kAdd, int kPieces>
 struct SumShape {
-  static constexpr int kWords = static_cast<int>(sizeof(O) / sizeof(S));  // of a thread
-  static constexpr int kCols = sum_values<S>() / kWords;  // of a word: 16 bytes of dW's
+  static constexpr int kWords = kPieces * static_cast<int>(sizeof(O) / sizeof(S));
+  static constexpr int kCols = 16 / static_cast<int>(sizeof(O));  // of a word: 16 bytes of dW's
   static constexpr int kRowBytes = kCols * static_cast<int>(sizeof(S));
-  static constexpr int kDepth = !kAdd ? 8 : kWords == 1 ? 6 : 4;
-  static constexpr int kSmem = kDepth * kThreads * kWords * (kRowBytes + (kAdd ? 16 : 0));
+  static constexpr int kBytes = kThreads * kWords * (kRowBytes + (kAdd ? 16 : 0));  // of a row
+  static constexpr int kDepth = 49152 / kBytes < 8 ? 49152 / kBytes : 8;
+  static constexpr int kSmem = kDepth * kBytes;
 };
-template <typename S, typename O, bool kAdd>
+template <typename S, typename O, bool kAdd, int kPieces>
 __global__ void __launch_bounds__(kThreads, kSumBlocks)
     embedding_sum_kernel(const GradArgs<S, O> a, const Ranges r, int64_t V) {
-  using Q = SumShape<S, O, kAdd>;
+  using Q = SumShape<S, O, kAdd, kPieces>;
   constexpr int kWords = Q::kWords, kCols = Q::kCols, kDepth = Q::kDepth;
   extern __shared__ __align__(16) unsigned char sum_smem[];
   grid_dependency_wait();
@@ -1000,20 +1004,23 @@ __global__ void __launch_bounds__(kThreads)
 
 struct GradPlan {
   bool few = false;        // one launch, no workspace
+  int pieces = 1;          // 16 bytes of a row of dY that a thread has
   int along = 8, slices = 1, ctas = 0;  // ctas of the sort (0: the places are ranked)
   int bits = 1, passes = 1;
   int64_t ranges = 1, slot_ld = 0, blocks = 1;
   size_t place_off[2] = {}, count_off = 0, list_off = 0, slots_off = 0, total = 0;
 };
 
-void grad_plan(int dtype, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g) {
-  const int per = 16 / elem_bytes_of(dtype);
-  const int64_t pieces = (D + per - 1) / per;
+// pieces: as many as the rows allow (see SumShape).
+void grad_plan(int dtype, int pieces, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g) {
+  const int per = 16 / elem_bytes_of(dtype) * pieces;
+  const int64_t items = (D + per - 1) / per;  // threads of a row
+  g->pieces = pieces;
   g->few = T <= kFewTokens;
   // groups of a quarter of a block, where a token may have many places
   const int widest = g->few && T > kThreads ? kThreads / 4 : kThreads;
-  while (g->along < widest && g->along < pieces) g->along *= 2;
-  g->slices = static_cast<int>((pieces + g->along - 1) / g->along);
+  while (g->along < widest && g->along < items) g->along *= 2;
+  g->slices = static_cast<int>((items + g->along - 1) / g->along);
   if (g->few) return;
   const int groups = kThreads / g->along;
   // as many ranges as are resident at once, of 8 places at least
@@ -1022,7 +1029,7 @@ void grad_plan(int dtype, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g)
   if (g->ranges < 1) g->ranges = 1;
   if (g->ranges > most) g->ranges = most;
   g->blocks = (g->ranges + groups - 1) / groups * g->slices;
-  g->slot_ld = pieces * per;
+  g->slot_ld = (D + 7) / 8 * 8;
   int width = 1;
   while (width < 31 && (V - 1) >> width) ++width;
   g->ctas = T <= kRanked ? 0 : T <= kEightCtas ? 8 : 16;
@@ -1039,6 +1046,11 @@ void grad_plan(int dtype, int64_t T, int64_t V, int64_t D, int sms, GradPlan* g)
   for (int i = 0; i < 2; ++i) g->place_off[i] = take(static_cast<size_t>(T) * sizeof(uint2));
   g->slots_off = take(static_cast<size_t>(g->ranges) * 2 * g->slot_ld * 4);
   g->total = at;
+}
+// Two pieces a thread where rows of one type start on 16 bytes and fill a warp so.
+int pieces_for(int dtype, int dtype_out, int64_t T, int64_t D, bool words) {
+  const int per = 16 / elem_bytes_of(dtype);
+  return words && T > kFewTokens && dtype == dtype_out && D >= 64 * per ? 2 : 1;
 }
 
 // Clusters of 16 are not portable: whether this device runs one, else 8 do.
@@ -1089,15 +1101,15 @@ cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
   return launch_sort<(kCtas > 8 ? 8 : kCtas)>(s, stream);
 }
 
-template <typename S, typename O, bool kAdd>
+template <typename S, typename O, bool kAdd, int kPieces>
 cudaError_t launch_sum(const GradArgs<S, O>& a, const Ranges& r, int64_t V, dim3 blocks,
                        cudaStream_t stream) {
   static DeviceOnce configured;
-  constexpr int kSmem = SumShape<S, O, kAdd>::kSmem;
-  const cudaError_t e = set_smem_once(configured, embedding_sum_kernel<S, O, kAdd>, kSmem);
+  constexpr int kSmem = SumShape<S, O, kAdd, kPieces>::kSmem;
+  const cudaError_t e = set_smem_once(configured, embedding_sum_kernel<S, O, kAdd, kPieces>, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(embedding_sum_kernel<S, O, kAdd>, blocks, dim3(kThreads), kSmem, stream, a,
-                       r, V);
+  return launch_kernel(embedding_sum_kernel<S, O, kAdd, kPieces>, blocks, dim3(kThreads), kSmem,
+                       stream, a, r, V);
 }
 
 template <typename S, typename O>
@@ -1107,20 +1119,20 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   const int sms = ctx.sm_count;
   const GradArgs<S, O> a{static_cast<const S*>(dY), lddy,  static_cast<O*>(dW), lddw, D, scale, beta,
                          rows_on(dW, lddw, sizeof(O), 16), ctx.err};
-  const bool any = !rows_on(dY, lddy, sizeof(S), 16);
-  // the rows without tokens: about 32 KB a block at least, two blocks an SM at most
-  // (each looks at all tokens)
+  const bool any_dy = !rows_on(dY, lddy, sizeof(S), 16), any = any_dy || !a.words;
+  // the rows without tokens: blocks of four times the bytes of the tokens, which
+  // each looks at, and 32 KB at least; two blocks an SM at most where that is more
   const int64_t row_bytes = D * static_cast<int64_t>(sizeof(O));
-  int64_t share = (32768 + row_bytes - 1) / row_bytes;
   const int64_t even = (k.V + static_cast<int64_t>(sms) * 2 - 1) / (static_cast<int64_t>(sms) * 2);
-  if (share < even) share = even;
+  const int64_t share =
+      std::max<int64_t>(1, std::min(even, std::max<int64_t>(32768, 32 * k.T) / row_bytes + 1));
   const int64_t rest = beta == 1.0f ? 0 : (k.V + share - 1) / share;
   if (g.few) {
     const int64_t blocks = k.T * g.slices + rest;
     if (blocks == 0) return GEMM14_OK;
     if (blocks > INT32_MAX) return GEMM14_ERR_INVALID_ARG;
     const auto kernel =
-        any ? embedding_grad_few_kernel<S, O, true> : embedding_grad_few_kernel<S, O, false>;
+        any_dy ? embedding_grad_few_kernel<S, O, true> : embedding_grad_few_kernel<S, O, false>;
     return finish_launch(launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
                                        0, stream, a, k, g.along, g.slices, share),
                          "embedding gradient launch", stream);
@@ -1151,11 +1163,14 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
                  reinterpret_cast<float*>(ws + g.slots_off), g.slot_ld,
                  static_cast<uint32_t>(g.ranges), g.along, g.slices};
   const dim3 blocks(static_cast<unsigned>(g.blocks));
+  constexpr int kTwo = sizeof(O) == sizeof(S) ? 2 : 1;  // (of mixed types one is two words)
   const cudaError_t summed =
-      any || !a.words ? launch_kernel(embedding_sum_any_kernel<S, O>, blocks, dim3(kThreads), 0,
-                                      stream, a, r, k.T, k.V)
-      : beta == 0.0f  ? launch_sum<S, O, false>(a, r, k.V, blocks, stream)
-                      : launch_sum<S, O, true>(a, r, k.V, blocks, stream);
+      any            ? launch_kernel(embedding_sum_any_kernel<S, O>, blocks, dim3(kThreads), 0, stream,
+                                     a, r, k.T, k.V)
+      : g.pieces > 1 ? beta == 0.0f ? launch_sum<S, O, false, kTwo>(a, r, k.V, blocks, stream)
+                                    : launch_sum<S, O, true, kTwo>(a, r, k.V, blocks, stream)
+      : beta == 0.0f ? launch_sum<S, O, false, 1>(a, r, k.V, blocks, stream)
+                     : launch_sum<S, O, true, 1>(a, r, k.V, blocks, stream);
   st = finish_launch(summed, "embedding gradient launch", stream);
   if (st != GEMM14_OK) return st;
   if (g.ranges == 1) return GEMM14_OK;
@@ -1233,9 +1248,14 @@ size_t gemm14_embedding_backward_workspace_bytes(int dtype, int64_t T, int64_t V
   if (!element_type(dtype) || T < 0 || T > kTrainMaxSize || V < 1 || V > kTrainMaxSize || D < 1 ||
       D > kTrainMaxSize)
     return 0;
-  GradPlan g;
-  grad_plan(dtype, T, V, D, sm_count, &g);
-  return g.total;
+  // rows may start anywhere or not, and the gradient be of either type
+  size_t most = 0;
+  for (int pieces = 1; pieces <= 2; ++pieces) {
+    GradPlan g;
+    grad_plan(dtype, pieces, T, V, D, sm_count, &g);
+    most = std::max(most, g.total);
+  }
+  return most;
 }
 
 int gemm14_embedding_backward(int dtype, int dtype_out, int64_t T, int64_t V, int64_t D,
@@ -1249,8 +1269,10 @@ int gemm14_embedding_backward(int dtype, int dtype_out, int64_t T, int64_t V, in
   if (workspace && !aligned(workspace, 16)) return GEMM14_ERR_INVALID_ARG;
   CallContext ctx;
   if ((st = call_device(&ctx)) != GEMM14_OK) return st;
+  const bool words = rows_on(dY, lddy, elem_bytes_of(dtype), 16) &&
+                     rows_on(dW, lddw, elem_bytes_of(dtype_out), 16);
   GradPlan g;
-  grad_plan(dtype, T, V, D, ctx.sm_count, &g);
+  grad_plan(dtype, pieces_for(dtype, dtype_out, T, D, words), T, V, D, ctx.sm_count, &g);
   if (g.total && (!workspace || workspace_bytes < g.total)) {
     note_error("gemm14_embedding_backward: %zu bytes of workspace given, %zu needed",
                workspace_bytes, g.total);
