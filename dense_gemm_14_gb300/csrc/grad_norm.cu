@@ -33,14 +33,38 @@ struct Entry {
   uint32_t first_unit;
   uint16_t type, dst_type;  // gemm14 dtypes
 };
-// Passed by value: the kernels' parameters hold up to 32764 bytes.
+// Passed by value: the kernels' parameters hold up to 32764 bytes. start, of the
+// longest: the tensor of each block's first unit (a search for it would wait for
+// one miss of the constant cache after another).
+constexpr int kMostBlocks = 640;
+constexpr int kMostEntries = 544;  // of a launch
 template <int kN>
 struct Table {
+  static constexpr bool kStarts = kN == kMostEntries;
   int n;
   uint32_t units;
+  uint16_t start[kStarts ? kMostBlocks : 1];
   Entry e[kN];
 };
-constexpr int kMostEntries = 576;  // of a launch
+// The tensor of unit u, of the block or one behind its first.
+template <int kN>
+__device__ __forceinline__ int tensor_of(const Table<kN>& t, uint32_t u) {
+  if constexpr (Table<kN>::kStarts) {
+    int i = t.start[blockIdx.x];
+    while (i + 1 < t.n && t.e[i + 1].first_unit <= u) ++i;
+    return i;
+  } else {
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.e[mid].first_unit <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+}
 
 constexpr int kUnitBytes = 4096;
 constexpr int kThreads = 256;
@@ -206,12 +230,7 @@ template <int kN>
 __device__ __forceinline__ void sum_units(const Table<kN>& t, uint32_t w, uint32_t warps, int lane,
                                           double* slots) {
   const uint32_t u0 = unit_at(t.units, w, warps), u1 = unit_at(t.units, w + 1, warps);
-  int lo = 0, hi = t.n - 1;  // the tensor of u0
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].first_unit <= u0) lo = mid; else hi = mid - 1;
-  }
-  int i = lo;
+  int i = tensor_of(t, u0);
   if (lane == 0 && w > 0 && i > 0 && t.e[i].first_unit == u0) slots[w + i - 1] = 0.0;
   for (uint32_t u = u0; u < u1;) {
     const Entry& e = t.e[i];
@@ -245,77 +264,145 @@ struct Finish {
   float* factor;       // for the scaling, or NULL
 };
 
-// The sum of v over the block's threads, to all of them; in an order of its own.
-__device__ __forceinline__ double block_sum(double v, double* smem) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  v = warp_sum(v);
-  __syncthreads();
-  if (lane == 0) smem[warp] = v;
-  __syncthreads();
-  return warp_sum(lane < warps ? smem[lane] : 0.0);
+// The root of s >= 0 (or NaN, infinite): sqrtf of s brought to [1, 4) by a power of
+// 4, and one step of Newton's iteration r + (s - r^2) / (2 r), whose correction
+// needs no more than fp32: right to some 2^-45, for a handful of fp64 operations in
+// place of sqrt's (an SM does two a cycle, so one of a warp's takes 16).
+__device__ __forceinline__ double root(double s) {
+  if (!(s > 0.0) || s - s != 0.0) return s;
+  const int k = ((__double2hiint(s) >> 20) - 1023) & ~1;  // (sums of squares are normal numbers)
+  const double m = __hiloint2double(__double2hiint(s) - k * (1 << 20), __double2loint(s));
+  const float r = sqrtf(static_cast<float>(m));
+  const double rd = static_cast<double>(r);
+  const float off = static_cast<float>(fma(-rd, rd, m));
+  const double y = rd + static_cast<double>(off * (0.5f / r));
+  return __hiloint2double(__double2hiint(y) + k / 2 * (1 << 20), __double2loint(y));
 }
+
 // Slots [a, b), every `step`-th from the `from`-th.
 __device__ __forceinline__ double slot_sum(const double* slots, uint32_t a, uint32_t b,
                                            uint32_t from, uint32_t step) {
   double s = 0.0;
-  for (uint32_t i0 = a + from; i0 < b; i0 += 8 * step) {
-    double v[8];
+  for (uint32_t i0 = a + from; i0 < b; i0 += 4 * step) {
+    double v[4];
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) v[k] = i0 + k * step < b ? __ldcg(slots + i0 + k * step) : 0.0;
-    s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    for (uint32_t k = 0; k < 4; ++k) v[k] = __ldcg(slots + min(i0 + k * step, b - 1));
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+      if (i0 + k * step < b) s += v[k];
   }
   return s;
 }
-
-// The norm and the factor, by one block.
-__device__ __forceinline__ void finish_total(const Finish& f, uint32_t slots, double* smem) {
-  const double total = block_sum(slot_sum(f.slots, 0u, slots, threadIdx.x, blockDim.x), smem);
-  if (threadIdx.x != 0) return;
-  double all = total;
-  for (int l = 0; l < f.launch; ++l) all += f.totals[l];
-  f.totals[f.launch] = total;
-  if (!f.last) return;
-  const double norm = sqrt(all) * fabs(static_cast<double>(f.scale));
-  *f.norm = static_cast<float>(norm);
-  if (f.factor) {
-    const bool over = norm > static_cast<double>(f.max_norm) && norm - norm == 0.0;
-    *f.factor = over ? static_cast<float>(f.scale * (f.max_norm / norm)) : f.scale;
+// The sum over the threads of the block's first kFinishThreads, to its warp 0; in
+// an order of its own. Every thread of the block calls it.
+constexpr int kFinishThreads = 256, kFinishCtas = 8;
+__device__ __forceinline__ double block_sum(double v, double* smem) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kFinishThreads / 32;
+  __syncthreads();
+  if (warp < kWarps) {
+    v = warp_sum(v);
+    if (lane == 0) smem[warp] = v;
   }
+  __syncthreads();
+  double s = 0.0;
+  if (warp == 0) {
+    s = lane < kWarps ? smem[lane] : 0.0;
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  }
+  return s;
 }
-// The norms of the tensors block, block + blocks, ..: a warp each, the block for
-// one of many slots. (All of them by one block took 35 us for 109 tensors: an SM
-// does two fp64 operations a cycle, and a root is some thirty of a warp's.)
+__device__ __forceinline__ double load_cluster_f64(uint32_t addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The norm and the factor, by the first kFinishThreads threads of each CTA of a
+// cluster of kFinishCtas, smem: 9 doubles of each.
+__device__ __forceinline__ void finish_total(const Finish& f, uint32_t slots, double* smem) {
+  const uint32_t rank = cluster_ctarank();
+  double mine = 0.0;
+  if (threadIdx.x < kFinishThreads)
+    mine = slot_sum(f.slots, 0u, slots, rank * kFinishThreads + threadIdx.x,
+                    kFinishCtas * kFinishThreads);
+  mine = block_sum(mine, smem);
+  if (threadIdx.x == 0) smem[kFinishThreads / 32] = mine;
+  cluster_sync();
+  if (rank == 0 && threadIdx.x < 32) {
+    double total = 0.0;
+    if (threadIdx.x < kFinishCtas)
+      total = load_cluster_f64(mapa_shared(smem_u32(smem + kFinishThreads / 32), threadIdx.x));
+#pragma unroll
+    for (int o = kFinishCtas / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (threadIdx.x == 0) {
+      double all = total;
+      for (int l = 0; l < f.launch; ++l) all += f.totals[l];
+      f.totals[f.launch] = total;
+      if (f.last) {
+        const double norm = root(all) * fabs(static_cast<double>(f.scale));
+        *f.norm = static_cast<float>(norm);
+        if (f.factor) {
+          const bool over = norm > static_cast<double>(f.max_norm) && norm - norm == 0.0;
+          *f.factor = over ? static_cast<float>(f.scale * (f.max_norm / norm)) : f.scale;
+        }
+      }
+    }
+  }
+  cluster_sync();  // no CTA ends while its sum is read; the factor is written
+}
+// The norms of the tensors block, block + blocks, ..: a warp each, the block's first
+// threads for one of many slots. (All of them by one block took 35 us for 109
+// tensors.)
 template <int kN>
 __device__ __forceinline__ void finish_each(const Parts<kN>& t, const Finish& f, int block,
                                             int blocks, double* smem) {
   constexpr uint32_t kLong = 1024;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const auto put = [&](int i, double s) {
+    f.each[i] = static_cast<float>(root(s) * fabs(static_cast<double>(f.scale)));
+  };
   for (int i = block + warp * blocks; i < t.n; i += warps * blocks) {
     if (t.first[i + 1] - t.first[i] > kLong) continue;
     const double s = warp_sum(slot_sum(f.slots, t.first[i], t.first[i + 1], lane, 32u));
-    if (lane == 0) f.each[i] = static_cast<float>(sqrt(s) * fabs(static_cast<double>(f.scale)));
+    if (lane == 0) put(i, s);
   }
   for (int i = block; i < t.n; i += blocks) {
     if (t.first[i + 1] - t.first[i] <= kLong) continue;
-    const double s =
-        block_sum(slot_sum(f.slots, t.first[i], t.first[i + 1], threadIdx.x, blockDim.x), smem);
-    if (threadIdx.x == 0)
-      f.each[i] = static_cast<float>(sqrt(s) * fabs(static_cast<double>(f.scale)));
+    double s = 0.0;
+    if (threadIdx.x < kFinishThreads)
+      s = slot_sum(f.slots, t.first[i], t.first[i + 1], threadIdx.x, kFinishThreads);
+    s = block_sum(s, smem);
+    if (threadIdx.x == 0) put(i, s);
   }
 }
-// Blocks that share finish_each.
-constexpr int kEachBlocks = 64;
 
 // ---- scaling
 
-// A lane's pieces of a unit: kPer values each, one 16-byte word of the output (so
-// a warp's stores lie side by side); the source's word, where it does not start
-// on its own size, is read as two and a shift. kEach of them are in flight.
+// A lane's pieces of a unit: kPer values each, 16 bytes of the source and 16 or 32
+// aligned ones of the output, stored at once; the source's word, where it does not
+// start on 16 bytes, is read as two and a shift. kEach of them are in flight.
+// (16 bytes of fp32 output a piece, 8 of a 16-bit source, took 207 us for 109 packed
+// fp16 tensors of 197 million values, @SCALE@ so.)
 // Products are rounded to fp32 and then to a 16-bit type: within half a step and
 // 2^-24 of the value.
+template <typename O, int kPer>
+union Output {
+  O x[kPer];
+  uint32_t w[kPer * sizeof(O) / 4];
+};
+__device__ __forceinline__ void store_output(void* to, const uint32_t (&w)[4]) {
+  *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_output(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 template <typename S, typename O, int kPer>
-__device__ __forceinline__ Pack<O, kPer> scaled(const Pack<S, kPer>& p, float f) {
-  Pack<O, kPer> y;
+__device__ __forceinline__ Output<O, kPer> scaled(const Pack<S, kPer>& p, float f) {
+  Output<O, kPer> y;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) y.x[j] = from_f32<O>(f * to_f32(p.x[j]));
   return y;
@@ -323,48 +410,41 @@ __device__ __forceinline__ Pack<O, kPer> scaled(const Pack<S, kPer>& p, float f)
 
 template <typename S, typename O, bool kAny>
 __device__ __forceinline__ void scale_whole(const S* src, O* dst, int lane, float f) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(O));
-  constexpr int kPieces = kUnitBytes / static_cast<int>(sizeof(S)) / kPer / 32;  // a lane's
-  using W = decltype(Pack<S, kPer>().raw);
+  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
   src += lane * kPer;
   dst += lane * kPer;
-#pragma unroll 1
-  for (int b = 0; b < kPieces; b += kEach) {
-    Pack<S, kPer> p[kEach];
+  Pack<S, kPer> p[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      if constexpr (kAny)
-        p[i].raw = load_word_any(src + i * 32 * kPer, W());
-      else
-        p[i].raw = *reinterpret_cast<const W*>(src + i * 32 * kPer);
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      *reinterpret_cast<uint4*>(dst + i * 32 * kPer) = scaled<S, O, kPer>(p[i], f).raw;
-    src += kEach * 32 * kPer;
-    dst += kEach * 32 * kPer;
+  for (int i = 0; i < kEach; ++i) {
+    if constexpr (kAny)
+      p[i].raw = load16_any(src + i * 32 * kPer);
+    else
+      p[i].raw = *reinterpret_cast<const uint4*>(src + i * 32 * kPer);
   }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    store_output(dst + i * 32 * kPer, scaled<S, O, kPer>(p[i], f).w);
 }
 
 template <typename S, typename O>
 __device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int lane, float f) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(O));
-  constexpr int kSourceBytes = kPer * static_cast<int>(sizeof(S));
+  constexpr int kPer = 16 / static_cast<int>(sizeof(S));
+  constexpr uintptr_t kOut = kPer * sizeof(O) - 1;
   const S* begin = static_cast<const S*>(e.src);
   const S* end = begin + (e.rows - 1) * e.ld_src + e.cols;
   const S* src = begin + u.row * e.ld_src;
   O* dst = static_cast<O*>(e.dst) + u.row * e.ld_dst;
   if (u.rows == 1) {
     const int before =
-        static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15u) / static_cast<int>(sizeof(O));
+        static_cast<int>(reinterpret_cast<uintptr_t>(dst) & kOut) / static_cast<int>(sizeof(O));
     const int64_t from = u.part * unit_values(e.type) - before;
     if (from >= 0 && from + unit_values(e.type) <= e.cols) {
-      if ((reinterpret_cast<uintptr_t>(src + from) & (kSourceBytes - 1)) == 0) {
+      if ((reinterpret_cast<uintptr_t>(src + from) & 15u) == 0) {
         scale_whole<S, O, false>(src + from, dst + from, lane, f);
         return;
       }
-      if (words_inside(src + from, kSourceBytes, begin, end) &&
-          words_inside(src + from + unit_values(e.type) - kPer, kSourceBytes, begin, end)) {
+      if (words_inside(src + from, 16, begin, end) &&
+          words_inside(src + from + unit_values(e.type) - kPer, 16, begin, end)) {
         scale_whole<S, O, true>(src + from, dst + from, lane, f);
         return;
       }
@@ -375,17 +455,17 @@ __device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int la
     const S* x = src + r * e.ld_src;
     O* y = dst + r * e.ld_dst;
     const int before =
-        static_cast<int>(reinterpret_cast<uintptr_t>(y) & 15u) / static_cast<int>(sizeof(O));
+        static_cast<int>(reinterpret_cast<uintptr_t>(y) & kOut) / static_cast<int>(sizeof(O));
     const int64_t from = u.part * unit_values(e.type) - before;
     const int64_t c1 = min(from + unit_values(e.type), e.cols);
-    const bool words = (reinterpret_cast<uintptr_t>(x + from) & (kSourceBytes - 1)) == 0;
+    const bool words = (reinterpret_cast<uintptr_t>(x + from) & 15u) == 0;
 #pragma unroll 2
     for (int64_t c = from + lx * kPer; c < c1; c += along * kPer) {
       const Pack<S, kPer> p = words ? load_pack<S, kPer, false>(x, c, e.cols, begin, end)
                                     : load_pack<S, kPer, true>(x, c, e.cols, begin, end);
-      const Pack<O, kPer> q = scaled<S, O, kPer>(p, f);
+      const Output<O, kPer> q = scaled<S, O, kPer>(p, f);
       if (c >= 0 && c + kPer <= e.cols) {
-        *reinterpret_cast<uint4*>(y + c) = q.raw;
+        store_output(y + c, q.w);
       } else {
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
@@ -400,12 +480,8 @@ template <int kN>
 __device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint32_t warps,
                                             int lane, float f) {
   const uint32_t u0 = unit_at(t.units, w, warps), u1 = unit_at(t.units, w + 1, warps);
-  int lo = 0, hi = t.n - 1;  // the tensor of u1 - 1
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].first_unit <= u1 - 1u) lo = mid; else hi = mid - 1;
-  }
-  for (uint32_t u = u1, i = lo; u > u0; --i) {
+  int i = tensor_of(t, u1 - 1u);
+  for (uint32_t u = u1; u > u0; --i) {
     const Entry& e = t.e[i];
     const uint32_t begin = max(u0, e.first_unit);
     if (e.src == e.dst && f == 1.0f) {  // nothing changes
@@ -442,16 +518,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (w < warps) sum_units(t, w, warps, threadIdx.x & 31, slots);
 }
 
+// Clusters of kFinishCtas CTAs: the first has the norm, the others those of each.
 template <int kN>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kFinishThreads)
     grad_finish_kernel(const __grid_constant__ Parts<kN> t, const Finish f) {
-  __shared__ double smem[32];
+  __shared__ double smem[kFinishThreads / 32 + 1];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (blockIdx.x == 0)
+  if (blockIdx.x < kFinishCtas)
     finish_total(f, t.first[t.n], smem);
   else
-    finish_each(t, f, blockIdx.x - 1, gridDim.x - 1, smem);
+    finish_each(t, f, blockIdx.x - kFinishCtas, gridDim.x - kFinishCtas, smem);
 }
 
 template <int kN>
@@ -465,22 +542,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
 // A short list: one cluster of kSmallCtas CTAs does all of it in one launch, its
 // barriers between the passes.
-constexpr int kSmallCtas = 8, kSmallThreads = 1024, kSmallEntries = 72;
+constexpr int kSmallCtas = kFinishCtas, kSmallThreads = 1024, kSmallEntries = 72;
 constexpr int64_t kSmallUnits = 1024;  // 4 MB
 template <int kN>
 __global__ void __launch_bounds__(kSmallThreads, 1)
     grad_small_kernel(const __grid_constant__ Table<kN> t, const __grid_constant__ Parts<kN> parts,
                       uint32_t warps, double* slots, const Finish f) {
-  __shared__ double smem[32];
+  __shared__ double smem[kFinishThreads / 32 + 1];
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t w = blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
   if (w < warps) sum_units(t, w, warps, threadIdx.x & 31, slots);
   cluster_sync();
-  if (blockIdx.x == 0) finish_total(f, parts.first[parts.n], smem);
+  finish_total(f, parts.first[parts.n], smem);
   if (f.each) finish_each(parts, f, blockIdx.x, kSmallCtas, smem);
   if (!f.factor) return;
-  cluster_sync();
   if (w < warps) scale_units(t, w, warps, threadIdx.x & 31, __ldcg(f.factor));
 }
 
@@ -490,7 +566,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 struct Layout {
   size_t totals = 0, factor = 0, slots = 0, total = 0;
 };
-uint32_t most_warps(int sms) { return static_cast<uint32_t>(sms) * kBlocksPerSm * (kThreads / 32); }
+uint32_t most_warps(int sms) {
+  return std::min(static_cast<uint32_t>(sms) * kBlocksPerSm, static_cast<uint32_t>(kMostBlocks)) *
+         (kThreads / 32);
+}
 void layout(int64_t n, int sms, Layout* l) {
   const int64_t launches = (n + kMostEntries - 1) / kMostEntries;
   l->totals = streamk_flag_bytes(sms);
@@ -605,9 +684,9 @@ struct Call {
   cudaStream_t stream;
 };
 
-// One launch's tensors, [i0, i0 + t.n).
+// One launch's tensors, [i0, i0 + t.n), for blocks of so many warps; returns all warps.
 template <int kN>
-void fill(const Call& c, int64_t i0, Table<kN>* t) {
+uint32_t fill(const Call& c, int64_t i0, uint32_t most, uint32_t block_warps, Table<kN>* t) {
   t->n = static_cast<int>(std::min<int64_t>(kN, c.n - i0));
   int64_t units = 0;
   for (int i = 0; i < t->n; ++i) {
@@ -616,9 +695,26 @@ void fill(const Call& c, int64_t i0, Table<kN>* t) {
     units += entry_units(t->e[i]);
   }
   t->units = static_cast<uint32_t>(units);
+  const uint32_t warps = std::min(t->units, most);
+  if (Table<kN>::kStarts) {
+    // block b's first unit, units b block_warps / warps rounded down, without a division each
+    const uint64_t step = static_cast<uint64_t>(t->units) * block_warps;
+    uint64_t u = 0, rest = 0;
+    int i = 0;
+    for (uint32_t b = 0; b * block_warps < warps; ++b) {
+      while (i + 1 < t->n && t->e[i + 1].first_unit <= u) ++i;
+      t->start[b] = static_cast<uint16_t>(i);
+      u += step / warps;
+      rest += step % warps;
+      if (rest >= warps) {
+        rest -= warps;
+        ++u;
+      }
+    }
+  }
+  return warps;
 }
 
-uint32_t warps_for(uint32_t units, int sms) { return std::min(units, most_warps(sms)); }
 dim3 blocks_for(uint32_t warps) { return dim3((warps + kThreads / 32 - 1) / (kThreads / 32)); }
 
 template <int kN>
@@ -644,50 +740,60 @@ Finish finish_of(const Call& c, int64_t i0, int n, int launch) {
   return f;
 }
 
-template <int kN>
-int small_call(const Call& c) {
-  Table<kN> t;
-  fill(c, 0, &t);
-  const uint32_t warps = std::min<uint32_t>(t.units, kSmallCtas * kSmallThreads / 32);
+// launch_kernel for clusters of `ctas` blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int ctas,
+                           cudaStream_t stream, Args&&... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kSmallCtas;
+  attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kSmallCtas);
-  cfg.blockDim = dim3(kSmallThreads);
-  cfg.stream = c.stream;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <int kN>
+int small_call(const Call& c) {
+  Table<kN> t;
+  const uint32_t warps =
+      fill(c, 0, kSmallCtas * kSmallThreads / 32, kSmallThreads / 32, &t);
   return finish_launch(
-      cudaLaunchKernelEx(&cfg, grad_small_kernel<kN>, t, parts_of(t, warps), warps,
-                         reinterpret_cast<double*>(c.ws + c.l.slots), finish_of(c, 0, t.n, 0)),
+      launch_cluster(grad_small_kernel<kN>, dim3(kSmallCtas), dim3(kSmallThreads), kSmallCtas,
+                     c.stream, t, parts_of(t, warps), warps,
+                     reinterpret_cast<double*>(c.ws + c.l.slots), finish_of(c, 0, t.n, 0)),
       "gradient norm launch", c.stream);
 }
 
 template <int kN>
 int sum_launch(const Call& c, int64_t i0, int launch) {
   Table<kN> t;
-  fill(c, i0, &t);
-  const uint32_t warps = warps_for(t.units, c.sms);
+  const uint32_t warps = fill(c, i0, most_warps(c.sms), kThreads / 32, &t);
   const int st = finish_launch(
       launch_kernel(grad_sum_kernel<kN>, blocks_for(warps), dim3(kThreads), 0, c.stream, t, warps,
                     reinterpret_cast<double*>(c.ws + c.l.slots)),
       "gradient norm launch", c.stream);
   if (st != GEMM14_OK) return st;
-  const int blocks = 1 + (c.each ? std::min(t.n, kEachBlocks) : 0);
-  return finish_launch(launch_kernel(grad_finish_kernel<kN>, dim3(blocks), dim3(1024), 0, c.stream,
-                                     parts_of(t, warps), finish_of(c, i0, t.n, launch)),
-                       "gradient norm launch", c.stream);
+  // a warp a tensor
+  const int each = c.each ? (t.n + kFinishThreads / 32 * kFinishCtas - 1) /
+                                (kFinishThreads / 32 * kFinishCtas)
+                          : 0;
+  return finish_launch(
+      launch_cluster(grad_finish_kernel<kN>, dim3((1 + each) * kFinishCtas), dim3(kFinishThreads),
+                     kFinishCtas, c.stream, parts_of(t, warps), finish_of(c, i0, t.n, launch)),
+      "gradient norm launch", c.stream);
 }
 template <int kN>
 int scale_launch(const Call& c, int64_t i0) {
   Table<kN> t;
-  fill(c, i0, &t);
-  const uint32_t warps = warps_for(t.units, c.sms);
+  const uint32_t warps = fill(c, i0, most_warps(c.sms), kThreads / 32, &t);
   return finish_launch(launch_kernel(grad_scale_kernel<kN>, blocks_for(warps), dim3(kThreads), 0,
                                      c.stream, t, warps,
                                      reinterpret_cast<const float*>(c.ws + c.l.factor)),
