@@ -119,6 +119,8 @@ def lib_path() -> str:
 def load():
     """Loads libgemm14.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:  # set once, under the lock, when it is complete
+        return _lib
     with _lock:
         if _lib is None:
             path = lib_path()

@@ -14,6 +14,7 @@ from .api import (_CODE, _FP32_MODES, _capturing, _graph_workspace, _workspace, 
                   _workspaces)
 
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice  # (of a context that operands' tensors have made)
 
 CKPT8_BLOCK = 32  # columns of a row that share a scale
 
@@ -31,7 +32,7 @@ def _on(stream, device: torch.device, body):
     current: what the call allocates then belongs to the stream its kernels run on."""
     if stream is None:
         # the handle itself: making a Stream object of it takes as long as a launch
-        if device.index == torch.cuda.current_device():
+        if device.index == _current_device():
             return body(_current_stream(device.index))
         with torch.cuda.device(device):
             return body(_current_stream(device.index))
@@ -286,6 +287,10 @@ def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = Non
     return _on(stream, dy.device, body)
 
 
+# Calls of up to this many tokens may need no workspace (and no lock for it).
+_FEW_TOKENS = 4096
+
+
 def _tokens(tokens: torch.Tensor, device: int) -> int:
     """The bytes of a token (a contiguous integer tensor on the device of this index)."""
     if tokens.dtype not in (torch.int64, torch.int32):
@@ -307,24 +312,27 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
     (default: the table's). Stream, allocation and autograd as for
     linear_cross_entropy; embedding_backward forms the gradient."""
     dtype = table.dtype if dtype is None else dtype
-    if table.dtype not in _CODE or dtype not in _CODE:
+    code, out_code = _CODE.get(table.dtype), _CODE.get(dtype)
+    if code is None or out_code is None:
         raise TypeError(f"unsupported dtypes {table.dtype}, {dtype}")
     ldw = _matrix(table, "table")
     size = _tokens(tokens, table.get_device())
     V, D = table.shape
     if V < 1 or D < 1:
         raise ValueError(f"table must not be empty, got shape {tuple(table.shape)}")
-    T = tokens.numel()
+    T, device = tokens.numel(), table.device
 
     def body(handle):
-        out = torch.empty((*tokens.shape, D), dtype=dtype, device=table.device)
+        out = torch.empty((*tokens.shape, D), dtype=dtype, device=device)
         if T:
-            _lib.embedding_raw(_CODE[table.dtype], _CODE[dtype], T, V, D, table.data_ptr(), ldw,
-                               tokens.data_ptr(), size, int(ignore_index), float(scale),
-                               out.data_ptr(), D, handle)
+            status = _lib.load().gemm14_embedding_forward(
+                code, out_code, T, V, D, table.data_ptr(), ldw, tokens.data_ptr(), size,
+                ignore_index, scale, out.data_ptr(), D, handle)
+            if status:
+                raise _lib.Gemm14Error(status, "gemm14_embedding_forward")
         return out
 
-    return _on(stream, table.device, body)
+    return _on(stream, device, body)
 
 
 def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None = None,
@@ -342,7 +350,8 @@ def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None 
     their weights. Tokens that are ignore_index or outside [0, V) add nothing. Sums
     are fp32, in an order that repeats. Stream and workspace as for
     linear_cross_entropy."""
-    if dy.dtype not in _CODE:
+    code = _CODE.get(dy.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dy.dtype}")
     if dy.dim() != tokens.dim() + 1 or dy.shape[:-1] != tokens.shape:
         raise ValueError(f"dy {tuple(dy.shape)} must have a row for each of the tokens {tuple(tokens.shape)}")
@@ -351,14 +360,16 @@ def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None 
             raise ValueError("dy must be contiguous where tokens is not one-dimensional")
         dy = dy.view(tokens.numel(), dy.size(-1))
     lddy = _matrix(dy, "dy")
-    size = _tokens(tokens, dy.get_device())
+    index = dy.get_device()
+    size = _tokens(tokens, index)
     T, D = dy.shape
     if out is None:
         if rows is None or beta != 0.0:
             raise ValueError("rows or out is needed, and out for beta != 0")
-        V, dtype = int(rows), dy.dtype if dtype is None else dtype
+        V, dtype, lddw = int(rows), dy.dtype if dtype is None else dtype, D
     else:
-        if out.dim() != 2 or out.size(1) != D or (rows is not None and out.size(0) != rows) or \
+        lddw = _matrix(out, "out", index)
+        if out.size(1) != D or (rows is not None and out.size(0) != rows) or \
                 dtype not in (None, out.dtype):
             raise ValueError(f"out {out.dtype} {tuple(out.shape)} does not fit rows {rows}, "
                              f"{D} columns and dtype {dtype}")
@@ -367,22 +378,24 @@ def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None 
         raise TypeError(f"the gradient is formed in dy's dtype or float32, not {dtype}")
     if V < 1 or D < 1:
         raise ValueError(f"an empty table has no gradient: {V} rows of {D}")
-    code = _CODE[dy.dtype]
+    device, out_code = dy.device, _CODE[dtype]
 
     def body(handle):
-        dw = out if out is not None else torch.empty((V, D), dtype=dtype, device=dy.device)
-        lddw = _matrix(dw, "out", dy.get_device())
-        _in_workspace(
-            dy.device, handle,
-            lambda ws, n: _lib.embedding_backward_raw(code, _CODE[dtype], T, V, D, _ptr(dy), lddy,
-                                                      _ptr(tokens), size, int(ignore_index),
-                                                      float(scale), float(beta), dw.data_ptr(),
-                                                      lddw, ws, n, handle, check=False),
-            lambda: _lib.embedding_backward_workspace_bytes(code, T, V, D),
-            "gemm14_embedding_backward")
+        dw = out if out is not None else torch.empty((V, D), dtype=dtype, device=device)
+        fn = _lib.load().gemm14_embedding_backward
+        args = (code, out_code, T, V, D, _ptr(dy), lddy, _ptr(tokens), size, ignore_index, scale,
+                beta, dw.data_ptr(), lddw)
+        if T <= _FEW_TOKENS and not _lib.embedding_backward_workspace_bytes(code, T, V, D):
+            status = fn(*args, None, 0, handle)
+            if status:
+                raise _lib.Gemm14Error(status, "gemm14_embedding_backward")
+        else:
+            _in_workspace(device, handle, lambda ws, n: fn(*args, ws, n, handle),
+                          lambda: _lib.embedding_backward_workspace_bytes(code, T, V, D),
+                          "gemm14_embedding_backward")
         return dw
 
-    return _on(stream, dy.device, body)
+    return _on(stream, device, body)
 
 
 def _as_rows(x: torch.Tensor) -> tuple[int, int, int]:
@@ -441,22 +454,23 @@ class GradList:
         return len(self._tensors)
 
 
-def _grad_call(grads, stream, call, where):
-    """(norm, each) of call(norm, each, workspace, bytes, stream handle)."""
+def _grad_call(grads, each, stream, call, where):
+    """The norm, or it and each, of call(norm, each, workspace, bytes, stream handle)."""
     device = grads._device or torch.device("cuda", torch.cuda.current_device())
-    n = len(grads)
+    n = len(grads._tensors)
 
     def body(handle):
         norm = torch.empty((), dtype=torch.float32, device=device)
-        each = torch.empty(n, dtype=torch.float32, device=device)
+        norms = torch.empty(n, dtype=torch.float32, device=device) if each else None
+        at, each_at = norm.data_ptr(), _ptr(norms)
         try:
-            _in_workspace(device, handle, lambda ws, b: call(norm.data_ptr(), _ptr(each), ws, b, handle),
+            _in_workspace(device, handle, lambda ws, b: call(at, each_at, ws, b, handle),
                           lambda: _lib.grad_workspace_bytes(n), where)
         except _lib.Gemm14Error as e:
             if e.status == _lib.GEMM14_ERR_INVALID_ARG:
                 raise ValueError(f"{where}: {_lib.last_error_string()}") from e
             raise
-        return norm, each
+        return (norm, norms) if each else norm
 
     return _on(stream, device, body)
 
@@ -471,13 +485,11 @@ def grad_norm(grads, scale: float = 1.0, each: bool = False, stream=None):
         grads = GradList(grads)
     if not math.isfinite(scale):
         raise ValueError(f"scale must be finite, got {scale}")
-    norm, norms = _grad_call(
-        grads, stream,
-        lambda norm, norms, ws, b, handle: _lib.grad_norm_raw(
-            len(grads), grads._args, float(scale), norm, norms if each else None, ws, b, handle,
-            check=False),
-        "gemm14_grad_norm")
-    return (norm, norms) if each else norm
+    n, args = len(grads._tensors), grads._args
+    fn = _lib.load().gemm14_grad_norm
+    return _grad_call(grads, each, stream,
+                      lambda norm, norms, ws, b, handle: fn(n, args, scale, norm, norms, ws, b, handle),
+                      "gemm14_grad_norm")
 
 
 def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, out=None, each: bool = False,
@@ -510,10 +522,9 @@ def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, out=None, each: b
                     (x.is_contiguous() and y.is_contiguous())):
                 raise ValueError(f"output {i} lies otherwise than its gradient: strides "
                                  f"{y.stride()}, {x.stride()}")
-    norm, norms = _grad_call(
-        grads, stream,
-        lambda norm, norms, ws, b, handle: _lib.grad_clip_raw(
-            len(grads), grads._args, None if out is None else out._args, float(scale),
-            float(max_norm), norm, norms if each else None, ws, b, handle, check=False),
-        "gemm14_grad_clip")
-    return (norm, norms) if each else norm
+    n, args, out_args = len(grads._tensors), grads._args, None if out is None else out._args
+    fn = _lib.load().gemm14_grad_clip
+    return _grad_call(grads, each, stream,
+                      lambda norm, norms, ws, b, handle: fn(n, args, out_args, scale, max_norm, norm,
+                                                            norms, ws, b, handle),
+                      "gemm14_grad_clip")
