@@ -94,17 +94,22 @@ __global__ void __launch_bounds__(kThreads)
     }
     const int64_t words = (D - lead) / kPer;
     const int tail = static_cast<int>(D - lead - words * kPer);
+    if (kAny && real && words > 0 &&
+        !(words_inside(from + lead, sizeof(WordS), W, end) &&
+          words_inside(from + lead + (words - 1) * kPer, sizeof(WordS), W, end))) {
+      // a row whose words reach past the table's ends
+      for (int64_t c = tx; c < D; c += along) one(c);
+      continue;
+    }
     for (int64_t i0 = tx; i0 < words; i0 += static_cast<int64_t>(along) * kAhead) {
       const S* x = from + lead + i0 * kPer;
       O* y = to + lead + i0 * kPer;
       const int step = along * kPer;
       const int64_t here = words - i0;
       Pack<S, kPer> p[kAhead];
-      bool in[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        in[u] = u * along < here && real && (!kAny || words_inside(x + u * step, sizeof(WordS), W, end));
-        if (!in[u]) continue;
+        if (u * along >= here || !real) break;
         if constexpr (kAny)
           p[u].raw = load_word_any(x + u * step, WordS());
         else
@@ -113,11 +118,6 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (u * along >= here) break;
-        if (kAny && real && !in[u]) {  // a word at the table's end
-#pragma unroll 1
-          for (int j = 0; j < kPer; ++j) one(lead + (i0 + u * along) * kPer + j);
-          continue;
-        }
         Pack<O, kPer> q;
         bool copied = false;
         if constexpr (sizeof(S) == sizeof(O)) {

@@ -209,7 +209,7 @@ __device__ __forceinline__ void add_unit(double& sum, const Entry& e, const Unit
     const int64_t c0 = from + lx * kPer, c1 = min(from + unit_values(e.type), e.cols);
     float s = 0.0f;
     uint32_t bits = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t c = c0; c < c1; c += along * kPer) {
       const Pack<S, kPer> p = load_pack<S, kPer, false>(at, c, c1, nullptr, nullptr);
       s += square_sum(0.0f, p);
@@ -232,8 +232,14 @@ __device__ __forceinline__ double warp_sum(double x) {
 template <int kN>
 __device__ __forceinline__ void sum_units(const Table<kN>& t, uint32_t w, uint32_t warps, int lane,
                                           double* slots) {
-  const uint32_t u0 = unit_at(t.units, w, warps), u1 = unit_at(t.units, w + 1, warps);
-  int i = tensor_of(t, u0);
+  // what the parameters say comes before the wait for the kernel before this one
+  const bool any = w < warps;
+  const uint32_t u0 = any ? unit_at(t.units, w, warps) : 0u;
+  const uint32_t u1 = any ? unit_at(t.units, w + 1, warps) : 0u;
+  int i = any ? tensor_of(t, u0) : 0;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (!any) return;
   if (lane == 0 && w > 0 && i > 0 && t.e[i].first_unit == u0) slots[w + i - 1] = 0.0;
   for (uint32_t u = u0; u < u1;) {
     const Entry& e = t.e[i];
@@ -511,10 +517,7 @@ __device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint
 template <int kN>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_sum_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, double* slots) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (w < warps) sum_units(t, w, warps, threadIdx.x & 31, slots);
+  sum_units(t, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), warps, threadIdx.x & 31, slots);
 }
 
 // Clusters of kFinishCtas CTAs: the first has the norm, the others those of each.
@@ -550,10 +553,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     grad_small_kernel(const __grid_constant__ Table<kN> t, const __grid_constant__ Parts<kN> parts,
                       uint32_t warps, double* slots, const Finish f) {
   __shared__ double smem[kFinishThreads / 32 + 1];
-  grid_dependency_wait();
-  grid_launch_dependents();
   const uint32_t w = blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
-  if (w < warps) sum_units(t, w, warps, threadIdx.x & 31, slots);
+  sum_units(t, w, warps, threadIdx.x & 31, slots);
   cluster_sync();
   finish_total(f, parts.first[parts.n], smem);
   if (f.each) finish_each(parts, f, blockIdx.x, kSmallCtas, smem);
