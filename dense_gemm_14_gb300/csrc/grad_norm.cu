@@ -830,27 +830,35 @@ int run(const Call& c, int64_t units) {
 
 bool finite(float x) { return x - x == 0.0f; }
 
-int grad_call(Call c, size_t workspace_bytes, const char* where) {
-  if (c.n < 0 || c.n > kMostTensors || (c.n > 0 && !c.grads)) return GEMM14_ERR_INVALID_ARG;
-  if (!finite(c.scale) || !c.norm || !aligned(c.norm, 4) || !aligned(c.each, 4))
-    return GEMM14_ERR_INVALID_ARG;
-  if (c.clip && !(c.max_norm >= 0.0f)) return GEMM14_ERR_INVALID_ARG;
-  int64_t units = 0;
+// What the arguments are checked for on the host, before any CUDA call.
+const char* fault_of(const Call& c, int64_t* units) {
+  if (c.n < 0 || c.n > kMostTensors || (c.n > 0 && !c.grads)) return "the number of tensors";
+  if (!finite(c.scale)) return "scale";
+  if (c.clip && !(c.max_norm >= 0.0f)) return "max_norm";
+  if (!c.norm || !aligned(c.norm, 4) || !aligned(c.each, 4)) return "norm or each";
+  if (c.ws && !aligned(c.ws, 16)) return "the workspace's alignment";
+  *units = 0;
   for (int64_t i = 0; i < c.n; ++i) {
     const gemm14_tensor& g = c.grads[i];
-    int st = validate_tensor(g);
-    if (st != GEMM14_OK) return st;
+    if (validate_tensor(g) != GEMM14_OK) return "a gradient";
     if (c.outs) {
       const gemm14_tensor& o = c.outs[i];
-      if ((st = validate_tensor(o)) != GEMM14_OK) return st;
-      if (o.rows != g.rows || o.cols != g.cols ||
+      if (validate_tensor(o) != GEMM14_OK || o.rows != g.rows || o.cols != g.cols ||
           (o.dtype != g.dtype && o.dtype != GEMM14_DTYPE_F32))
-        return GEMM14_ERR_INVALID_ARG;
+        return "an output";
     }
-    units += entry_units(entry_of(g, c.outs ? c.outs + i : nullptr));
-    if (units > INT32_MAX) return GEMM14_ERR_INVALID_ARG;
+    *units += entry_units(entry_of(g, c.outs ? c.outs + i : nullptr));
+    if (*units > INT32_MAX) return "the gradients' total size";
   }
-  if (c.ws && !aligned(c.ws, 16)) return GEMM14_ERR_INVALID_ARG;
+  return nullptr;
+}
+
+int grad_call(Call c, size_t workspace_bytes, const char* where) {
+  int64_t units = 0;
+  if (const char* fault = fault_of(c, &units)) {
+    note_error("%s: invalid: %s", where, fault);
+    return GEMM14_ERR_INVALID_ARG;
+  }
   int st = c.clip ? check_apart(c.n, c.grads, c.outs) : GEMM14_OK;
   if (st != GEMM14_OK) return st;
   if ((st = current_sm_count(&c.sms)) != GEMM14_OK) return st;

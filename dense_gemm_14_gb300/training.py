@@ -398,16 +398,17 @@ def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None 
     return _on(stream, device, body)
 
 
-def _as_rows(x: torch.Tensor) -> tuple[int, int, int]:
+def _as_rows(x: torch.Tensor) -> tuple[int, int, int, object]:
     """(rows, cols, pitch) of a tensor's elements: a row-major matrix as it is,
-    another in the order its elements lie in memory, one row where without gaps."""
+    another in the order its elements lie in memory, one row where without gaps;
+    and that order (equal for tensors whose elements follow one another alike)."""
     if x.numel() == 0:
-        return 0, 0, 1
+        return 0, 0, 1, None
     if x.dim() == 2 and (x.size(1) == 1 or x.stride(1) == 1) and \
             (x.size(0) == 1 or x.stride(0) >= x.size(1)):
-        return x.size(0), x.size(1), max(x.stride(0), x.size(1))
+        return x.size(0), x.size(1), max(x.stride(0), x.size(1)), "rows"
     if x.is_contiguous():
-        return 1, x.numel(), x.numel()
+        return 1, x.numel(), x.numel(), "dense"
     dims = sorted((s, n) for s, n in zip(x.stride(), x.shape) if n > 1)
     cols, rows, ld = 1, 1, 1
     while dims and dims[0][0] == cols:
@@ -421,30 +422,35 @@ def _as_rows(x: torch.Tensor) -> tuple[int, int, int]:
             rows *= n
     if ld < cols and rows > 1 or ld == 0:
         raise ValueError(f"strides {x.stride()} of shape {tuple(x.shape)} are not rows of one pitch")
-    return rows, cols, max(ld, cols)
+    return rows, cols, max(ld, cols), x.stride()
 
 
 class GradList:
     """Tensors that grad_norm and clip_grad_norm take together: float32, bfloat16
     and float16 CUDA tensors of one GPU, in any mixture, each without gaps or rows
     of one pitch. A program that keeps its gradients keeps the list of them too:
-    making it costs a microsecond a tensor. It keeps the tensors, and reads what they
-    hold when a call runs."""
+    making it costs a microsecond or two a tensor. Calls read and write the memory
+    that the tensors have when the list is made, which it keeps: a tensor that is
+    given other memory (resize_, set_, .data) needs a new list."""
 
-    __slots__ = ("_tensors", "_args", "_device")
+    __slots__ = ("_tensors", "_args", "_device", "_layouts", "_dtypes", "_storages")
 
     def __init__(self, tensors):
         self._tensors = tuple(tensors)
         self._args = (_lib.TensorArg * len(self._tensors))()
         self._device = None
+        self._layouts, self._dtypes = [], []
+        self._storages = [x.untyped_storage() for x in self._tensors]
         for i, (x, a) in enumerate(zip(self._tensors, self._args)):
             if x.dtype not in _CODE:
                 raise TypeError(f"tensor {i}: unsupported dtype {x.dtype}")
             if not x.is_cuda or (self._device is not None and x.device != self._device):
                 raise ValueError(f"tensor {i} must be a CUDA tensor on the others' device, is on {x.device}")
             self._device = x.device
-            a.rows, a.cols, a.ld = _as_rows(x)
+            a.rows, a.cols, a.ld, order = _as_rows(x)
             a.data, a.dtype = _ptr(x), _CODE[x.dtype]
+            self._layouts.append((x.shape, order))
+            self._dtypes.append(a.dtype)
 
     @property
     def tensors(self) -> tuple[torch.Tensor, ...]:
@@ -512,16 +518,13 @@ def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, out=None, each: b
     if out is not None:
         if len(out) != len(grads) or (len(out) and out._device != grads._device):
             raise ValueError(f"{len(grads)} gradients and {len(out)} outputs, on one device each")
-        for i, (x, y) in enumerate(zip(grads._tensors, out._tensors)):
-            if x.shape != y.shape or y.dtype not in (x.dtype, torch.float32):
-                raise ValueError(f"output {i} ({y.dtype} {tuple(y.shape)}) does not fit its gradient "
-                                 f"({x.dtype} {tuple(x.shape)})")
-            a, b = grads._args[i], out._args[i]
-            if (a.rows, a.cols) != (b.rows, b.cols) or not (
-                    x.dim() == 2 or x.stride() == y.stride() or
-                    (x.is_contiguous() and y.is_contiguous())):
-                raise ValueError(f"output {i} lies otherwise than its gradient: strides "
-                                 f"{y.stride()}, {x.stride()}")
+        if grads._layouts != out._layouts or \
+                (grads._dtypes != out._dtypes and any(out._dtypes)):  # (0 is float32)
+            for i, (x, y) in enumerate(zip(grads._tensors, out._tensors)):
+                if y.dtype not in (x.dtype, torch.float32) or grads._layouts[i] != out._layouts[i]:
+                    raise ValueError(f"output {i} ({y.dtype} {tuple(y.shape)}, strides {y.stride()}) "
+                                     f"does not fit its gradient ({x.dtype} {tuple(x.shape)}, "
+                                     f"{x.stride()})")
     n, args, out_args = len(grads._tensors), grads._args, None if out is None else out._args
     fn = _lib.load().gemm14_grad_clip
     return _grad_call(grads, each, stream,

@@ -172,7 +172,7 @@ def test_other_layouts():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("n", [15, 16, 17, 72, 73, 576, 577, 1500])
+@pytest.mark.parametrize("n", [15, 16, 17, 72, 73, 544, 545, 577, 1500])
 def test_long_lists(n):
     """Lists of one and several launches, tensors of all sizes among them."""
     g = torch.Generator().manual_seed(n)
