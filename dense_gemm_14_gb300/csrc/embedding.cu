@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads)
 // exchange between them. A block has 32 places, a lane each, and a warp every
 // 32nd chunk of 32 tokens to compare them with. (A radix sort by one SM took
 // 7.5 us for 300 places and 18 for 8192, @RANK@.)
-constexpr int kRankThreads = 1024, kRanked = 8192;
+constexpr int kRankThreads = 1024, kRanked = 4096;
 
 __global__ void __launch_bounds__(kRankThreads)
     embedding_rank_kernel(const Tokens k, uint2* list, uint32_t* count) {
@@ -897,10 +897,11 @@ __global__ void __launch_bounds__(kThreads, kSumBlocks)
   }
 }
 
-// The sums that lie in several ranges, 128 columns of one an item (a block's items
-// are of different sums). A warp adds an item's slots; those of many are the block's, whose warps add every eighth each,
-// and then the warps' sums in order. (The list's order, which varies, decides
-// nothing but who that is.)
+// The sums that lie in several ranges, 128 columns of one an item. Where the items
+// are few a block has one, whose warps add every eighth of its slots each, and then
+// the warps' sums in order; else a warp has one, a block's being of different sums,
+// and those of many slots are the block's all the same. (The list's order, which
+// varies, decides nothing but who adds what.)
 constexpr uint32_t kManySlots = 48;
 
 // Every `each`-th of slots 0 .. behind from the `from`-th; slot 0 is the first
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(kThreads)
                           int64_t V, unsigned* err) {
   constexpr int kWarps = kThreads / 32, kTests = 4;
   __shared__ float4 sums[kWarps][32];
-  __shared__ uint32_t many[kWarps];  // ranges behind the warp's item, 0: it is done
+  __shared__ uint32_t many[kWarps][4];  // the warp's item, [0] 0: it is done
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t n = r.count[0], listed = r.count[1];
@@ -950,52 +951,72 @@ __global__ void __launch_bounds__(kThreads)
   const auto slots_of = [&](uint32_t range, int64_t c) {
     return r.slots + 2 * static_cast<int64_t>(range) * r.slot_ld + (c < r.slot_ld ? c : 0);
   };
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kWarps; base < items;
-       base += static_cast<int64_t>(gridDim.x) * kWarps) {
-    uint32_t behind = 0;  // ranges behind the item's that begin within the sum
-    if (base + warp < items) {
-      const int64_t slice = (base + warp) / listed, entry = base + warp - slice * listed;
-      const int64_t c = slice * 128 + lane * 4;
-      const uint32_t range = r.list[entry], token = r.place[(range + 1) * length].x;
-      for (bool more = true; more;) {
-        uint32_t in[kTests];
+  // places of the sum that begins in a range: the token, and the ranges behind it
+  // that begin within the sum
+  const auto behind_of = [&](uint32_t range, uint32_t token) {
+    uint32_t behind = 0;
+    for (bool more = true; more;) {
+      uint32_t in[kTests];
 #pragma unroll
-        for (int u = 0; u < kTests; ++u) {
-          const int64_t i = static_cast<int64_t>(range + 1 + behind + 32 * u + lane) * length;
-          in[u] = __ballot_sync(0xffffffffu, i < n && r.place[i].x == token);
-        }
-#pragma unroll
-        for (int u = 0; u < kTests; ++u) {
-          if (more) behind += __popc(in[u]);
-          more = more && in[u] == ~0u;
-        }
+      for (int u = 0; u < kTests; ++u) {
+        const int64_t i = static_cast<int64_t>(range + 1 + behind + 32 * u + lane) * length;
+        in[u] = __ballot_sync(0xffffffffu, i < n && r.place[i].x == token);
       }
-      if (behind < kManySlots)
-        put(token, c, add_slots(slots_of(range, c), r.slot_ld, behind, 0u, 1u));
+#pragma unroll
+      for (int u = 0; u < kTests; ++u) {
+        if (more) behind += __popc(in[u]);
+        more = more && in[u] == ~0u;
+      }
     }
-    if (lane == 0) many[warp] = behind < kManySlots ? 0u : behind;
+    return behind;
+  };
+  const auto by_block = [&](uint32_t range, uint32_t token, uint32_t behind, int64_t c) {
+    sums[warp][lane] = add_slots(slots_of(range, c), r.slot_ld, behind, warp, kWarps);
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-      if (many[w] == 0u) continue;
-      const int64_t slice = (base + w) / listed, entry = base + w - slice * listed;
-      const int64_t c = slice * 128 + lane * 4;
-      const uint32_t range = r.list[entry];
-      sums[warp][lane] = add_slots(slots_of(range, c), r.slot_ld, many[w], warp, kWarps);
-      __syncthreads();
-      if (warp == 0) {
-        float4 s = sums[0][lane];
+    if (warp == 0) {
+      float4 s = sums[0][lane];
 #pragma unroll
-        for (int k = 1; k < kWarps; ++k) {
-          const float4 v = sums[k][lane];
-          s.x += v.x;
-          s.y += v.y;
-          s.z += v.z;
-          s.w += v.w;
-        }
-        put(r.place[(range + 1) * length].x, c, s);
+      for (int k = 1; k < kWarps; ++k) {
+        const float4 v = sums[k][lane];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
       }
-      __syncthreads();
+      put(token, c, s);
     }
+    __syncthreads();
+  };
+  const bool few = items <= 2 * static_cast<int64_t>(gridDim.x);
+  const int each = few ? 1 : kWarps;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * each; base < items;
+       base += static_cast<int64_t>(gridDim.x) * each) {
+    const int64_t item = few ? base : base + warp;
+    uint32_t behind = 0, range = 0, token = 0;
+    int64_t c = 0;
+    if (item < items) {
+      const int64_t slice = item / listed;
+      c = slice * 128 + lane * 4;
+      range = r.list[item - slice * listed];
+      token = r.place[(range + 1) * length].x;
+      behind = behind_of(range, token);
+    }
+    if (few) {
+      by_block(range, token, behind, c);
+      continue;
+    }
+    if (item < items && behind < kManySlots)
+      put(token, c, add_slots(slots_of(range, c), r.slot_ld, behind, 0u, 1u));
+    if (lane == 0) {
+      many[warp][0] = behind < kManySlots ? 0u : behind;
+      many[warp][1] = range;
+      many[warp][2] = token;
+      many[warp][3] = static_cast<uint32_t>(c / 128);  // (lane 0's is the slice's first)
+    }
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w)
+      if (many[w][0] != 0u)
+        by_block(many[w][1], many[w][2], many[w][0], static_cast<int64_t>(many[w][3]) * 128 + lane * 4);
     __syncthreads();
   }
 }
@@ -1081,10 +1102,10 @@ cudaError_t sort_config(cudaStream_t stream, cudaLaunchConfig_t* cfg, cudaLaunch
         if (r == cudaSuccess && kCtas > 8)
           r = cudaFuncSetAttribute(embedding_sort_kernel<kCtas>,
                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        int clusters = 1;
+        int fit = 1;
         if (r == cudaSuccess && kCtas > 8)
-          r = cudaOccupancyMaxActiveClusters(&clusters, embedding_sort_kernel<kCtas>, cfg);
-        if (r == cudaSuccess && clusters < 1) r = cudaErrorInvalidConfiguration;
+          r = cudaOccupancyMaxActiveClusters(&fit, embedding_sort_kernel<kCtas>, cfg);
+        if (r == cudaSuccess && fit < 1) r = cudaErrorInvalidConfiguration;
         return static_cast<int>(r);
       },
       [](int r) { return r == static_cast<int>(cudaSuccess) ||

@@ -316,23 +316,27 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
     if code is None or out_code is None:
         raise TypeError(f"unsupported dtypes {table.dtype}, {dtype}")
     ldw = _matrix(table, "table")
-    size = _tokens(tokens, table.get_device())
-    V, D = table.shape
-    if V < 1 or D < 1:
+    index = table.get_device()
+    size = _tokens(tokens, index)
+    if table.numel() == 0:
         raise ValueError(f"table must not be empty, got shape {tuple(table.shape)}")
-    T, device = tokens.numel(), table.device
+    if stream is None and index == _current_device():  # (the time of a lookup of few tokens is the host's)
+        return _lookup(_current_stream(index), code, out_code, table, ldw, tokens, size, ignore_index, scale, dtype)
+    return _on(stream, table.device,
+               lambda handle: _lookup(handle, code, out_code, table, ldw, tokens, size, ignore_index, scale, dtype))
 
-    def body(handle):
-        out = torch.empty((*tokens.shape, D), dtype=dtype, device=device)
-        if T:
-            status = _lib.load().gemm14_embedding_forward(
-                code, out_code, T, V, D, table.data_ptr(), ldw, tokens.data_ptr(), size,
-                ignore_index, scale, out.data_ptr(), D, handle)
-            if status:
-                raise _lib.Gemm14Error(status, "gemm14_embedding_forward")
-        return out
 
-    return _on(stream, device, body)
+def _lookup(handle, code, out_code, table, ldw, tokens, size, ignore_index, scale, dtype):
+    V, D = table.shape
+    T = tokens.numel()
+    out = torch.empty((*tokens.shape, D), dtype=dtype, device=table.device)
+    if T:
+        status = _lib.load().gemm14_embedding_forward(code, out_code, T, V, D, table.data_ptr(), ldw,
+                                                      tokens.data_ptr(), size, ignore_index, scale,
+                                                      out.data_ptr(), D, handle)
+        if status:
+            raise _lib.Gemm14Error(status, "gemm14_embedding_forward")
+    return out
 
 
 def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None = None,
