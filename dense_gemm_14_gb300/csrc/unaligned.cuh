@@ -15,11 +15,8 @@ __device__ __forceinline__ bool words_inside(const void* p, int bytes, const voi
          base + 2 * bytes <= reinterpret_cast<uintptr_t>(end);
 }
 
-// 16 bytes at p (2-byte aligned; words_inside(p, 16, ..) holds).
-__device__ __forceinline__ uint4 load16_any(const void* p) {
-  const uint32_t a = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
-  const uint4* base = reinterpret_cast<const uint4*>(static_cast<const char*>(p) - a);
-  const uint4 lo = base[0], hi = base[1];
+// The 16 bytes from byte a (even, below 16) of lo on, those behind lo's from hi.
+__device__ __forceinline__ uint4 shift16(const uint4& lo, const uint4& hi, uint32_t a) {
   uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
   for (int i = 0; i < 6; ++i) w[i] = (a & 8u) ? w[i + 2] : w[i];
@@ -28,6 +25,13 @@ __device__ __forceinline__ uint4 load16_any(const void* p) {
   const uint32_t s = (a & 3u) * 8u;
   return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
                     __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+}
+
+// 16 bytes at p (2-byte aligned; words_inside(p, 16, ..) holds).
+__device__ __forceinline__ uint4 load16_any(const void* p) {
+  const uint32_t a = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+  const uint4* base = reinterpret_cast<const uint4*>(static_cast<const char*>(p) - a);
+  return shift16(base[0], base[1], a);
 }
 
 // 8 bytes at any p (words_inside(p, 8, ..) holds).
