@@ -894,16 +894,24 @@ __global__ void __launch_bounds__(kThreads, kSumBlocks)
   const char* begin = reinterpret_cast<const char*>(a.dY);
   const char* end = reinterpret_cast<const char*>(a.dY + (T - 1) * a.lddy + a.D);
   float* slot = r.slots + 2 * static_cast<int64_t>(g.range) * r.slot_ld + c;
-  const auto row_of = [&](uint32_t at) {
-    return reinterpret_cast<const char*>(a.dY + static_cast<int64_t>(at & ~kFlag) * a.lddy + c);
-  };
+  // a row's byte in its word where the thread's columns begin, in 32 bits
+  const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.dY + c));
+  const uint32_t pitch = static_cast<uint32_t>(a.lddy * static_cast<int64_t>(sizeof(S)));
+  const auto byte_of = [&](uint32_t at) { return (low + (at & ~kFlag) * pitch) & 15u; };
+  // words of rows that others lie before and behind are all inside
+  const uint32_t inner = a.lddy * static_cast<int64_t>(sizeof(S)) >= 32 && T > 2 ? static_cast<uint32_t>(T - 2) : 0u;
   const auto fetch = [&](uint32_t i, const uint2& v, int at) {
     if (i < length && c < a.D + kPer) {  // (a lane behind the last column: its neighbour's word)
-      const char* p = row_of(v.y);
-      const char* from = p - (reinterpret_cast<uintptr_t>(p) & 15);
-      copy_inside<S>(words + at * AnyShape::kWords + threadIdx.x, from, begin, end);
-      if (last_lane)
-        copy_inside<S>(words + at * AnyShape::kWords + kThreads + threadIdx.x / 8, from + 16, begin, end);
+      const uint32_t place = v.y & ~kFlag;
+      const char* from = reinterpret_cast<const char*>(a.dY + static_cast<int64_t>(place) * a.lddy + c) - byte_of(v.y);
+      uint4* to = words + at * AnyShape::kWords;
+      if (place - 1u < inner) {
+        copy_async<16>(smem_u32(to + threadIdx.x), from, 16);
+        if (last_lane) copy_async<16>(smem_u32(to + kThreads + threadIdx.x / 8), from + 16, 16);
+      } else {
+        copy_inside<S>(to + threadIdx.x, from, begin, end);
+        if (last_lane) copy_inside<S>(to + kThreads + threadIdx.x / 8, from + 16, begin, end);
+      }
       if (a.beta != 0.0f && live && (v.y & kFlag) && !(v.x & kFlag) &&
           dev_check(index_ok(v.x, V), a.err))
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dW + v.x * a.lddw + c));
@@ -926,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, kSumBlocks)
         const uint4* w = words + at * AnyShape::kWords;
         Pack<S, kPer> x;
         x.raw = shift16(w[threadIdx.x], w[last_lane ? kThreads + threadIdx.x / 8 : threadIdx.x + 1],
-                        static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_of(v.y))) & 15u);
+                        byte_of(v.y));
         add_to<S, kPer>(sum, x);
       }
       if (v.y & kFlag) {
@@ -1122,13 +1130,16 @@ void grad_plan(int dtype, int pieces, int64_t T, int64_t V, int64_t D, int sms, 
   // groups of a quarter of a block, where a token may have many places
   const int widest = g->few && T > kThreads ? kThreads / 4 : kThreads;
   while (g->along < widest && g->along < items) g->along *= 2;
+  // a warp's time for a row is the same whatever its lanes have: as few idle as may be
+  const auto threads = [&](int along) { return (items + along - 1) / along * along; };
+  for (int x = g->along; !g->few && x > 32; x /= 2)
+    if (threads(x / 2) < threads(g->along)) g->along = x / 2;
   g->slices = static_cast<int>((items + g->along - 1) / g->along);
   if (g->few) return;
   const int groups = kThreads / g->along;
   // as many ranges as are resident at once, of 8 places at least
   const int64_t most = (T + kLeastRange - 1) / kLeastRange;
-  g->ranges = static_cast<int64_t>(sms) * kSumBlocks * groups / g->slices;
-  if (g->ranges < 1) g->ranges = 1;
+  g->ranges = std::max<int64_t>(1, static_cast<int64_t>(sms) * kSumBlocks / g->slices) * groups;
   if (g->ranges > most) g->ranges = most;
   g->blocks = (g->ranges + groups - 1) / groups * g->slices;
   g->slot_ld = (D + 7) / 8 * 8;
