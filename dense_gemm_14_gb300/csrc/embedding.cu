@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(kRankThreads)
 // the warp goes through its range again and moves the places there, in order:
 // a ballot for each bit of the digit finds the lanes that have the same one.
 // Two passes for a vocabulary of up to 2^18; the first leaves out what takes no
-// part. Between passes the list lies in L2.
-// @SORT@
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+// part. Between passes the list lies in L2. A pass takes some 5 us for its barriers
+// and the sums alone: 13 us for 16384 places, 21 for 65536 (with the lanes of a
+// digit from match.any, and a store for each of token and place, 44).
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSortAhead = 8;  // words in flight a lane
 
@@ -480,8 +480,13 @@ struct SortArgs {
   unsigned* err;
 };
 
-constexpr int kEightCtas = 16384;  // places that a cluster of 8 sorts, 16 where there are more
-constexpr size_t kSortSmem = (static_cast<size_t>(kSortWarps) * kDigits + 2 * kDigits + 32) * 4;
+// A cluster of 8 CTAs of 16 warps sorts up to kEightCtas places, 16 of them up to
+// kHalfCtas, 16 of 32 warps more (5467 places: 12 us with 32 warps, 11 so; 65536: 21
+// with 32, 22 with 16).
+constexpr int kEightCtas = 16384, kHalfCtas = 32768;
+constexpr size_t sort_smem_bytes(int warps) {
+  return (static_cast<size_t>(warps) * kDigits + 2 * kDigits + 32) * 4;
+}
 
 __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -489,8 +494,8 @@ __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t addr) {
   return v;
 }
 
-template <int kCtas>
-__global__ void __launch_bounds__(kSortThreads)
+template <int kCtas, int kSortWarps>
+__global__ void __launch_bounds__(kSortWarps * 32)
     embedding_sort_kernel(const SortArgs a) {
   extern __shared__ __align__(16) uint32_t sort_smem[];
   uint32_t* hist = sort_smem;                     // [warp][digit]
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kSortThreads)
     const uint32_t cta_begin = min(n, rank * per_cta), cta_end = min(n, cta_begin + per_cta);
     const uint32_t begin = min(cta_end, cta_begin + warp * per_warp);
     const uint32_t end = min(cta_end, begin + per_warp);
-    for (int i = tid; i < kSortWarps * kDigits / 4; i += kSortThreads)
+    for (int i = tid; i < kSortWarps * kDigits / 4; i += kSortWarps * 32)
       reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     // ~0u: takes no part (tokens are below 2^31)
@@ -1167,7 +1172,7 @@ int pieces_for(int dtype, int dtype_out, int64_t T, int64_t D, bool words) {
 }
 
 // Clusters of 16 are not portable: whether this device runs one, else 8 do.
-template <int kCtas>
+template <int kCtas, int kSortWarps>
 cudaError_t sort_config(cudaStream_t stream, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr) {
   static DeviceOnce configured;
   int dev = 0;
@@ -1180,38 +1185,38 @@ cudaError_t sort_config(cudaStream_t stream, cudaLaunchConfig_t* cfg, cudaLaunch
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg->gridDim = dim3(kCtas);
-  cfg->blockDim = dim3(kSortThreads);
-  cfg->dynamicSmemBytes = kSortSmem;
+  cfg->blockDim = dim3(kSortWarps * 32);
+  cfg->dynamicSmemBytes = sort_smem_bytes(kSortWarps);
   cfg->stream = stream;
   cfg->attrs = attr;
   cfg->numAttrs = 2;
   return static_cast<cudaError_t>(configured.get(
       dev,
       [&] {
-        cudaError_t r = cudaFuncSetAttribute(embedding_sort_kernel<kCtas>,
+        cudaError_t r = cudaFuncSetAttribute(embedding_sort_kernel<kCtas, kSortWarps>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(cfg->dynamicSmemBytes));
         if (r == cudaSuccess && kCtas > 8)
-          r = cudaFuncSetAttribute(embedding_sort_kernel<kCtas>,
+          r = cudaFuncSetAttribute(embedding_sort_kernel<kCtas, kSortWarps>,
                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         int fit = 1;
         if (r == cudaSuccess && kCtas > 8)
-          r = cudaOccupancyMaxActiveClusters(&fit, embedding_sort_kernel<kCtas>, cfg);
+          r = cudaOccupancyMaxActiveClusters(&fit, embedding_sort_kernel<kCtas, kSortWarps>, cfg);
         if (r == cudaSuccess && fit < 1) r = cudaErrorInvalidConfiguration;
         return static_cast<int>(r);
       },
       [](int r) { return r == static_cast<int>(cudaSuccess) ||
                        r == static_cast<int>(cudaErrorInvalidConfiguration); }));
 }
-template <int kCtas>
+template <int kCtas, int kSortWarps>
 cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg{};
-  const cudaError_t e = sort_config<kCtas>(stream, &cfg, attr);
-  if (e == cudaSuccess) return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<kCtas>, s);
+  const cudaError_t e = sort_config<kCtas, kSortWarps>(stream, &cfg, attr);
+  if (e == cudaSuccess) return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<kCtas, kSortWarps>, s);
   if (kCtas <= 8) return e;
   cudaGetLastError();
-  return launch_sort<(kCtas > 8 ? 8 : kCtas)>(s, stream);
+  return launch_sort<(kCtas > 8 ? 8 : kCtas), kSortWarps>(s, stream);
 }
 
 template <typename S, typename O, bool kAdd, int kPieces>
@@ -1270,8 +1275,9 @@ int grad_as(const Tokens& k, int64_t D, const void* dY, int64_t lddy, void* dW, 
   const cudaError_t e =
       g.ctas == 0 ? launch_kernel(embedding_rank_kernel, dim3(static_cast<unsigned>((k.T + 31) / 32)),
                                   dim3(kRankThreads), 0, stream, k, s.list[0], s.count)
-      : g.ctas == 8 ? launch_sort<8>(s, stream)
-                    : launch_sort<16>(s, stream);
+      : g.ctas == 8        ? launch_sort<8, 16>(s, stream)
+      : k.T <= kHalfCtas ? launch_sort<16, 16>(s, stream)
+                         : launch_sort<16, 32>(s, stream);
   int st = finish_launch(e, "embedding sort launch", stream);
   if (st != GEMM14_OK) return st;
   if (rest) {
