@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(kThreads)
 // Up to kRanked places: each place's position is counted, the places of a lower
 // token and the earlier ones of its own, T^2 comparisons over all SMs with no
 // exchange between them. A block has 32 places, a lane each, and a warp every
-// 32nd chunk of 32 tokens to compare them with. (A radix sort by one SM took
-// 7.5 us for 300 places and 18 for 8192, @RANK@.)
+// 32nd chunk of 32 tokens to compare them with. 5.5 us for 4096 places, where the
+// radix sort below takes 12; 13.8 for 8192, where it takes 12 too.
 constexpr int kRankThreads = 1024, kRanked = 4096;
 
 __global__ void __launch_bounds__(kRankThreads)
@@ -729,7 +729,8 @@ constexpr int kSumBlocks = 4;  // resident of an SM
 // and where sums are added to rows that are there (kAdd), the old words of a sum
 // that ends come with the row that ends it. (With the words in registers, 4 or 8
 // rows loaded and then added, 65536 places of 2048 columns, bf16 added to fp32,
-// took 165 us for 597 MB; @SUMADD@ so.)
+// took 165 us for 597 MB;
+// 97 so, 6.2 TB/s.)
 // kPieces: 16 bytes of dY's columns that a thread has; two where a row has enough
 // for a warp, as a row costs a thread some forty instructions whatever it moves.
 template <typename S, typename O, bool kAdd, int kPieces>
@@ -741,12 +742,24 @@ struct SumShape {
   static constexpr int kDepth = 49152 / kBytes < 8 ? 49152 / kBytes : 8;
   static constexpr int kSmem = kDepth * kBytes;
 };
+// Sums of the words that a thread adds, two values an instruction.
+__device__ __forceinline__ void add_pair(uint64_t& sum, float a, float b) {
+  asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}"
+      : "+l"(sum)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float2 pair(uint64_t sum) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(sum)),
+                     __uint_as_float(static_cast<uint32_t>(sum >> 32)));
+}
+
 template <typename S, typename O, bool kAdd, int kPieces>
 __global__ void __launch_bounds__(kThreads, kSumBlocks)
     embedding_sum_kernel(const GradArgs<S, O> a, const Ranges r, int64_t V) {
   using Q = SumShape<S, O, kAdd, kPieces>;
   constexpr int kWords = Q::kWords, kCols = Q::kCols, kDepth = Q::kDepth;
   extern __shared__ __align__(16) unsigned char sum_smem[];
+  __shared__ uint2 staged[kThreads * 2];  // two stages of places a lane
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t n = *r.count;
@@ -761,93 +774,120 @@ __global__ void __launch_bounds__(kThreads, kSumBlocks)
   unsigned char* rows = sum_smem + threadIdx.x * Q::kRowBytes;
   unsigned char* olds = sum_smem + kDepth * kWords * kThreads * Q::kRowBytes + threadIdx.x * 16;
   int left[kWords];  // columns of a word that there are
+  bool all_there = true;
 #pragma unroll
-  for (int w = 0; w < kWords; ++w)
+  for (int w = 0; w < kWords; ++w) {
     left[w] = static_cast<int>(max(int64_t(0), min(int64_t(kCols), a.D - c - w * apart)));
-  const auto fetch = [&](uint32_t i, const uint2& v, int at) {
-    if (i < length) {
-      const S* row = from + static_cast<int64_t>(v.y & ~kFlag) * a.lddy;
-      const bool ends = kAdd && (v.y & kFlag) && !(v.x & kFlag) && dev_check(index_ok(v.x, V), a.err);
-      const O* old = to + (ends ? v.x * a.lddw : 0);
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        if (left[w] == 0) break;
-        copy_async<Q::kRowBytes>(smem_u32(rows + (at * kWords + w) * kThreads * Q::kRowBytes),
-                                 row + w * apart, left[w] * static_cast<int>(sizeof(S)));
-        if (ends)
-          copy_async<16>(smem_u32(olds + (at * kWords + w) * kThreads * 16), old + w * apart,
-                         left[w] * static_cast<int>(sizeof(O)));
-      }
-    }
-    copy_commit();
-  };
-  const int stage = min(r.along, 32);
-  uint2 now = places_of(r, g, n, 0, stage), next = places_of(r, g, n, stage, stage);
-#pragma unroll 1
-  for (int i = 0; i < kDepth; ++i) fetch(i, from_lane(now, i, stage), i);
-  float sum[kWords][kCols] = {};
-  bool began_before = g.began_before;
-  int at = 0, j = 0;  // the ring's place, the stage's
-#pragma unroll 1
-  for (uint32_t i = 0; i < g.most; ++i) {
-    copy_wait<kDepth - 1>();
-    const uint2 v = from_lane(now, j, stage);
-    if (i < length) {
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        Pack<S, kCols> x;
-        x.raw = *reinterpret_cast<const decltype(x.raw)*>(rows + (at * kWords + w) * kThreads *
-                                                                     Q::kRowBytes);
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) sum[w][k] += to_f32(x.x[k]);
-      }
-      if (v.y & kFlag) {
-        const bool part = began_before || (v.x & kFlag);
-        float* s = began_before ? slot : slot + r.slot_ld;
-        if (c == 0 && part && !began_before) r.list[atomicAdd(r.count + 1, 1u)] = g.range;
-        const bool mine = !part && dev_check(index_ok(v.x, V), a.err);
-        O* row = to + (mine ? v.x * a.lddw : 0);
+    all_there = all_there && left[w] == kCols;
+  }
+  // places of the range, two stages of them in shared memory, the next in a register
+  const int stage = min(r.along, 32), in_stage = threadIdx.x & (stage - 1);
+  uint2* places = staged + (threadIdx.x & ~(stage - 1)) * 2;
+  const uint32_t ring = 2u * stage - 1u;
+  places[in_stage] = places_of(r, g, n, 0, stage);
+  places[stage + in_stage] = places_of(r, g, n, stage, stage);
+  uint2 next = places_of(r, g, n, 2 * stage, stage);
+  __syncwarp();
+
+  const auto run = [&](auto whole) {
+    constexpr bool kWhole_ = decltype(whole)::value;  // no word reaches past the columns
+    const auto fetch = [&](uint32_t i, int at) {
+      if (i < length) {
+        const uint2 v = places[i & ring];
+        const S* row = from + static_cast<int64_t>(v.y & ~kFlag) * a.lddy;
+        const bool ends = kAdd && (v.y & kFlag) && !(v.x & kFlag) && dev_check(index_ok(v.x, V), a.err);
+        const O* old = to + (ends ? v.x * a.lddw : 0);
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
-          if (left[w] == 0) break;
-          if (part) {
+          if (!kWhole_ && left[w] == 0) break;
+          copy_async<Q::kRowBytes>(smem_u32(rows + (at * kWords + w) * kThreads * Q::kRowBytes),
+                                   row + w * apart,
+                                   kWhole_ ? Q::kRowBytes : left[w] * static_cast<int>(sizeof(S)));
+          if (ends)
+            copy_async<16>(smem_u32(olds + (at * kWords + w) * kThreads * 16), old + w * apart,
+                           kWhole_ ? 16 : left[w] * static_cast<int>(sizeof(O)));
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kDepth; ++i) fetch(i, i);
+    uint64_t sum[kWords][kCols / 2] = {};  // two columns each
+    bool began_before = g.began_before;
+    int at = 0;  // the ring's place
+#pragma unroll 1
+    for (uint32_t i = 0; i < g.most; ++i) {
+      copy_wait<kDepth - 1>();
+      if (i < length) {
+        const uint2 v = places[i & ring];
 #pragma unroll
-            for (int k = 0; k < kCols; k += 4)
-              *reinterpret_cast<float4*>(s + w * apart + k) =
-                  make_float4(sum[w][k], sum[w][k + 1], sum[w][k + 2], sum[w][k + 3]);
-          } else if (mine) {
-            Pack<O, kCols> y, old;
-            if (kAdd)
-              old.raw = *reinterpret_cast<const decltype(old.raw)*>(olds + (at * kWords + w) *
-                                                                               kThreads * 16);
+        for (int w = 0; w < kWords; ++w) {
+          Pack<S, kCols> x;
+          x.raw = *reinterpret_cast<const decltype(x.raw)*>(rows + (at * kWords + w) * kThreads *
+                                                                       Q::kRowBytes);
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) {
-              const float p = a.scale * sum[w][k];
-              y.x[k] = from_f32<O>(kAdd ? fmaf(a.beta, to_f32(old.x[k]), p) : p);
+          for (int k = 0; k < kCols; k += 2) add_pair(sum[w][k / 2], to_f32(x.x[k]), to_f32(x.x[k + 1]));
+        }
+        if (v.y & kFlag) {
+          const bool part = began_before || (v.x & kFlag);
+          float* s = began_before ? slot : slot + r.slot_ld;
+          if (c == 0 && part && !began_before) r.list[atomicAdd(r.count + 1, 1u)] = g.range;
+          const bool mine = !part && dev_check(index_ok(v.x, V), a.err);
+          O* row = to + (mine ? v.x * a.lddw : 0);
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            if (!kWhole_ && left[w] == 0) break;
+            float p[kCols];
+#pragma unroll
+            for (int k = 0; k < kCols; k += 2) {
+              const float2 two = pair(sum[w][k / 2]);
+              p[k] = two.x;
+              p[k + 1] = two.y;
+              sum[w][k / 2] = 0;
             }
-            if (left[w] == kCols) {
-              *reinterpret_cast<decltype(y.raw)*>(row + w * apart) = y.raw;
-            } else {
+            if (part) {
 #pragma unroll
-              for (int k = 0; k < kCols; ++k)
-                if (k < left[w]) row[w * apart + k] = y.x[k];
+              for (int k = 0; k < kCols; k += 4)
+                *reinterpret_cast<float4*>(s + w * apart + k) =
+                    make_float4(p[k], p[k + 1], p[k + 2], p[k + 3]);
+            } else if (mine) {
+              Pack<O, kCols> y;
+              if (kAdd) {
+                y.raw = *reinterpret_cast<const decltype(y.raw)*>(olds + (at * kWords + w) * kThreads * 16);
+#pragma unroll
+                for (int k = 0; k < kCols; ++k)
+                  y.x[k] = from_f32<O>(a.beta == 1.0f ? fmaf(a.scale, p[k], to_f32(y.x[k]))
+                                                      : fmaf(a.beta, to_f32(y.x[k]), a.scale * p[k]));
+              } else {
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) y.x[k] = from_f32<O>(a.scale * p[k]);
+              }
+              if (kWhole_ || left[w] == kCols) {
+                *reinterpret_cast<decltype(y.raw)*>(row + w * apart) = y.raw;
+              } else {
+#pragma unroll
+                for (int k = 0; k < kCols; ++k)
+                  if (k < left[w]) row[w * apart + k] = y.x[k];
+              }
             }
           }
-#pragma unroll
-          for (int k = 0; k < kCols; ++k) sum[w][k] = 0.0f;
+          began_before = false;
         }
-        began_before = false;
+      }
+      fetch(i + kDepth, at);
+      at = at + 1 == kDepth ? 0 : at + 1;
+      if (((i + 1) & (stage - 1)) == 0) {  // a stage is done: the one after the next takes its place
+        __syncwarp();
+        places[(i & ring & ~(stage - 1)) + in_stage] = next;
+        next = places_of(r, g, n, i + 1 + 2 * stage, stage);
+        __syncwarp();
       }
     }
-    const int ahead = j + kDepth;
-    fetch(i + kDepth, ahead < stage ? from_lane(now, ahead, stage) : from_lane(next, ahead - stage, stage), at);
-    at = at + 1 == kDepth ? 0 : at + 1;
-    if (++j == stage) {
-      j = 0;
-      now = next;
-      next = places_of(r, g, n, i + 1 + stage, stage);
-    }
-  }
+  };
+  if (__all_sync(0xffffffffu, all_there))
+    run(std::true_type());
+  else
+    run(std::false_type());
 }
 
 // Rows of dY or dW at any address, the same way: a thread copies the aligned word
@@ -855,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, kSumBlocks)
 // last lane copies a second one). A row of dW is moved a value a lane, side by side,
 // from sums that the warp's lanes hand each other through shared memory. (With two
 // words a lane loaded and shifted and 8 or 4 values of dW a lane moved one by one,
-// 18826 places of 1258 columns, bf16, took 40 us of the kernel, @ANY@ so.)
+// 18826 places of 1258 columns, bf16, took 40 us, 27 so.)
 struct AnyShape {
   static constexpr int kDepth = 8;
   static constexpr int kWords = kThreads + kThreads / 8;  // of a row; groups have 8 lanes at least

@@ -393,7 +393,8 @@ __device__ __forceinline__ void finish_each(const Parts<kN>& t, const Finish& f,
 // aligned ones of the output, stored at once; the source's word, where it does not
 // start on 16 bytes, is read as two and a shift. kEach of them are in flight.
 // (16 bytes of fp32 output a piece, 8 of a 16-bit source, took 207 us for 109 packed
-// fp16 tensors of 197 million values, @SCALE@ so.)
+// fp16 tensors of 197 million values, 193
+// so.)
 // Products are rounded to fp32 and then to a 16-bit type: within half a step and
 // 2^-24 of the value.
 template <typename O, int kPer>
