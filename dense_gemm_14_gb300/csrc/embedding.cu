@@ -729,8 +729,8 @@ constexpr int kSumBlocks = 4;  // resident of an SM
 // and where sums are added to rows that are there (kAdd), the old words of a sum
 // that ends come with the row that ends it. (With the words in registers, 4 or 8
 // rows loaded and then added, 65536 places of 2048 columns, bf16 added to fp32,
-// took 165 us for 597 MB;
-// 87 so, 6.9 TB/s.)
+// took 165 us for 597 MB; 95
+// so, 6.3 TB/s.)
 // kPieces: 16 bytes of dY's columns that a thread has; two where a row has enough
 // for a warp, as a row costs a thread some forty instructions whatever it moves.
 template <typename S, typename O, bool kAdd, int kPieces>

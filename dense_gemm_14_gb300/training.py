@@ -321,9 +321,11 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
     if table.numel() == 0:
         raise ValueError(f"table must not be empty, got shape {tuple(table.shape)}")
     if stream is None and index == _current_device():  # (the time of a lookup of few tokens is the host's)
-        return _lookup(_current_stream(index), code, out_code, table, ldw, tokens, size, ignore_index, scale, dtype)
+        return _lookup(_current_stream(index), code, out_code, table, ldw, tokens, size, ignore_index,
+                       scale, dtype)
     return _on(stream, table.device,
-               lambda handle: _lookup(handle, code, out_code, table, ldw, tokens, size, ignore_index, scale, dtype))
+               lambda handle: _lookup(handle, code, out_code, table, ldw, tokens, size, ignore_index,
+                                      scale, dtype))
 
 
 def _lookup(handle, code, out_code, table, ldw, tokens, size, ignore_index, scale, dtype):
@@ -332,8 +334,8 @@ def _lookup(handle, code, out_code, table, ldw, tokens, size, ignore_index, scal
     out = torch.empty((*tokens.shape, D), dtype=dtype, device=table.device)
     if T:
         status = _lib.load().gemm14_embedding_forward(code, out_code, T, V, D, table.data_ptr(), ldw,
-                                                      tokens.data_ptr(), size, ignore_index, scale,
-                                                      out.data_ptr(), D, handle)
+                                                      tokens.data_ptr(), size, int(ignore_index),
+                                                      float(scale), out.data_ptr(), D, handle)
         if status:
             raise _lib.Gemm14Error(status, "gemm14_embedding_forward")
     return out
@@ -387,8 +389,8 @@ def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None 
     def body(handle):
         dw = out if out is not None else torch.empty((V, D), dtype=dtype, device=device)
         fn = _lib.load().gemm14_embedding_backward
-        args = (code, out_code, T, V, D, _ptr(dy), lddy, _ptr(tokens), size, ignore_index, scale,
-                beta, dw.data_ptr(), lddw)
+        args = (code, out_code, T, V, D, _ptr(dy), lddy, _ptr(tokens), size, int(ignore_index),
+                float(scale), float(beta), dw.data_ptr(), lddw)
         if T <= _FEW_TOKENS and not _lib.embedding_backward_workspace_bytes(code, T, V, D):
             status = fn(*args, None, 0, handle)
             if status:
@@ -495,7 +497,7 @@ def grad_norm(grads, scale: float = 1.0, each: bool = False, stream=None):
         grads = GradList(grads)
     if not math.isfinite(scale):
         raise ValueError(f"scale must be finite, got {scale}")
-    n, args = len(grads._tensors), grads._args
+    n, args, scale = len(grads._tensors), grads._args, float(scale)
     fn = _lib.load().gemm14_grad_norm
     return _grad_call(grads, each, stream,
                       lambda norm, norms, ws, b, handle: fn(n, args, scale, norm, norms, ws, b, handle),
@@ -530,6 +532,7 @@ def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, out=None, each: b
                                      f"does not fit its gradient ({x.dtype} {tuple(x.shape)}, "
                                      f"{x.stride()})")
     n, args, out_args = len(grads._tensors), grads._args, None if out is None else out._args
+    scale, max_norm = float(scale), float(max_norm)
     fn = _lib.load().gemm14_grad_clip
     return _grad_call(grads, each, stream,
                       lambda norm, norms, ws, b, handle: fn(n, args, out_args, scale, max_norm, norm,

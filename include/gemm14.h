@@ -620,8 +620,8 @@ int gemm14_set_pair_kernel(int enable);
  * block and cluster barriers, with no mbarrier wait to expire: a call that
  * runs on it consumes the request and computes C as usual; so do
  * gemm14_linear_ce_* calls of fp32 rows that run on the CUDA cores and
- * gemm14_ckpt8_wgrad calls of up to 16 rows. (gemm14_ckpt8_save and _restore wait for nothing and leave the
- * request to the next call.)
+ * gemm14_ckpt8_wgrad calls of up to 16 rows. (gemm14_ckpt8_save and _restore, gemm14_embedding_* and
+ * gemm14_grad_* wait for nothing but barriers and leave the request to the next call.)
  * Returns GEMM14_ERR_INVALID_ARG for an unknown mode.
  */
 int gemm14_debug_inject(int fault, uint64_t wait_limit_ns);
