@@ -76,8 +76,10 @@ __host__ __device__ inline int type_bytes(int type) { return type == GEMM14_DTYP
 __host__ __device__ inline int unit_shift(int type) { return type == GEMM14_DTYPE_F32 ? 10 : 11; }
 __host__ __device__ inline int64_t unit_values(int type) { return int64_t(1) << unit_shift(type); }
 static_assert((4 << 10) == kUnitBytes && (2 << 11) == kUnitBytes, "a unit's values");
-// Units of a row (its first may begin up to 7 elements before an aligned word),
-// and the rows that share a unit.
+// Units of a row of several (its first may begin up to 7 elements before an aligned
+// word) and of a dense tensor (up to 63, before a line of 128 bytes: loads that
+// straddle lines took 73 us for 109 packed tensors of 394 MB, 71 so), and the rows
+// that share a unit.
 __host__ __device__ inline int64_t row_units(int64_t cols, int type) {
   return (cols + 7 + unit_values(type) - 1) >> unit_shift(type);
 }
@@ -86,6 +88,7 @@ __host__ __device__ inline int64_t unit_rows(int64_t cols, int type) {
   return r > 1 ? r : 1;
 }
 __host__ inline int64_t entry_units(const Entry& e) {
+  if (e.rows == 1) return row_units(e.cols + 56, e.type);
   const int64_t u = row_units(e.cols, e.type);
   return u > 1 ? e.rows * u : (e.rows + unit_rows(e.cols, e.type) - 1) / unit_rows(e.cols, e.type);
 }
@@ -113,6 +116,12 @@ struct Unit {
   int64_t row, part;
   int rows;
 };
+// Elements between the boundary that units are counted from and a row's first.
+template <typename T>
+__device__ __forceinline__ int before_of(const Entry& e, const T* row, int bytes) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(row) & ((e.rows == 1 ? 128 : bytes) - 1)) /
+         static_cast<int>(sizeof(T));
+}
 __device__ __forceinline__ Unit unit_of(const Entry& e, uint32_t u) {
   if (e.rows == 1) return Unit{0, u, 1};
   const int64_t per = row_units(e.cols, e.type);
@@ -180,8 +189,7 @@ __device__ __forceinline__ void add_unit(double& sum, const Entry& e, const Unit
   constexpr int kPer = 16 / static_cast<int>(sizeof(S));
   const S* row = static_cast<const S*>(e.src) + u.row * e.ld_src;
   if (u.rows == 1) {
-    const int before =
-        static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / static_cast<int>(sizeof(S));
+    const int before = before_of(e, row, 16);
     const int64_t from = u.part * unit_values(e.type) - before;
     if (from >= 0 && from + unit_values(e.type) <= e.cols) {  // a whole unit
       const uint4* at = reinterpret_cast<const uint4*>(row + from) + lane;
@@ -203,8 +211,7 @@ __device__ __forceinline__ void add_unit(double& sum, const Entry& e, const Unit
   const int along = lanes_along(u, e.cols, kPer), lx = lane & (along - 1);
   for (int r = lane / along; r < u.rows; r += 32 / along) {
     const S* at = row + r * e.ld_src;
-    const int before =
-        static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u) / static_cast<int>(sizeof(S));
+    const int before = before_of(e, at, 16);
     const int64_t from = u.part * unit_values(e.type) - before;
     const int64_t c0 = from + lx * kPer, c1 = min(from + unit_values(e.type), e.cols);
     float s = 0.0f;
@@ -439,14 +446,13 @@ __device__ __forceinline__ void scale_whole(const S* src, O* dst, int lane, floa
 template <typename S, typename O>
 __device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int lane, float f) {
   constexpr int kPer = 16 / static_cast<int>(sizeof(S));
-  constexpr uintptr_t kOut = kPer * sizeof(O) - 1;
+  constexpr int kOut = kPer * static_cast<int>(sizeof(O));
   const S* begin = static_cast<const S*>(e.src);
   const S* end = begin + (e.rows - 1) * e.ld_src + e.cols;
   const S* src = begin + u.row * e.ld_src;
   O* dst = static_cast<O*>(e.dst) + u.row * e.ld_dst;
   if (u.rows == 1) {
-    const int before =
-        static_cast<int>(reinterpret_cast<uintptr_t>(dst) & kOut) / static_cast<int>(sizeof(O));
+    const int before = before_of(e, dst, kOut);
     const int64_t from = u.part * unit_values(e.type) - before;
     if (from >= 0 && from + unit_values(e.type) <= e.cols) {
       if ((reinterpret_cast<uintptr_t>(src + from) & 15u) == 0) {
@@ -464,8 +470,7 @@ __device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int la
   for (int r = lane / along; r < u.rows; r += 32 / along) {
     const S* x = src + r * e.ld_src;
     O* y = dst + r * e.ld_dst;
-    const int before =
-        static_cast<int>(reinterpret_cast<uintptr_t>(y) & kOut) / static_cast<int>(sizeof(O));
+    const int before = before_of(e, y, kOut);
     const int64_t from = u.part * unit_values(e.type) - before;
     const int64_t c1 = min(from + unit_values(e.type), e.cols);
     const bool words = (reinterpret_cast<uintptr_t>(x + from) & 15u) == 0;
