@@ -620,11 +620,10 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 // ---- sums over ranges of the sorted places
 
 // A group of `along` threads takes one range of the sorted places and a slice of
-// the columns, kPer of them a thread (16 bytes of dY's type), kRowsAhead rows in
-// flight. A token of up to kWhole places is one range's, the one where it begins;
-// the sum of a longer one may lie in several: what a range holds of a sum that
-// began before it, or goes on behind it, goes to the range's first or second slot,
-// and the range where it began goes on a list for the join.
+// the columns. A token of up to kWhole places is one range's, the one where it
+// begins; the sum of a longer one may lie in several: what a range holds of a sum
+// that began before it, or goes on behind it, goes to the range's first or second
+// slot, and the range where it began goes on a list for the join.
 struct Ranges {
   const uint2* place;  // sorted: token, place
   uint32_t* count;     // places, and long sums
@@ -729,8 +728,8 @@ constexpr int kSumBlocks = 4;  // resident of an SM
 // and where sums are added to rows that are there (kAdd), the old words of a sum
 // that ends come with the row that ends it. (With the words in registers, 4 or 8
 // rows loaded and then added, 65536 places of 2048 columns, bf16 added to fp32,
-// took 165 us for 597 MB; 95
-// so, 6.3 TB/s.)
+// took 165 us for 597 MB; 95 so,
+// 6.3 TB/s.)
 // kPieces: 16 bytes of dY's columns that a thread has; two where a row has enough
 // for a warp, as a row costs a thread some forty instructions whatever it moves.
 template <typename S, typename O, bool kAdd, int kPieces>
