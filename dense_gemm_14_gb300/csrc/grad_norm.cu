@@ -302,7 +302,7 @@ struct Finish {
   float scale, max_norm;
   float* norm;         // written by the last launch
   float* each;         // of this launch's tensors, or NULL
-  float* factor;       // for the scaling, or NULL
+  double* factor;      // for the scaling, or NULL
 };
 
 // The root of s >= 0 (or NaN, infinite): sqrtf of s brought to [1, 4) by a power of
@@ -361,10 +361,12 @@ __device__ __forceinline__ double load_cluster_f64(uint32_t addr) {
 }
 
 // The norm of a sum of squares, and the factor that the gradients are scaled by.
-__device__ __forceinline__ float factor_of(const Finish& f, double squares, double* norm) {
+// (The norm of finite values is finite here, and clips, also where fp32 has no number
+// for it.)
+__device__ __forceinline__ double factor_of(const Finish& f, double squares, double* norm) {
   *norm = root(squares) * fabs(static_cast<double>(f.scale));
   const bool over = *norm > static_cast<double>(f.max_norm) && *norm - *norm == 0.0;
-  return over ? static_cast<float>(f.scale * (f.max_norm / *norm)) : f.scale;
+  return over ? f.scale * (f.max_norm / *norm) : f.scale;
 }
 
 // The norm and the factor, by the first kFinishThreads threads of each CTA of a
@@ -390,7 +392,7 @@ __device__ __forceinline__ void finish_total(const Finish& f, uint32_t slots, do
       f.totals[f.launch] = total;
       if (f.last) {
         double norm;
-        const float factor = factor_of(f, all, &norm);
+        const double factor = factor_of(f, all, &norm);
         *f.norm = static_cast<float>(norm);
         if (f.factor) *f.factor = factor;
       }
@@ -539,11 +541,56 @@ __device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int la
   }
 }
 
+// A factor below fp32's normal numbers has fewer than 24 bits there, or is 0, while
+// its products with large values are normal numbers: it is multiplied in fp64, an
+// element at a time. Limits some 2^126 below the norm alone come here, so it stays out
+// of the others' registers. (100 fp32 tensors of 419 MB into others, values of 1e37: 1051 us
+// a call, 529 with a factor of 1e-11.)
+__device__ __forceinline__ bool small_factor(double by) {
+  const float f = static_cast<float>(by);
+  return fabsf(f) < 0x1p-126f && static_cast<double>(f) != by;
+}
+template <typename S, typename O>
+__device__ __forceinline__ void scale_small_as(const S* src, O* dst, int64_t n, int lane, double by) {
+  for (int64_t c = lane; c < n; c += 32)
+    dst[c] = from_f32<O>(static_cast<float>(by * static_cast<double>(to_f32(src[c]))));
+}
+__device__ __noinline__ void scale_small(const void* src, void* dst, int type, int dst_type,
+                                         int64_t n, int lane, double by) {
+  if (type == GEMM14_DTYPE_BF16) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(src);
+    if (dst_type == GEMM14_DTYPE_F32)
+      scale_small_as(x, static_cast<float*>(dst), n, lane, by);
+    else
+      scale_small_as(x, static_cast<__nv_bfloat16*>(dst), n, lane, by);
+  } else if (type == GEMM14_DTYPE_F16) {
+    const __half* x = static_cast<const __half*>(src);
+    if (dst_type == GEMM14_DTYPE_F32)
+      scale_small_as(x, static_cast<float*>(dst), n, lane, by);
+    else
+      scale_small_as(x, static_cast<__half*>(dst), n, lane, by);
+  } else {
+    scale_small_as(static_cast<const float*>(src), static_cast<float*>(dst), n, lane, by);
+  }
+}
+// (Units are counted from a row's first element here, whatever its address: they are
+// enough for that, and those left over are empty.)
+__device__ __forceinline__ void scale_small_unit(const Entry& e, const Unit& u, int lane, double by) {
+  const int64_t lo = min(e.cols, u.part * unit_values(e.type));
+  const int64_t n = min(e.cols - lo, unit_values(e.type));
+  for (int64_t r = u.row; r < u.row + u.rows; ++r)
+    scale_small(static_cast<const char*>(e.src) + (r * e.ld_src + lo) * type_bytes(e.type),
+                static_cast<char*>(e.dst) + (r * e.ld_dst + lo) * type_bytes(e.dst_type), e.type,
+                e.dst_type, n, lane, by);
+}
+
 // Every warps-th unit from the last down, so that the units at work at any time lie
 // side by side: reads and writes of one stretch of memory each.
 template <int kN>
 __device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint32_t warps,
-                                            int lane, float f) {
+                                            int lane, double by) {
+  const float f = static_cast<float>(by);
+  const bool small = small_factor(by);
   int i = t.n - 1;
   for (uint32_t left = t.units - w; left > 0; left = left > warps ? left - warps : 0u) {
     const uint32_t u = left - 1u;
@@ -551,7 +598,9 @@ __device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint
     const Entry& e = t.e[i];
     if (e.src == e.dst && f == 1.0f) continue;  // nothing changes
     const Unit at = unit_of(e, u - e.first_unit);
-    if (e.type == GEMM14_DTYPE_BF16) {
+    if (small) {
+      scale_small_unit(e, at, lane, by);
+    } else if (e.type == GEMM14_DTYPE_BF16) {
       if (e.dst_type == GEMM14_DTYPE_F32)
         scale_unit<__nv_bfloat16, float>(e, at, lane, f);
       else
@@ -590,13 +639,13 @@ __global__ void __launch_bounds__(kFinishThreads)
 
 template <int kN>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-    grad_scale_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, const float* factor) {
+    grad_scale_kernel(const __grid_constant__ Table<kN> t, uint32_t warps, const double* factor) {
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const float f = *factor;
-  if (t.in_place && f == 1.0f) return;  // nothing changes
-  if (w < warps) scale_units(t, w, warps, threadIdx.x & 31, f);
+  const double by = *factor;
+  if (t.in_place && static_cast<float>(by) == 1.0f) return;  // nothing changes
+  if (w < warps) scale_units(t, w, warps, threadIdx.x & 31, by);
 }
 
 // The scaling of a list of few units: each block forms the total itself, which costs
@@ -610,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                             const Finish f) {
   static_assert(kThreads == kFinishThreads, "a block forms the total");
   __shared__ double smem[kFinishThreads / 32 + 1];
-  __shared__ float factor;
+  __shared__ double factor;
   grid_dependency_wait();
   grid_launch_dependents();
   const double total =
@@ -622,8 +671,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   }
   if (f.each) finish_each(parts, f, blockIdx.x, gridDim.x, smem);
   __syncthreads();
-  const float by = factor;
-  if (t.in_place && by == 1.0f) return;  // nothing changes
+  const double by = factor;
+  if (t.in_place && static_cast<float>(by) == 1.0f) return;  // nothing changes
   const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (w < warps) scale_units(t, w, warps, threadIdx.x & 31, by);
 }
@@ -827,7 +876,7 @@ Finish finish_of(const Call& c, int64_t i0, int n, int launch) {
   f.max_norm = c.max_norm;
   f.norm = c.norm;
   f.each = c.each ? c.each + i0 : nullptr;
-  f.factor = c.clip ? reinterpret_cast<float*>(c.ws + c.l.factor) : nullptr;
+  f.factor = c.clip ? reinterpret_cast<double*>(c.ws + c.l.factor) : nullptr;
   return f;
 }
 
@@ -902,7 +951,7 @@ int scale_launch(const Call& c, int64_t i0) {
   const uint32_t warps = fill(c, i0, most_warps(c.sms), kThreads / 32, &t);
   return finish_launch(launch_kernel(grad_scale_kernel<kN>, blocks_for(warps), dim3(kThreads), 0,
                                      c.stream, t, warps,
-                                     reinterpret_cast<const float*>(c.ws + c.l.factor)),
+                                     reinterpret_cast<const double*>(c.ws + c.l.factor)),
                        "gradient scaling launch", c.stream);
 }
 

@@ -536,7 +536,8 @@ int gemm14_grad_norm(int64_t n, const gemm14_tensor* grads, float scale, float* 
  *     out = f g,   f = scale * min(1, max_norm / N),
  * written over them (out NULL) or into n tensors of the same sizes, each of its
  * gradient's dtype or F32. The factor is worked out on the device, in fp64, and
- * held in fp32; products are fp32, rounded to the output's type. A norm that is
+ * held in fp32 (in fp64 where it is below fp32's normal numbers); products are fp32,
+ * rounded to the output's type. A norm that is
  * infinite or NaN clips nothing: f = scale, and *norm says so. f == 1 in place:
  * nothing is written. max_norm >= 0 (infinity: only scale).
  * What is written must share no element with any other tensor of the lists (the

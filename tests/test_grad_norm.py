@@ -244,6 +244,35 @@ def test_a_norm_that_is_no_number_clips_nothing(value):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1.0, -0.25])
+@pytest.mark.parametrize("dtype,out,size,limits", [
+    ("f32", "f32", 1e37, (1e-3, 1e-7)), ("bf16", "bf16", 1e37, (1e-3, 1e-7)), ("bf16", "f32", 1e37, (1e-3, 1e-7)),
+    ("f32", "f32", 3.0, (1e-37, 1e-40)), ("f16", "f32", 1e4, (1e-33, 1e-38))])
+@pytest.mark.parametrize("shapes", [[(300,), (7,)], [(600001,), (17, 33)], [(400, 30)] * 90],
+                         ids=["one launch", "two launches", "long"])
+def test_factors_below_the_normal_numbers(shapes, dtype, out, size, limits, scale):
+    """A limit so far below the norm that fp32 does not hold the factor to 24 bits, or at all: the
+    bounds are those of any other factor. Rows of a pitch and unaligned ones among them."""
+    xs, _ = tensors_of(shapes, [dtype], len(shapes), 3, 1)
+    xs.append(torch.ones(40, 70, dtype=DT[dtype], device="cuda")[:, 1:67])
+    for x in xs:
+        x.copy_(x.float().clamp(-4, 4) * size)
+    true = abs(scale) * math.sqrt(math.fsum(squares(x) for x in xs))
+    for limit in limits:
+        assert abs(scale) * f32(limit) / true < 2.0 ** -126
+        ys = [torch.full_like(x, math.nan, dtype=DT[out]) for x in xs]
+        norm = g14.clip_grad_norm(xs, limit, scale=scale, out=ys)
+        norm_check(norm, true)
+        for y, x in zip(ys, xs):
+            out_check(y, x, factor_of(true, limit, scale))
+    if dtype == out:
+        olds = [x.clone() for x in xs]
+        g14.clip_grad_norm(xs, limits[0], scale=scale)
+        for x, old in zip(xs, olds):
+            out_check(x, old, factor_of(true, limits[0], scale))
+
+
+@pytest.mark.gpu
 def test_limits():
     x = torch.randn(1000, device="cuda")
     old, true = x.clone(), math.sqrt(squares(x))
