@@ -509,9 +509,11 @@ def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, out=None, each: b
     """Scales grads (a GradList or a sequence of tensors) by scale * min(1, max_norm
     / norm), in place or into out (as many tensors of the same shapes and strides,
     each of its gradient's dtype or float32), and returns the norm, as grad_norm
-    does, of before (gemm14_grad_clip). scale takes gradients out of a loss scale. A
-    norm that is infinite or NaN clips nothing: out = scale * grads, for the caller
-    to leave alone. No tensor that is written may share memory with another of the
+    does, of before (gemm14_grad_clip). scale takes gradients out of a loss scale. Where
+    an element is infinite or NaN, so is the norm, and nothing is clipped: out =
+    scale * grads, for the caller to leave alone. Finite elements are clipped always,
+    also where their norm is beyond float32's largest number and so returned as
+    infinite. No tensor that is written may share memory with another of the
     lists. Nothing is copied to the host."""
     if not isinstance(grads, GradList):
         grads = GradList(grads)

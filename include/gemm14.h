@@ -523,7 +523,8 @@ typedef struct gemm14_tensor {
  * returns. scale: out of a loss scale, 1 / it. Squares are summed in fp32 over at
  * most 64 values, those sums in fp64, and values whose squares fp32 does not hold
  * are squared in fp64: values of any size add what they should. A call repeats bit
- * for bit. Infinities give an infinite norm, NaN gives NaN. n == 0: *norm = 0.
+ * for bit. Infinities give an infinite norm (so does a norm beyond fp32's largest
+ * number), NaN gives NaN. n == 0: *norm = 0.
  * n at most 2^20; scale must be finite.
  * workspace: caller-owned, 16-byte aligned, gemm14_grad_workspace_bytes(n, ...)
  * bytes at least; its contents do not matter, and one kept for other calls serves.
@@ -537,9 +538,11 @@ int gemm14_grad_norm(int64_t n, const gemm14_tensor* grads, float scale, float* 
  * written over them (out NULL) or into n tensors of the same sizes, each of its
  * gradient's dtype or F32. The factor is worked out on the device, in fp64, and
  * held in fp32 (in fp64 where it is below fp32's normal numbers); products are fp32,
- * rounded to the output's type. A norm that is
- * infinite or NaN clips nothing: f = scale, and *norm says so. f == 1 in place:
- * nothing is written. max_norm >= 0 (infinity: only scale).
+ * rounded to the output's type. Where an element is infinite or NaN nothing is
+ * clipped: f = scale, and *norm, infinite or NaN, says so. Where all are finite N is
+ * finite, and clips, also beyond fp32's largest number, where *norm is infinite for
+ * want of another. f == 1 in place: nothing is written. max_norm >= 0 (infinity: only
+ * scale).
  * What is written must share no element with any other tensor of the lists (the
  * same tensor twice in a list is GEMM14_ERR_INVALID_ARG; an output may be its own
  * gradient, with the same layout).

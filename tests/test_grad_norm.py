@@ -244,6 +244,22 @@ def test_a_norm_that_is_no_number_clips_nothing(value):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [50, 600001, 5000001])  # one launch, two, three for the clipping
+def test_finite_elements_are_clipped_where_their_norm_is_beyond_fp32(n):
+    x = torch.full((n,), 3e38, device="cuda")
+    true = math.sqrt(squares(x))
+    assert true > torch.finfo(torch.float32).max
+    y = torch.empty_like(x)
+    norm, each = g14.clip_grad_norm([x], 2.0, out=[y], each=True)
+    assert norm == math.inf and each[0] == math.inf and g14.grad_norm([x]) == math.inf
+    out_check(y, x, 2.0 / true)
+    # the same norm for an element that is infinite: nothing is clipped
+    x[n // 2] = math.inf
+    assert g14.clip_grad_norm([x], 2.0, scale=0.5, out=[y]) == math.inf
+    assert torch.equal(y, x * 0.5)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [1.0, -0.25])
 @pytest.mark.parametrize("dtype,out,size,limits", [
     ("f32", "f32", 1e37, (1e-3, 1e-7)), ("bf16", "bf16", 1e37, (1e-3, 1e-7)), ("bf16", "f32", 1e37, (1e-3, 1e-7)),
