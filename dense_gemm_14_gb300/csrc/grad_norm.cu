@@ -760,14 +760,16 @@ struct Span {
   bool written;
   int64_t i;
 };
-// Whether two tensors whose spans cross share an element: not where both are
-// columns of one matrix (rows of one pitch) and their columns lie apart.
+// Whether two tensors whose spans cross share an element: not where the second lies
+// between the first's rows, in one row or in several of the same pitch (columns of
+// one matrix). Rows of another pitch between them count as shared.
 bool share_elements(const Span& a, const Span& b) {
   const gemm14_tensor &x = *a.g, &y = *b.g;
   const int size = type_bytes(x.dtype);
-  if (x.rows <= 1 || y.rows <= 1 || x.ld * size != y.ld * type_bytes(y.dtype)) return true;
+  if (x.rows <= 1 || (y.rows > 1 && x.ld * size != y.ld * type_bytes(y.dtype))) return true;
   const int64_t pitch = x.ld * size, wide_x = x.cols * size, wide_y = y.cols * type_bytes(y.dtype);
-  const int64_t off = static_cast<int64_t>(b.begin - a.begin) % pitch;  // b begins no earlier
+  // b begins no earlier, and where it begins behind a row that is not a's last
+  const int64_t off = static_cast<int64_t>(b.begin - a.begin) % pitch;
   return off < wide_x || off + wide_y > pitch;
 }
 // What is written may share no element with anything else of the lists, its own source aside.

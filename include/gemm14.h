@@ -545,7 +545,9 @@ int gemm14_grad_norm(int64_t n, const gemm14_tensor* grads, float scale, float* 
  * scale).
  * What is written must share no element with any other tensor of the lists (the
  * same tensor twice in a list is GEMM14_ERR_INVALID_ARG; an output may be its own
- * gradient, with the same layout).
+ * gradient, with the same layout). Tensors may lie between another's rows: a single
+ * row, or rows of the same pitch in bytes; of another pitch they are refused. Each
+ * pair of n such columns of a matrix is looked at on the host.
  */
 int gemm14_grad_clip(int64_t n, const gemm14_tensor* grads, const gemm14_tensor* out, float scale,
                      float max_norm, float* norm, float* each, void* workspace,

@@ -427,6 +427,46 @@ def test_memory_that_is_not_shared_passes(grads, outs):
     assert "share memory" not in g14.last_error_string() or st != g14.GEMM14_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("grads,outs,shared", [
+    ([(P, 10, 20, 64, 1), (P + 40, 1, 44, 44, 1)], None, False),      # a row behind a row of columns, up to the next
+    ([(P, 10, 20, 64, 1), (P + 40, 1, 44, 7, 1)], None, False),       # (one row has no pitch)
+    ([(P, 10, 20, 64, 1), (P + 8 * 128 + 42, 1, 43, 43, 1)], None, False),  # behind the last row but one
+    ([(P, 10, 20, 64, 1), (P + 9 * 128 + 40, 1, 500, 500, 1)], None, False),  # behind the last
+    ([(P + 128, 10, 20, 64, 1), (P, 1, 64, 64, 1)], None, False),     # before the first
+    ([(P, 10, 20, 64, 1), (P + 40, 1, 22, 22, 0)], None, False),      # of another type
+    ([(P, 10, 20, 64, 1), (P + 38, 1, 4, 4, 1)], None, True),         # from a row's last element
+    ([(P, 10, 20, 64, 1), (P + 40, 1, 45, 45, 1)], None, True),       # into the next row
+    ([(P, 10, 20, 64, 1), (P + 40, 1, 1000, 1000, 1)], None, True),   # over several
+    ([(P, 10, 20, 64, 1), (P + 9 * 128 + 38, 1, 4, 4, 1)], None, True),  # the last row's last element
+    ([(P + 126, 10, 20, 64, 1), (P, 1, 64, 64, 1)], None, True),      # before the first, and its first
+    ([(P, 1, 100, 100, 1), (P + 150, 3, 5, 64, 1)], None, True),      # rows that begin within a single one
+    ([(P, 10, 20, 64, 1), (P + 40, 10, 20, 128, 1)], None, True),     # another pitch is refused
+    ([(P, 10, 20, 64, 1)], [(Q, 10, 20, 64, 0)], False),
+    ([(P, 10, 20, 64, 1), (P + 40, 1, 44, 44, 1)], [(Q, 10, 20, 64, 1), (P + 168, 1, 44, 44, 1)], False),
+    ([(P, 10, 20, 64, 1), (P + 40, 1, 44, 44, 1)], [(Q, 10, 20, 64, 1), (P + 160, 1, 44, 44, 1)], True)])
+def test_a_row_between_rows(grads, outs, shared):
+    """(Without a GPU a call that passes ends at the device, with one at its workspace.)"""
+    g14.grad_clip_raw(1, args_of(GOOD), args_of((P, 4, 7, 8, 1)), 1.0, 1.0, P, None, P, 0, check=False)
+    assert "share memory" not in g14.last_error_string()
+    st = g14.grad_clip_raw(len(grads), args_of(*grads), args_of(*outs) if outs else None, 1.0, 1.0, P + 0x100000, None,
+                           None, 0, check=False)
+    assert st != g14.GEMM14_OK and ("share memory" in g14.last_error_string()) == shared
+
+
+@pytest.mark.gpu
+def test_a_row_beside_columns_is_clipped():
+    """A matrix's first columns and, in the same memory, a vector behind one of its rows."""
+    for pick in (slice(0, 1), slice(4, 5), slice(39, 40)):
+        x = torch.randn(40, 30, device="cuda")
+        old, vector = x.clone(), torch.zeros(40, 30, dtype=torch.bool, device="cuda")
+        vector[pick, 10:] = True
+        vector[:, :10] = True
+        true = math.sqrt(squares(old[vector]))
+        norm_check(g14.clip_grad_norm([x[pick, 10:], x[:, :10]], 1.0), true)
+        out_check(x[vector], old[vector], 1.0 / true)
+        assert torch.equal(x[~vector], old[~vector])
+
+
 def test_workspace_sizes():
     need = g14.grad_workspace_bytes
     assert need(0, 152) == 0 and need(-1, 152) == 0 and need((1 << 20) + 1, 152) == 0
