@@ -287,8 +287,8 @@ def ckpt8_weight_grad(dy: torch.Tensor, c: Ckpt8, out: torch.Tensor | None = Non
     return _on(stream, dy.device, body)
 
 
-# Calls of up to this many tokens may need no workspace (and no lock for it).
-_FEW_TOKENS = 4096
+# Calls of up to this many tokens need no workspace (and no lock for it), others one.
+_FEW_TOKENS = 1024
 
 
 def _tokens(tokens: torch.Tensor, device: int) -> int:
@@ -391,7 +391,7 @@ def embedding_backward(dy: torch.Tensor, tokens: torch.Tensor, rows: int | None 
         fn = _lib.load().gemm14_embedding_backward
         args = (code, out_code, T, V, D, _ptr(dy), lddy, _ptr(tokens), size, int(ignore_index),
                 float(scale), float(beta), dw.data_ptr(), lddw)
-        if T <= _FEW_TOKENS and not _lib.embedding_backward_workspace_bytes(code, T, V, D):
+        if T <= _FEW_TOKENS:
             status = fn(*args, None, 0, handle)
             if status:
                 raise _lib.Gemm14Error(status, "gemm14_embedding_backward")

@@ -415,6 +415,17 @@ def test_workspace_sizes():
     assert (1 << 24) < big <= (1 << 24) + 2 * 608 * 2 * 4096 * 4 + (1 << 16)
 
 
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("V,D", [(1, 1), (50021, 769), (300, 4096), (1 << 30, 8)])
+def test_the_tokens_that_need_no_workspace(V, D, dtype):
+    """The tensor-level call asks for none up to as many tokens as the library needs none for."""
+    from dense_gemm_14_gb300 import training
+    few = training._FEW_TOKENS
+    for sms in (1, 152):
+        need = [g14.embedding_backward_workspace_bytes(dtype, T, V, D, sms) for T in (0, 1, few // 2, few, few + 1, 2 * few)]
+        assert need[:4] == [0] * 4 and min(need[4:]) > 0
+
+
 @pytest.mark.gpu
 def test_small_workspace_is_refused():
     T = 5000
