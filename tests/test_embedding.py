@@ -235,6 +235,27 @@ def test_gradient_pitches_and_offsets(T, D, pad, offset, opad, ooffset, dtype, o
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale,beta", [(0.75, 0.5), (0.0, -1.0), (-2.0, 1.0)])
+@pytest.mark.parametrize("dtype,out", PAIRS)
+@pytest.mark.parametrize("T,V,D,pad,offset,opad,ooffset,kind", [
+    (1100, 61, 7, 1, 1, 1, 1, "text"), (2500, 3001, 130, 3, 5, 2, 7, "text"), (4096, 40, 257, 0, 0, 0, 0, "uniform"),
+    (5000, 900, 1001, 0, 0, 0, 0, "text"), (6000, 513, 257, 0, 1, 1, 0, "runs"), (5000, 7, 64, 0, 0, 1, 0, "uniform"),
+    (5000, 7, 64, 1, 0, 0, 0, "same"), (20000, 4001, 333, 0, 0, 0, 0, "text"), (40000, 300, 65, 1, 3, 0, 1, "text")])
+def test_gradient_of_rows_anywhere_with_any_factors(T, V, D, pad, offset, opad, ooffset, kind, dtype, out, scale, beta):
+    """Ranked and sorted places, sums at any address and joins; rows without tokens (whose
+    beta is theirs too), and what lies beside dW's rows."""
+    dy, tokens, dw0 = gradient_case(T, V, D, dtype, out, kind)
+    tokens[tokens == V - 3] = V - 2  # a row without tokens
+    _, dyv = view_of(dy, pad, offset, math.nan)
+    buf, dw = view_of(dw0, opad, ooffset, math.nan)
+    g14.embedding_backward(dyv, tokens.cuda(), out=dw, scale=scale, beta=beta)
+    gradient_check(dy, tokens, dw, scale, -100, beta, dw0)
+    assert torch.equal(dw[V - 3].cpu(), (dw0[V - 3].float() * beta).to(DT[out]))
+    dw.fill_(math.nan)
+    assert bool(torch.isnan(buf).all())  # nothing beside the rows was written
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,V,D", [(70000, 300001, 4), (300000, 50, 8), (131072, 1 << 20, 3), (3000, 1 << 19, 1)])
 @pytest.mark.parametrize("kind", ["uniform", "text", "ends"])
 def test_many_tokens_and_large_vocabularies(T, V, D, kind):
