@@ -433,8 +433,10 @@ __device__ __forceinline__ void finish_each(const Parts<kN>& t, const Finish& f,
 // start on 16 bytes, is read as two and a shift. kEach of them are in flight.
 // (As two stores of 16 bytes of fp32 output a clipping of 109 packed fp16 tensors of
 // 197 million values takes 316 us, 264 so.)
-// nvcc 13.0 writes only the first element of a store of 32 bytes, this one's or that of
-// a ulonglong4_32a, in a function that is not inlined: all that stand above one are.
+// With nvcc 13.0 a store of 32 bytes, this one's or that of a ulonglong4_32a, wrote only
+// its first element in a function that was not inlined; why is not known. So all that
+// stand above one are inlined, and tests hold the build to that and look at every
+// element that is stored, at each alignment.
 // Products are rounded to fp32 and then to a 16-bit type: within half a step and
 // 2^-24 of the value.
 template <typename O, int kPer>
@@ -650,7 +652,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
 // The scaling of a list of few units: each block forms the total itself, which costs
 // no more than a launch of grad_finish_kernel does, and saves the host that launch
-// (10 tensors of 8.3 MB, in place: 20.9 us a call with it, 15.6 so).
+// (10 tensors of 8 MB: 17.6 us of the host in place so and 20.3 with it, 21.3 and 23.6
+// into others; on the GPU alone 8.4 and 7.8, 11.8 and 10.5; of 2 MB 4.5 and 7.0, 7.2 and
+// 8.8; of 16 MB 10.7 and 8.8, 14.7 and 12.1).
 constexpr int64_t kFewUnits = 4096;
 template <int kN>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
@@ -680,9 +684,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // A short list: one cluster of kSmallCtas CTAs does all of it in one launch, its
 // barriers between the passes.
 constexpr int kSmallCtas = kFinishCtas, kSmallThreads = 1024, kSmallEntries = 72;
-// 4 MB, and 1 MB where they are scaled too: a call of 10 tensors of 2.6 MB takes 10.9 us
-// of the host so and 14.1 as two launches, its clipping 11.8 and 17.9 as three, but
-// eight SMs read and write 3.3 MB in 25 us.
+// 4 MB, and 1 MB where they are scaled too. What it saves is the host's time, which such
+// calls from a program are bound by: 10 tensors of 1 MB take 13.9 us so and 15.5 as two
+// launches, in place 14.6 and 17.1, into others 17.7 and 21.1; of 4 MB the norm 12.1 and
+// 15.2. On the GPU alone, as in a graph's replays, the launches are faster: of 1 MB 8.4
+// against 6.0 us for the norm, 9.0 against 4.7 in place, 12.0 against 7.0 into others; of
+// 4 MB the norm 10.9 against 6.4.
 constexpr int64_t kSmallUnits = 1024, kSmallScaled = 256;
 template <int kN>
 __global__ void __launch_bounds__(kSmallThreads, 1)
@@ -957,7 +964,9 @@ int scale_launch(const Call& c, int64_t i0) {
                        "gradient scaling launch", c.stream);
 }
 
-// Tables of three sizes: a launch's parameters are copied with it.
+// Tables of three sizes: a launch's parameters are copied with it (10 tensors in the
+// table of 544: 17.3 us of the host for the norm, 15.9 in that of 16; in three launches
+// into others 25.3 and 23.4; 40 tensors 25.1 and 23.7 in that of 72, 41.7 and 39.3).
 int run(const Call& c, int64_t units) {
   if (c.n <= kSmallEntries && units <= (c.clip ? kSmallScaled : kSmallUnits))
     return c.n <= 16 ? small_call<16>(c) : small_call<kSmallEntries>(c);
@@ -972,7 +981,9 @@ int run(const Call& c, int64_t units) {
     if (st != GEMM14_OK) return st;
   }
   if (!c.clip) return GEMM14_OK;
-  // from the last tensors to the first: what was read last is in L2 still
+  // from the last tensors to the first, for what L2 still holds of them: a list of 43 MB
+  // is read again from there (2 to 5 MB of it from DRAM), of 90 MB a third, as the norm's
+  // last readings are the ends of all warps' stretches
   for (int64_t i0 = (c.n - 1) / kMostEntries * kMostEntries; i0 >= 0; i0 -= kMostEntries) {
     const int64_t m = c.n - i0;
     const int st = m <= 16   ? scale_launch<16>(c, i0)

@@ -467,6 +467,21 @@ def test_a_row_beside_columns_is_clipped():
         assert torch.equal(x[~vector], old[~vector])
 
 
+def test_stores_of_32_bytes_stand_in_kernels():
+    """What the kernels are built of is inlined, but for the function that stores single elements."""
+    import os
+    import re
+
+    from dense_gemm_14_gb300 import build
+    log = os.path.join(build.BUILD_DIR, "grad_norm.ptxas.log")
+    if not os.path.exists(log):
+        pytest.skip("the build has left no log")
+    text = open(log).read()
+    kernels = set(re.findall(r"Compiling entry function '(\w+)'", text))
+    functions = set(re.findall(r"Function properties for (\w+)", text)) - kernels
+    assert kernels and all("scale_small" in f for f in functions), functions
+
+
 def test_workspace_sizes():
     need = g14.grad_workspace_bytes
     assert need(0, 152) == 0 and need(-1, 152) == 0 and need((1 << 20) + 1, 152) == 0
