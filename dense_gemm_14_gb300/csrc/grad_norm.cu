@@ -546,8 +546,8 @@ __device__ __forceinline__ void scale_unit(const Entry& e, const Unit& u, int la
 // A factor below fp32's normal numbers has fewer than 24 bits there, or is 0, while
 // its products with large values are normal numbers: it is multiplied in fp64, an
 // element at a time. Limits some 2^126 below the norm alone come here, so it stays out
-// of the others' registers. (100 fp32 tensors of 419 MB into others, values of 1e37: 1051 us
-// a call, 529 with a factor of 1e-11.)
+// of the others' registers. (100 fp32 tensors of 419 MB into others, values of 1e37: 1038 us
+// a call, 528 with a factor of 1e-11.)
 __device__ __forceinline__ bool small_factor(double by) {
   const float f = static_cast<float>(by);
   return fabsf(f) < 0x1p-126f && static_cast<double>(f) != by;
@@ -585,14 +585,26 @@ __device__ __forceinline__ void scale_small_unit(const Entry& e, const Unit& u, 
                 static_cast<char*>(e.dst) + (r * e.ld_dst + lo) * type_bytes(e.dst_type), e.type,
                 e.dst_type, n, lane, by);
 }
+template <int kN>
+__device__ __forceinline__ void scale_small_units(const Table<kN>& t, uint32_t w, uint32_t warps,
+                                                  int lane, double by) {
+  int i = 0;
+  for (uint32_t u = w; u < t.units; u += warps) {
+    while (i + 1 < t.n && t.e[i + 1].first_unit <= u) ++i;
+    scale_small_unit(t.e[i], unit_of(t.e[i], u - t.e[i].first_unit), lane, by);
+  }
+}
 
 // Every warps-th unit from the last down, so that the units at work at any time lie
 // side by side: reads and writes of one stretch of memory each.
 template <int kN>
 __device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint32_t warps,
                                             int lane, double by) {
+  if (small_factor(by)) {
+    scale_small_units(t, w, warps, lane, by);
+    return;
+  }
   const float f = static_cast<float>(by);
-  const bool small = small_factor(by);
   int i = t.n - 1;
   for (uint32_t left = t.units - w; left > 0; left = left > warps ? left - warps : 0u) {
     const uint32_t u = left - 1u;
@@ -600,9 +612,7 @@ __device__ __forceinline__ void scale_units(const Table<kN>& t, uint32_t w, uint
     const Entry& e = t.e[i];
     if (e.src == e.dst && f == 1.0f) continue;  // nothing changes
     const Unit at = unit_of(e, u - e.first_unit);
-    if (small) {
-      scale_small_unit(e, at, lane, by);
-    } else if (e.type == GEMM14_DTYPE_BF16) {
+    if (e.type == GEMM14_DTYPE_BF16) {
       if (e.dst_type == GEMM14_DTYPE_F32)
         scale_unit<__nv_bfloat16, float>(e, at, lane, f);
       else
